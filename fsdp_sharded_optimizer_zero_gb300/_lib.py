@@ -36,6 +36,8 @@ EXPORTS = (
     "fsdp_gather_rows", "fsdp_unit_forward", "fsdp_transpose_cat", "fsdp_unit_backward_workspace", "fsdp_unit_backward", "fsdp_mlp_forward",
     "fsdp_zero3_step_workspace", "fsdp_zero3_step", "fsdp_zero3_mlp_step_workspace", "fsdp_zero3_mlp_step",
     "fsdp_unit_forward_static_scratch",
+    "fsdp_checkpoint8_pack", "fsdp_checkpoint8_unpack", "fsdp_linear_forward", "fsdp_act_backward", "fsdp_linear_dx",
+    "fsdp_linear_dw",
     "zero_last_error", "zero_device_status", "zero_selftest_bounded_wait", "zero_set_fused_kernel", "zero_set_gemm_kernel", "zero_version",
 )
 
@@ -83,6 +85,13 @@ FSDP_BACKWARD_PREFETCH = 2
 FSDP_OVERLAP_OPTIMIZER = 4
 FSDP_SEPARATE_OPTIMIZER = 8
 
+FSDP_ACT_NONE = 0
+FSDP_ACT_RELU = 1
+FSDP_ACT_GELU = 2
+FSDP_ACT_GELU_TANH = 3
+FSDP_ACT_SILU = 4
+FSDP_CHECKPOINT8_GROUP = 32  # columns that share a scale byte
+
 
 class zero_adam(C.Structure):
     _fields_ = [("lr", C.c_float), ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float),
@@ -128,6 +137,12 @@ def _load():
         "fsdp_zero3_mlp_step_workspace": (I, [I, I, C.POINTER(fsdp_mlp_unit_state), I64, C.POINTER(U64)]),
         "fsdp_zero3_mlp_step": (I, [I, I, C.POINTER(fsdp_mlp_unit_state), I64, VP, VP, C.POINTER(zero_adam), I64, I,
                                     VP, U64, VP]),
+        "fsdp_checkpoint8_pack": (I, [VP, I64, I64, VP, VP, VP]),
+        "fsdp_checkpoint8_unpack": (I, [VP, VP, I64, I64, I, VP, VP]),
+        "fsdp_linear_forward": (I, [I, PP, I64, I64, VP, I64, VP, I, VP, VP, VP, VP, VP, VP]),
+        "fsdp_act_backward": (I, [VP, VP, VP, VP, I64, I64, I, VP, VP, VP]),
+        "fsdp_linear_dx": (I, [I, PP, I64, I64, VP, I64, VP, VP, VP, I, VP, VP, VP]),
+        "fsdp_linear_dw": (I, [VP, VP, VP, VP, I64, I64, I64, C.c_float, VP, VP, VP]),
         "zero_set_gemm_kernel": (I, [I]),
         "zero_version": (I, []),
     }
@@ -570,6 +585,104 @@ def fsdp_unit_forward_static_scratch(w_shards, A, Y, Y_bf16=None, stream=None):
     _check(_lib.fsdp_unit_forward_static_scratch(
         n, _ptr_array(w_shards, torch.bfloat16, "w_shards"), rows, k, _dev(A, torch.bfloat16, "A"),
         m_tok, _dev(Y, torch.float32, "Y"), _dev(Y_bf16, torch.bfloat16, "Y_bf16"), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------
+# linear unit with its epilogue, 8-bit activation checkpoints
+# ---------------------------------------------------------------------------------------
+
+def _is(t, shape, dtype, name: str):
+    """Device pointer of a tensor of exactly this shape and dtype (None passes as NULL)."""
+    if t is None:
+        return None
+    p = _dev(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    return p
+
+
+def _rows_cols(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return int(t.shape[0]), int(t.shape[1])
+
+
+def _kept(pair, shape, name: str):
+    """Pointers of an 8-bit checkpoint (codes, scales) of a [rows, cols] activation."""
+    if pair is None:
+        return None, None
+    codes, scales = pair
+    groups = -(-shape[1] // FSDP_CHECKPOINT8_GROUP)
+    return (_is(codes, shape, torch.int8, f"{name}[0] (codes)"),
+            _is(scales, (shape[0], groups), torch.uint8, f"{name}[1] (scales)"))
+
+
+def fsdp_checkpoint8_pack(x, codes, scales, stream=None):
+    """codes [rows, cols] int8, scales [rows, ceil(cols / 32)] uint8 = the 8-bit checkpoint of
+    x [rows, cols] bf16: value = code * 2^(scale - 127)."""
+    rows, cols = _rows_cols(x, "x")
+    pc, ps = _kept((codes, scales), (rows, cols), "checkpoint")
+    _check(_lib.fsdp_checkpoint8_pack(_dev(x, torch.bfloat16, "x"), rows, cols, pc, ps, _stream(stream)))
+
+
+def fsdp_checkpoint8_unpack(codes, scales, out, act: int = FSDP_ACT_NONE, stream=None):
+    """out [rows, cols] bf16 = act(values of the checkpoint)."""
+    rows, cols = _rows_cols(codes, "codes")
+    pc, ps = _kept((codes, scales), (rows, cols), "checkpoint")
+    _check(_lib.fsdp_checkpoint8_unpack(pc, ps, rows, cols, act, _is(out, (rows, cols), torch.bfloat16, "out"),
+                                        _stream(stream)))
+
+
+def fsdp_linear_forward(w_shards, X, Y, bias=None, act: int = FSDP_ACT_NONE, residual=None, z=None, z8=None,
+                        stream=None):
+    """Y = bf16(act(X W^T + bias) + residual); z (bf16) or z8 = (codes, scales) receives the
+    pre-activation X W^T + bias for the backward."""
+    n = len(w_shards)
+    rs, k = _shards_shape(w_shards, "w_shards")
+    m = _rows_cols(X, "X")[0]
+    r, bf = n * rs, torch.bfloat16
+    pc, ps = _kept(z8, (m, r), "z8")
+    _check(_lib.fsdp_linear_forward(
+        n, _ptr_array(w_shards, bf, "w_shards"), r, k, _is(X, (m, k), bf, "X"), m, _is(bias, (r,), bf, "bias"), act,
+        _is(residual, (m, r), bf, "residual"), _is(Y, (m, r), bf, "Y"), _is(z, (m, r), bf, "z"), pc, ps,
+        _stream(stream)))
+
+
+def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT_NONE, stream=None):
+    """dZ = bf16(dY act'(Z)), db = the fp32 column sums of dY act'(Z); Z as z (bf16) or z8 =
+    (codes, scales)."""
+    rows, cols = _rows_cols(dY, "dY")
+    bf = torch.bfloat16
+    pc, ps = _kept(z8, (rows, cols), "z8")
+    _check(_lib.fsdp_act_backward(
+        _dev(dY, bf, "dY"), _is(z, (rows, cols), bf, "z"), pc, ps, rows, cols, act, _is(dZ, (rows, cols), bf, "dZ"),
+        _is(db, (cols,), torch.float32, "db"), _stream(stream)))
+
+
+def fsdp_linear_dx(w_shards, dZ, dX, z=None, z8=None, act: int = FSDP_ACT_NONE, residual=None, stream=None):
+    """dX = bf16((dZ W) act'(Z) + residual), Z (z or z8) the kept pre-activation of the layer
+    that produced this layer's input."""
+    n = len(w_shards)
+    rs, k = _shards_shape(w_shards, "w_shards")
+    m = _rows_cols(dZ, "dZ")[0]
+    r, bf = n * rs, torch.bfloat16
+    pc, ps = _kept(z8, (m, k), "z8")
+    _check(_lib.fsdp_linear_dx(
+        n, _ptr_array(w_shards, bf, "w_shards"), r, k, _is(dZ, (m, r), bf, "dZ"), m, _is(z, (m, k), bf, "z"), pc, ps,
+        act, _is(residual, (m, k), bf, "residual"), _is(dX, (m, k), bf, "dX"), _stream(stream)))
+
+
+def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, stream=None):
+    """dW [rows_out, k_in] (fp32 or bf16) = scale * dZ^T X, X as x (bf16) or x8 = (codes,
+    scales)."""
+    m, r = _rows_cols(dZ, "dZ")
+    k = _rows_cols(dW, "dW")[1]
+    bf = torch.bfloat16
+    pc, ps = _kept(x8, (m, k), "x8")
+    wide = dW.dtype == torch.float32
+    pw = _is(dW, (r, k), torch.float32 if wide else bf, "dW")
+    _check(_lib.fsdp_linear_dw(_dev(dZ, bf, "dZ"), _is(x, (m, k), bf, "x"), pc, ps, m, r, k, scale,
+                               pw if wide else None, None if wide else pw, _stream(stream)))
 
 
 def zero_device_status(stream=None):

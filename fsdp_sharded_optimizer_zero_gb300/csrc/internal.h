@@ -149,6 +149,10 @@ class OncePerDevice {
 // gather, no scratch) under the current zero_set_gemm_kernel choice.
 bool fsdp_fused_gather_ok(int n_ranks, int64_t rows_out);
 
+// ---- linear unit (fsdp_linear.cu, fsdp_checkpoint8.cu) ----
+// act, and the kept activation it reads: bf16 z, or codes and scales (ZERO_ERR_INVALID_ARG)
+int check_kept_activation(const uint16_t* z, const int8_t* codes, const uint8_t* scales, int act, const char* who);
+
 // ---- errors (capi.cu) ----
 int set_error(int code, const char* fmt, ...);
 // Adam hyper-parameters and step validated as the step calls do (ZERO_ERR_INVALID_ARG)

@@ -24,7 +24,8 @@
  *     16-byte-aligned buffers take the vectorised path, others a scalar path with
  *     bit-identical results. The GEMM-based FSDP calls (fsdp_unit_forward and its static-
  *     scratch variant, fsdp_unit_backward, fsdp_mlp_forward), whose operands are TMA tensor
- *     maps, require 16-byte-aligned buffers and return ZERO_ERR_INVALID_ARG otherwise.
+ *     maps, and the linear-unit and 8-bit checkpoint calls require 16-byte-aligned buffers
+ *     and return ZERO_ERR_INVALID_ARG otherwise.
  *   - Arrays of per-rank pointers (grads[], masters[], w_shards[]) are HOST arrays of
  *     n_ranks device pointers; they are copied into the kernel's parameters, so the host
  *     array may be reused as soon as the call returns.
@@ -493,6 +494,83 @@ ZERO_API int fsdp_zero3_mlp_step(int n_ranks, int n_units, const fsdp_mlp_unit_s
 ZERO_API int fsdp_unit_forward_static_scratch(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out,
                                               int64_t k_in, const zero_bf16* A, int64_t m_tokens, float* Y,
                                               zero_bf16* Y_bf16, zero_stream_t stream);
+
+/* ------------------------------------------------------------------------------------ */
+/* Linear unit with its epilogue, and 8-bit activation checkpoints                        */
+/* ------------------------------------------------------------------------------------ */
+/* A linear layer as models have it, Y = act(X W^T + b) + R, its backward, and the activations
+ * kept between the two, which after ZeRO-3 / FSDP sharding of the states are most of what a
+ * card holds ([Interview] worked table: the 16 bytes per parameter exclude activations).
+ *
+ * 8-bit checkpoint of a [rows, cols] activation: int8 codes [rows, cols] and one scale byte
+ * per row and group of 32 columns, scales [rows, ceil(cols / 32)] (the last group of a row
+ * may be shorter): 1 + 1/32 bytes per element. value = code * 2^(byte - 127). The byte is the
+ * least with amax / 2^(byte - 127) < 127.5 (amax: the group's largest magnitude), kept in
+ * 1..248; code = the nearest integer (ties to even) to x / 2^(byte - 127), in [-127, 127]. So
+ * |x - value| <= 2^(byte - 127) / 2 <= amax / 127.5 (where 2^-127 is larger: 2^-127), and
+ * every value is exact in bf16. A group that holds an infinity or a NaN has byte 255 and zero
+ * codes: it reads back as NaN throughout.
+ *
+ * Activations: the FSDP_ACT_* values; GELU is x Phi(x), GELU_TANH its tanh form, SILU x / (1 +
+ * exp(-x)). They and their derivatives are computed in fp32 (relative error of a few 2^-20)
+ * from the fp32 sum or the kept activation, with one rounding to the output's type.
+ *
+ * Calls take every m_tokens / rows >= 1; widths (rows_out, k_in, cols) are multiples of 8,
+ * every buffer is 16-byte aligned, row-major and contiguous, and W is held as n_ranks (1..16)
+ * row shards of rows_out / n_ranks rows, a multiple of 8, read where they lie. Anything else
+ * is ZERO_ERR_INVALID_ARG and launches nothing. Outputs may not overlap inputs, except that
+ * fsdp_act_backward's dZ may be dY. A kept activation is passed either as z (bf16) or as
+ * z_codes and z_scales; both are ignored by FSDP_ACT_NONE. */
+#define FSDP_ACT_NONE 0
+#define FSDP_ACT_RELU 1
+#define FSDP_ACT_GELU 2
+#define FSDP_ACT_GELU_TANH 3
+#define FSDP_ACT_SILU 4
+
+/* codes, scales = the 8-bit checkpoint of x [rows, cols] bf16. */
+ZERO_API int fsdp_checkpoint8_pack(const zero_bf16* x, int64_t rows, int64_t cols, int8_t* codes, uint8_t* scales,
+                                   zero_stream_t stream);
+
+/* out [rows, cols] bf16 = act(values of the checkpoint). With FSDP_ACT_NONE the values
+ * themselves, exactly; with an activation, the layer's output recomputed from its kept
+ * pre-activation. */
+ZERO_API int fsdp_checkpoint8_unpack(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int act,
+                                     zero_bf16* out, zero_stream_t stream);
+
+/* Forward: Z = X W^T + bias (fp32), Y = bf16(act(Z) + residual).
+ * X [m_tokens, k_in], W [rows_out, k_in] as its row shards, bias [rows_out] (nullable),
+ * residual [m_tokens, rows_out] (nullable), Y [m_tokens, rows_out], all bf16.
+ * What the backward needs of Z, optionally: z [m_tokens, rows_out] bf16, or its 8-bit
+ * checkpoint z_codes / z_scales, taken from the fp32 Z (not both). The sum over k_in is an
+ * fp32 sum of exact bf16 products in an unspecified order (bound as fsdp_unit_forward). */
+ZERO_API int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t k_in,
+                                 const zero_bf16* X, int64_t m_tokens, const zero_bf16* bias, int act,
+                                 const zero_bf16* residual, zero_bf16* Y, zero_bf16* z, int8_t* z_codes,
+                                 uint8_t* z_scales, zero_stream_t stream);
+
+/* Backward of the activation and the bias: dZ = bf16(dY act'(Z)), db = sum over the rows of
+ * the unrounded dY act'(Z), fp32, in a fixed order (the same bits every call). dY, dZ [rows,
+ * cols] bf16, dZ nullable when db is asked for; db [cols] fp32, nullable. With FSDP_ACT_NONE, db is the column sum of
+ * dY. The residual's gradient is dY itself. */
+ZERO_API int fsdp_act_backward(const zero_bf16* dY, const zero_bf16* z, const int8_t* z_codes, const uint8_t* z_scales,
+                               int64_t rows, int64_t cols, int act, zero_bf16* dZ, float* db, zero_stream_t stream);
+
+/* Input gradient: dX = bf16((dZ W) act'(Z) + residual), with Z the kept pre-activation of the
+ * layer that produced this layer's input (so dX is that layer's dZ) and residual the gradient
+ * that reaches the input past this layer (nullable). dZ [m_tokens, rows_out]; dX, z, residual
+ * [m_tokens, k_in] bf16. */
+ZERO_API int fsdp_linear_dx(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t k_in,
+                            const zero_bf16* dZ, int64_t m_tokens, const zero_bf16* z, const int8_t* z_codes,
+                            const uint8_t* z_scales, int act, const zero_bf16* residual, zero_bf16* dX,
+                            zero_stream_t stream);
+
+/* Weight gradient: dW = scale * dZ^T X, [rows_out, k_in], fp32 (dW) or bf16 (dW_bf16), one of
+ * the two: the gradient types the step calls reduce. dZ [m_tokens, rows_out] bf16; X
+ * [m_tokens, k_in] as bf16 (x) or as its 8-bit checkpoint (x_codes, x_scales), whose values
+ * are multiplied exactly. scale (finite) is applied to the fp32 sum. */
+ZERO_API int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int8_t* x_codes, const uint8_t* x_scales,
+                            int64_t m_tokens, int64_t rows_out, int64_t k_in, float scale, float* dW,
+                            zero_bf16* dW_bf16, zero_stream_t stream);
 
 /* ------------------------------------------------------------------------------------ */
 /* status                                                                                */

@@ -529,13 +529,14 @@ extern "C" int zero_device_status(zero_stream_t stream) {
   const unsigned int a = step_kernels_read_clear_error();
   const unsigned int f = fused_step_read_clear_error();
   const unsigned int b = fsdp_gemm_read_clear_error();
-  if (a == 0xffffffffu || f == 0xffffffffu || b == 0xffffffffu)
+  const unsigned int l = fsdp_linear_read_clear_error();
+  if (a == 0xffffffffu || f == 0xffffffffu || b == 0xffffffffu || l == 0xffffffffu)
     return set_error(ZERO_ERR_CUDA, "zero_device_status: cannot read the device error word");
-  if (a || f || b)
+  if (a || f || b || l)
     return set_error(ZERO_ERR_DEVICE,
                      "zero_device_status: a bounded wait gave up (step kernels code 0x%x, fused step code 0x%x, "
-                     "FSDP GEMM code 0x%x; high byte = kernel, low byte = wait)",
-                     a, f, b);
+                     "FSDP GEMM code 0x%x, linear unit code 0x%x; high byte = kernel, low byte = wait)",
+                     a, f, b, l);
   return ZERO_OK;
 }
 

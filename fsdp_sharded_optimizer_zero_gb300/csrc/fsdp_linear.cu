@@ -1,146 +1,1014 @@
-// The linear unit with its epilogue: forward (bias, activation, residual, the kept
-// pre-activation), input gradient (activation's derivative, residual gradient) and weight
-// gradient (from bf16 or 8-bit activations).
+// The linear unit with its epilogue on the 5th-generation tensor cores: forward (bias,
+// activation, residual, the kept pre-activation), input gradient (activation's derivative,
+// residual gradient) and weight gradient (from bf16 or 8-bit activations).
 //
-// One simple kernel for the three products: a 32 x 32 output tile per block of 256 threads,
-// operands staged in shared memory as fp32, fp32 fused multiply-adds. 32 columns are one
-// group of the 8-bit checkpoint, so the epilogue runs row by row over the staged tile.
+//   forward  Y [m, r]  = epilogue(X [m, k] W^T)       contraction over k,  both K-major
+//   dx       dX [m, k] = epilogue(dZ [m, r] W)        contraction over r,  W read MN-major
+//   dw       dW [r, k] = scale dZ^T X                 contraction over m,  both MN-major
+//
+// Every operand is read where it lies: W from its row shards, transposed operands as
+// MN-major tiles. Two kernels:
+//   linear_wide_kernel    256 x 256 output tiles on CTA pairs (tcgen05.mma.cta_group::2),
+//                         persistent, the epilogue of one tile beside the main loop of the next;
+//   linear_narrow_kernel  128 output columns x TN output rows per CTA, the contraction split
+//                         over the CTAs of a cluster, which add their parts through
+//                         distributed shared memory in a fixed order. For outputs of too few
+//                         256 x 256 tiles to fill the GPU.
+// All sums are fp32 in tensor memory; every output is rounded once. Every mbarrier wait is
+// bounded: after one gives up the CTA's roles leave their loops, copies and MMAs in flight
+// are waited for, and zero_device_status reports it.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <string.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "linear_math.cuh"
+#include "tcgen05.cuh"
 
 namespace zgb {
+
+ZGB_DECLARE_ERROR_WORD();
+
 namespace {
 
 enum { OP_FWD, OP_DX, OP_DW };
 
+constexpr int BK = 64;                        // contraction elements of one stage (128 bytes of bf16)
+constexpr uint32_t kHalf = 128 * BK * 2;      // 128 rows (or MN-major columns) of one operand: 16 KiB
+constexpr uint32_t kChunk = 64 * BK * 2;      // 64 columns of an MN-major operand: 8 KiB
+
+constexpr unsigned int kErrEmpty = (5u << 8) | 1u;  // producer or converter waiting for a free stage
+constexpr unsigned int kErrFull = (5u << 8) | 2u;   // MMA waiting for a filled stage
+constexpr unsigned int kErrAccE = (5u << 8) | 3u;   // MMA waiting for a drained accumulator
+constexpr unsigned int kErrAccF = (5u << 8) | 4u;   // epilogue waiting for a finished accumulator
+constexpr unsigned int kErrDrain = (5u << 8) | 5u;  // waiting for copies or MMAs in flight
+
 struct LinearParams {
-  const uint16_t* w[kGemmMaxPieces];  // row shards of W [rows_out, k_in]
-  int shard_rows;
-  int m, n, k;                // the product: out [m, n], contraction over k
-  const uint16_t *a, *b;      // fwd: X; dx: dZ; dw: a = dZ, b = X (bf16)
-  const int8_t* b_codes;      // dw: X in 8 bits
-  const uint8_t* b_scales;
-  const uint16_t *bias, *res;
+  CUtensorMap w[kGemmMaxPieces];  // fwd, dx: the row shards of W, boxes of 64 columns x w_box rows
+  CUtensorMap a;                  // fwd: X, dx: dZ (K-major, box 64 x 128 or TN rows); dw: dZ (MN-major, box 64 x 64)
+  CUtensorMap b;                  // dw: X in bf16 (MN-major, box 64 x 64)
+  CUtensorMap out;                // wide kernel: the output, boxes of 64 bf16 or 32 fp32 columns x 32 rows
+  int m, n, k;                    // the product: out [m, n], contraction over k
+  int n_shards, shard_rows;       // fwd, dx
+  int w_box, w_box_log;           // rows of W per copy: the largest power of two <= 128 (fwd) or 64 (dx) that divides shard_rows
+  const int8_t* x_codes;          // dw: X in 8 bits
+  const uint8_t* x_scales;
+  const uint16_t *bias, *res;     // fwd: bias; fwd, dx: residual
   int act;
-  const uint16_t* z_in;       // dx: the kept pre-activation
+  const uint16_t* z_in;           // dx: the kept pre-activation
   const int8_t* zc_in;
   const uint8_t* zs_in;
-  uint16_t* out;              // bf16 output
-  float* out32;               // dw: fp32 output
-  uint16_t* z;                // fwd: kept pre-activation
-  int8_t* zc;
+  uint16_t* y;                    // bf16 output
+  float* y32;                     // dw: fp32 output
+  uint16_t* z;                    // fwd: pre-activation kept in bf16
+  int8_t* zc;                     // fwd: ... in 8 bits
   uint8_t* zs;
-  float scale;
+  float scale;                    // dw
+  int chunks, chunk_blocks;       // dw, fp32: the contraction in chunks of chunk_blocks K blocks (1 chunk otherwise)
 };
 
-template <int OP>
-__device__ __forceinline__ float load_a(const LinearParams& p, int i, int k) {
-  if (i >= p.m || k >= p.k) return 0.0f;
-  if constexpr (OP == OP_DW) return bf16_bits_to_f32(p.a[static_cast<size_t>(k) * p.m + i]);
-  return bf16_bits_to_f32(p.a[static_cast<size_t>(i) * p.k + k]);
-}
-template <int OP>
-__device__ __forceinline__ float load_b(const LinearParams& p, int j, int k) {
-  if (j >= p.n || k >= p.k) return 0.0f;
-  if constexpr (OP == OP_FWD) {
-    const int s = j / p.shard_rows;
-    return bf16_bits_to_f32(p.w[s][static_cast<size_t>(j - s * p.shard_rows) * p.k + k]);
-  } else if constexpr (OP == OP_DX) {
-    const int s = k / p.shard_rows;
-    return bf16_bits_to_f32(p.w[s][static_cast<size_t>(k - s * p.shard_rows) * p.n + j]);
+// ------------------------------------------------------------------------------------
+// operand copies: what one lane of the producer warp loads for each stage
+// ------------------------------------------------------------------------------------
+struct Copy {
+  const CUtensorMap* map;
+  uint32_t dst;   // byte offset in the stage
+  int x, y;       // coordinates of the first K block
+  bool k_major;   // x advances with K, y otherwise
+  bool w_rows;    // y walks W's rows through the shards (dx)
+  int shard;
+};
+__device__ __forceinline__ void copy_advance(const LinearParams& p, Copy& c) {
+  if (c.k_major) {
+    c.x += BK;
   } else {
-    const size_t at = static_cast<size_t>(k) * p.n + j;
-    if (!p.b_codes) return bf16_bits_to_f32(p.b[at]);
-    const float s = ckpt_scale(p.b_scales[static_cast<size_t>(k) * ((p.n + 31) / 32) + j / 32]);
-    return __fmul_rn(static_cast<float>(p.b_codes[at]), s);
+    c.y += BK;
+    if (c.w_rows)
+      while (c.y >= p.shard_rows && c.shard + 1 < p.n_shards) c.y -= p.shard_rows, ++c.shard, ++c.map;
+  }
+}
+// the shard that holds row `row` of W; rows past the last one stay in the last shard, past
+// its end (they read zeros)
+__device__ __forceinline__ void copy_seek(const LinearParams& p, Copy& c, int row) {
+  c.shard = min(row / p.shard_rows, p.n_shards - 1);
+  c.map = &p.w[c.shard];
+  c.y = row - c.shard * p.shard_rows;
+}
+// copies of W (fwd): 128 output columns from n0, K-major, 128 / w_box copies of w_box rows
+__device__ __forceinline__ int w_copies_k_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c) {
+  const int count = 128 >> p.w_box_log;
+  if (i >= 0 && i < count) {
+    c.k_major = true, c.w_rows = false;
+    copy_seek(p, c, n0 + i * p.w_box);
+    c.x = kb0 * BK;
+    c.dst = dst + static_cast<uint32_t>(i * p.w_box) * 128u;
+  }
+  return count;
+}
+// copies of W (dx): 128 output columns from n0, MN-major: two chunks of 64 columns, the 64 rows
+// of a K block in 64 / w_box copies each
+__device__ __forceinline__ int w_copies_mn_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c) {
+  const int per = 64 >> p.w_box_log, count = 2 * per;
+  if (i >= 0 && i < count) {
+    const int chunk = i / per, sub = i - chunk * per;
+    c.k_major = false, c.w_rows = true;
+    copy_seek(p, c, kb0 * BK + sub * p.w_box);
+    c.x = n0 + 64 * chunk;
+    c.dst = dst + static_cast<uint32_t>(chunk) * kChunk + static_cast<uint32_t>(sub * p.w_box) * 128u;
+  }
+  return count;
+}
+// an MN-major operand in one piece: `chunks` chunks of 64 columns from c0
+__device__ __forceinline__ int mn_copies(const CUtensorMap* map, int chunks, int i, int c0, int kb0, uint32_t dst, Copy& c) {
+  if (i >= 0 && i < chunks) {
+    c.map = map, c.k_major = false, c.w_rows = false, c.shard = 0;
+    c.x = c0 + 64 * i, c.y = kb0 * BK;
+    c.dst = dst + static_cast<uint32_t>(i) * kChunk;
+  }
+  return chunks;
+}
+// a K-major operand in one piece: one box of rows from r0
+__device__ __forceinline__ int k_copies(const CUtensorMap* map, int i, int r0, int kb0, uint32_t dst, Copy& c) {
+  if (i == 0) c.map = map, c.k_major = true, c.w_rows = false, c.shard = 0, c.x = kb0 * BK, c.y = r0, c.dst = dst;
+  return 1;
+}
+
+// ------------------------------------------------------------------------------------
+// 8-bit operand: 64 tokens x 128 columns of codes turned into the MN-major bf16 tile that the
+// MMA reads (two chunks of 64 columns; a token's 128-byte row of a chunk holds its 16-byte
+// pieces j at slot j ^ (token % 8)). 128 threads: thread c takes the 8 columns of unit c % 16 of
+// the tokens c / 16 + 8 i, so its slot is the same for all of them. The codes of the next
+// block are loaded before this one is converted.
+// ------------------------------------------------------------------------------------
+struct Codes {
+  uint2 w[8];
+  uint32_t scale[8];  // fp32 bits of 2^e
+};
+__device__ __forceinline__ void codes_load(const LinearParams& p, int kb, int c0, int c, Codes& r) {
+  const int col = c0 + (c & 15) * 8;
+  const int64_t groups = (p.n + 31) / 32;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t t = static_cast<int64_t>(kb) * BK + (c >> 4) + 8 * i;
+    const bool in = t < p.k && col < p.n;
+    r.w[i] = in ? __ldg(reinterpret_cast<const uint2*>(p.x_codes + t * p.n + col)) : make_uint2(0u, 0u);
+    r.scale[i] = in ? static_cast<uint32_t>(__ldg(p.x_scales + t * groups + (col >> 5))) << 23 : 0u;
+  }
+}
+__device__ __forceinline__ void codes_store(const Codes& r, uint8_t* tile, int c) {
+  const int u = c & 15, t0 = c >> 4;
+  uint8_t* at = tile + static_cast<uint32_t>(u >> 3) * kChunk + t0 * 128 + (((u & 7) ^ t0) * 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = __uint_as_float(r.scale[i]);
+    const uint32_t lo = r.w[i].x ^ 0x80808080u, hi = r.w[i].y ^ 0x80808080u;
+    // exact: a 7-bit integer times a power of two is a bf16 number
+    *reinterpret_cast<uint4*>(at + i * 1024) =
+        make_uint4(pack_bf16x2(ckpt_value(lo, 0, s), ckpt_value(lo, 1, s)),
+                   pack_bf16x2(ckpt_value(lo, 2, s), ckpt_value(lo, 3, s)),
+                   pack_bf16x2(ckpt_value(hi, 0, s), ckpt_value(hi, 1, s)),
+                   pack_bf16x2(ckpt_value(hi, 2, s), ckpt_value(hi, 3, s)));
   }
 }
 
-// the 32 columns col0 .. of one output row, from their fp32 sums
+// ------------------------------------------------------------------------------------
+// epilogues
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(v[j]), x[2 * j + 1] = bf16_hi(v[j]);
+}
+
+// wide kernel: 32 columns col0 .. of output row `row`, one thread, v their fp32 sums: the
+// output's values in place, and the forward's kept pre-activation stored. 32 columns are one
+// group of the 8-bit checkpoint; its scale byte is returned. Sums past column n are zero.
 template <int OP>
-__device__ void epilogue_row(const LinearParams& p, int row, int col0, const float* acc) {
-  const int n = min(32, p.n - col0);
+__device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, int col0, float (&v)[32]) {
   const size_t at = static_cast<size_t>(row) * p.n + col0;
-  const size_t group = static_cast<size_t>(row) * ((p.n + 31) / 32) + col0 / 32;
-  if constexpr (OP == OP_DW) {
-    for (int j = 0; j < n; ++j) {
-      const float v = __fmul_rn(acc[j], p.scale);
-      if (p.out32) p.out32[at + j] = v;
-      else p.out[at + j] = f32_to_bf16_bits(v);
+  const bool live = row < p.m;
+  uint32_t byte = 0;
+  if constexpr (OP == OP_FWD) {
+    if (p.bias) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (col0 + 8 * q < p.n) {
+          float b[8];
+          unpack8(ldg16(p.bias + col0 + 8 * q), b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * q + j] = __fadd_rn(v[8 * q + j], b[j]);
+        }
+    }
+    if (p.z && live) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (col0 + 8 * q < p.n)
+          __stcs(reinterpret_cast<uint4*>(p.z + at + 8 * q),
+                 make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                            pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])));
+    }
+    if (p.zc) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) amax = max_nan(amax, fabsf(v[j]));
+      byte = ckpt_byte(amax);
+      const float inv = ckpt_inv_scale(byte);
+      uint32_t w[8];
+      if (byte < 248u) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = ckpt_code4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], inv);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          w[q] = ckpt_code4(ckpt_clamped(v[4 * q], byte), ckpt_clamped(v[4 * q + 1], byte),
+                            ckpt_clamped(v[4 * q + 2], byte), ckpt_clamped(v[4 * q + 3], byte), inv);
+      }
+      if (live) {
+        if (col0 + 32 <= p.n && (p.n & 15) == 0) {
+          __stcs(reinterpret_cast<uint4*>(p.zc + at), make_uint4(w[0], w[1], w[2], w[3]));
+          __stcs(reinterpret_cast<uint4*>(p.zc + at) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (col0 + 8 * q < p.n) *reinterpret_cast<uint2*>(p.zc + at + 8 * q) = make_uint2(w[2 * q], w[2 * q + 1]);
+        }
+      }
+    }
+    with_act(p.act, [&](auto a) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
+    });
+  } else if constexpr (OP == OP_DX) {
+    if (p.act != FSDP_ACT_NONE && live) {
+      float s = 0.0f;
+      if (p.zc_in) s = ckpt_scale(__ldg(p.zs_in + static_cast<size_t>(row) * ((p.n + 31) / 32) + (col0 >> 5)));
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (col0 + 8 * q < p.n) {
+          float z[8];
+          if (p.zc_in) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(p.zc_in + at + 8 * q));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              z[j] = ckpt_value(c.x ^ 0x80808080u, j, s), z[4 + j] = ckpt_value(c.y ^ 0x80808080u, j, s);
+          } else {
+            unpack8(ldg16(p.z_in + at + 8 * q), z);
+          }
+          with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * q + j] = __fmul_rn(v[8 * q + j], act_grad<decltype(a)::value>(z[j]));
+          });
+        }
     }
   } else {
-    float amax = 0.0f;
-    for (int j = 0; j < n; ++j) {
-      float v = acc[j];
-      if constexpr (OP == OP_FWD) {
-        if (p.bias) v = __fadd_rn(v, bf16_bits_to_f32(p.bias[col0 + j]));
-        if (p.z) p.z[at + j] = f32_to_bf16_bits(v);
-        amax = max_nan(amax, fabsf(v));
-        with_act(p.act, [&](auto a) { v = act_fwd<decltype(a)::value>(v); });
-      } else if (p.act != FSDP_ACT_NONE) {
-        const float z = p.z_in ? bf16_bits_to_f32(p.z_in[at + j])
-                               : __fmul_rn(static_cast<float>(p.zc_in[at + j]), ckpt_scale(p.zs_in[group]));
-        with_act(p.act, [&](auto a) { v = __fmul_rn(v, act_grad<decltype(a)::value>(z)); });
-      }
-      if (p.res) v = __fadd_rn(v, bf16_bits_to_f32(p.res[at + j]));
-      p.out[at + j] = f32_to_bf16_bits(v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], p.scale);
+  }
+  if constexpr (OP != OP_DW) {
+    if (p.res && live) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (col0 + 8 * q < p.n) {
+          float r[8];
+          unpack8(ldg16(p.res + at + 8 * q), r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * q + j] = __fadd_rn(v[8 * q + j], r[j]);
+        }
     }
-    if (OP == OP_FWD && p.zc) {
-      const uint32_t b = ckpt_byte(amax);
-      const float inv = ckpt_inv_scale(b);
-      for (int j = 0; j < n; ++j) {
-        float v = acc[j];
-        if (p.bias) v = __fadd_rn(v, bf16_bits_to_f32(p.bias[col0 + j]));
-        if (b >= 248u) v = ckpt_clamped(v, b);
-        p.zc[at + j] = static_cast<int8_t>(ckpt_code_word(v, inv) & 0xFFu);
-      }
-      p.zs[group] = static_cast<uint8_t>(b);
+  }
+  return byte;
+}
+
+// narrow kernel: 4 columns of one output row per lane, 32 lanes across 128 columns; the 8 lanes
+// of a group of 32 columns share its scale byte through shuffles. Called by whole warps.
+template <int OP>
+__device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int col, float (&v)[4]) {
+  const size_t at = static_cast<size_t>(row) * p.n + col;
+  const bool live = row < p.m && col < p.n;
+  const size_t group = static_cast<size_t>(row) * ((p.n + 31) / 32) + (col >> 5);
+  if constexpr (OP == OP_DW) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], p.scale);
+    if (live && p.y32) __stcs(reinterpret_cast<float4*>(p.y32 + at), make_float4(v[0], v[1], v[2], v[3]));
+    if (live && !p.y32)
+      *reinterpret_cast<uint2*>(p.y + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    return;
+  }
+  if constexpr (OP == OP_FWD) {
+    if (p.bias && live) {
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
+      v[0] = __fadd_rn(v[0], bf16_lo(b.x)), v[1] = __fadd_rn(v[1], bf16_hi(b.x));
+      v[2] = __fadd_rn(v[2], bf16_lo(b.y)), v[3] = __fadd_rn(v[3], bf16_hi(b.y));
     }
+    if (p.z && live)
+      *reinterpret_cast<uint2*>(p.z + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    if (p.zc) {
+      float amax = max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int d = 1; d < 8; d *= 2) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      const uint32_t byte = ckpt_byte(amax);
+      const float inv = ckpt_inv_scale(byte);
+      uint32_t w;
+      if (byte < 248u)
+        w = ckpt_code4(v[0], v[1], v[2], v[3], inv);
+      else
+        w = ckpt_code4(ckpt_clamped(v[0], byte), ckpt_clamped(v[1], byte), ckpt_clamped(v[2], byte),
+                       ckpt_clamped(v[3], byte), inv);
+      if (live) {
+        *reinterpret_cast<uint32_t*>(p.zc + at) = w;
+        if ((col & 31) == 0) p.zs[group] = static_cast<uint8_t>(byte);
+      }
+    }
+    with_act(p.act, [&](auto a) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
+    });
+  } else if (p.act != FSDP_ACT_NONE && live) {
+    float z[4];
+    if (p.zc_in) {
+      const float s = ckpt_scale(__ldg(p.zs_in + group));
+      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.zc_in + at)) ^ 0x80808080u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = ckpt_value(c, j, s);
+    } else {
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.z_in + at));
+      z[0] = bf16_lo(b.x), z[1] = bf16_hi(b.x), z[2] = bf16_lo(b.y), z[3] = bf16_hi(b.y);
+    }
+    with_act(p.act, [&](auto a) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], act_grad<decltype(a)::value>(z[j]));
+    });
+  }
+  if (!live) return;
+  if (p.res) {
+    const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.res + at));
+    v[0] = __fadd_rn(v[0], bf16_lo(b.x)), v[1] = __fadd_rn(v[1], bf16_hi(b.x));
+    v[2] = __fadd_rn(v[2], bf16_lo(b.y)), v[3] = __fadd_rn(v[3], bf16_hi(b.y));
+  }
+  *reinterpret_cast<uint2*>(p.y + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// ------------------------------------------------------------------------------------
+// wide kernel
+// ------------------------------------------------------------------------------------
+// A cluster of two CTAs on two SMs per 256 x 256 output tile: each CTA loads 128 rows of the
+// first operand and 128 columns of the second, and the even CTA's MMA (M = N = 256) reads both
+// CTAs' shared memory. Persistent, two accumulators in tensor memory.
+//   warp 0       producer: lane i issues the i-th copy of a stage (TMA), both CTAs
+//   warp 1       MMA issuer (even CTA), tensor-memory allocation
+//   warps 2-9    epilogue: two warps per tensor-memory lane quarter, 128 columns each
+//   warps 10-13  (8-bit X) converters: the second operand's tile from codes
+template <bool X8> struct Wide {
+  static constexpr int STAGES = 5;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int CONV_WARPS = X8 ? 4 : 0;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS + CONV_WARPS);
+  static constexpr uint32_t STAGE = 2 * kHalf;
+  static constexpr uint32_t EPI = EPI_WARPS * 2u * 4096u;  // two 4 KiB staging buffers per warp
+  static constexpr uint32_t SMEM = STAGES * STAGE + EPI + 1024;
+};
+
+// tile order: bands of 12 row blocks, down the rows of one tile column, then the next: the
+// tiles in flight share few operand tiles, which stay in L2
+__device__ __forceinline__ void wide_tile_coords(int tile, int num_m, int num_n, int& mb, int& nb) {
+  constexpr int kBand = 12;
+  const int rows_in_band = kBand < num_m ? kBand : num_m;
+  const int band = tile / (rows_in_band * num_n), in_band = tile - band * rows_in_band * num_n;
+  const int rows = min(rows_in_band, num_m - band * rows_in_band);
+  mb = band * rows_in_band + in_band % rows;
+  nb = in_band / rows;
+}
+
+// a whole warp waits; lane 0 polls, sleeping between polls so that the epilogue warps leave the
+// issue slots to the producer and the MMA while a main loop runs
+__device__ __forceinline__ bool warp_wait_sleeping(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int code) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) {
+    if (mbar_try_wait(bar, parity)) {
+      ok = 1;
+    } else {
+      const unsigned long long t0 = globaltimer_ns();
+      for (unsigned int ns = 64;;) {
+        __nanosleep(ns);
+        if (mbar_try_wait(bar, parity)) {
+          ok = 1;
+          break;
+        }
+        if (*abort) break;
+        if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+          atomicCAS(&g_zgb_dev_error, 0u, code);
+          *abort = 1;
+          break;
+        }
+        if (ns < 512) ns *= 2;
+      }
+    }
+  }
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// fp32 add of a shared-memory box to global memory, in L2
+__device__ __forceinline__ void tma_reduce_add_2d(const void* tmap, int32_t x, int32_t y, uint32_t src_smem) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap),
+               "r"(x), "r"(y), "r"(src_smem)
+               : "memory");
+}
+
+template <int OP, bool X8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1)
+    linear_wide_kernel(const __grid_constant__ LinearParams p) {
+  static_assert(!X8 || OP == OP_DW, "8-bit operands: the weight gradient's X");
+  using C = Wide<X8>;
+  constexpr bool A_MN = OP == OP_DW, B_MN = OP != OP_FWD;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+  __shared__ __align__(8) uint64_t accf_bar[2];
+  __shared__ __align__(8) uint64_t acce_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  const int num_m = (p.m + 255) / 256, num_n = (p.n + 255) / 256, num_k = (p.k + BK - 1) / BK;
+  // work items: a tile's chunks one after the other on the same pair
+  const int tiles = num_m * num_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1 + 2 * C::CONV_WARPS);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&accf_bar[a]), 1);
+      mbar_init(smem_u32(&acce_bar[a]), 2 * C::EPI_WARPS);
+    }
+    mbar_init(smem_u32(&drain_bar), 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&tmem_base_sh), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers initialised and tensor memory allocated before any copy
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+
+  if (warp == 0) {
+    // ---------------- producer (both CTAs) ----------------
+    uint32_t it = 0, s = 0, ph = 0;  // K blocks issued; their stage and its phase parity
+    bool stop = false;
+    for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+      int mb, nb;
+      wide_tile_coords(tile, num_m, num_n, mb, nb);
+      const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
+      Copy c;
+      int i = lane;
+      if constexpr (A_MN) i -= mn_copies(&p.a, 2, i, m0, 0, 0, c);
+      else i -= k_copies(&p.a, i, m0, 0, 0, c);
+      if constexpr (OP == OP_FWD) i -= w_copies_k_major(p, i, n0, 0, kHalf, c);
+      else if constexpr (OP == OP_DX) i -= w_copies_mn_major(p, i, n0, 0, kHalf, c);
+      else if constexpr (!X8) i -= mn_copies(&p.b, 2, i, n0, 0, kHalf, c);
+      const bool mine = i < 0;
+      for (int kb = 0; kb < num_k; ++kb, ++it) {
+        bool ok = true;
+        if (it >= static_cast<uint32_t>(C::STAGES))
+          ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
+        if (!__all_sync(0xffffffffu, ok)) {
+          stop = true;
+          break;
+        }
+        if (rank == 0 && lane == 0)
+          mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * (X8 ? kHalf : 2 * kHalf));
+        if (mine) {
+          tma_load_2d_pair(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y,
+                           mapa_shared(smem_u32(&full_bar[s]), 0));
+          copy_advance(p, c);
+        }
+        __syncwarp();
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+    }
+    // every stage this CTA filled is read by the even CTA's MMAs: wait until they released it
+    if (lane == 0) {
+      int never = 0;
+      const uint32_t first = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
+      for (uint32_t j = first; j < it; ++j)
+        mbar_wait_bounded(smem_u32(&empty_bar[j % C::STAGES]), (j / C::STAGES) & 1u, &never, &g_zgb_dev_error, kErrDrain);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (even CTA) ----------------
+    if (rank == 0 && lane == 0) {
+      // the next 16 contraction elements: +32 bytes K-major, +2048 bytes MN-major
+      constexpr uint32_t a_step = A_MN ? 128u : 2u, b_step = B_MN ? 128u : 2u;
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, A_MN, B_MN);
+      uint32_t i = 0, s = 0, ph = 0;
+      bool stop = false, issued = false;
+      for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+        for (int kb = 0; kb < num_k && !stop; ++i) {  // one accumulator per chunk
+          const int kb_end = min(kb + p.chunk_blocks, num_k), kb_first = kb;
+          const uint32_t a = i & 1u, u = i >> 1;
+          if (u >= 1 && !mbar_wait_cluster_bounded(smem_u32(&acce_bar[a]), (u - 1) & 1u, abort, &g_zgb_dev_error, kErrAccE)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + a * 256;
+          for (; kb < kb_end; ++kb) {
+            if (!mbar_wait_cluster_bounded(smem_u32(&full_bar[s]), ph, abort, &g_zgb_dev_error, kErrFull)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem) + s * C::STAGE;
+            const uint64_t ad = A_MN ? sw128_mnmajor_desc(sa, kChunk) : sw128_kmajor_desc(sa);
+            const uint64_t bd = B_MN ? sw128_mnmajor_desc(sa + kHalf, kChunk) : sw128_kmajor_desc(sa + kHalf);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              umma_bf16_pair(d, ad + a_step * k, bd + b_step * k, idesc, (kb != kb_first || k != 0) ? 1u : 0u);
+            umma_commit_pair(smem_u32(&empty_bar[s]), 0x3);
+            issued = true;
+            if (++s == C::STAGES) s = 0, ph ^= 1u;
+          }
+          if (!stop) umma_commit_pair(smem_u32(&accf_bar[a]), 0x3);
+        }
+      }
+      if (*abort && issued) {
+        int never = 0;
+        umma_commit_pair(smem_u32(&drain_bar), 0x1);
+        mbar_wait_bounded(smem_u32(&drain_bar), 0, &never, &g_zgb_dev_error, kErrDrain);
+      }
+    }
+  } else if (warp < 2 + C::EPI_WARPS) {
+    // ---------------- epilogue (both CTAs, own 128 rows) ----------------
+    const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
+    const int part = (warp - 2) >> 2;  // which 128 columns
+    uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 2u * 4096u;
+    uint32_t i = 0, staged = 0;
+    bool stop = false;
+    for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+      int mb, nb;
+      wide_tile_coords(tile, num_m, num_n, mb, nb);
+      const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
+      const int c0 = nb * 256 + part * 128;
+      for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
+        const uint32_t a = i & 1u, u = i >> 1;
+        if (!warp_wait_sleeping(smem_u32(&accf_bar[a]), u & 1u, abort, kErrAccF)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * 128;
+        if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
+        if (OP == OP_DW && p.y32) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32cols(taddr + c, r);
+            if (c0 + c >= p.n) continue;
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            epilogue32<OP>(p, row, c0 + c, v);
+            uint8_t* buf = stage + (staged & 1u) * 4096u;
+            if (lane == 0 && staged >= 2) bulk_wait_group_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
+              else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(buf));
+              bulk_commit_group();
+            }
+            ++staged;
+          }
+        } else {
+          uint32_t bytes = 0;  // four scale bytes of this row
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t w[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              tmem_ld_32cols(taddr + c + 32 * h, r);
+              float v[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+              if (c0 + c + 32 * h < p.n) {
+                const uint32_t b = epilogue32<OP>(p, row, c0 + c + 32 * h, v);
+                bytes |= b << (8 * (c / 32 + h));
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            }
+            if (c0 + c >= p.n) continue;
+            uint8_t* buf = stage + (staged & 1u) * 4096u;
+            if (lane == 0 && staged >= 2) bulk_wait_group_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
+              bulk_commit_group();
+            }
+            ++staged;
+          }
+          if (OP == OP_FWD && p.zc && row < p.m) {
+            const int groups = (p.n + 31) / 32, g0 = c0 >> 5;
+            uint8_t* zs = p.zs + static_cast<size_t>(row) * groups + g0;
+            if ((groups & 3) == 0 && g0 + 4 <= groups) {
+              *reinterpret_cast<uint32_t*>(zs) = bytes;
+            } else {
+              for (int g = 0; g < 4; ++g)
+                if (g0 + g < groups) zs[g] = static_cast<uint8_t>(bytes >> (8 * g));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[a]), 0));
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();  // no store may still read this CTA's shared memory
+  } else if constexpr (X8) {
+    // ---------------- converters (both CTAs, own 128 columns) ----------------
+    const int c = static_cast<int>(threadIdx.x) - 32 * (2 + C::EPI_WARPS);
+    uint32_t it = 0, s = 0, ph = 0;
+    bool stop = false;
+    for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+      int mb, nb;
+      wide_tile_coords(tile, num_m, num_n, mb, nb);
+      const int n0 = nb * 256 + static_cast<int>(rank) * 128;
+      Codes next;
+      codes_load(p, 0, n0, c, next);
+      for (int kb = 0; kb < num_k; ++kb, ++it) {
+        const Codes now = next;
+        if (kb + 1 < num_k) codes_load(p, kb + 1, n0, c, next);
+        bool ok = true;
+        if (it >= static_cast<uint32_t>(C::STAGES))
+          ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
+        if (!__all_sync(0xffffffffu, ok)) {
+          stop = true;
+          break;
+        }
+        codes_store(now, smem + s * C::STAGE + kHalf, c);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[s]), 0));
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync_all();  // neither CTA's copies, MMAs or arrivals still target the other
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
-template <int OP>
-__global__ void __launch_bounds__(256) linear_kernel(const __grid_constant__ LinearParams p) {
-  __shared__ float sa[32][33], sb[32][33];  // [k][row], [k][column]
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int tiles_n = (p.n + 31) / 32;
-  const int64_t tiles = static_cast<int64_t>((p.m + 31) / 32) * tiles_n;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int i0 = static_cast<int>(tile / tiles_n) * 32, j0 = static_cast<int>(tile % tiles_n) * 32;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};  // rows ty + 8 q, column tx
-    for (int k0 = 0; k0 < p.k; k0 += 32) {
-      for (int q = 0; q < 4; ++q) {
-        const int t = ty + 8 * q;
-        // lanes along the operand's contiguous index
-        if constexpr (OP == OP_DW) sa[t][tx] = load_a<OP>(p, i0 + tx, k0 + t);
-        else sa[tx][t] = load_a<OP>(p, i0 + t, k0 + tx);
-        if constexpr (OP == OP_FWD) sb[tx][t] = load_b<OP>(p, j0 + t, k0 + tx);
-        else sb[t][tx] = load_b<OP>(p, j0 + tx, k0 + t);
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int q = 0; q < 4; ++q) acc[q] = __fmaf_rn(sa[k][ty + 8 * q], sb[k][tx], acc[q]);
-      __syncthreads();
+// ------------------------------------------------------------------------------------
+// narrow kernel
+// ------------------------------------------------------------------------------------
+// One tile per cluster: 128 output columns (the MMA's M side) x TN output rows (its N side, so
+// a few tokens cost a narrow MMA and a small copy). The cluster's CTAs split the K blocks;
+// each leaves its fp32 part in shared memory as [row][128 columns], and CTA c adds the parts of
+// rows c TN / S .. in CTA order and runs the epilogue on them, 4 columns a lane.
+//   warp 0      producer: lane i issues the i-th copy of a stage
+//   warp 1      MMA issuer, tensor-memory allocation
+//   warps 2-5   (8-bit X) converters
+//   all warps   the sum over the parts and the epilogue
+template <int TN> struct Narrow {
+  static constexpr uint32_t QB = TN * BK * 2;               // the row-side operand of a stage
+  static constexpr uint32_t STAGE = kHalf + QB;
+  static constexpr int STAGES = TN == 128 ? 3 : 5;          // two CTAs per SM
+  static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
+  static constexpr uint32_t TMEM_COLS = TN;
+  static_assert(STAGES * STAGE >= TN * 128 * 4, "the fp32 part takes the stages' place");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int OP, int TN, bool X8>
+__global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
+  static_assert(!X8 || OP == OP_DW, "8-bit operands: the weight gradient's X");
+  using C = Narrow<TN>;
+  constexpr bool P_MN = OP != OP_FWD, Q_MN = OP == OP_DW;  // P: the column side, Q: the row side
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+  __shared__ __align__(8) uint64_t acc_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster per tile
+  const int n0 = static_cast<int>(blockIdx.y) * 128, m0 = static_cast<int>(blockIdx.z) * TN;
+  const int num_k = (p.k + BK - 1) / BK;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(num_k) * rank / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(num_k) * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), X8 ? 5 : 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
     }
-    for (int q = 0; q < 4; ++q) sa[ty + 8 * q][tx] = acc[q];
-    __syncthreads();
-    if (threadIdx.x < 32 && i0 + static_cast<int>(threadIdx.x) < p.m)
-      epilogue_row<OP>(p, i0 + threadIdx.x, j0, sa[threadIdx.x]);
-    __syncthreads();
+    mbar_init(smem_u32(&acc_bar), 1);
+    abort_flag = 0;
+    fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_sh), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+
+  if (warp == 0) {
+    Copy c;
+    int i = lane;
+    if constexpr (OP == OP_FWD) i -= w_copies_k_major(p, i, n0, kb0, 0, c);
+    else if constexpr (OP == OP_DX) i -= w_copies_mn_major(p, i, n0, kb0, 0, c);
+    else if constexpr (!X8) i -= mn_copies(&p.b, 2, i, n0, kb0, 0, c);
+    if constexpr (Q_MN) i -= mn_copies(&p.a, TN / 64, i, m0, kb0, kHalf, c);
+    else i -= k_copies(&p.a, i, m0, kb0, kHalf, c);
+    const bool mine = i < 0;
+    uint32_t s = 0, ph = 0;
+    int issued = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+      bool ok = true;
+      if (issued >= C::STAGES)
+        ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), X8 ? C::QB : C::STAGE);
+      if (mine) {
+        tma_load_2d(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y, smem_u32(&full_bar[s]));
+        copy_advance(p, c);
+      }
+      __syncwarp();
+      if (++s == C::STAGES) s = 0, ph ^= 1u;
+    }
+    if (*abort && lane == 0) {  // copies in flight still write this CTA's shared memory
+      int never = 0;
+      for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+        mbar_wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never,
+                          &g_zgb_dev_error, kErrDrain);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t p_step = P_MN ? 128u : 2u, q_step = Q_MN ? 128u : 2u;
+      constexpr uint32_t idesc = idesc_bf16_f32(128, TN, P_MN, Q_MN);
+      uint32_t s = 0, ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(smem_u32(&full_bar[s]), ph, abort, &g_zgb_dev_error, kErrFull)) break;
+        tc_fence_after();
+        const uint32_t sp = smem_u32(smem) + s * C::STAGE;
+        const uint64_t pd = P_MN ? sw128_mnmajor_desc(sp, kChunk) : sw128_kmajor_desc(sp);
+        const uint64_t qd = Q_MN ? sw128_mnmajor_desc(sp + kHalf, kChunk) : sw128_kmajor_desc(sp + kHalf);
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k)
+          umma_bf16(tmem_base, pd + p_step * k, qd + q_step * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+        umma_commit(smem_u32(&empty_bar[s]));
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+      umma_commit(smem_u32(&acc_bar));  // every MMA issued, also after a wait that gave up
+    }
+    __syncwarp();
+  } else if (X8 && warp < 6) {
+    const int c = static_cast<int>(threadIdx.x) - 64;
+    uint32_t s = 0, ph = 0;
+    Codes next;
+    codes_load(p, kb0, n0, c, next);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const Codes now = next;
+      if (kb + 1 < kb1) codes_load(p, kb + 1, n0, c, next);
+      bool ok = true;
+      if (kb - kb0 >= C::STAGES)
+        ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      codes_store(now, smem + s * C::STAGE, c);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
+      if (++s == C::STAGES) s = 0, ph ^= 1u;
+    }
+  }
+
+  // the accumulator is complete (or, after an abort, no MMA runs any more)
+  int never = 0;
+  mbar_wait_bounded(smem_u32(&acc_bar), 0, &never, &g_zgb_dev_error, kErrAccF);
+  __syncthreads();
+  tc_fence_after();
+  // tensor memory lane l = output column n0 + l, column t = output row m0 + t
+  float* part = reinterpret_cast<float*>(smem);
+  {
+    const int q = warp & 3, half = warp >> 2;
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    for (int t0 = half * 32; t0 < TN; t0 += 64) {
+      uint32_t r[32];
+      tmem_ld_32cols(taddr + t0, r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) part[(t0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();  // every CTA's part is in its shared memory
+  const int rows = TN / splits;
+  const uint32_t base = smem_u32(smem);
+  for (int t = rank * rows + warp; t < (rank + 1) * rows; t += 8) {
+    if (m0 + t >= p.m) break;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) {
+      const float4 f = ld_cluster_f4(mapa_shared(base, s) + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
+      v[0] = __fadd_rn(v[0], f.x), v[1] = __fadd_rn(v[1], f.y);
+      v[2] = __fadd_rn(v[2], f.z), v[3] = __fadd_rn(v[3], f.w);
+    }
+    epilogue4<OP>(p, m0 + t, n0 + lane * 4, v);
+  }
+  cluster_sync_all();  // no CTA leaves while its part is read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// row-major [rows, cols] of bf16 or fp32, boxes of box_cols x box_rows (128 bytes wide) in the
+// 128-byte swizzle; out of range reads zeros, writes nothing
+int encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows, bool fp32,
+           const char* who) {
+  std::call_once(g_encode_once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return set_error(ZERO_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", who);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (fp32 ? 4 : 2)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(ZERO_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, (int)r);
+  return ZERO_OK;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <int OP>
-int launch(const LinearParams& p, cudaStream_t st, const char* who) {
-  const int64_t tiles = static_cast<int64_t>((p.m + 31) / 32) * ((p.n + 31) / 32);
-  linear_kernel<OP><<<static_cast<unsigned int>(std::min<int64_t>(tiles, 1 << 20)), 256, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+OncePerDevice g_attr_once[16];
+
+template <class K>
+int set_smem(OncePerDevice& once, K kernel, uint32_t bytes, const char* who) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = once.run(dev, [&] {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    });
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
+template <int OP, bool X8>
+int launch_wide(const LinearParams& p, cudaStream_t st, const char* who) {
+  using C = Wide<X8>;
+  int rc = set_smem(g_attr_once[OP + (X8 ? 1 : 0)], linear_wide_kernel<OP, X8>, C::SMEM, who);
+  if (rc) return rc;
+  const int64_t tiles = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + 255) / 256);
+  if (tiles > INT32_MAX / 2)
+    return set_error(ZERO_ERR_UNSUPPORTED, "%s: an output of %d x %d is more than 2^30 tiles", who, p.m, p.n);
+  const unsigned int pairs = static_cast<unsigned int>(std::min<int64_t>(tiles, std::max(1, num_sms() / 2)));
+  linear_wide_kernel<OP, X8><<<2 * pairs, C::THREADS, C::SMEM, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+}
+
+template <int OP, int TN, bool X8>
+int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char* who) {
+  using C = Narrow<TN>;
+  int rc = set_smem(g_attr_once[4 + (OP + (X8 ? 1 : 0)) * 2 + (TN == 128 ? 1 : 0)], linear_narrow_kernel<OP, TN, X8>,
+                    C::SMEM, who);
+  if (rc) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>((p.n + 127) / 128),
+                     static_cast<unsigned>((p.m + TN - 1) / TN));
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_narrow_kernel<OP, TN, X8>, p);
+  return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+}
+
+// fp32 weight gradients: the tensor cores add to the accumulator with truncation, about
+// 2^-24 of it per step, always toward zero (measured: 1.9e-5 of the result's norm over 16384
+// terms, 4.4e-6 over 4096). So an fp32 result is summed in parts of at most 64 blocks (4096
+// tokens), which are added with rounding to nearest: the narrow kernel's splits, or the wide
+// kernel's chunks, added in memory by the same warp in order. bf16 results round 2^-8 anyway
+// and take one part.
+constexpr int kMaxChunkBlocks = 64;
+
+// Kernel choice: the wide kernel once its tiles keep most CTA pairs busy, the narrow one with
+// the contraction split over up to 8 CTAs below that and for up to 32 rows.
+struct Choice {
+  bool wide;
+  int tn, splits;
+};
+Choice choose(int op, int64_t m, int64_t n, int64_t k, bool fp32) {
+  const int64_t wide_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t blocks = (k + BK - 1) / BK, col_tiles = (n + 127) / 128;
+  const bool few_rows = op != OP_DW && m <= 32;
+  Choice c{true, 128, 1};
+  if ((wide_tiles * 8 >= num_sms() * 3 && !few_rows) || (fp32 && blocks > 8 * kMaxChunkBlocks) || col_tiles > 65535)
+    return c;
+  c.wide = false;
+  if (few_rows) c.tn = 32;
+  const int64_t tiles = ((m + c.tn - 1) / c.tn) * col_tiles;
+  while (c.splits < 8 && blocks >= 4 * c.splits && tiles * c.splits * 2 <= 2 * num_sms()) c.splits *= 2;
+  while (fp32 && c.splits < 8 && blocks > static_cast<int64_t>(c.splits) * kMaxChunkBlocks) c.splits *= 2;
+  return c;
+}
+
+// the product's operands as the entry points get them
+struct Operands {
+  int n_shards;
+  const uint16_t* const* w;  // fwd, dx
+  const uint16_t* a;         // X, dZ, dZ
+  const uint16_t* x;         // dw: X in bf16 (null: in 8 bits)
+};
+
+template <int OP, bool X8>
+int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who) {
+  const bool fp32 = p.y32 != nullptr;
+  const Choice c = choose(OP, p.m, p.n, p.k, fp32);
+  const int blocks = (p.k + BK - 1) / BK;
+  p.chunk_blocks = c.wide && fp32 ? kMaxChunkBlocks : blocks;
+  p.chunks = (blocks + p.chunk_blocks - 1) / p.chunk_blocks;
+  int rc;
+  if constexpr (OP == OP_DW) {
+    if ((rc = encode(&p.a, o.a, p.k, p.m, 64, BK, false, who))) return rc;
+    if (!X8 && (rc = encode(&p.b, o.x, p.k, p.n, 64, BK, false, who))) return rc;
+  } else {
+    if ((rc = encode(&p.a, o.a, p.m, p.k, BK, c.wide ? 128 : c.tn, false, who))) return rc;
+    const int most = OP == OP_FWD ? 128 : BK;
+    p.n_shards = o.n_shards;
+    p.w_box = std::min(p.shard_rows & -p.shard_rows, most);
+    for (p.w_box_log = 3; (1 << p.w_box_log) < p.w_box;) ++p.w_box_log;
+    const int64_t w_cols = OP == OP_FWD ? p.k : p.n;
+    for (int s = 0; s < o.n_shards; ++s)
+      if ((rc = encode(&p.w[s], o.w[s], p.shard_rows, w_cols, 64, p.w_box, false, who))) return rc;
+  }
+  if (c.wide) {
+    rc = fp32 ? encode(&p.out, p.y32, p.m, p.n, 32, 32, true, who) : encode(&p.out, p.y, p.m, p.n, 64, 32, false, who);
+    if (rc) return rc;
+    return launch_wide<OP, X8>(p, st, who);
+  }
+  if constexpr (OP != OP_DW)
+    if (c.tn == 32) return launch_narrow<OP, 32, false>(p, c.splits, st, who);
+  return launch_narrow<OP, 128, X8>(p, c.splits, st, who);
 }
 
 int check_sizes(int64_t m, int64_t r, int64_t k, const char* who) {
@@ -153,7 +1021,7 @@ int check_sizes(int64_t m, int64_t r, int64_t k, const char* who) {
   return ZERO_OK;
 }
 
-int load_shards(LinearParams* p, int n, const zero_bf16* const w_shards[], int64_t rows_out, const char* who) {
+int check_shards(LinearParams* p, int n, const zero_bf16* const w_shards[], int64_t rows_out, const char* who) {
   if (n < 1 || n > kGemmMaxPieces)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: n_ranks %d outside 1..%d", who, n, kGemmMaxPieces);
   if (rows_out % n || (rows_out / n) % 8)
@@ -165,13 +1033,21 @@ int load_shards(LinearParams* p, int n, const zero_bf16* const w_shards[], int64
       return set_error(ZERO_ERR_INVALID_ARG, "%s: w_shards[%d] is NULL (missing rank)", who, q);
     if (!aligned16(w_shards[q]))
       return set_error(ZERO_ERR_INVALID_ARG, "%s: w_shards[%d] must be 16-byte aligned", who, q);
-    p->w[q] = w_shards[q];
   }
   p->shard_rows = static_cast<int>(rows_out / n);
   return ZERO_OK;
 }
 
+
 }  // namespace
+
+unsigned int fsdp_linear_read_clear_error() {
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_zgb_dev_error, sizeof(v)) != cudaSuccess) return 0xffffffffu;
+  if (v) cudaMemcpyToSymbol(g_zgb_dev_error, &zero, sizeof(zero));
+  return v;
+}
+
 }  // namespace zgb
 
 using namespace zgb;
@@ -185,7 +1061,7 @@ extern "C" int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[
   memset(&p, 0, sizeof(p));
   int rc;
   if ((rc = check_sizes(m_tokens, rows_out, k_in, who))) return rc;
-  if ((rc = load_shards(&p, n_ranks, w_shards, rows_out, who))) return rc;
+  if ((rc = check_shards(&p, n_ranks, w_shards, rows_out, who))) return rc;
   if (act < FSDP_ACT_NONE || act > FSDP_ACT_SILU)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: act %d is not one of FSDP_ACT_*", who, act);
   if (!X || !Y) return set_error(ZERO_ERR_INVALID_ARG, "%s: X or Y is NULL", who);
@@ -195,9 +1071,10 @@ extern "C" int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[
       !aligned16(z_codes) || !aligned16(z_scales))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: every buffer must be 16-byte aligned", who);
   p.m = static_cast<int>(m_tokens), p.n = static_cast<int>(rows_out), p.k = static_cast<int>(k_in);
-  p.a = X, p.bias = bias, p.res = residual, p.act = act;
-  p.out = Y, p.z = z, p.zc = z_codes, p.zs = z_scales;
-  return launch<OP_FWD>(p, reinterpret_cast<cudaStream_t>(stream), who);
+  p.bias = bias, p.res = residual, p.act = act;
+  p.y = Y, p.z = z, p.zc = z_codes, p.zs = z_scales;
+  const Operands o{n_ranks, w_shards, X, nullptr};
+  return launch<OP_FWD, false>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
 }
 
 extern "C" int fsdp_linear_dx(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t k_in,
@@ -209,15 +1086,16 @@ extern "C" int fsdp_linear_dx(int n_ranks, const zero_bf16* const w_shards[], in
   memset(&p, 0, sizeof(p));
   int rc;
   if ((rc = check_sizes(m_tokens, rows_out, k_in, who))) return rc;
-  if ((rc = load_shards(&p, n_ranks, w_shards, rows_out, who))) return rc;
+  if ((rc = check_shards(&p, n_ranks, w_shards, rows_out, who))) return rc;
   if (!dZ || !dX) return set_error(ZERO_ERR_INVALID_ARG, "%s: dZ or dX is NULL", who);
   if ((rc = check_kept_activation(z, z_codes, z_scales, act, who))) return rc;
   if (!aligned16(dZ) || !aligned16(residual) || !aligned16(dX))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: every buffer must be 16-byte aligned", who);
   p.m = static_cast<int>(m_tokens), p.n = static_cast<int>(k_in), p.k = static_cast<int>(rows_out);
-  p.a = dZ, p.res = residual, p.act = act, p.out = dX;
+  p.res = residual, p.act = act, p.y = dX;
   if (act != FSDP_ACT_NONE) p.z_in = z, p.zc_in = z_codes, p.zs_in = z_scales;
-  return launch<OP_DX>(p, reinterpret_cast<cudaStream_t>(stream), who);
+  const Operands o{n_ranks, w_shards, dZ, nullptr};
+  return launch<OP_DX, false>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
 }
 
 extern "C" int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int8_t* x_codes, const uint8_t* x_scales,
@@ -238,7 +1116,9 @@ extern "C" int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int
       !aligned16(dW_bf16))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: every buffer must be 16-byte aligned", who);
   p.m = static_cast<int>(rows_out), p.n = static_cast<int>(k_in), p.k = static_cast<int>(m_tokens);
-  p.a = dZ, p.b = x, p.b_codes = x_codes, p.b_scales = x_scales, p.scale = scale;
-  p.out32 = dW, p.out = dW_bf16;
-  return launch<OP_DW>(p, reinterpret_cast<cudaStream_t>(stream), who);
+  p.x_codes = x_codes, p.x_scales = x_scales, p.scale = scale;
+  p.y32 = dW, p.y = dW_bf16;
+  const Operands o{0, nullptr, dZ, x};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return x_codes ? launch<OP_DW, true>(p, o, st, who) : launch<OP_DW, false>(p, o, st, who);
 }

@@ -152,6 +152,7 @@ bool fsdp_fused_gather_ok(int n_ranks, int64_t rows_out);
 // ---- linear unit (fsdp_linear.cu, fsdp_checkpoint8.cu) ----
 // act, and the kept activation it reads: bf16 z, or codes and scales (ZERO_ERR_INVALID_ARG)
 int check_kept_activation(const uint16_t* z, const int8_t* codes, const uint8_t* scales, int act, const char* who);
+unsigned int fsdp_linear_read_clear_error();
 
 // ---- errors (capi.cu) ----
 int set_error(int code, const char* fmt, ...);

@@ -37,7 +37,7 @@ EXPORTS = (
     "fsdp_zero3_step_workspace", "fsdp_zero3_step", "fsdp_zero3_mlp_step_workspace", "fsdp_zero3_mlp_step",
     "fsdp_unit_forward_static_scratch",
     "fsdp_checkpoint8_pack", "fsdp_checkpoint8_unpack", "fsdp_linear_forward", "fsdp_act_backward", "fsdp_linear_dx",
-    "fsdp_linear_dw",
+    "fsdp_linear_dw", "fsdp_linear_dw_workspace",
     "zero_last_error", "zero_device_status", "zero_selftest_bounded_wait", "zero_set_fused_kernel", "zero_set_gemm_kernel", "zero_version",
 )
 
@@ -142,7 +142,8 @@ def _load():
         "fsdp_linear_forward": (I, [I, PP, I64, I64, VP, I64, VP, I, VP, VP, VP, VP, VP, VP]),
         "fsdp_act_backward": (I, [VP, VP, VP, VP, I64, I64, I, VP, VP, VP]),
         "fsdp_linear_dx": (I, [I, PP, I64, I64, VP, I64, VP, VP, VP, I, VP, VP, VP]),
-        "fsdp_linear_dw": (I, [VP, VP, VP, VP, I64, I64, I64, C.c_float, VP, VP, VP]),
+        "fsdp_linear_dw": (I, [VP, VP, VP, VP, I64, I64, I64, C.c_float, VP, VP, VP, U64, VP]),
+        "fsdp_linear_dw_workspace": (I, [I64, I64, C.POINTER(U64)]),
         "zero_set_gemm_kernel": (I, [I]),
         "zero_version": (I, []),
     }
@@ -161,8 +162,8 @@ def _check(rc: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the raw handle of torch.cuda.current_stream(), without building its object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -171,6 +172,12 @@ def _stream(stream) -> int:
 def _dev(t: torch.Tensor, dtype, name: str) -> int:
     if t is None:
         return None
+    # the common case in a few attribute reads: a call with eight shards checks fifteen tensors
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == torch._C._cuda_getDevice()):
+        return t.data_ptr()
+    if isinstance(name, tuple):  # element of a list, named only when it is refused
+        name = "%s[%d]" % name
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device.type != "cuda":
@@ -188,7 +195,7 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
 def _ptr_array(ts, dtype, name):
     arr = (C.c_void_p * len(ts))()
     for i, t in enumerate(ts):
-        arr[i] = _dev(t, dtype, f"{name}[{i}]")
+        arr[i] = _dev(t, dtype, (name, i))
     return arr
 
 
@@ -258,10 +265,10 @@ def _check_step(plan: "Plan", rank: int, grads=None, state=(), param_out=None):
 
 def _shards_shape(shards, name: str):
     """(rows of one shard, columns): every shard the same 2-D shape."""
-    shapes = {tuple(s.shape) for s in shards}
-    if len(shapes) != 1 or len(next(iter(shapes))) != 2:
-        raise ValueError(f"{name} must be 2-D tensors of one shape (got {sorted(shapes)})")
-    return next(iter(shapes))
+    first = shards[0].shape if len(shards) else None
+    if first is None or len(first) != 2 or any(s.shape != first for s in shards):
+        raise ValueError(f"{name} must be 2-D tensors of one shape (got {sorted({tuple(s.shape) for s in shards})})")
+    return first[0], first[1]
 
 
 # ---------------------------------------------------------------------------------------
@@ -596,7 +603,7 @@ def _is(t, shape, dtype, name: str):
     if t is None:
         return None
     p = _dev(t, dtype, name)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     return p
 
@@ -672,17 +679,31 @@ def fsdp_linear_dx(w_shards, dZ, dX, z=None, z8=None, act: int = FSDP_ACT_NONE, 
         act, _is(residual, (m, k), bf, "residual"), _is(dX, (m, k), bf, "dX"), _stream(stream)))
 
 
-def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, stream=None):
+def fsdp_linear_dw_workspace(m_tokens: int, k_in: int) -> int:
+    """Workspace bytes of fsdp_linear_dw with X in 8 bits."""
+    b = C.c_uint64()
+    _check(_lib.fsdp_linear_dw_workspace(m_tokens, k_in, C.byref(b)))
+    return b.value
+
+
+def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, workspace=None, stream=None):
     """dW [rows_out, k_in] (fp32 or bf16) = scale * dZ^T X, X as x (bf16) or x8 = (codes,
-    scales)."""
+    scales). workspace (with x8): a uint8 CUDA tensor of fsdp_linear_dw_workspace(...) bytes;
+    None takes it from PyTorch's allocator for this call."""
     m, r = _rows_cols(dZ, "dZ")
     k = _rows_cols(dW, "dW")[1]
     bf = torch.bfloat16
     pc, ps = _kept(x8, (m, k), "x8")
     wide = dW.dtype == torch.float32
     pw = _is(dW, (r, k), torch.float32 if wide else bf, "dW")
+    if pc is not None and workspace is None:
+        workspace = torch.empty(fsdp_linear_dw_workspace(m, k), dtype=torch.uint8, device=dZ.device)
+        if stream is not None:  # not to be reused before that stream is done with it
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(stream))
     _check(_lib.fsdp_linear_dw(_dev(dZ, bf, "dZ"), _is(x, (m, k), bf, "x"), pc, ps, m, r, k, scale,
-                               pw if wide else None, None if wide else pw, _stream(stream)))
+                               pw if wide else None, None if wide else pw, _dev(workspace, torch.uint8, "workspace"),
+                               0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 def zero_device_status(stream=None):

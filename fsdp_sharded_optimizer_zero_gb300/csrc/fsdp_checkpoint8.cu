@@ -5,9 +5,10 @@
 //   unpack   act(code * 2^(byte - 127)) -> bf16
 //   act_backward   dZ = bf16(dY act'(Z)), db = column sums of dY act'(Z) in fp32
 //
-// A thread works on 8 columns (16 bytes of bf16, 8 codes), four neighbouring lanes on one
-// group of 32. cols is a multiple of 8, so each 8-column unit is whole; the last group of a
-// row may have fewer than four units, and the lanes past it hold zeros.
+// Widths that are multiples of 32 have no partial group, so a checkpoint is flat: pack and
+// unpack walk it 8 elements a lane (four lanes to a group) without knowing rows. Other
+// widths go row by row, a warp to four rows; the
+// last group of a row may then have fewer than four lanes with data, the others hold zeros.
 #include <algorithm>
 
 #include "linear_math.cuh"
@@ -17,131 +18,324 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(v[j]), x[2 * j + 1] = bf16_hi(v[j]);
+// 8 values as 4 pairs
+__device__ __forceinline__ void widen8(const uint4& w, f2 (&x)[4]) {
+  x[0] = f2_from_bf16x2(w.x), x[1] = f2_from_bf16x2(w.y), x[2] = f2_from_bf16x2(w.z), x[3] = f2_from_bf16x2(w.w);
 }
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow8(const f2 (&x)[4]) {
+  return make_uint4(f2_to_bf16x2(x[0]), f2_to_bf16x2(x[1]), f2_to_bf16x2(x[2]), f2_to_bf16x2(x[3]));
 }
-__device__ __forceinline__ void decode8(const uint2& c, uint32_t byte, float (&x)[8]) {
+__device__ __forceinline__ void decode8(const uint2& c, uint32_t byte, f2 (&x)[4]) {
   const float s = ckpt_scale(byte);
-  const uint32_t lo = c.x ^ 0x80808080u, hi = c.y ^ 0x80808080u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = ckpt_value(lo, j, s), x[4 + j] = ckpt_value(hi, j, s);
+  for (int j = 0; j < 2; ++j) x[j] = ckpt_values2(c.x, j, s), x[2 + j] = ckpt_values2(c.y, j, s);
+}
+// codes of 8 values whose group has scale byte b
+__device__ __forceinline__ uint2 encode8(f2 (&v)[4], uint32_t b) {
+  if (b >= 248u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = ckpt_clamped(v[j], b);
+  }
+  const float inv = ckpt_inv_scale(b);
+  return make_uint2(ckpt_code4(v[0], v[1], inv), ckpt_code4(v[2], v[3], inv));
+}
+__device__ __forceinline__ float amax8(const f2 (&v)[4]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = amax2(m, v[j]);
+  return m;
 }
 
-__global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __restrict__ x, int64_t rows,
-                                                              int64_t cols, int8_t* __restrict__ codes,
-                                                              uint8_t* __restrict__ scales) {
-  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup, per_row = 4 * groups, total = rows * per_row;
+constexpr int kFlatBlocks = 16;  // blocks per SM of the flat kernels
+constexpr int kFlat = 4;  // units a thread has in flight in the flat kernels
+
+// flat: units of 8 elements, four lanes to a group; every access of a warp is contiguous
+__global__ void __launch_bounds__(kThreads) ckpt8_pack_flat_kernel(const uint16_t* __restrict__ x, int64_t units,
+                                                                   int8_t* __restrict__ codes,
+                                                                   uint8_t* __restrict__ scales) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  // total and stride are multiples of 4: the four lanes of a group stay together
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += stride) {
-    const int64_t row = i / per_row, u = i - row * per_row;
-    const bool valid = u * 8 < cols;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (valid) widen8(__ldcs(reinterpret_cast<const uint4*>(x + row * cols + u * 8)), v);
-    float amax = 0.0f;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += kFlat * stride) {
+    uint4 w[kFlat];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[j]));
-    const uint32_t four = 0xFu << (threadIdx.x & 28u);
-    amax = max_nan(amax, __shfl_xor_sync(four, amax, 1));
-    amax = max_nan(amax, __shfl_xor_sync(four, amax, 2));
-    const uint32_t b = ckpt_byte(amax);
-    if (b >= 248u) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = ckpt_clamped(v[j], b);
+    for (int k = 0; k < kFlat; ++k) {
+      const int64_t i = i0 + k * stride;
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < units) w[k] = __ldcs(reinterpret_cast<const uint4*>(x) + i);
     }
-    const float inv = ckpt_inv_scale(b);
-    if (valid)
-      *reinterpret_cast<uint2*>(codes + row * cols + u * 8) =
-          make_uint2(ckpt_code4(v[0], v[1], v[2], v[3], inv), ckpt_code4(v[4], v[5], v[6], v[7], inv));
-    if ((u & 3) == 0) scales[row * groups + (u >> 2)] = static_cast<uint8_t>(b);
+#pragma unroll
+    for (int k = 0; k < kFlat; ++k) {
+      const int64_t i = i0 + k * stride;
+      f2 v[4];
+      widen8(w[k], v);
+      float amax = amax8(v);
+      // units and stride are multiples of 4: a group's lanes are in the loop together
+      const uint32_t four = 0xFu << (threadIdx.x & 28u);
+      amax = max_nan(amax, __shfl_xor_sync(four, amax, 1));
+      amax = max_nan(amax, __shfl_xor_sync(four, amax, 2));
+      const uint32_t byte = ckpt_byte(amax);
+      const uint2 c = encode8(v, byte);
+      if (i < units) {
+        reinterpret_cast<uint2*>(codes)[i] = c;
+        if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(byte);
+      }
+    }
   }
 }
 
 template <int ACT>
-__global__ void __launch_bounds__(kThreads) ckpt8_unpack_kernel(const int8_t* __restrict__ codes,
-                                                                const uint8_t* __restrict__ scales, int64_t rows,
-                                                                int64_t cols, uint16_t* __restrict__ out) {
-  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup, units = cols / 8, total = rows * units;
+__global__ void __launch_bounds__(kThreads) ckpt8_unpack_flat_kernel(const int8_t* __restrict__ codes,
+                                                                     const uint8_t* __restrict__ scales,
+                                                                     int64_t units, uint16_t* __restrict__ out) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += stride) {
-    const int64_t row = i / units, u = i - row * units;
-    float v[8];
-    decode8(__ldcs(reinterpret_cast<const uint2*>(codes + row * cols + u * 8)), scales[row * groups + (u >> 2)], v);
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += kFlat * stride) {
+    uint2 w[kFlat];
+    uint32_t byte[kFlat];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = act_fwd<ACT>(v[j]);
-    __stcs(reinterpret_cast<uint4*>(out + row * cols + u * 8), narrow8(v));
-  }
-}
-
-// One block per strip of 64 columns: 8 lanes across a row's strip, 32 rows at a time. Each
-// thread sums its rows in order; the 32 row lanes are then summed in order in shared memory.
-template <int ACT, bool Z8>
-__global__ void __launch_bounds__(kThreads) act_backward_kernel(const uint16_t* __restrict__ dy,
-                                                                const uint16_t* __restrict__ z,
-                                                                const int8_t* __restrict__ codes,
-                                                                const uint8_t* __restrict__ scales, int64_t rows,
-                                                                int64_t cols, uint16_t* dz, float* __restrict__ db) {
-  __shared__ float part[32][65];
-  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
-  const int lane = threadIdx.x & 7, rl = threadIdx.x >> 3;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane * 8;
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (col < cols) {
-    for (int64_t row = rl; row < rows; row += 32) {
-      float g[8], v[8];
-      widen8(*reinterpret_cast<const uint4*>(dy + row * cols + col), g);
-      if constexpr (ACT != FSDP_ACT_NONE) {
-        if constexpr (Z8)
-          decode8(__ldcs(reinterpret_cast<const uint2*>(codes + row * cols + col)), scales[row * groups + (col >> 5)],
-                  v);
-        else
-          widen8(__ldcs(reinterpret_cast<const uint4*>(z + row * cols + col)), v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], act_grad<ACT>(v[j]));
+    for (int k = 0; k < kFlat; ++k) {
+      const int64_t i = i0 + k * stride;
+      if (i < units) {
+        w[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i);
+        byte[k] = scales[i >> 2];
       }
-      if (dz) *reinterpret_cast<uint4*>(dz + row * cols + col) = narrow8(g);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] = __fadd_rn(sum[j], g[j]);
+    for (int k = 0; k < kFlat; ++k) {
+      const int64_t i = i0 + k * stride;
+      if (i < units) {
+        f2 v[4];
+        decode8(w[k], byte[k], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = act_fwd<ACT>(v[j]);
+        __stcs(reinterpret_cast<uint4*>(out) + i, narrow8(v));
+      }
     }
   }
-  if (!db) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) part[rl][lane * 8 + j] = sum[j];
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    float s = part[0][threadIdx.x];
-    for (int i = 1; i < 32; ++i) s = __fadd_rn(s, part[i][threadIdx.x]);
-    if (c < cols) db[c] = s;
-  }
 }
 
-unsigned int grid_streaming(int64_t units) {
-  const int64_t blocks = (units + kThreads - 1) / kThreads;
-  return static_cast<unsigned int>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms()) * 8));
+// row by row: warp w takes rows 4 w .. 4 w + 3, lane l the columns 8 (l + 32 c)
+constexpr int kRows = 4;
+__global__ void __launch_bounds__(kThreads) ckpt8_pack_rows_kernel(const uint16_t* __restrict__ x, int64_t rows,
+                                                                   int64_t cols, int8_t* __restrict__ codes,
+                                                                   uint8_t* __restrict__ scales) {
+  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t r0 = kRows * (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)); r0 < rows;
+       r0 += kRows * warps)
+    for (int64_t u0 = 0; u0 < 4 * groups; u0 += 32) {
+      const int64_t col = (u0 + lane) * 8;
+      uint4 w[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        w[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r0 + k < rows && col < cols) w[k] = __ldcs(reinterpret_cast<const uint4*>(x + (r0 + k) * cols + col));
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        f2 v[4];
+        widen8(w[k], v);
+        float amax = amax8(v);
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t byte = ckpt_byte(amax);
+        const uint2 c = encode8(v, byte);
+        if (r0 + k < rows && col < cols) {
+          *reinterpret_cast<uint2*>(codes + (r0 + k) * cols + col) = c;
+          if ((lane & 3) == 0) scales[(r0 + k) * groups + (col >> 5)] = static_cast<uint8_t>(byte);
+        }
+      }
+    }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kThreads) ckpt8_unpack_rows_kernel(const int8_t* __restrict__ codes,
+                                                                     const uint8_t* __restrict__ scales, int64_t rows,
+                                                                     int64_t cols, uint16_t* __restrict__ out) {
+  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t r0 = kRows * (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)); r0 < rows;
+       r0 += kRows * warps)
+    for (int64_t col = lane * 8; col < cols; col += 256) {
+      uint2 w[kRows];
+      uint32_t byte[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (r0 + k < rows) {
+          w[k] = __ldcs(reinterpret_cast<const uint2*>(codes + (r0 + k) * cols + col));
+          byte[k] = scales[(r0 + k) * groups + (col >> 5)];
+        }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (r0 + k < rows) {
+          f2 v[4];
+          decode8(w[k], byte[k], v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = act_fwd<ACT>(v[j]);
+          __stcs(reinterpret_cast<uint4*>(out + (r0 + k) * cols + col), narrow8(v));
+        }
+    }
+}
+
+// Activation backward with the column sums. A cluster of blocks takes a strip of 8 LANES
+// columns, each block a run of its rows: LANES threads across the strip (8 columns each),
+// kThreads / LANES rows at a time, four of a thread's rows in flight. A thread sums its rows in
+// order; a block adds its row lanes in order through shared memory, and block c of the cluster
+// the columns c, c + blocks, .. of all blocks' sums, in block order: the same bits every call, and no
+// memory between launches.
+#ifndef ACT_UN
+#define ACT_UN 4
+#endif
+#ifndef ACT_MB
+#define ACT_MB 2
+#endif
+template <int ACT, bool Z8, int LANES>
+__global__ void __launch_bounds__(kThreads, ACT_MB) act_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
+                                                                   const int8_t* __restrict__ codes,
+                                                                   const uint8_t* __restrict__ scales, int64_t rows,
+                                                                   int64_t cols, int64_t rows_per_block, int64_t strip0,
+                                                                   uint16_t* dz, float* __restrict__ db) {
+  constexpr int RL = kThreads / LANES, STRIP = 8 * LANES, UN = ACT == FSDP_ACT_NONE ? 8 : ACT_UN;
+  __shared__ float part[RL][STRIP + 1];
+  __shared__ float sums[STRIP];
+  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
+  const int lane = threadIdx.x % LANES, rl = threadIdx.x / LANES;
+  const int64_t col0 = (strip0 + blockIdx.y) * STRIP, col = col0 + lane * 8;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows_per_block, last = min(first + rows_per_block, rows);
+  f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+  if (col < cols) {
+    for (int64_t r0 = first + rl; r0 < last; r0 += UN * RL) {
+      uint4 gw[UN], zw[UN];
+      uint2 cw[UN];
+      uint32_t byte[UN];
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        const int64_t row = r0 + k * RL;
+        if (row < last) {
+          gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy + row * cols + col));
+          if constexpr (ACT != FSDP_ACT_NONE) {
+            if constexpr (Z8) {
+              cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes + row * cols + col));
+              byte[k] = scales[row * groups + (col >> 5)];
+            } else {
+              zw[k] = __ldcs(reinterpret_cast<const uint4*>(z + row * cols + col));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        const int64_t row = r0 + k * RL;
+        if (row < last) {
+          f2 g[4], v[4];
+          widen8(gw[k], g);
+          if constexpr (ACT != FSDP_ACT_NONE) {
+            if constexpr (Z8) decode8(cw[k], byte[k], v);
+            else widen8(zw[k], v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
+          }
+          if (dz) __stcs(reinterpret_cast<uint4*>(dz + row * cols + col), narrow8(g));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], g[j]);
+        }
+      }
+    }
+  }
+  if (!db) return;  // the same for every block of a cluster
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f2_split(sum[j], part[rl][lane * 8 + 2 * j], part[rl][lane * 8 + 2 * j + 1]);
+  __syncthreads();
+  if (threadIdx.x < STRIP) {
+    float s = part[0][threadIdx.x];
+#pragma unroll 8
+    for (int i = 1; i < RL; ++i) s = __fadd_rn(s, part[i][threadIdx.x]);
+    sums[threadIdx.x] = s;
+  }
+  cluster_sync_all();
+  const int blocks = static_cast<int>(gridDim.x);  // one cluster across the rows
+  const int c = static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.x) * blocks;
+  if (c < STRIP) {
+    float s = 0.0f;
+    for (int b = 0; b < blocks; ++b) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&sums[c]), b)) : "memory");
+      s = b == 0 ? v : __fadd_rn(s, v);
+    }
+    if (col0 + c < cols) db[col0 + c] = s;
+  }
+  cluster_sync_all();  // no block leaves while its sums are read
+}
+
+unsigned int grid_for(int64_t threads, int blocks_per_sm) {
+  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+  return static_cast<unsigned int>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms()) * blocks_per_sm));
+}
+
+template <int ACT, bool Z8, int LANES>
+cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales,
+                          int64_t rows, int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
+  constexpr int RL = kThreads / LANES, STRIP = 8 * LANES;
+  int blocks = 1;  // across the rows: no fewer than four rows a thread
+  while (blocks < 8 && rows > static_cast<int64_t>(blocks) * RL * 4) blocks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int64_t per = (rows + blocks - 1) / blocks;
+  // strips in launches of at most 65535 (the grid's y limit)
+  for (int64_t s0 = 0, strips = (cols + STRIP - 1) / STRIP; s0 < strips; s0 += 65535) {
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min<int64_t>(strips - s0, 65535)), 1);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, act_backward_kernel<ACT, Z8, LANES>, dy, z, codes, scales, rows, cols,
+                                             per, s0, dz, db);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// Strips of 128 columns (a row of a strip is two lines of dY) where their blocks fill the GPU;
+// narrower ones, down to 32 columns (one group), for narrow matrices
+template <int ACT, bool Z8>
+cudaError_t launch_act(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales, int64_t rows,
+                       int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
+  const int64_t want = 2 * num_sms();
+  if ((cols + 127) / 128 * 8 >= want) return launch_strips<ACT, Z8, 16>(dy, z, codes, scales, rows, cols, dz, db, st);
+  return launch_strips<ACT, Z8, 4>(dy, z, codes, scales, rows, cols, dz, db, st);
 }
 
 template <int ACT>
 cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales,
                                 int64_t rows, int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
-  const unsigned int grid = static_cast<unsigned int>((cols + 63) / 64);
-  if (codes && ACT != FSDP_ACT_NONE)
-    act_backward_kernel<ACT, true><<<grid, kThreads, 0, st>>>(dy, z, codes, scales, rows, cols, dz, db);
-  else
-    act_backward_kernel<ACT, false><<<grid, kThreads, 0, st>>>(dy, z, codes, scales, rows, cols, dz, db);
+  if constexpr (ACT != FSDP_ACT_NONE)
+    if (codes) return launch_act<ACT, true>(dy, z, codes, scales, rows, cols, dz, db, st);
+  return launch_act<ACT, false>(dy, z, codes, scales, rows, cols, dz, db, st);
+}
+
+cudaError_t launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, uint8_t* scales, cudaStream_t st) {
+  if (cols % kCkptGroup == 0) {
+    const int64_t units = rows * (cols / 8);
+    ckpt8_pack_flat_kernel<<<grid_for(units, kFlatBlocks), kThreads, 0, st>>>(x, units, codes, scales);
+  } else {
+    ckpt8_pack_rows_kernel<<<grid_for((rows + kRows - 1) / kRows * 32, 8), kThreads, 0, st>>>(x, rows, cols, codes, scales);
+  }
   return cudaGetLastError();
 }
 
 template <int ACT>
 cudaError_t launch_unpack(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
                           cudaStream_t st) {
-  ckpt8_unpack_kernel<ACT><<<grid_streaming(rows * (cols / 8)), kThreads, 0, st>>>(codes, scales, rows, cols, out);
+  if (cols % kCkptGroup == 0) {
+    const int64_t units = rows * (cols / 8);
+    ckpt8_unpack_flat_kernel<ACT><<<grid_for(units, kFlatBlocks), kThreads, 0, st>>>(codes, scales, units, out);
+  } else {
+    ckpt8_unpack_rows_kernel<ACT><<<grid_for((rows + kRows - 1) / kRows * 32, 8), kThreads, 0, st>>>(codes, scales, rows,
+                                                                                                 cols, out);
+  }
   return cudaGetLastError();
 }
 
@@ -184,10 +378,7 @@ extern "C" int fsdp_checkpoint8_pack(const zero_bf16* x, int64_t rows, int64_t c
   if (!x || !codes || !scales) return set_error(ZERO_ERR_INVALID_ARG, "%s: NULL argument", who);
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: x, codes and scales must be 16-byte aligned", who);
-  const int64_t units = rows * (4 * ((cols + kCkptGroup - 1) / kCkptGroup));
-  ckpt8_pack_kernel<<<grid_streaming(units), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(x, rows, cols,
-                                                                                                    codes, scales);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pack(x, rows, cols, codes, scales, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 

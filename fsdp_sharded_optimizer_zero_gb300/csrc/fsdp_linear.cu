@@ -39,7 +39,7 @@ constexpr int BK = 64;                        // contraction elements of one sta
 constexpr uint32_t kHalf = 128 * BK * 2;      // 128 rows (or MN-major columns) of one operand: 16 KiB
 constexpr uint32_t kChunk = 64 * BK * 2;      // 64 columns of an MN-major operand: 8 KiB
 
-constexpr unsigned int kErrEmpty = (5u << 8) | 1u;  // producer or converter waiting for a free stage
+constexpr unsigned int kErrEmpty = (5u << 8) | 1u;  // producer waiting for a free stage
 constexpr unsigned int kErrFull = (5u << 8) | 2u;   // MMA waiting for a filled stage
 constexpr unsigned int kErrAccE = (5u << 8) | 3u;   // MMA waiting for a drained accumulator
 constexpr unsigned int kErrAccF = (5u << 8) | 4u;   // epilogue waiting for a finished accumulator
@@ -48,13 +48,11 @@ constexpr unsigned int kErrDrain = (5u << 8) | 5u;  // waiting for copies or MMA
 struct LinearParams {
   CUtensorMap w[kGemmMaxPieces];  // fwd, dx: the row shards of W, boxes of 64 columns x w_box rows
   CUtensorMap a;                  // fwd: X, dx: dZ (K-major, box 64 x 128 or TN rows); dw: dZ (MN-major, box 64 x 64)
-  CUtensorMap b;                  // dw: X in bf16 (MN-major, box 64 x 64)
+  CUtensorMap b;                  // dw: X (MN-major, box 64 x 64)
   CUtensorMap out;                // wide kernel: the output, boxes of 64 bf16 or 32 fp32 columns x 32 rows
   int m, n, k;                    // the product: out [m, n], contraction over k
   int n_shards, shard_rows;       // fwd, dx
   int w_box, w_box_log;           // rows of W per copy: the largest power of two <= 128 (fwd) or 64 (dx) that divides shard_rows
-  const int8_t* x_codes;          // dw: X in 8 bits
-  const uint8_t* x_scales;
   const uint16_t *bias, *res;     // fwd: bias; fwd, dx: residual
   int act;
   const uint16_t* z_in;           // dx: the kept pre-activation
@@ -136,95 +134,54 @@ __device__ __forceinline__ int k_copies(const CUtensorMap* map, int i, int r0, i
 }
 
 // ------------------------------------------------------------------------------------
-// 8-bit operand: 64 tokens x 128 columns of codes turned into the MN-major bf16 tile that the
-// MMA reads (two chunks of 64 columns; a token's 128-byte row of a chunk holds its 16-byte
-// pieces j at slot j ^ (token % 8)). 128 threads: thread c takes the 8 columns of unit c % 16 of
-// the tokens c / 16 + 8 i, so its slot is the same for all of them. The codes of the next
-// block are loaded before this one is converted.
-// ------------------------------------------------------------------------------------
-struct Codes {
-  uint2 w[8];
-  uint32_t scale[8];  // fp32 bits of 2^e
-};
-__device__ __forceinline__ void codes_load(const LinearParams& p, int kb, int c0, int c, Codes& r) {
-  const int col = c0 + (c & 15) * 8;
-  const int64_t groups = (p.n + 31) / 32;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t t = static_cast<int64_t>(kb) * BK + (c >> 4) + 8 * i;
-    const bool in = t < p.k && col < p.n;
-    r.w[i] = in ? __ldg(reinterpret_cast<const uint2*>(p.x_codes + t * p.n + col)) : make_uint2(0u, 0u);
-    r.scale[i] = in ? static_cast<uint32_t>(__ldg(p.x_scales + t * groups + (col >> 5))) << 23 : 0u;
-  }
-}
-__device__ __forceinline__ void codes_store(const Codes& r, uint8_t* tile, int c) {
-  const int u = c & 15, t0 = c >> 4;
-  uint8_t* at = tile + static_cast<uint32_t>(u >> 3) * kChunk + t0 * 128 + (((u & 7) ^ t0) * 16);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = __uint_as_float(r.scale[i]);
-    const uint32_t lo = r.w[i].x ^ 0x80808080u, hi = r.w[i].y ^ 0x80808080u;
-    // exact: a 7-bit integer times a power of two is a bf16 number
-    *reinterpret_cast<uint4*>(at + i * 1024) =
-        make_uint4(pack_bf16x2(ckpt_value(lo, 0, s), ckpt_value(lo, 1, s)),
-                   pack_bf16x2(ckpt_value(lo, 2, s), ckpt_value(lo, 3, s)),
-                   pack_bf16x2(ckpt_value(hi, 0, s), ckpt_value(hi, 1, s)),
-                   pack_bf16x2(ckpt_value(hi, 2, s), ckpt_value(hi, 3, s)));
-  }
-}
-
-// ------------------------------------------------------------------------------------
 // epilogues
 // ------------------------------------------------------------------------------------
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(v[j]), x[2 * j + 1] = bf16_hi(v[j]);
+__device__ __forceinline__ void unpack8(const uint4& w, f2* x) {
+  x[0] = f2_from_bf16x2(w.x), x[1] = f2_from_bf16x2(w.y), x[2] = f2_from_bf16x2(w.z), x[3] = f2_from_bf16x2(w.w);
 }
 
-// wide kernel: 32 columns col0 .. of output row `row`, one thread, v their fp32 sums: the
+// wide kernel: 32 columns col0 .. of output row `row`, one thread, v their fp32 sums in pairs: the
 // output's values in place, and the forward's kept pre-activation stored. 32 columns are one
-// group of the 8-bit checkpoint; its scale byte is returned. Sums past column n are zero.
+// group of the 8-bit checkpoint; its scale byte is returned. Sums past column n are zero. bias:
+// the 32 columns' biases in fp32 in shared memory (null: none).
 template <int OP>
-__device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, int col0, float (&v)[32]) {
+__device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, int col0, const float* bias,
+                                               f2 (&v)[16]) {
   const size_t at = static_cast<size_t>(row) * p.n + col0;
   const bool live = row < p.m;
   uint32_t byte = 0;
   if constexpr (OP == OP_FWD) {
-    if (p.bias) {
+    if (bias) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (col0 + 8 * q < p.n) {
-          float b[8];
-          unpack8(ldg16(p.bias + col0 + 8 * q), b);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[8 * q + j] = __fadd_rn(v[8 * q + j], b[j]);
-        }
+      for (int q = 0; q < 8; ++q) {
+        const float4 b = *reinterpret_cast<const float4*>(bias + 4 * q);
+        v[2 * q] = f2_add(v[2 * q], f2_make(b.x, b.y));
+        v[2 * q + 1] = f2_add(v[2 * q + 1], f2_make(b.z, b.w));
+      }
     }
     if (p.z && live) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (col0 + 8 * q < p.n)
           __stcs(reinterpret_cast<uint4*>(p.z + at + 8 * q),
-                 make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                            pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])));
+                 make_uint4(f2_to_bf16x2(v[4 * q]), f2_to_bf16x2(v[4 * q + 1]), f2_to_bf16x2(v[4 * q + 2]),
+                            f2_to_bf16x2(v[4 * q + 3])));
     }
     if (p.zc) {
       float amax = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) amax = max_nan(amax, fabsf(v[j]));
+      for (int j = 0; j < 16; ++j) amax = amax2(amax, v[j]);
       byte = ckpt_byte(amax);
       const float inv = ckpt_inv_scale(byte);
       uint32_t w[8];
       if (byte < 248u) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = ckpt_code4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], inv);
+        for (int q = 0; q < 8; ++q) w[q] = ckpt_code4(v[2 * q], v[2 * q + 1], inv);
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          w[q] = ckpt_code4(ckpt_clamped(v[4 * q], byte), ckpt_clamped(v[4 * q + 1], byte),
-                            ckpt_clamped(v[4 * q + 2], byte), ckpt_clamped(v[4 * q + 3], byte), inv);
+          w[q] = ckpt_code4(ckpt_clamped(v[2 * q], byte), ckpt_clamped(v[2 * q + 1], byte), inv);
       }
       if (live) {
         if (col0 + 32 <= p.n && (p.n & 15) == 0) {
@@ -239,44 +196,59 @@ __device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, i
     }
     with_act(p.act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
+      for (int j = 0; j < 16; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
     });
   } else if constexpr (OP == OP_DX) {
     if (p.act != FSDP_ACT_NONE && live) {
-      float s = 0.0f;
-      if (p.zc_in) s = ckpt_scale(__ldg(p.zs_in + static_cast<size_t>(row) * ((p.n + 31) / 32) + (col0 >> 5)));
+      f2 z[16];
+      if (p.zc_in) {
+        const float s = ckpt_scale(__ldg(p.zs_in + static_cast<size_t>(row) * ((p.n + 31) / 32) + (col0 >> 5)));
+        uint2 c[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (col0 + 8 * q < p.n) {
-          float z[8];
-          if (p.zc_in) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(p.zc_in + at + 8 * q));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              z[j] = ckpt_value(c.x ^ 0x80808080u, j, s), z[4 + j] = ckpt_value(c.y ^ 0x80808080u, j, s);
-          } else {
-            unpack8(ldg16(p.z_in + at + 8 * q), z);
-          }
-          with_act(p.act, [&](auto a) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * q + j] = __fmul_rn(v[8 * q + j], act_grad<decltype(a)::value>(z[j]));
-          });
+        for (int q = 0; q < 4; ++q) {
+          c[q] = make_uint2(0u, 0u);
+          if (col0 + 8 * q < p.n) c[q] = __ldg(reinterpret_cast<const uint2*>(p.zc_in + at + 8 * q));
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            z[4 * q + j] = ckpt_values2(c[q].x, j, s), z[4 * q + 2 + j] = ckpt_values2(c[q].y, j, s);
+      } else {
+        uint4 c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          c[q] = make_uint4(0u, 0u, 0u, 0u);
+          if (col0 + 8 * q < p.n) c[q] = ldg16(p.z_in + at + 8 * q);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) unpack8(c[q], z + 4 * q);
+      }
+      with_act(p.act, [&](auto a) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], act_grad<decltype(a)::value>(z[j]));
+      });
     }
   } else {
+    const f2 s = f2_both(p.scale);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], p.scale);
+    for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], s);
   }
   if constexpr (OP != OP_DW) {
     if (p.res && live) {
+      uint4 c[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (col0 + 8 * q < p.n) {
-          float r[8];
-          unpack8(ldg16(p.res + at + 8 * q), r);
+      for (int q = 0; q < 4; ++q) {
+        c[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (col0 + 8 * q < p.n) c[q] = ldg16(p.res + at + 8 * q);
+      }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[8 * q + j] = __fadd_rn(v[8 * q + j], r[j]);
-        }
+      for (int q = 0; q < 4; ++q) {
+        f2 r[4];
+        unpack8(c[q], r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
+      }
     }
   }
   return byte;
@@ -285,38 +257,32 @@ __device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, i
 // narrow kernel: 4 columns of one output row per lane, 32 lanes across 128 columns; the 8 lanes
 // of a group of 32 columns share its scale byte through shuffles. Called by whole warps.
 template <int OP>
-__device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int col, float (&v)[4]) {
+__device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int col, f2 (&v)[2]) {
   const size_t at = static_cast<size_t>(row) * p.n + col;
   const bool live = row < p.m && col < p.n;
   const size_t group = static_cast<size_t>(row) * ((p.n + 31) / 32) + (col >> 5);
   if constexpr (OP == OP_DW) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], p.scale);
-    if (live && p.y32) __stcs(reinterpret_cast<float4*>(p.y32 + at), make_float4(v[0], v[1], v[2], v[3]));
-    if (live && !p.y32)
-      *reinterpret_cast<uint2*>(p.y + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    v[0] = f2_mul(v[0], f2_both(p.scale)), v[1] = f2_mul(v[1], f2_both(p.scale));
+    if (!live) return;
+    if (p.y32) __stcs(reinterpret_cast<ulonglong2*>(p.y32 + at), make_ulonglong2(v[0], v[1]));
+    else *reinterpret_cast<uint2*>(p.y + at) = make_uint2(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]));
     return;
   }
   if constexpr (OP == OP_FWD) {
     if (p.bias && live) {
       const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
-      v[0] = __fadd_rn(v[0], bf16_lo(b.x)), v[1] = __fadd_rn(v[1], bf16_hi(b.x));
-      v[2] = __fadd_rn(v[2], bf16_lo(b.y)), v[3] = __fadd_rn(v[3], bf16_hi(b.y));
+      v[0] = f2_add(v[0], f2_from_bf16x2(b.x)), v[1] = f2_add(v[1], f2_from_bf16x2(b.y));
     }
     if (p.z && live)
-      *reinterpret_cast<uint2*>(p.z + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      *reinterpret_cast<uint2*>(p.z + at) = make_uint2(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]));
     if (p.zc) {
-      float amax = max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
+      float amax = amax2(amax2(0.0f, v[0]), v[1]);
 #pragma unroll
       for (int d = 1; d < 8; d *= 2) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
       const uint32_t byte = ckpt_byte(amax);
       const float inv = ckpt_inv_scale(byte);
-      uint32_t w;
-      if (byte < 248u)
-        w = ckpt_code4(v[0], v[1], v[2], v[3], inv);
-      else
-        w = ckpt_code4(ckpt_clamped(v[0], byte), ckpt_clamped(v[1], byte), ckpt_clamped(v[2], byte),
-                       ckpt_clamped(v[3], byte), inv);
+      const uint32_t w = byte < 248u ? ckpt_code4(v[0], v[1], inv)
+                                     : ckpt_code4(ckpt_clamped(v[0], byte), ckpt_clamped(v[1], byte), inv);
       if (live) {
         *reinterpret_cast<uint32_t*>(p.zc + at) = w;
         if ((col & 31) == 0) p.zs[group] = static_cast<uint8_t>(byte);
@@ -324,31 +290,29 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
     }
     with_act(p.act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
+      for (int j = 0; j < 2; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
     });
   } else if (p.act != FSDP_ACT_NONE && live) {
-    float z[4];
+    f2 z[2];
     if (p.zc_in) {
       const float s = ckpt_scale(__ldg(p.zs_in + group));
-      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.zc_in + at)) ^ 0x80808080u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = ckpt_value(c, j, s);
+      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.zc_in + at));
+      z[0] = ckpt_values2(c, 0, s), z[1] = ckpt_values2(c, 1, s);
     } else {
       const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.z_in + at));
-      z[0] = bf16_lo(b.x), z[1] = bf16_hi(b.x), z[2] = bf16_lo(b.y), z[3] = bf16_hi(b.y);
+      z[0] = f2_from_bf16x2(b.x), z[1] = f2_from_bf16x2(b.y);
     }
     with_act(p.act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], act_grad<decltype(a)::value>(z[j]));
+      for (int j = 0; j < 2; ++j) v[j] = f2_mul(v[j], act_grad<decltype(a)::value>(z[j]));
     });
   }
   if (!live) return;
   if (p.res) {
     const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.res + at));
-    v[0] = __fadd_rn(v[0], bf16_lo(b.x)), v[1] = __fadd_rn(v[1], bf16_hi(b.x));
-    v[2] = __fadd_rn(v[2], bf16_lo(b.y)), v[3] = __fadd_rn(v[3], bf16_hi(b.y));
+    v[0] = f2_add(v[0], f2_from_bf16x2(b.x)), v[1] = f2_add(v[1], f2_from_bf16x2(b.y));
   }
-  *reinterpret_cast<uint2*>(p.y + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  *reinterpret_cast<uint2*>(p.y + at) = make_uint2(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]));
 }
 
 // ------------------------------------------------------------------------------------
@@ -359,16 +323,19 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
 // CTAs' shared memory. Persistent, two accumulators in tensor memory.
 //   warp 0       producer: lane i issues the i-th copy of a stage (TMA), both CTAs
 //   warp 1       MMA issuer (even CTA), tensor-memory allocation
-//   warps 2-9    epilogue: two warps per tensor-memory lane quarter, 128 columns each
-//   warps 10-13  (8-bit X) converters: the second operand's tile from codes
-template <bool X8> struct Wide {
-  static constexpr int STAGES = 5;
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int CONV_WARPS = X8 ? 4 : 0;
-  static constexpr int THREADS = 32 * (2 + EPI_WARPS + CONV_WARPS);
+//   then 8 (dw: 4) epilogue warps, two (one) per tensor-memory lane quarter, sharing its columns
+// FAST: every operand of a stage is one copy (W's shards of whole 128-row, dx: 64-row blocks, MN-
+// major widths of whole 64-column chunks), issued by one lane; otherwise lane i of the producer
+// warp issues the i-th of up to 18.
+template <int OP> struct Wide {
+  static constexpr int EPI_WARPS = OP == OP_DW ? 4 : 8;     // dw's epilogue is a scale and a store
+  static constexpr int EPI_COLS = 1024 / EPI_WARPS;         // output columns of one epilogue warp
+  static constexpr int STAGES = OP == OP_DW ? 6 : 5;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr uint32_t STAGE = 2 * kHalf;
-  static constexpr uint32_t EPI = EPI_WARPS * 2u * 4096u;  // two 4 KiB staging buffers per warp
-  static constexpr uint32_t SMEM = STAGES * STAGE + EPI + 1024;
+  static constexpr uint32_t EPI = EPI_WARPS * 4096u;        // a 4 KiB staging buffer per warp
+  static constexpr uint32_t BIAS = OP == OP_FWD ? 8u * 128u * 4u : 0u;
+  static constexpr uint32_t SMEM = STAGES * STAGE + EPI + BIAS + 1024;
 };
 
 // tile order: bands of 12 row blocks, down the rows of one tile column, then the next: the
@@ -384,7 +351,8 @@ __device__ __forceinline__ void wide_tile_coords(int tile, int num_m, int num_n,
 
 // a whole warp waits; lane 0 polls, sleeping between polls so that the epilogue warps leave the
 // issue slots to the producer and the MMA while a main loop runs
-__device__ __forceinline__ bool warp_wait_sleeping(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int code) {
+__device__ __forceinline__ bool warp_wait_sleeping(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int code,
+                                                   unsigned int most_ns) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) {
     if (mbar_try_wait(bar, parity)) {
@@ -403,7 +371,7 @@ __device__ __forceinline__ bool warp_wait_sleeping(uint32_t bar, uint32_t parity
           *abort = 1;
           break;
         }
-        if (ns < 512) ns *= 2;
+        ns = min(2 * ns, most_ns);
       }
     }
   }
@@ -417,11 +385,10 @@ __device__ __forceinline__ void tma_reduce_add_2d(const void* tmap, int32_t x, i
                : "memory");
 }
 
-template <int OP, bool X8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1)
+template <int OP, bool FAST>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1)
     linear_wide_kernel(const __grid_constant__ LinearParams p) {
-  static_assert(!X8 || OP == OP_DW, "8-bit operands: the weight gradient's X");
-  using C = Wide<X8>;
+  using C = Wide<OP>;
   constexpr bool A_MN = OP == OP_DW, B_MN = OP != OP_FWD;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[C::STAGES];
@@ -443,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1 + 2 * C::CONV_WARPS);
+      mbar_init(smem_u32(&full_bar[s]), 1);
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -467,6 +434,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
     // ---------------- producer (both CTAs) ----------------
     uint32_t it = 0, s = 0, ph = 0;  // K blocks issued; their stage and its phase parity
     bool stop = false;
+    if constexpr (FAST) {
+      if (lane == 0) {
+        for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+          int mb, nb;
+          wide_tile_coords(tile, num_m, num_n, mb, nb);
+          const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
+          int shard = 0, row = 0;  // W: the shard and its row of this tile (fwd) or K block (dx)
+          if constexpr (OP == OP_FWD) shard = min(n0 / p.shard_rows, p.n_shards - 1), row = n0 - shard * p.shard_rows;
+          for (int kb = 0; kb < num_k; ++kb, ++it) {
+            if (it >= static_cast<uint32_t>(C::STAGES) &&
+                !mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty)) {
+              stop = true;
+              break;
+            }
+            const uint32_t fb = mapa_shared(smem_u32(&full_bar[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 4 * kHalf);
+            const uint32_t sa = smem_u32(smem) + s * C::STAGE;
+            if constexpr (A_MN) tma_load_3d_pair(sa, &p.a, 0, kb * BK, m0 / 64, fb);
+            else tma_load_2d_pair(sa, &p.a, kb * BK, m0, fb);
+            if constexpr (OP == OP_FWD) {
+              tma_load_2d_pair(sa + kHalf, &p.w[shard], kb * BK, row, fb);
+            } else if constexpr (OP == OP_DX) {
+              tma_load_3d_pair(sa + kHalf, &p.w[shard], 0, row, n0 / 64, fb);
+              if ((row += BK) >= p.shard_rows && shard + 1 < p.n_shards) row = 0, ++shard;
+            } else {
+              tma_load_3d_pair(sa + kHalf, &p.b, 0, kb * BK, n0 / 64, fb);
+            }
+            if (++s == C::STAGES) s = 0, ph ^= 1u;
+          }
+        }
+      }
+    } else
     for (int tile = pair; tile < tiles && !stop; tile += pairs) {
       int mb, nb;
       wide_tile_coords(tile, num_m, num_n, mb, nb);
@@ -477,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
       else i -= k_copies(&p.a, i, m0, 0, 0, c);
       if constexpr (OP == OP_FWD) i -= w_copies_k_major(p, i, n0, 0, kHalf, c);
       else if constexpr (OP == OP_DX) i -= w_copies_mn_major(p, i, n0, 0, kHalf, c);
-      else if constexpr (!X8) i -= mn_copies(&p.b, 2, i, n0, 0, kHalf, c);
+      else i -= mn_copies(&p.b, 2, i, n0, 0, kHalf, c);
       const bool mine = i < 0;
       for (int kb = 0; kb < num_k; ++kb, ++it) {
         bool ok = true;
@@ -488,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
           break;
         }
         if (rank == 0 && lane == 0)
-          mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * (X8 ? kHalf : 2 * kHalf));
+          mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 4 * kHalf);
         if (mine) {
           tma_load_2d_pair(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y,
                            mapa_shared(smem_u32(&full_bar[s]), 0));
@@ -524,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
           tc_fence_after();
           const uint32_t d = tmem_base + a * 256;
           for (; kb < kb_end; ++kb) {
-            if (!mbar_wait_cluster_bounded(smem_u32(&full_bar[s]), ph, abort, &g_zgb_dev_error, kErrFull)) {
+            if (!mbar_wait_bounded(smem_u32(&full_bar[s]), ph, abort, &g_zgb_dev_error, kErrFull)) {
               stop = true;
               break;
             }
@@ -551,84 +550,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
   } else if (warp < 2 + C::EPI_WARPS) {
     // ---------------- epilogue (both CTAs, own 128 rows) ----------------
     const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
-    const int part = (warp - 2) >> 2;  // which 128 columns
-    uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 2u * 4096u;
-    uint32_t i = 0, staged = 0;
+    const int part = (warp - 2) >> 2;  // which of the quarter's warps
+    uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 4096u;
+    float* bias = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI) + (warp - 2) * C::EPI_COLS;
+    const unsigned int poll_ns = min(max(32u * static_cast<unsigned int>(num_k), 128u), 2048u);  // a tenth of a main loop
+    uint32_t i = 0;
     bool stop = false;
     for (int tile = pair; tile < tiles && !stop; tile += pairs) {
       int mb, nb;
       wide_tile_coords(tile, num_m, num_n, mb, nb);
       const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
-      const int c0 = nb * 256 + part * 128;
+      const int c0 = nb * 256 + part * C::EPI_COLS;
+      if (OP == OP_FWD && p.bias) {  // this warp's 128 columns, 4 a lane, while the main loop runs
+        const int col = c0 + lane * 4;
+        const uint2 b = col < p.n ? __ldg(reinterpret_cast<const uint2*>(p.bias + col)) : make_uint2(0u, 0u);
+        __syncwarp();
+        reinterpret_cast<float4*>(bias)[lane] = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
+        __syncwarp();
+      }
       for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
         const uint32_t a = i & 1u, u = i >> 1;
-        if (!warp_wait_sleeping(smem_u32(&accf_bar[a]), u & 1u, abort, kErrAccF)) {
+        if (!warp_wait_sleeping(smem_u32(&accf_bar[a]), u & 1u, abort, kErrAccF, poll_ns)) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * 128;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
         if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
         if (OP == OP_DW && p.y32) {
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < C::EPI_COLS; c += 32) {
             uint32_t r[32];
             tmem_ld_32cols(taddr + c, r);
             if (c0 + c >= p.n) continue;
-            float v[32];
+            f2 v[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-            epilogue32<OP>(p, row, c0 + c, v);
-            uint8_t* buf = stage + (staged & 1u) * 4096u;
-            if (lane == 0 && staged >= 2) bulk_wait_group_read<1>();
+            for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            epilogue32<OP>(p, row, c0 + c, nullptr, v);
+            if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<float4*>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              *reinterpret_cast<ulonglong2*>(stage + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                  make_ulonglong2(v[2 * j], v[2 * j + 1]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
-              else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(buf));
+              if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(stage));
+              else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(stage));
               bulk_commit_group();
             }
-            ++staged;
           }
         } else {
           uint32_t bytes = 0;  // four scale bytes of this row
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 64) {
+          for (int c = 0; c < C::EPI_COLS; c += 64) {
             uint32_t w[32];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t r[32];
               tmem_ld_32cols(taddr + c + 32 * h, r);
-              float v[32];
+              f2 v[16];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+              for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               if (c0 + c + 32 * h < p.n) {
-                const uint32_t b = epilogue32<OP>(p, row, c0 + c + 32 * h, v);
+                const uint32_t b = epilogue32<OP>(p, row, c0 + c + 32 * h, p.bias ? bias + c + 32 * h : nullptr, v);
                 bytes |= b << (8 * (c / 32 + h));
               }
 #pragma unroll
-              for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+              for (int j = 0; j < 16; ++j) w[16 * h + j] = f2_to_bf16x2(v[j]);
             }
             if (c0 + c >= p.n) continue;
-            uint8_t* buf = stage + (staged & 1u) * 4096u;
-            if (lane == 0 && staged >= 2) bulk_wait_group_read<1>();
+            if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                   make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
+              tma_store_2d(&p.out, c0 + c, r0, smem_u32(stage));
               bulk_commit_group();
             }
-            ++staged;
           }
           if (OP == OP_FWD && p.zc && row < p.m) {
             const int groups = (p.n + 31) / 32, g0 = c0 >> 5;
@@ -647,34 +651,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
       }
     }
     if (lane == 0) bulk_wait_group_all();  // no store may still read this CTA's shared memory
-  } else if constexpr (X8) {
-    // ---------------- converters (both CTAs, own 128 columns) ----------------
-    const int c = static_cast<int>(threadIdx.x) - 32 * (2 + C::EPI_WARPS);
-    uint32_t it = 0, s = 0, ph = 0;
-    bool stop = false;
-    for (int tile = pair; tile < tiles && !stop; tile += pairs) {
-      int mb, nb;
-      wide_tile_coords(tile, num_m, num_n, mb, nb);
-      const int n0 = nb * 256 + static_cast<int>(rank) * 128;
-      Codes next;
-      codes_load(p, 0, n0, c, next);
-      for (int kb = 0; kb < num_k; ++kb, ++it) {
-        const Codes now = next;
-        if (kb + 1 < num_k) codes_load(p, kb + 1, n0, c, next);
-        bool ok = true;
-        if (it >= static_cast<uint32_t>(C::STAGES))
-          ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
-        if (!__all_sync(0xffffffffu, ok)) {
-          stop = true;
-          break;
-        }
-        codes_store(now, smem + s * C::STAGE + kHalf, c);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[s]), 0));
-        if (++s == C::STAGES) s = 0, ph ^= 1u;
-      }
-    }
   }
 
   tc_fence_before();
@@ -695,12 +671,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<X8>::THREADS, 1
 // rows c TN / S .. in CTA order and runs the epilogue on them, 4 columns a lane.
 //   warp 0      producer: lane i issues the i-th copy of a stage
 //   warp 1      MMA issuer, tensor-memory allocation
-//   warps 2-5   (8-bit X) converters
 //   all warps   the sum over the parts and the epilogue
 template <int TN> struct Narrow {
   static constexpr uint32_t QB = TN * BK * 2;               // the row-side operand of a stage
   static constexpr uint32_t STAGE = kHalf + QB;
-  static constexpr int STAGES = TN == 128 ? 3 : 5;          // two CTAs per SM
+  static constexpr int STAGES = TN == 128 ? 3 : 5;  // two CTAs per SM
   static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
   static constexpr uint32_t TMEM_COLS = TN;
   static_assert(STAGES * STAGE >= TN * 128 * 4, "the fp32 part takes the stages' place");
@@ -715,9 +690,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-template <int OP, int TN, bool X8>
+template <int OP, int TN>
 __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
-  static_assert(!X8 || OP == OP_DW, "8-bit operands: the weight gradient's X");
   using C = Narrow<TN>;
   constexpr bool P_MN = OP != OP_FWD, Q_MN = OP == OP_DW;  // P: the column side, Q: the row side
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -738,7 +712,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), X8 ? 5 : 1);
+      mbar_init(smem_u32(&full_bar[s]), 1);
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     mbar_init(smem_u32(&acc_bar), 1);
@@ -759,7 +733,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
     int i = lane;
     if constexpr (OP == OP_FWD) i -= w_copies_k_major(p, i, n0, kb0, 0, c);
     else if constexpr (OP == OP_DX) i -= w_copies_mn_major(p, i, n0, kb0, 0, c);
-    else if constexpr (!X8) i -= mn_copies(&p.b, 2, i, n0, kb0, 0, c);
+    else i -= mn_copies(&p.b, 2, i, n0, kb0, 0, c);
     if constexpr (Q_MN) i -= mn_copies(&p.a, TN / 64, i, m0, kb0, kHalf, c);
     else i -= k_copies(&p.a, i, m0, kb0, kHalf, c);
     const bool mine = i < 0;
@@ -770,7 +744,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       if (issued >= C::STAGES)
         ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), X8 ? C::QB : C::STAGE);
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), C::STAGE);
       if (mine) {
         tma_load_2d(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y, smem_u32(&full_bar[s]));
         copy_advance(p, c);
@@ -804,24 +778,6 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       umma_commit(smem_u32(&acc_bar));  // every MMA issued, also after a wait that gave up
     }
     __syncwarp();
-  } else if (X8 && warp < 6) {
-    const int c = static_cast<int>(threadIdx.x) - 64;
-    uint32_t s = 0, ph = 0;
-    Codes next;
-    codes_load(p, kb0, n0, c, next);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const Codes now = next;
-      if (kb + 1 < kb1) codes_load(p, kb + 1, n0, c, next);
-      bool ok = true;
-      if (kb - kb0 >= C::STAGES)
-        ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      codes_store(now, smem + s * C::STAGE, c);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
-      if (++s == C::STAGES) s = 0, ph ^= 1u;
-    }
   }
 
   // the accumulator is complete (or, after an abort, no MMA runs any more)
@@ -847,11 +803,10 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   const uint32_t base = smem_u32(smem);
   for (int t = rank * rows + warp; t < (rank + 1) * rows; t += 8) {
     if (m0 + t >= p.m) break;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    f2 v[2] = {0ull, 0ull};
     for (int s = 0; s < splits; ++s) {
       const float4 f = ld_cluster_f4(mapa_shared(base, s) + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
-      v[0] = __fadd_rn(v[0], f.x), v[1] = __fadd_rn(v[1], f.y);
-      v[2] = __fadd_rn(v[2], f.z), v[3] = __fadd_rn(v[3], f.w);
+      v[0] = f2_add(v[0], f2_make(f.x, f.y)), v[1] = f2_add(v[1], f2_make(f.z, f.w));
     }
     epilogue4<OP>(p, m0 + t, n0 + lane * 4, v);
   }
@@ -868,10 +823,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// row-major [rows, cols] of bf16 or fp32, boxes of box_cols x box_rows (128 bytes wide) in the
-// 128-byte swizzle; out of range reads zeros, writes nothing
-int encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows, bool fp32,
-           const char* who) {
+int encoder(const char* who) {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
@@ -879,7 +831,15 @@ int encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int b
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode) return set_error(ZERO_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", who);
+  return g_encode ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", who);
+}
+
+// row-major [rows, cols] of bf16 or fp32, boxes of box_cols x box_rows (128 bytes wide) in the
+// 128-byte swizzle; out of range reads zeros, writes nothing
+int encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows, bool fp32,
+           const char* who) {
+  const int rc = encoder(who);
+  if (rc) return rc;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (fp32 ? 4 : 2)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
@@ -892,9 +852,23 @@ int encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int b
   return ZERO_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// row-major [rows, cols] bf16 (cols % 64 == 0) read MN-major: element (x, y, z) is row y, column 64 z +
+// x; boxes of 64 x BK x 2 land as two chunks of 64 columns
+int encode_mn(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, const char* who) {
+  int rc = encoder(who);
+  if (rc) return rc;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(BK), 2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(ZERO_ERR_CUDA, "%s: cuTensorMapEncodeTiled (MN-major) failed (%d)", who, (int)r);
+  return ZERO_OK;
+}
 
-OncePerDevice g_attr_once[16];
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <class K>
 int set_smem(OncePerDevice& once, K kernel, uint32_t bytes, const char* who) {
@@ -907,25 +881,26 @@ int set_smem(OncePerDevice& once, K kernel, uint32_t bytes, const char* who) {
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 
-template <int OP, bool X8>
+template <int OP, bool FAST>
 int launch_wide(const LinearParams& p, cudaStream_t st, const char* who) {
-  using C = Wide<X8>;
-  int rc = set_smem(g_attr_once[OP + (X8 ? 1 : 0)], linear_wide_kernel<OP, X8>, C::SMEM, who);
+  using C = Wide<OP>;
+  static OncePerDevice once;
+  int rc = set_smem(once, linear_wide_kernel<OP, FAST>, C::SMEM, who);
   if (rc) return rc;
   const int64_t tiles = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + 255) / 256);
   if (tiles > INT32_MAX / 2)
     return set_error(ZERO_ERR_UNSUPPORTED, "%s: an output of %d x %d is more than 2^30 tiles", who, p.m, p.n);
   const unsigned int pairs = static_cast<unsigned int>(std::min<int64_t>(tiles, std::max(1, num_sms() / 2)));
-  linear_wide_kernel<OP, X8><<<2 * pairs, C::THREADS, C::SMEM, st>>>(p);
+  linear_wide_kernel<OP, FAST><<<2 * pairs, C::THREADS, C::SMEM, st>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 
-template <int OP, int TN, bool X8>
+template <int OP, int TN>
 int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char* who) {
   using C = Narrow<TN>;
-  int rc = set_smem(g_attr_once[4 + (OP + (X8 ? 1 : 0)) * 2 + (TN == 128 ? 1 : 0)], linear_narrow_kernel<OP, TN, X8>,
-                    C::SMEM, who);
+  static OncePerDevice once;
+  int rc = set_smem(once, linear_narrow_kernel<OP, TN>, C::SMEM, who);
   if (rc) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>((p.n + 127) / 128),
@@ -939,7 +914,7 @@ int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_narrow_kernel<OP, TN, X8>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_narrow_kernel<OP, TN>, p);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 
@@ -977,10 +952,10 @@ struct Operands {
   int n_shards;
   const uint16_t* const* w;  // fwd, dx
   const uint16_t* a;         // X, dZ, dZ
-  const uint16_t* x;         // dw: X in bf16 (null: in 8 bits)
+  const uint16_t* x;         // dw: X
 };
 
-template <int OP, bool X8>
+template <int OP>
 int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who) {
   const bool fp32 = p.y32 != nullptr;
   const Choice c = choose(OP, p.m, p.n, p.k, fp32);
@@ -988,27 +963,40 @@ int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who)
   p.chunk_blocks = c.wide && fp32 ? kMaxChunkBlocks : blocks;
   p.chunks = (blocks + p.chunk_blocks - 1) / p.chunk_blocks;
   int rc;
+  bool fast = c.wide;  // one copy per operand and stage
   if constexpr (OP == OP_DW) {
-    if ((rc = encode(&p.a, o.a, p.k, p.m, 64, BK, false, who))) return rc;
-    if (!X8 && (rc = encode(&p.b, o.x, p.k, p.n, 64, BK, false, who))) return rc;
+    fast = fast && p.m % 64 == 0 && p.n % 64 == 0;
+    if ((rc = fast ? encode_mn(&p.a, o.a, p.k, p.m, who) : encode(&p.a, o.a, p.k, p.m, 64, BK, false, who))) return rc;
+    if ((rc = fast ? encode_mn(&p.b, o.x, p.k, p.n, who) : encode(&p.b, o.x, p.k, p.n, 64, BK, false, who)))
+      return rc;
   } else {
     if ((rc = encode(&p.a, o.a, p.m, p.k, BK, c.wide ? 128 : c.tn, false, who))) return rc;
     const int most = OP == OP_FWD ? 128 : BK;
     p.n_shards = o.n_shards;
-    p.w_box = std::min(p.shard_rows & -p.shard_rows, most);
+    // shards that lie back to back are one matrix: one map, and boxes of any height
+    const int64_t shard_elems = static_cast<int64_t>(p.shard_rows) * (OP == OP_FWD ? p.k : p.n);
+    bool joined = true;
+    for (int s = 1; s < o.n_shards; ++s) joined = joined && o.w[s] == o.w[0] + s * shard_elems;
+    if (joined) p.shard_rows *= p.n_shards, p.n_shards = 1;
+    // one shard: rows past the last are zeros in any box, so it may be whole
+    p.w_box = p.n_shards == 1 ? most : std::min(p.shard_rows & -p.shard_rows, most);
     for (p.w_box_log = 3; (1 << p.w_box_log) < p.w_box;) ++p.w_box_log;
+    fast = fast && p.w_box == most && (OP == OP_FWD || p.n % 64 == 0);
     const int64_t w_cols = OP == OP_FWD ? p.k : p.n;
-    for (int s = 0; s < o.n_shards; ++s)
-      if ((rc = encode(&p.w[s], o.w[s], p.shard_rows, w_cols, 64, p.w_box, false, who))) return rc;
+    for (int s = 0; s < p.n_shards; ++s) {
+      rc = OP == OP_DX && fast ? encode_mn(&p.w[s], o.w[s], p.shard_rows, w_cols, who)
+                               : encode(&p.w[s], o.w[s], p.shard_rows, w_cols, 64, p.w_box, false, who);
+      if (rc) return rc;
+    }
   }
   if (c.wide) {
     rc = fp32 ? encode(&p.out, p.y32, p.m, p.n, 32, 32, true, who) : encode(&p.out, p.y, p.m, p.n, 64, 32, false, who);
     if (rc) return rc;
-    return launch_wide<OP, X8>(p, st, who);
+    return fast ? launch_wide<OP, true>(p, st, who) : launch_wide<OP, false>(p, st, who);
   }
   if constexpr (OP != OP_DW)
-    if (c.tn == 32) return launch_narrow<OP, 32, false>(p, c.splits, st, who);
-  return launch_narrow<OP, 128, X8>(p, c.splits, st, who);
+    if (c.tn == 32) return launch_narrow<OP, 32>(p, c.splits, st, who);
+  return launch_narrow<OP, 128>(p, c.splits, st, who);
 }
 
 int check_sizes(int64_t m, int64_t r, int64_t k, const char* who) {
@@ -1074,7 +1062,7 @@ extern "C" int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[
   p.bias = bias, p.res = residual, p.act = act;
   p.y = Y, p.z = z, p.zc = z_codes, p.zs = z_scales;
   const Operands o{n_ranks, w_shards, X, nullptr};
-  return launch<OP_FWD, false>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
+  return launch<OP_FWD>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
 }
 
 extern "C" int fsdp_linear_dx(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t k_in,
@@ -1095,12 +1083,25 @@ extern "C" int fsdp_linear_dx(int n_ranks, const zero_bf16* const w_shards[], in
   p.res = residual, p.act = act, p.y = dX;
   if (act != FSDP_ACT_NONE) p.z_in = z, p.zc_in = z_codes, p.zs_in = z_scales;
   const Operands o{n_ranks, w_shards, dZ, nullptr};
-  return launch<OP_DX, false>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
+  return launch<OP_DX>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
+}
+
+// X from an 8-bit checkpoint is unpacked into the workspace first, 3 bytes of traffic per element
+// against 2 rows_out flops: 3 % of the product's time at rows_out = 4096. Converting codes inside
+// the product's operand loads saves that traffic but repeats the conversion for every 256 rows of
+// dW: measured 2.5 times the whole product's time at rows_out = 14336.
+extern "C" int fsdp_linear_dw_workspace(int64_t m_tokens, int64_t k_in, uint64_t* bytes) {
+  const char* who = "fsdp_linear_dw_workspace";
+  if (!bytes) return set_error(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+  const int rc = check_sizes(m_tokens, 8, k_in, who);
+  if (rc) return rc;
+  *bytes = (2 * static_cast<uint64_t>(m_tokens) * static_cast<uint64_t>(k_in) + 255) & ~uint64_t(255);
+  return ZERO_OK;
 }
 
 extern "C" int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int8_t* x_codes, const uint8_t* x_scales,
                               int64_t m_tokens, int64_t rows_out, int64_t k_in, float scale, float* dW,
-                              zero_bf16* dW_bf16, zero_stream_t stream) {
+                              zero_bf16* dW_bf16, void* workspace, uint64_t workspace_bytes, zero_stream_t stream) {
   const char* who = "fsdp_linear_dw";
   LinearParams p;
   memset(&p, 0, sizeof(p));
@@ -1113,12 +1114,21 @@ extern "C" int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int
     return set_error(ZERO_ERR_INVALID_ARG, "%s: pass one of dW and dW_bf16", who);
   if (!(scale - scale == 0.0f)) return set_error(ZERO_ERR_INVALID_ARG, "%s: scale must be finite", who);
   if (!aligned16(dZ) || !aligned16(x) || !aligned16(x_codes) || !aligned16(x_scales) || !aligned16(dW) ||
-      !aligned16(dW_bf16))
+      !aligned16(dW_bf16) || (x_codes && !aligned16(workspace)))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: every buffer must be 16-byte aligned", who);
+  if (x_codes) {
+    uint64_t need = 0;
+    if ((rc = fsdp_linear_dw_workspace(m_tokens, k_in, &need))) return rc;
+    if (!workspace || workspace_bytes < need)
+      return set_error(ZERO_ERR_INVALID_ARG, "%s: workspace of %llu bytes is below the %llu needed", who,
+                       workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)need);
+    if ((rc = fsdp_checkpoint8_unpack(x_codes, x_scales, m_tokens, k_in, FSDP_ACT_NONE,
+                                      static_cast<zero_bf16*>(workspace), stream)))
+      return rc;
+    x = static_cast<const zero_bf16*>(workspace);
+  }
   p.m = static_cast<int>(rows_out), p.n = static_cast<int>(k_in), p.k = static_cast<int>(m_tokens);
-  p.x_codes = x_codes, p.x_scales = x_scales, p.scale = scale;
-  p.y32 = dW, p.y = dW_bf16;
+  p.scale = scale, p.y32 = dW, p.y = dW_bf16;
   const Operands o{0, nullptr, dZ, x};
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return x_codes ? launch<OP_DW, true>(p, o, st, who) : launch<OP_DW, false>(p, o, st, who);
+  return launch<OP_DW>(p, o, reinterpret_cast<cudaStream_t>(stream), who);
 }

@@ -9,6 +9,41 @@
 namespace zgb {
 
 // ------------------------------------------------------------------------------------
+// pairs of fp32: one instruction for two lanes' worth of add, multiply and fused multiply-add.
+// The epilogues run beside tensor-core work at the power limit, where each instruction's issue
+// is paid in clock rate as much as in time.
+// ------------------------------------------------------------------------------------
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 f2_both(float x) { return f2_make(x, x); }
+__device__ __forceinline__ void f2_split(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t f2_to_bf16x2(f2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ f2 f2_from_bf16x2(uint32_t w) { return f2_make(bf16_lo(w), bf16_hi(w)); }
+
+// ------------------------------------------------------------------------------------
 // activations
 // ------------------------------------------------------------------------------------
 // min / max that return NaN when an operand is one (the IEEE-754 2019 minimum / maximum)
@@ -22,59 +57,93 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
-// 1 / (1 + exp(-x)) = (x >= 0 ? 1 : t) / (1 + t) with t = exp(-|x|): the denominator stays in
-// [1, 2], so the approximate reciprocal needs no scaling, and small results keep their
-// precision down to the subnormals: t is the square of 2^(-|x| log2(e) / 2), which is normal
-// for every t that is not zero. Relative error a few 2^-22 for |x| < 20, |x| 2^-24 beyond,
-// far inside the bf16 rounding of what it goes into; 0 and 1 at the ends, NaN for NaN.
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  float h, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(__fmul_rn(fabsf(x), -0.72134752f)));
-  const float t = __fmul_rn(h, h);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, t)));
-  return __fmul_rn(x >= 0.0f ? 1.0f : t, r);
+// max(m, |a|, |b|)
+__device__ __forceinline__ float amax2(float m, f2 v) {
+  float a, b, r;
+  f2_split(v, a, b);
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
 }
 
-constexpr float kGeluA = 1.5957691216057308f;      // 2 sqrt(2 / pi)
-constexpr float kGeluB = 0.044715f;                // the cubic term of the tanh form
-constexpr float kSqrtHalf = 0.70710678118654752f;  // 1 / sqrt(2)
+constexpr float kHalfLog2e = 0.72134752044448170f;  // log2(e) / 2
+constexpr float kGeluA = 1.5957691216057308f;       // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;                 // the cubic term of the tanh form
+constexpr float kSqrtHalf = 0.70710678118654752f;   // 1 / sqrt(2)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
+// 2^8 / (1 + exp(-x)) from m = -x log2(e) / 2 - 4: with h = 2^m, h^2 = 2^-8 exp(-x), so
+// 1 / (h^2 + 2^-8). The factor 2^8 keeps the reciprocal normal wherever the sigmoid is more than
+// the smallest subnormal bf16; halving the exponent keeps h in range. Fast exponential and
+// reciprocal: relative error a few 2^-22 + |x| 2^-23, far inside the bf16 rounding of what it
+// goes into. h -> inf gives 0, h -> 0 gives 2^8, NaN stays.
+__device__ __forceinline__ f2 sigmoid256(f2 m) {
+  float a, b, ra, rb;
+  f2_split(m, a, b);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(a));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(b));
+  const f2 h = f2_make(ra, rb);
+  f2_split(f2_fma(h, h, f2_both(0.00390625f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(b));
+  return f2_make(ra, rb);
+}
+
 // act(x). The tanh form of GELU uses (1 + tanh u) / 2 = 1 / (1 + exp(-2u)): one exponential,
-// no cancellation for negative x.
+// no cancellation for negative x; where x^2 overflows the argument is infinite with the right
+// sign.
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float x) {
-  if constexpr (ACT == FSDP_ACT_RELU) return x < 0.0f ? 0.0f : x;  // NaN stays
-  if constexpr (ACT == FSDP_ACT_GELU) return __fmul_rn(__fmul_rn(0.5f, x), erfcf(__fmul_rn(-kSqrtHalf, x)));
-  if constexpr (ACT == FSDP_ACT_GELU_TANH) {
-    const float u = __fmul_rn(__fmul_rn(kGeluA, x), __fmaf_rn(__fmul_rn(kGeluB, x), x, 1.0f));
-    return __fmul_rn(x, sigmoid_fast(u));
+__device__ __forceinline__ f2 act_fwd(f2 x) {
+  if constexpr (ACT == FSDP_ACT_RELU || ACT == FSDP_ACT_GELU) {
+    float a, b;
+    f2_split(x, a, b);
+    if constexpr (ACT == FSDP_ACT_RELU) return f2_make(a < 0.0f ? 0.0f : a, b < 0.0f ? 0.0f : b);  // NaN stays
+    return f2_mul(f2_mul(x, f2_both(0.5f)), f2_make(erfcf(__fmul_rn(-kSqrtHalf, a)), erfcf(__fmul_rn(-kSqrtHalf, b))));
   }
-  if constexpr (ACT == FSDP_ACT_SILU) return __fmul_rn(x, sigmoid_fast(x));
+  if constexpr (ACT == FSDP_ACT_GELU_TANH) {
+    const f2 w = f2_fma(f2_mul(x, x), f2_both(-kGeluA * kGeluB * kHalfLog2e), f2_both(-kGeluA * kHalfLog2e));
+    return f2_mul(f2_mul(x, f2_both(0.00390625f)), sigmoid256(f2_fma(x, w, f2_both(-4.0f))));
+  }
+  if constexpr (ACT == FSDP_ACT_SILU)
+    return f2_mul(f2_mul(x, f2_both(0.00390625f)), sigmoid256(f2_fma(x, f2_both(-kHalfLog2e), f2_both(-4.0f))));
   return x;
 }
 
 // act'(x); NaN for NaN, so that a checkpoint's NaN group never looks like a zero gradient
 template <int ACT>
-__device__ __forceinline__ float act_grad(float x) {
-  if constexpr (ACT == FSDP_ACT_RELU) return x > 0.0f ? 1.0f : x != x ? x : 0.0f;
-  if constexpr (ACT == FSDP_ACT_GELU) {
-    const float pdf = __fmul_rn(kInvSqrt2Pi, __expf(__fmul_rn(__fmul_rn(-0.5f, x), x)));
-    return __fmaf_rn(x, pdf, __fmul_rn(0.5f, erfcf(__fmul_rn(-kSqrtHalf, x))));
+__device__ __forceinline__ f2 act_grad(f2 x) {
+  if constexpr (ACT == FSDP_ACT_RELU || ACT == FSDP_ACT_GELU) {
+    float v[2];
+    f2_split(x, v[0], v[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = v[i];
+      if constexpr (ACT == FSDP_ACT_RELU) {
+        v[i] = a > 0.0f ? 1.0f : a != a ? a : 0.0f;
+      } else {
+        const float pdf = __fmul_rn(kInvSqrt2Pi, __expf(__fmul_rn(__fmul_rn(-0.5f, a), a)));
+        v[i] = __fmaf_rn(a, pdf, __fmul_rn(0.5f, erfcf(__fmul_rn(-kSqrtHalf, a))));
+      }
+    }
+    return f2_make(v[0], v[1]);
   }
   if constexpr (ACT == FSDP_ACT_GELU_TANH) {
-    // past |x| = 30 the sigmoid is 0 or 1 exactly: clamping keeps x^2 * 0 from being inf * 0
-    const float c = min_nan(max_nan(x, -30.0f), 30.0f), c2 = __fmul_rn(c, c);
-    const float s = sigmoid_fast(__fmul_rn(__fmul_rn(kGeluA, c), __fmaf_rn(kGeluB, c2, 1.0f)));
-    const float du = __fmul_rn(kGeluA, __fmaf_rn(3.0f * kGeluB, c2, 1.0f));
-    return __fmaf_rn(__fmul_rn(__fmul_rn(c, s), __fsub_rn(1.0f, s)), du, s);
+    // s + x s (1 - s) du with du = A (1 + 3 B x^2). Past |x| = 100 s is 0 or 1: holding x^2
+    // there keeps the last term from being 0 * inf.
+    float a, b;
+    f2_split(f2_mul(x, x), a, b);
+    const f2 p = f2_make(min_nan(a, 1e4f), min_nan(b, 1e4f));
+    const f2 w = f2_fma(p, f2_both(-kGeluA * kGeluB * kHalfLog2e), f2_both(-kGeluA * kHalfLog2e));
+    const f2 r = sigmoid256(f2_fma(x, w, f2_both(-4.0f)));
+    const f2 s = f2_mul(r, f2_both(0.00390625f)), q = f2_fma(r, f2_both(-0.00390625f), f2_both(1.0f));
+    const f2 du = f2_fma(p, f2_both(3.0f * kGeluA * kGeluB), f2_both(kGeluA));
+    return f2_fma(f2_mul(f2_mul(x, s), q), du, s);
   }
-  if constexpr (ACT == FSDP_ACT_SILU) {
-    const float s = sigmoid_fast(x);
-    return __fmul_rn(s, __fmaf_rn(x, __fsub_rn(1.0f, s), 1.0f));
+  if constexpr (ACT == FSDP_ACT_SILU) {  // s (1 + x (1 - s))
+    const f2 r = sigmoid256(f2_fma(x, f2_both(-kHalfLog2e), f2_both(-4.0f)));
+    const f2 q = f2_fma(r, f2_both(-0.00390625f), f2_both(1.0f));
+    return f2_mul(f2_mul(r, f2_both(0.00390625f)), f2_fma(x, q, f2_both(1.0f)));
   }
-  return 1.0f;
+  return f2_both(1.0f);
 }
 
 // f(integral constant) for the run-time activation (already checked on the host)
@@ -116,28 +185,32 @@ __device__ __forceinline__ uint32_t ckpt_byte(float amax) {
 __device__ __forceinline__ float ckpt_inv_scale(uint32_t b) { return __uint_as_float(b == 255u ? 0u : (254u - b) << 23); }
 // 2^(b - 127); inf for b = 255
 __device__ __forceinline__ float ckpt_scale(uint32_t b) { return __uint_as_float(b << 23); }
-// the code of x in a word whose low byte holds it (the other bytes: the magic number)
-__device__ __forceinline__ uint32_t ckpt_code_word(float x, float inv) {
-  return __float_as_uint(__fmaf_rn(x, inv, kRoundMagic));
-}
-// four codes, first in the lowest byte
-__device__ __forceinline__ uint32_t ckpt_code4(float a, float b, float c, float d, float inv) {
-  const uint32_t lo = __byte_perm(ckpt_code_word(a, inv), ckpt_code_word(b, inv), 0x0040);
-  const uint32_t hi = __byte_perm(ckpt_code_word(c, inv), ckpt_code_word(d, inv), 0x0040);
+// four codes of two pairs, first in the lowest byte: x / 2^e + 1.5 * 2^23 holds the rounded
+// integer in its low byte
+__device__ __forceinline__ uint32_t ckpt_code4(f2 x, f2 y, float inv) {
+  float a, b, c, d;
+  f2_split(f2_fma(x, f2_both(inv), f2_both(kRoundMagic)), a, b);
+  f2_split(f2_fma(y, f2_both(inv), f2_both(kRoundMagic)), c, d);
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
   return __byte_perm(lo, hi, 0x5410);
 }
-// value `i` of a word of four codes (biased: word ^ 0x80808080) with scale s = 2^e: the byte
-// in a float's low mantissa bits is 2^23 + 128 + code; both operations are exact (removing
-// the offset after scaling, in one fused multiply-add, would overflow for large s)
-__device__ __forceinline__ float ckpt_value(uint32_t biased, int i, float s) {
-  const uint32_t w = __byte_perm(biased, 0x4B000000u, 0x7540 + i);
-  return __fmul_rn(__fsub_rn(__uint_as_float(w), 8388736.0f), s);
+// the pair of values of codes 2 i, 2 i + 1 of a word with scale s = 2^e: the biased code in a
+// float's low mantissa bits is 2^23 + 128 + code. Both operations are exact; they are separate
+// because removing the offset after scaling, in one fused multiply-add, overflows for large s.
+__device__ __forceinline__ f2 ckpt_values2(uint32_t word, int i, float s) {
+  const uint32_t v = word ^ 0x80808080u;
+  const f2 w = f2_make(__uint_as_float(__byte_perm(v, 0x4B000000u, 0x7540 + 2 * i)),
+                       __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7541 + 2 * i)));
+  return f2_mul(f2_add(w, f2_both(-8388736.0f)), f2_both(s));
 }
 
 // values past the largest code of b = 248, held to it; inputs that are not finite (b = 255)
 // are zeroed, so that their codes are 0
-__device__ __forceinline__ float ckpt_clamped(float x, uint32_t b) {
-  return b == 255u ? 0.0f : fminf(fmaxf(x, -kCodeLimit), kCodeLimit);
+__device__ __forceinline__ f2 ckpt_clamped(f2 v, uint32_t b) {
+  float x, y;
+  f2_split(v, x, y);
+  return b == 255u ? 0ull : f2_make(fminf(fmaxf(x, -kCodeLimit), kCodeLimit), fminf(fmaxf(y, -kCodeLimit), kCodeLimit));
 }
 
 }  // namespace zgb

@@ -564,13 +564,19 @@ ZERO_API int fsdp_linear_dx(int n_ranks, const zero_bf16* const w_shards[], int6
                             const uint8_t* z_scales, int act, const zero_bf16* residual, zero_bf16* dX,
                             zero_stream_t stream);
 
+/* Bytes of device workspace fsdp_linear_dw needs when X is given in 8 bits: its bf16 values, 2 *
+ * m_tokens * k_in rounded up to 256. */
+ZERO_API int fsdp_linear_dw_workspace(int64_t m_tokens, int64_t k_in, uint64_t* bytes);
+
 /* Weight gradient: dW = scale * dZ^T X, [rows_out, k_in], fp32 (dW) or bf16 (dW_bf16), one of
  * the two: the gradient types the step calls reduce. dZ [m_tokens, rows_out] bf16; X
  * [m_tokens, k_in] as bf16 (x) or as its 8-bit checkpoint (x_codes, x_scales), whose values
- * are multiplied exactly. scale (finite) is applied to the fp32 sum. */
+ * are multiplied exactly; then workspace holds fsdp_linear_dw_workspace() bytes (else NULL).
+ * scale (finite) is applied to the fp32 sum, which an fp32 dW takes in parts of at most 4096
+ * tokens, added with rounding to nearest. */
 ZERO_API int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int8_t* x_codes, const uint8_t* x_scales,
                             int64_t m_tokens, int64_t rows_out, int64_t k_in, float scale, float* dW,
-                            zero_bf16* dW_bf16, zero_stream_t stream);
+                            zero_bf16* dW_bf16, void* workspace, uint64_t workspace_bytes, zero_stream_t stream);
 
 /* ------------------------------------------------------------------------------------ */
 /* status                                                                                */

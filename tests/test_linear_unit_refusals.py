@@ -43,10 +43,10 @@ def dx(z, **kw):
 
 
 def dw(z, **kw):
-    a = dict(dz=P, x=P, xc=None, xs=None, m=4, r=64, k=32, scale=1.0, dw=P, dwb=None)
+    a = dict(dz=P, x=P, xc=None, xs=None, m=4, r=64, k=32, scale=1.0, dw=P, dwb=None, ws=None, wsb=0)
     a.update(kw)
     return z.library().fsdp_linear_dw(a["dz"], a["x"], a["xc"], a["xs"], a["m"], a["r"], a["k"], a["scale"], a["dw"],
-                                      a["dwb"], None)
+                                      a["dwb"], a["ws"], a["wsb"], None)
 
 
 def actb(z, **kw):
@@ -82,7 +82,9 @@ def test_dx_refuses(z, kw, word):
     (dict(m=0), "1..2^30"), (dict(r=12), "multiples of 8"), (dict(dz=None), "NULL"), (dict(x=None), "pass X"),
     (dict(xc=P, xs=P), "pass X"), (dict(x=None, xc=P), "pass X"), (dict(dw=None), "one of dW"),
     (dict(dwb=P), "one of dW"), (dict(scale=float("nan")), "finite"), (dict(scale=float("inf")), "finite"),
-    (dict(dz=P + 2), "16-byte"), (dict(dw=P + 4), "16-byte"), (dict(x=None, xc=P + 8, xs=P), "16-byte")])
+    (dict(dz=P + 2), "16-byte"), (dict(dw=P + 4), "16-byte"), (dict(x=None, xc=P + 8, xs=P), "16-byte"),
+    (dict(x=None, xc=P, xs=P), "workspace of 0"), (dict(x=None, xc=P, xs=P, ws=P, wsb=255), "workspace of 255"),
+    (dict(x=None, xc=P, xs=P, ws=P + 4, wsb=256), "16-byte")])
 def test_dw_refuses(z, kw, word):
     refused(z, dw(z, **kw), word)
 
@@ -110,3 +112,10 @@ def test_pack_refuses(z, args, word):
     ((P, P, 4, 32, 0, P + 2), "16-byte")])
 def test_unpack_refuses(z, args, word):
     refused(z, z.library().fsdp_checkpoint8_unpack(*args, None), word)
+
+
+def test_dw_workspace(z):
+    assert z.fsdp_linear_dw_workspace(3, 40) == 256 and z.fsdp_linear_dw_workspace(8192, 4096) == 2 * 8192 * 4096
+    with pytest.raises(z.ZeroError):
+        z.fsdp_linear_dw_workspace(0, 40)
+    refused(z, z.library().fsdp_linear_dw_workspace(4, 32, None), "NULL")

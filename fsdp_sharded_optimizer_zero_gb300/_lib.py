@@ -193,10 +193,11 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
 
 
 def _ptr_array(ts, dtype, name):
-    arr = (C.c_void_p * len(ts))()
-    for i, t in enumerate(ts):
-        arr[i] = _dev(t, dtype, (name, i))
-    return arr
+    dev = torch._C._cuda_getDevice()
+    return (C.c_void_p * len(ts))(*[
+        t.data_ptr() if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == dev
+                         and t.is_contiguous())
+        else _dev(t, dtype, (name, i)) for i, t in enumerate(ts)])
 
 
 def _adam(hp) -> zero_adam:

@@ -46,8 +46,8 @@ __device__ __forceinline__ float amax8(const f2 (&v)[4]) {
   return m;
 }
 
-constexpr int kFlatBlocks = 16;  // blocks per SM of the flat kernels
-constexpr int kFlat = 4;  // units a thread has in flight in the flat kernels
+constexpr int kFlatBlocks = 32;  // blocks per SM of the flat kernels
+constexpr int kFlat = 3;  // units a thread has in flight in the flat kernels
 
 // flat: units of 8 elements, four lanes to a group; every access of a warp is contiguous
 __global__ void __launch_bounds__(kThreads) ckpt8_pack_flat_kernel(const uint16_t* __restrict__ x, int64_t units,
@@ -183,19 +183,14 @@ __global__ void __launch_bounds__(kThreads) ckpt8_unpack_rows_kernel(const int8_
 // order; a block adds its row lanes in order through shared memory, and block c of the cluster
 // the columns c, c + blocks, .. of all blocks' sums, in block order: the same bits every call, and no
 // memory between launches.
-#ifndef ACT_UN
-#define ACT_UN 4
-#endif
-#ifndef ACT_MB
-#define ACT_MB 2
-#endif
+constexpr int kActBlocks = 2;  // resident blocks per SM of act_backward_kernel (its registers allow no more)
 template <int ACT, bool Z8, int LANES>
-__global__ void __launch_bounds__(kThreads, ACT_MB) act_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
+__global__ void __launch_bounds__(kThreads, kActBlocks) act_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
                                                                    const int8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
                                                                    int64_t cols, int64_t rows_per_block, int64_t strip0,
                                                                    uint16_t* dz, float* __restrict__ db) {
-  constexpr int RL = kThreads / LANES, STRIP = 8 * LANES, UN = ACT == FSDP_ACT_NONE ? 8 : ACT_UN;
+  constexpr int RL = kThreads / LANES, STRIP = 8 * LANES, UN = ACT == FSDP_ACT_NONE ? 4 : 2;
   __shared__ float part[RL][STRIP + 1];
   __shared__ float sums[STRIP];
   const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
@@ -204,34 +199,38 @@ __global__ void __launch_bounds__(kThreads, ACT_MB) act_backward_kernel(const ui
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows_per_block, last = min(first + rows_per_block, rows);
   f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
   if (col < cols) {
-    for (int64_t r0 = first + rl; r0 < last; r0 += UN * RL) {
-      uint4 gw[UN], zw[UN];
-      uint2 cw[UN];
-      uint32_t byte[UN];
+    struct Batch {
+      uint4 g[UN], z[Z8 ? 1 : UN];
+      uint2 c[Z8 ? UN : 1];
+      uint32_t byte[Z8 ? UN : 1];
+    };
+    const auto load = [&](int64_t r0, Batch& t) {
 #pragma unroll
       for (int k = 0; k < UN; ++k) {
         const int64_t row = r0 + k * RL;
         if (row < last) {
-          gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy + row * cols + col));
+          t.g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + row * cols + col));
           if constexpr (ACT != FSDP_ACT_NONE) {
             if constexpr (Z8) {
-              cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes + row * cols + col));
-              byte[k] = scales[row * groups + (col >> 5)];
+              t.c[k] = __ldcs(reinterpret_cast<const uint2*>(codes + row * cols + col));
+              t.byte[k] = scales[row * groups + (col >> 5)];
             } else {
-              zw[k] = __ldcs(reinterpret_cast<const uint4*>(z + row * cols + col));
+              t.z[k] = __ldcs(reinterpret_cast<const uint4*>(z + row * cols + col));
             }
           }
         }
       }
+    };
+    const auto use = [&](int64_t r0, const Batch& t) {
 #pragma unroll
       for (int k = 0; k < UN; ++k) {
         const int64_t row = r0 + k * RL;
         if (row < last) {
           f2 g[4], v[4];
-          widen8(gw[k], g);
+          widen8(t.g[k], g);
           if constexpr (ACT != FSDP_ACT_NONE) {
-            if constexpr (Z8) decode8(cw[k], byte[k], v);
-            else widen8(zw[k], v);
+            if constexpr (Z8) decode8(t.c[k], t.byte[k], v);
+            else widen8(t.z[k], v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
           }
@@ -240,6 +239,15 @@ __global__ void __launch_bounds__(kThreads, ACT_MB) act_backward_kernel(const ui
           for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], g[j]);
         }
       }
+    };
+    // two batches of rows: one is loaded while the other is used
+    Batch t[2];
+    load(first + rl, t[0]);
+    for (int64_t r0 = first + rl; r0 < last; r0 += 2 * UN * RL) {
+      load(r0 + UN * RL, t[1]);
+      use(r0, t[0]);
+      load(r0 + 2 * UN * RL, t[0]);
+      use(r0 + UN * RL, t[1]);
     }
   }
   if (!db) return;  // the same for every block of a cluster
@@ -276,8 +284,17 @@ template <int ACT, bool Z8, int LANES>
 cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales,
                           int64_t rows, int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
   constexpr int RL = kThreads / LANES, STRIP = 8 * LANES;
-  int blocks = 1;  // across the rows: no fewer than four rows a thread
-  while (blocks < 8 && rows > static_cast<int64_t>(blocks) * RL * 4) blocks *= 2;
+  // Blocks across the rows, no fewer than four rows a thread: the count (one cluster: at most 8)
+  // whose blocks fill their last wave best (8192 x 14336, 56 strips: 5 blocks, one wave of 280 where 304
+  // fit, 109 us).
+  const int64_t strips_all = (cols + STRIP - 1) / STRIP, resident = static_cast<int64_t>(num_sms()) * kActBlocks;
+  int blocks = 1;
+  double best = 0.0;
+  for (int n = 1; n <= 8 && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
+    const int64_t total = strips_all * n, waves = (total + resident - 1) / resident;
+    const double fill = static_cast<double>(total) / static_cast<double>(waves * resident);
+    if (fill > best + 0.01) best = fill, blocks = n;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = st;
@@ -303,8 +320,7 @@ cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* c
 template <int ACT, bool Z8>
 cudaError_t launch_act(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales, int64_t rows,
                        int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
-  const int64_t want = 2 * num_sms();
-  if ((cols + 127) / 128 * 8 >= want) return launch_strips<ACT, Z8, 16>(dy, z, codes, scales, rows, cols, dz, db, st);
+  if (cols > 4096) return launch_strips<ACT, Z8, 32>(dy, z, codes, scales, rows, cols, dz, db, st);
   return launch_strips<ACT, Z8, 4>(dy, z, codes, scales, rows, cols, dz, db, st);
 }
 

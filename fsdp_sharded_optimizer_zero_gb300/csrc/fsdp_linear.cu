@@ -49,7 +49,7 @@ struct LinearParams {
   CUtensorMap w[kGemmMaxPieces];  // fwd, dx: the row shards of W, boxes of 64 columns x w_box rows
   CUtensorMap a;                  // fwd: X, dx: dZ (K-major, box 64 x 128 or TN rows); dw: dZ (MN-major, box 64 x 64)
   CUtensorMap b;                  // dw: X (MN-major, box 64 x 64)
-  CUtensorMap out;                // wide kernel: the output, boxes of 64 bf16 or 32 fp32 columns x 32 rows
+  CUtensorMap out;                // wide kernel, fp32 dW: the output, boxes of 32 columns x 32 rows
   int m, n, k;                    // the product: out [m, n], contraction over k
   int n_shards, shard_rows;       // fwd, dx
   int w_box, w_box_log;           // rows of W per copy: the largest power of two <= 128 (fwd) or 64 (dx) that divides shard_rows
@@ -141,32 +141,52 @@ __device__ __forceinline__ void unpack8(const uint4& w, f2* x) {
   x[0] = f2_from_bf16x2(w.x), x[1] = f2_from_bf16x2(w.y), x[2] = f2_from_bf16x2(w.z), x[3] = f2_from_bf16x2(w.w);
 }
 
+// 4 or 8 bytes of codes a column unit of 8, or 16 where rows allow
+__device__ __forceinline__ void load_codes32(const LinearParams& p, size_t at, int col0, uint32_t (&c)[8]) {
+  if (col0 + 32 <= p.n && (p.n & 15) == 0) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.zc_in + at) + q);
+      c[4 * q] = w.x, c[4 * q + 1] = w.y, c[4 * q + 2] = w.z, c[4 * q + 3] = w.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint2 w = make_uint2(0u, 0u);
+      if (col0 + 8 * q < p.n) w = __ldg(reinterpret_cast<const uint2*>(p.zc_in + at + 8 * q));
+      c[2 * q] = w.x, c[2 * q + 1] = w.y;
+    }
+  }
+}
+
 // wide kernel: 32 columns col0 .. of output row `row`, one thread, v their fp32 sums in pairs: the
-// output's values in place, and the forward's kept pre-activation stored. 32 columns are one
-// group of the 8-bit checkpoint; its scale byte is returned. Sums past column n are zero. bias:
-// the 32 columns' biases in fp32 in shared memory (null: none).
+// output's values in place. 32 columns are one group of the 8-bit checkpoint: the forward stores
+// its codes and returns its scale byte in `byte`; for dx from 8 bits `byte` is the kept
+// activation's. side: the 32 columns' bf16 words of the tensor read beside the sums (forward: the
+// residual; dx: the kept activation in bf16, or else the residual). zw (forward): the
+// pre-activation in bf16, where it is kept so. bias: the columns' biases in shared memory. Sums
+// past column n are zero.
 template <int OP>
-__device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, int col0, const float* bias,
-                                               f2 (&v)[16]) {
+__device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int col0, const uint4* bias,
+                                           const uint4 (&side)[4], uint4 (&zw)[4], uint32_t& byte, f2 (&v)[16]) {
   const size_t at = static_cast<size_t>(row) * p.n + col0;
   const bool live = row < p.m;
-  uint32_t byte = 0;
+  bool side_is_res = p.res != nullptr;
   if constexpr (OP == OP_FWD) {
-    if (bias) {
+    if (p.bias) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 b = *reinterpret_cast<const float4*>(bias + 4 * q);
-        v[2 * q] = f2_add(v[2 * q], f2_make(b.x, b.y));
-        v[2 * q + 1] = f2_add(v[2 * q + 1], f2_make(b.z, b.w));
+      for (int q = 0; q < 4; ++q) {
+        f2 b[4];
+        unpack8(bias[q], b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], b[j]);
       }
     }
-    if (p.z && live) {
+    if (p.z) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (col0 + 8 * q < p.n)
-          __stcs(reinterpret_cast<uint4*>(p.z + at + 8 * q),
-                 make_uint4(f2_to_bf16x2(v[4 * q]), f2_to_bf16x2(v[4 * q + 1]), f2_to_bf16x2(v[4 * q + 2]),
-                            f2_to_bf16x2(v[4 * q + 3])));
+        zw[q] = make_uint4(f2_to_bf16x2(v[4 * q]), f2_to_bf16x2(v[4 * q + 1]), f2_to_bf16x2(v[4 * q + 2]),
+                           f2_to_bf16x2(v[4 * q + 3]));
     }
     if (p.zc) {
       float amax = 0.0f;
@@ -199,30 +219,18 @@ __device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, i
       for (int j = 0; j < 16; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
     });
   } else if constexpr (OP == OP_DX) {
-    if (p.act != FSDP_ACT_NONE && live) {
+    if (p.act != FSDP_ACT_NONE) {
       f2 z[16];
       if (p.zc_in) {
-        const float s = ckpt_scale(__ldg(p.zs_in + static_cast<size_t>(row) * ((p.n + 31) / 32) + (col0 >> 5)));
-        uint2 c[4];
+        uint32_t c[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        if (live) load_codes32(p, at, col0, c);
+        const float s = ckpt_scale(byte);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          c[q] = make_uint2(0u, 0u);
-          if (col0 + 8 * q < p.n) c[q] = __ldg(reinterpret_cast<const uint2*>(p.zc_in + at + 8 * q));
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            z[4 * q + j] = ckpt_values2(c[q].x, j, s), z[4 * q + 2 + j] = ckpt_values2(c[q].y, j, s);
+        for (int j = 0; j < 16; ++j) z[j] = ckpt_values2(c[j >> 1], j & 1, s);
       } else {
-        uint4 c[4];
+        side_is_res = false;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          c[q] = make_uint4(0u, 0u, 0u, 0u);
-          if (col0 + 8 * q < p.n) c[q] = ldg16(p.z_in + at + 8 * q);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) unpack8(c[q], z + 4 * q);
+        for (int q = 0; q < 4; ++q) unpack8(side[q], z + 4 * q);
       }
       with_act(p.act, [&](auto a) {
 #pragma unroll
@@ -235,23 +243,25 @@ __device__ __forceinline__ uint32_t epilogue32(const LinearParams& p, int row, i
     for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], s);
   }
   if constexpr (OP != OP_DW) {
-    if (p.res && live) {
-      uint4 c[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        c[q] = make_uint4(0u, 0u, 0u, 0u);
-        if (col0 + 8 * q < p.n) c[q] = ldg16(p.res + at + 8 * q);
-      }
+    if (side_is_res) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f2 r[4];
-        unpack8(c[q], r);
+        unpack8(side[q], r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
       }
+    } else if (OP == OP_DX && p.res && live) {  // beside a bf16 kept activation, which has the staging buffers
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (col0 + 8 * q < p.n) {
+          f2 r[4];
+          unpack8(ldg16(p.res + at + 8 * q), r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
+        }
     }
   }
-  return byte;
 }
 
 // narrow kernel: 4 columns of one output row per lane, 32 lanes across 128 columns; the 8 lanes
@@ -333,8 +343,8 @@ template <int OP> struct Wide {
   static constexpr int STAGES = OP == OP_DW ? 6 : 5;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr uint32_t STAGE = 2 * kHalf;
-  static constexpr uint32_t EPI = EPI_WARPS * 4096u;        // a 4 KiB staging buffer per warp
-  static constexpr uint32_t BIAS = OP == OP_FWD ? 8u * 128u * 4u : 0u;
+  static constexpr uint32_t EPI = EPI_WARPS * 2u * 4096u;   // two 4 KiB staging buffers per warp
+  static constexpr uint32_t BIAS = OP == OP_FWD ? 2u * 256u * 2u : 0u;  // a tile's biases, twice
   static constexpr uint32_t SMEM = STAGES * STAGE + EPI + BIAS + 1024;
 };
 
@@ -376,6 +386,36 @@ __device__ __forceinline__ bool warp_wait_sleeping(uint32_t bar, uint32_t parity
     }
   }
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// A 4 KiB staging buffer holds 32 rows x 64 bf16 columns, the 16-byte piece j of row i at slot j ^
+// (i % 8): a thread's own row and the warp's rows in order are both free of bank conflicts.
+// The epilogue moves it to and from global memory with ordinary accesses, eight lanes to a row of
+// 128 bytes: bulk copies would need a proxy fence by every thread, which waits for the warp's
+// stores in flight (about 1000 cycles, twice a tile).
+__device__ __forceinline__ uint32_t staged_at(int i, int j) { return static_cast<uint32_t>(i * 128 + ((j ^ (i & 7)) * 16)); }
+// rows r0 .., columns c0 .. c0 + 63 of src [m, n] to the buffer, asynchronously; zeros outside
+__device__ __forceinline__ void stage_load(uint32_t buf, const uint16_t* src, int r0, int c0, int m, int n, int lane) {
+  const int j = lane & 7, col = c0 + 8 * j;
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int i = it * 4 + (lane >> 3);
+    const bool in = r0 + i < m && col < n;
+    const uint16_t* at = in ? src + static_cast<size_t>(r0 + i) * n + col : src;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(buf + staged_at(i, j)), "l"(at), "r"(in ? 16u : 0u)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// the buffer to rows r0 .., columns c0 .. of dst [m, n]
+__device__ __forceinline__ void stage_store(const uint8_t* buf, uint16_t* dst, int r0, int c0, int m, int n, int lane) {
+  const int j = lane & 7, col = c0 + 8 * j;
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int i = it * 4 + (lane >> 3);
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + staged_at(i, j));
+    if (r0 + i < m && col < n) __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(r0 + i) * n + col), w);
+  }
 }
 
 // fp32 add of a shared-memory box to global memory, in L2
@@ -549,24 +589,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
     }
   } else if (warp < 2 + C::EPI_WARPS) {
     // ---------------- epilogue (both CTAs, own 128 rows) ----------------
+    // A thread has a row of the tile; a warp's 64-column chunk of bf16 output goes through one of
+    // its staging buffers. A bf16 tensor that the epilogue reads beside the sums (residual, kept
+    // activation) is loaded into the buffers before the sums are ready, and each thread replaces
+    // its row by the output.
     const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
     const int part = (warp - 2) >> 2;  // which of the quarter's warps
-    uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 4096u;
-    float* bias = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI) + (warp - 2) * C::EPI_COLS;
+    uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;
+    uint8_t* bias_sm = smem + C::STAGES * C::STAGE + C::EPI;
     const unsigned int poll_ns = min(max(32u * static_cast<unsigned int>(num_k), 128u), 2048u);  // a tenth of a main loop
-    uint32_t i = 0;
+    const int groups = (p.n + 31) / 32;
+    const uint16_t* side_src = nullptr;
+    if constexpr (OP != OP_DW) side_src = OP == OP_DX && p.z_in ? p.z_in : p.res;
+    uint32_t i = 0, bias_turn = 0;
     bool stop = false;
-    for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+    for (int tile = pair; tile < tiles && !stop; tile += pairs, bias_turn ^= 1u) {
       int mb, nb;
       wide_tile_coords(tile, num_m, num_n, mb, nb);
       const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
       const int c0 = nb * 256 + part * C::EPI_COLS;
-      if (OP == OP_FWD && p.bias) {  // this warp's 128 columns, 4 a lane, while the main loop runs
-        const int col = c0 + lane * 4;
-        const uint2 b = col < p.n ? __ldg(reinterpret_cast<const uint2*>(p.bias + col)) : make_uint2(0u, 0u);
-        __syncwarp();
-        reinterpret_cast<float4*>(bias)[lane] = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
-        __syncwarp();
+      uint32_t bytes = 0;  // the row's scale bytes of four groups
+      const uint4* bias = nullptr;
+      if constexpr (OP == OP_FWD) {
+        if (p.bias) {
+          // one warp of the four that share these 128 columns copies them; the other half of the
+          // area is the last tile's, so one barrier is enough
+          uint8_t* at = bias_sm + bias_turn * 512u + part * 256u;
+          if (q == 0 && lane < 16) {
+            const int col = c0 + 8 * lane;
+            reinterpret_cast<uint4*>(at)[lane] = col < p.n ? ldg16(p.bias + col) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+          bias = reinterpret_cast<const uint4*>(at);
+        }
+      }
+      if constexpr (OP != OP_DW) {
+        if (side_src)
+          for (int b = 0; b < 2; ++b) stage_load(smem_u32(stage) + 4096u * b, side_src, r0, c0 + 64 * b, p.m, p.n, lane);
+        if (OP == OP_DX && p.zc_in && row < p.m) {
+          const uint8_t* zs = p.zs_in + static_cast<size_t>(row) * groups + (c0 >> 5);
+          if ((groups & 3) == 0) {
+            if (c0 < p.n) bytes = __ldg(reinterpret_cast<const uint32_t*>(zs));
+          } else {
+            for (int g = 0; g < 4; ++g)
+              if (c0 + 32 * g < p.n) bytes |= static_cast<uint32_t>(__ldg(zs + g)) << (8 * g);
+          }
+        }
       }
       for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
         const uint32_t a = i & 1u, u = i >> 1;
@@ -576,35 +644,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
         }
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
-        if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
         if (OP == OP_DW && p.y32) {
+          if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
 #pragma unroll 1
           for (int c = 0; c < C::EPI_COLS; c += 32) {
             uint32_t r[32];
             tmem_ld_32cols(taddr + c, r);
             if (c0 + c >= p.n) continue;
-            f2 v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-            epilogue32<OP>(p, row, c0 + c, nullptr, v);
-            if (lane == 0) bulk_wait_group_read<0>();
+            const f2 s = f2_both(p.scale);
+            uint8_t* buf = stage + ((c >> 5) & 1) * 4096;
+            if (lane == 0) bulk_wait_group_read<1>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<ulonglong2*>(stage + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-                  make_ulonglong2(v[2 * j], v[2 * j + 1]);
+              *reinterpret_cast<ulonglong2*>(buf + staged_at(lane, j)) =
+                  make_ulonglong2(f2_mul(f2_make(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), s),
+                                  f2_mul(f2_make(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), s));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(stage));
-              else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(stage));
+              if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
+              else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(buf));
               bulk_commit_group();
             }
           }
         } else {
-          uint32_t bytes = 0;  // four scale bytes of this row
 #pragma unroll 1
           for (int c = 0; c < C::EPI_COLS; c += 64) {
+            uint8_t* buf = stage + ((c >> 6) & 1) * 4096;
+            const bool any = c0 + c < p.n;  // warp-uniform
+            if (OP != OP_DW && side_src) {
+              if (c == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+              else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncwarp();  // the buffer is loaded, or its last store has read it
             uint32_t w[32];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -613,44 +686,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
               f2 v[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-              if (c0 + c + 32 * h < p.n) {
-                const uint32_t b = epilogue32<OP>(p, row, c0 + c + 32 * h, p.bias ? bias + c + 32 * h : nullptr, v);
-                bytes |= b << (8 * (c / 32 + h));
+              if (any) {
+                uint4 side[4], zw[4];
+                if (OP != OP_DW && side_src) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) side[j] = *reinterpret_cast<const uint4*>(buf + staged_at(lane, 4 * h + j));
+                }
+                const int g = (c >> 5) + h;
+                uint32_t byte = OP == OP_DX ? (bytes >> (8 * g)) & 0xFFu : 0u;
+                epilogue32<OP>(p, row, c0 + c + 32 * h, bias + 4 * g, side, zw, byte, v);
+                if (OP == OP_FWD) {
+                  bytes |= byte << (8 * g);
+                  if (p.z) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = zw[j];
+                  }
+                }
               }
 #pragma unroll
               for (int j = 0; j < 16; ++j) w[16 * h + j] = f2_to_bf16x2(v[j]);
             }
-            if (c0 + c >= p.n) continue;
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
+            if (!any) continue;
+            if (OP == OP_FWD && p.z) {
+              __syncwarp();
+              stage_store(buf, p.z, r0, c0 + c, p.m, p.n, lane);
+              __syncwarp();
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+              *reinterpret_cast<uint4*>(buf + staged_at(lane, j)) =
                   make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&p.out, c0 + c, r0, smem_u32(stage));
-              bulk_commit_group();
-            }
+            stage_store(buf, p.y, r0, c0 + c, p.m, p.n, lane);
           }
+          __syncwarp();  // before the next tile's loads into the buffers
           if (OP == OP_FWD && p.zc && row < p.m) {
-            const int groups = (p.n + 31) / 32, g0 = c0 >> 5;
-            uint8_t* zs = p.zs + static_cast<size_t>(row) * groups + g0;
-            if ((groups & 3) == 0 && g0 + 4 <= groups) {
-              *reinterpret_cast<uint32_t*>(zs) = bytes;
+            uint8_t* zs = p.zs + static_cast<size_t>(row) * groups + (c0 >> 5);
+            if ((groups & 3) == 0) {
+              if (c0 < p.n) *reinterpret_cast<uint32_t*>(zs) = bytes;
             } else {
               for (int g = 0; g < 4; ++g)
-                if (g0 + g < groups) zs[g] = static_cast<uint8_t>(bytes >> (8 * g));
+                if (c0 + 32 * g < p.n) zs[g] = static_cast<uint8_t>(bytes >> (8 * g));
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[a]), 0));
+        // relaxed: the arrival only says that the tensor-memory loads are done (ordered by the fence
+        // above); a release at cluster scope would wait for every store the epilogue just made
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           mapa_shared(smem_u32(&acce_bar[a]), 0))
+                       : "memory");
       }
     }
-    if (lane == 0) bulk_wait_group_all();  // no store may still read this CTA's shared memory
+    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy may still write this CTA's shared memory
+    if (lane == 0) bulk_wait_group_all();             // and no store still read it
   }
 
   tc_fence_before();
@@ -685,8 +776,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
 }
 
@@ -799,16 +889,29 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   }
   tc_fence_before();
   cluster_sync_all();  // every CTA's part is in its shared memory
+  // four rows at a time, so that a row's remote loads do not wait for the last row's
   const int rows = TN / splits;
   const uint32_t base = smem_u32(smem);
-  for (int t = rank * rows + warp; t < (rank + 1) * rows; t += 8) {
-    if (m0 + t >= p.m) break;
-    f2 v[2] = {0ull, 0ull};
+  for (int b = warp; b < rows; b += 32) {
+    f2 v[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j][0] = v[j][1] = 0ull;
     for (int s = 0; s < splits; ++s) {
-      const float4 f = ld_cluster_f4(mapa_shared(base, s) + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
-      v[0] = f2_add(v[0], f2_make(f.x, f.y)), v[1] = f2_add(v[1], f2_make(f.z, f.w));
+      const uint32_t part_s = mapa_shared(base, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = rank * rows + b + 8 * j;
+        if (b + 8 * j < rows && m0 + t < p.m) {
+          const float4 f = ld_cluster_f4(part_s + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
+          v[j][0] = f2_add(v[j][0], f2_make(f.x, f.y)), v[j][1] = f2_add(v[j][1], f2_make(f.z, f.w));
+        }
+      }
     }
-    epilogue4<OP>(p, m0 + t, n0 + lane * 4, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = rank * rows + b + 8 * j;
+      if (b + 8 * j < rows && m0 + t < p.m) epilogue4<OP>(p, m0 + t, n0 + lane * 4, v[j]);
+    }
   }
   cluster_sync_all();  // no CTA leaves while its part is read
   if (warp == 1) {
@@ -926,8 +1029,11 @@ int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char
 // and take one part.
 constexpr int kMaxChunkBlocks = 64;
 
-// Kernel choice: the wide kernel once its tiles keep most CTA pairs busy, the narrow one with
-// the contraction split over up to 8 CTAs below that and for up to 32 rows.
+// Kernel choice, from both kernels timed over 19 shapes (forward, dx, dw; splits 1 to 8): the wide
+// kernel from 34 tiles for its 76 CTA pairs on (36 tiles, 1024 x 2304 from 768: 13.0 us against 13.9; 48
+// tiles, 4096 x 768 from 2304: 20.8 against 27.3), the narrow one below (32 tiles, 512 x 4096 from 4096: 24.3
+// against 29.0) and for up to 128 rows, which leave half of a 256-row tile or more empty. The narrow
+// kernel's splits double while every CTA keeps two blocks and all CTAs are resident at once (two per SM).
 struct Choice {
   bool wide;
   int tn, splits;
@@ -935,14 +1041,14 @@ struct Choice {
 Choice choose(int op, int64_t m, int64_t n, int64_t k, bool fp32) {
   const int64_t wide_tiles = ((m + 255) / 256) * ((n + 255) / 256);
   const int64_t blocks = (k + BK - 1) / BK, col_tiles = (n + 127) / 128;
-  const bool few_rows = op != OP_DW && m <= 32;
+  const bool few_rows = op != OP_DW && m <= 128;
   Choice c{true, 128, 1};
-  if ((wide_tiles * 8 >= num_sms() * 3 && !few_rows) || (fp32 && blocks > 8 * kMaxChunkBlocks) || col_tiles > 65535)
+  if ((wide_tiles * 9 >= num_sms() * 2 && !few_rows) || (fp32 && blocks > 8 * kMaxChunkBlocks) || col_tiles > 65535)
     return c;
   c.wide = false;
-  if (few_rows) c.tn = 32;
+  if (op != OP_DW && m <= 32) c.tn = 32;
   const int64_t tiles = ((m + c.tn - 1) / c.tn) * col_tiles;
-  while (c.splits < 8 && blocks >= 4 * c.splits && tiles * c.splits * 2 <= 2 * num_sms()) c.splits *= 2;
+  while (c.splits < 8 && blocks >= 4 * c.splits && tiles * c.splits <= num_sms()) c.splits *= 2;
   while (fp32 && c.splits < 8 && blocks > static_cast<int64_t>(c.splits) * kMaxChunkBlocks) c.splits *= 2;
   return c;
 }
@@ -990,8 +1096,7 @@ int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who)
     }
   }
   if (c.wide) {
-    rc = fp32 ? encode(&p.out, p.y32, p.m, p.n, 32, 32, true, who) : encode(&p.out, p.y, p.m, p.n, 64, 32, false, who);
-    if (rc) return rc;
+    if (fp32 && (rc = encode(&p.out, p.y32, p.m, p.n, 32, 32, true, who))) return rc;
     return fast ? launch_wide<OP, true>(p, st, who) : launch_wide<OP, false>(p, st, who);
   }
   if constexpr (OP != OP_DW)

@@ -782,6 +782,39 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// The sum of S CTAs' parts (shared-memory address `base` in each) over this CTA's rows, in CTA order,
+// and the epilogue on it: rows warp, warp + 8, .., with eight remote loads of a lane in flight (each
+// takes most of a microsecond).
+template <int OP, int TN, int S>
+__device__ __forceinline__ void add_parts(const LinearParams& p, uint32_t base, int rank, int m0, int n0, int warp,
+                                          int lane) {
+  constexpr int ROWS = TN / S, R = 8 / S;
+  for (int b = warp; b < ROWS; b += 8 * R) {
+    float4 f[R][S];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int t = rank * ROWS + b + 8 * j;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        f[j][s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (b + 8 * j < ROWS && m0 + t < p.m)
+          f[j][s] = ld_cluster_f4(mapa_shared(base, s) + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int t = rank * ROWS + b + 8 * j;
+      if (b + 8 * j < ROWS && m0 + t < p.m) {  // the same for the whole warp
+        f2 v[2] = {f2_make(f[j][0].x, f[j][0].y), f2_make(f[j][0].z, f[j][0].w)};
+#pragma unroll
+        for (int s = 1; s < S; ++s)
+          v[0] = f2_add(v[0], f2_make(f[j][s].x, f[j][s].y)), v[1] = f2_add(v[1], f2_make(f[j][s].z, f[j][s].w));
+        epilogue4<OP>(p, m0 + t, n0 + lane * 4, v);
+      }
+    }
+  }
+}
+
 template <int OP, int TN>
 __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
   using C = Narrow<TN>;
@@ -891,29 +924,12 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   }
   tc_fence_before();
   cluster_sync_all();  // every CTA's part is in its shared memory
-  // four rows at a time, so that a row's remote loads do not wait for the last row's
-  const int rows = TN / splits;
   const uint32_t base = smem_u32(smem);
-  for (int b = warp; b < rows; b += 32) {
-    f2 v[4][2];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j][0] = v[j][1] = 0ull;
-    for (int s = 0; s < splits; ++s) {
-      const uint32_t part_s = mapa_shared(base, s);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = rank * rows + b + 8 * j;
-        if (b + 8 * j < rows && m0 + t < p.m) {
-          const float4 f = ld_cluster_f4(part_s + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
-          v[j][0] = f2_add(v[j][0], f2_make(f.x, f.y)), v[j][1] = f2_add(v[j][1], f2_make(f.z, f.w));
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = rank * rows + b + 8 * j;
-      if (b + 8 * j < rows && m0 + t < p.m) epilogue4<OP>(p, m0 + t, n0 + lane * 4, v[j]);
-    }
+  switch (splits) {
+    case 1: add_parts<OP, TN, 1>(p, base, rank, m0, n0, warp, lane); break;
+    case 2: add_parts<OP, TN, 2>(p, base, rank, m0, n0, warp, lane); break;
+    case 4: add_parts<OP, TN, 4>(p, base, rank, m0, n0, warp, lane); break;
+    default: add_parts<OP, TN, 8>(p, base, rank, m0, n0, warp, lane); break;
   }
   cluster_sync_all();  // no CTA leaves while its part is read
   if (warp == 1) {

@@ -166,6 +166,14 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint32_t bar, uint32_t
   }
 }
 
+// ---- programmatic dependent launch ----
+// Wait until the grids this one depends on have completed and their writes are visible; every
+// thread that touches global memory calls it first. A no-op without the launch attribute.
+__device__ __forceinline__ void wait_for_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Let the next grid of the stream be launched once every block has called this (or left): its
+// blocks take their places, set up and wait as above.
+__device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 1-D bulk copy global -> shared, completing `bytes` transactions on `bar`.
 // Both addresses 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst_smem, const void* src, uint32_t bytes, uint32_t bar) {

@@ -53,6 +53,8 @@ constexpr int kFlat = 3;  // units a thread has in flight in the flat kernels
 __global__ void __launch_bounds__(kThreads) ckpt8_pack_flat_kernel(const uint16_t* __restrict__ x, int64_t units,
                                                                    int8_t* __restrict__ codes,
                                                                    uint8_t* __restrict__ scales) {
+  allow_next_grid();
+  wait_for_prior_grids();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += kFlat * stride) {
     uint4 w[kFlat];
@@ -86,6 +88,8 @@ template <int ACT>
 __global__ void __launch_bounds__(kThreads) ckpt8_unpack_flat_kernel(const int8_t* __restrict__ codes,
                                                                      const uint8_t* __restrict__ scales,
                                                                      int64_t units, uint16_t* __restrict__ out) {
+  allow_next_grid();
+  wait_for_prior_grids();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += kFlat * stride) {
     uint2 w[kFlat];
@@ -117,6 +121,8 @@ constexpr int kRows = 4;
 __global__ void __launch_bounds__(kThreads) ckpt8_pack_rows_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                    int64_t cols, int8_t* __restrict__ codes,
                                                                    uint8_t* __restrict__ scales) {
+  allow_next_grid();
+  wait_for_prior_grids();
   const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
@@ -151,6 +157,8 @@ template <int ACT>
 __global__ void __launch_bounds__(kThreads) ckpt8_unpack_rows_kernel(const int8_t* __restrict__ codes,
                                                                      const uint8_t* __restrict__ scales, int64_t rows,
                                                                      int64_t cols, uint16_t* __restrict__ out) {
+  allow_next_grid();
+  wait_for_prior_grids();
   const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
@@ -193,6 +201,8 @@ __global__ void __launch_bounds__(kThreads, kActBlocks) act_backward_kernel(cons
   constexpr int RL = kThreads / LANES, STRIP = 8 * LANES, UN = ACT == FSDP_ACT_NONE ? 4 : 2;
   __shared__ float part[RL][STRIP + 1];
   __shared__ float sums[STRIP];
+  allow_next_grid();
+  wait_for_prior_grids();
   const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
   const int lane = threadIdx.x % LANES, rl = threadIdx.x / LANES;
   const int64_t col0 = (strip0 + blockIdx.y) * STRIP, col = col0 + lane * 8;
@@ -295,21 +305,13 @@ cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* c
     const double fill = static_cast<double>(total) / static_cast<double>(waves * resident);
     if (fill > best + 0.01) best = fill, blocks = n;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const int64_t per = (rows + blocks - 1) / blocks;
   // strips in launches of at most 65535 (the grid's y limit)
   for (int64_t s0 = 0, strips = (cols + STRIP - 1) / STRIP; s0 < strips; s0 += 65535) {
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min<int64_t>(strips - s0, 65535)), 1);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, act_backward_kernel<ACT, Z8, LANES>, dy, z, codes, scales, rows, cols,
-                                             per, s0, dz, db);
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min<int64_t>(strips - s0, 65535)), 1);
+    const cudaError_t e = launch_overlapped(act_backward_kernel<ACT, Z8, LANES>, grid, dim3(kThreads), 0,
+                                            static_cast<unsigned>(blocks), st, dy, z, codes, scales, rows, cols, per, s0,
+                                            dz, db);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -335,11 +337,11 @@ cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, const int
 cudaError_t launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, uint8_t* scales, cudaStream_t st) {
   if (cols % kCkptGroup == 0) {
     const int64_t units = rows * (cols / 8);
-    ckpt8_pack_flat_kernel<<<grid_for(units, kFlatBlocks), kThreads, 0, st>>>(x, units, codes, scales);
-  } else {
-    ckpt8_pack_rows_kernel<<<grid_for((rows + kRows - 1) / kRows * 32, 8), kThreads, 0, st>>>(x, rows, cols, codes, scales);
+    return launch_overlapped(ckpt8_pack_flat_kernel, dim3(grid_for(units, kFlatBlocks)), dim3(kThreads), 0, 1, st, x,
+                             units, codes, scales);
   }
-  return cudaGetLastError();
+  return launch_overlapped(ckpt8_pack_rows_kernel, dim3(grid_for((rows + kRows - 1) / kRows * 32, 8)), dim3(kThreads), 0,
+                           1, st, x, rows, cols, codes, scales);
 }
 
 template <int ACT>
@@ -347,12 +349,11 @@ cudaError_t launch_unpack(const int8_t* codes, const uint8_t* scales, int64_t ro
                           cudaStream_t st) {
   if (cols % kCkptGroup == 0) {
     const int64_t units = rows * (cols / 8);
-    ckpt8_unpack_flat_kernel<ACT><<<grid_for(units, kFlatBlocks), kThreads, 0, st>>>(codes, scales, units, out);
-  } else {
-    ckpt8_unpack_rows_kernel<ACT><<<grid_for((rows + kRows - 1) / kRows * 32, 8), kThreads, 0, st>>>(codes, scales, rows,
-                                                                                                 cols, out);
+    return launch_overlapped(ckpt8_unpack_flat_kernel<ACT>, dim3(grid_for(units, kFlatBlocks)), dim3(kThreads), 0, 1, st,
+                             codes, scales, units, out);
   }
-  return cudaGetLastError();
+  return launch_overlapped(ckpt8_unpack_rows_kernel<ACT>, dim3(grid_for((rows + kRows - 1) / kRows * 32, 8)),
+                           dim3(kThreads), 0, 1, st, codes, scales, rows, cols, out);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

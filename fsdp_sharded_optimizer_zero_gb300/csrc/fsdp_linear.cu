@@ -471,6 +471,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers initialised and tensor memory allocated before any copy
   tc_fence_after();
+  allow_next_grid();
+  wait_for_prior_grids();
   const uint32_t tmem_base = tmem_base_sh;
 
   if (warp == 0) {
@@ -851,6 +853,8 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  allow_next_grid();
+  wait_for_prior_grids();
   const uint32_t tmem_base = tmem_base_sh;
 
   if (warp == 0) {
@@ -1012,8 +1016,8 @@ int launch_wide(const LinearParams& p, cudaStream_t st, const char* who) {
   if (tiles > INT32_MAX / 2)
     return set_error(ZERO_ERR_UNSUPPORTED, "%s: an output of %d x %d is more than 2^30 tiles", who, p.m, p.n);
   const unsigned int pairs = static_cast<unsigned int>(std::min<int64_t>(tiles, std::max(1, num_sms() / 2)));
-  linear_wide_kernel<OP, FAST><<<2 * pairs, C::THREADS, C::SMEM, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_overlapped(linear_wide_kernel<OP, FAST>, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, 1, st, p);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 
@@ -1023,19 +1027,10 @@ int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char
   static OncePerDevice once;
   int rc = set_smem(once, linear_narrow_kernel<OP, TN>, C::SMEM, who);
   if (rc) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>((p.n + 127) / 128),
-                     static_cast<unsigned>((p.m + TN - 1) / TN));
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_narrow_kernel<OP, TN>, p);
+  const dim3 grid(static_cast<unsigned>(splits), static_cast<unsigned>((p.n + 127) / 128),
+                  static_cast<unsigned>((p.m + TN - 1) / TN));
+  const cudaError_t e = launch_overlapped(linear_narrow_kernel<OP, TN>, grid, dim3(256), C::SMEM,
+                                          static_cast<unsigned>(splits), st, p);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 

@@ -145,6 +145,28 @@ class OncePerDevice {
   std::mutex mu_;
 };
 
+// Launch `kernel` on `st` with `cluster` blocks per cluster (1: none) and programmatic dependent
+// launch: its blocks may be placed while the stream's previous kernel drains, so the kernel calls
+// wait_for_prior_grids() before its first access to global memory.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, unsigned int cluster,
+                              cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // True when fsdp_unit_forward can read W straight from its n_ranks row shards (the fused
 // gather, no scratch) under the current zero_set_gemm_kernel choice.
 bool fsdp_fused_gather_ok(int n_ranks, int64_t rows_out);

@@ -700,8 +700,8 @@ def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, workspace=None, 
     if pc is not None and workspace is None:
         workspace = torch.empty(fsdp_linear_dw_workspace(m, k), dtype=torch.uint8, device=dZ.device)
         if stream is not None:  # not to be reused before that stream is done with it
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(stream))
+            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream
+                                    else stream or torch.cuda.default_stream())
     _check(_lib.fsdp_linear_dw(_dev(dZ, bf, "dZ"), _is(x, (m, k), bf, "x"), pc, ps, m, r, k, scale,
                                pw if wide else None, None if wide else pw, _dev(workspace, torch.uint8, "workspace"),
                                0 if workspace is None else workspace.numel(), _stream(stream)))

@@ -511,8 +511,8 @@ ZERO_API int fsdp_unit_forward_static_scratch(int n_ranks, const zero_bf16* cons
  * every value is exact in bf16. A group that holds an infinity or a NaN has byte 255 and zero
  * codes: it reads back as NaN throughout.
  *
- * Activations: the FSDP_ACT_* values; GELU is x Phi(x), GELU_TANH its tanh form, SILU x / (1 +
- * exp(-x)). They and their derivatives are computed in fp32 (relative error of a few 2^-20)
+ * Activations: the FSDP_ACT_* values; RELU's derivative at 0 is 0, GELU is x Phi(x), GELU_TANH
+ * its tanh form, SILU x / (1 + exp(-x)). They and their derivatives are computed in fp32 (relative error of a few 2^-20)
  * from the fp32 sum or the kept activation, with one rounding to the output's type.
  *
  * Calls take every m_tokens / rows >= 1; widths (rows_out, k_in, cols) are multiples of 8,

@@ -36,7 +36,8 @@ EXPORTS = (
     "fsdp_gather_rows", "fsdp_unit_forward", "fsdp_transpose_cat", "fsdp_unit_backward_workspace", "fsdp_unit_backward", "fsdp_mlp_forward",
     "fsdp_zero3_step_workspace", "fsdp_zero3_step", "fsdp_zero3_mlp_step_workspace", "fsdp_zero3_mlp_step",
     "fsdp_unit_forward_static_scratch",
-    "fsdp_checkpoint8_pack", "fsdp_checkpoint8_unpack", "fsdp_linear_forward", "fsdp_act_backward", "fsdp_linear_dx",
+    "fsdp_checkpoint8_pack", "fsdp_checkpoint8_unpack", "fsdp_linear_forward", "fsdp_act_backward",
+    "fsdp_act_backward_workspace", "fsdp_linear_dx",
     "fsdp_linear_dw", "fsdp_linear_dw_workspace",
     "zero_last_error", "zero_device_status", "zero_selftest_bounded_wait", "zero_set_fused_kernel", "zero_set_gemm_kernel", "zero_version",
 )
@@ -140,7 +141,8 @@ def _load():
         "fsdp_checkpoint8_pack": (I, [VP, I64, I64, VP, VP, VP]),
         "fsdp_checkpoint8_unpack": (I, [VP, VP, I64, I64, I, VP, VP]),
         "fsdp_linear_forward": (I, [I, PP, I64, I64, VP, I64, VP, I, VP, VP, VP, VP, VP, VP]),
-        "fsdp_act_backward": (I, [VP, VP, VP, VP, I64, I64, I, VP, VP, VP]),
+        "fsdp_act_backward": (I, [VP, VP, VP, VP, I64, I64, I, VP, VP, VP, U64, VP]),
+        "fsdp_act_backward_workspace": (I, [I64, I64, C.POINTER(U64)]),
         "fsdp_linear_dx": (I, [I, PP, I64, I64, VP, I64, VP, VP, VP, I, VP, VP, VP]),
         "fsdp_linear_dw": (I, [VP, VP, VP, VP, I64, I64, I64, C.c_float, VP, VP, VP, U64, VP]),
         "fsdp_linear_dw_workspace": (I, [I64, I64, C.POINTER(U64)]),
@@ -656,15 +658,37 @@ def fsdp_linear_forward(w_shards, X, Y, bias=None, act: int = FSDP_ACT_NONE, res
         _stream(stream)))
 
 
-def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT_NONE, stream=None):
+def _call_workspace(nbytes: int, device, stream):
+    """Device memory for one call on `stream`, from PyTorch's allocator; not reused before that
+    stream is done with it."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream
+                         else stream or torch.cuda.default_stream())
+    return ws
+
+
+def fsdp_act_backward_workspace(rows: int, cols: int) -> int:
+    """Workspace bytes with which fsdp_act_backward sums db faster (0: none is used)."""
+    b = C.c_uint64()
+    _check(_lib.fsdp_act_backward_workspace(rows, cols, C.byref(b)))
+    return b.value
+
+
+def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT_NONE, workspace=None, stream=None):
     """dZ = bf16(dY act'(Z)), db = the fp32 column sums of dY act'(Z); Z as z (bf16) or z8 =
-    (codes, scales)."""
+    (codes, scales). workspace: a uint8 CUDA tensor of fsdp_act_backward_workspace(...) bytes; None
+    takes it from PyTorch's allocator for this call where db of a large matrix uses one."""
     rows, cols = _rows_cols(dY, "dY")
     bf = torch.bfloat16
     pc, ps = _kept(z8, (rows, cols), "z8")
+    if workspace is None and db is not None and act and rows * cols >= 1 << 22:
+        nbytes = fsdp_act_backward_workspace(rows, cols)
+        workspace = _call_workspace(nbytes, dY.device, stream) if nbytes else None
     _check(_lib.fsdp_act_backward(
         _dev(dY, bf, "dY"), _is(z, (rows, cols), bf, "z"), pc, ps, rows, cols, act, _is(dZ, (rows, cols), bf, "dZ"),
-        _is(db, (cols,), torch.float32, "db"), _stream(stream)))
+        _is(db, (cols,), torch.float32, "db"), _dev(workspace, torch.uint8, "workspace"),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 def fsdp_linear_dx(w_shards, dZ, dX, z=None, z8=None, act: int = FSDP_ACT_NONE, residual=None, stream=None):
@@ -698,10 +722,7 @@ def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, workspace=None, 
     wide = dW.dtype == torch.float32
     pw = _is(dW, (r, k), torch.float32 if wide else bf, "dW")
     if pc is not None and workspace is None:
-        workspace = torch.empty(fsdp_linear_dw_workspace(m, k), dtype=torch.uint8, device=dZ.device)
-        if stream is not None:  # not to be reused before that stream is done with it
-            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream
-                                    else stream or torch.cuda.default_stream())
+        workspace = _call_workspace(fsdp_linear_dw_workspace(m, k), dZ.device, stream)
     _check(_lib.fsdp_linear_dw(_dev(dZ, bf, "dZ"), _is(x, (m, k), bf, "x"), pc, ps, m, r, k, scale,
                                pw if wide else None, None if wide else pw, _dev(workspace, torch.uint8, "workspace"),
                                0 if workspace is None else workspace.numel(), _stream(stream)))

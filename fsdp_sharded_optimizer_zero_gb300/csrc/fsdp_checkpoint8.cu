@@ -185,7 +185,135 @@ __global__ void __launch_bounds__(kThreads) ckpt8_unpack_rows_kernel(const int8_
     }
 }
 
-// Activation backward with the column sums. A cluster of blocks takes a strip of 8 LANES
+// Activation backward without column sums: flat, as pack and unpack (8 bits: widths that are
+// multiples of 32). One sweep over memory: 8192 x 14336 from 8 bits 91 us, 106 us in the strips below.
+template <int ACT, bool Z8>
+__global__ void __launch_bounds__(kThreads) act_backward_flat_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
+                                                                     const int8_t* __restrict__ codes,
+                                                                     const uint8_t* __restrict__ scales, int64_t units,
+                                                                     uint16_t* dz) {
+  constexpr int UN = 2;
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += UN * stride) {
+    uint4 gw[UN], zw[UN];
+    uint2 cw[UN];
+    uint32_t byte[UN];
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      const int64_t i = i0 + k * stride;
+      if (i < units) {
+        gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy) + i);
+        if constexpr (Z8) {
+          cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i);
+          byte[k] = scales[i >> 2];
+        } else {
+          zw[k] = __ldcs(reinterpret_cast<const uint4*>(z) + i);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      const int64_t i = i0 + k * stride;
+      if (i < units) {
+        f2 g[4], v[4];
+        widen8(gw[k], g);
+        if constexpr (Z8) decode8(cw[k], byte[k], v);
+        else widen8(zw[k], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
+        __stcs(reinterpret_cast<uint4*>(dz) + i, narrow8(g));
+      }
+    }
+  }
+}
+
+// Activation backward with the column sums over a large matrix: the same sweep, by a number of
+// threads that is a multiple of the 8-column units of a row, so that a thread stays in its columns
+// and sums them over its rows. `lanes` rows are swept at a time and leave as many partial sums a
+// column in the workspace, [lanes][cols] fp32.
+constexpr int kSweepBlocks = 4;  // blocks per SM, all resident
+template <int ACT, bool Z8>
+__global__ void __launch_bounds__(kThreads, kSweepBlocks) act_backward_sweep_kernel(
+    const uint16_t* dy, const uint16_t* __restrict__ z, const int8_t* __restrict__ codes,
+    const uint8_t* __restrict__ scales, int64_t rows, int64_t cols, int lanes, uint16_t* dz, float* __restrict__ partial) {
+  constexpr int UN = 2;
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int row_units = static_cast<int>(cols / 8), tid = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
+  const int lane = tid / row_units, col = (tid - lane * row_units) * 8;
+  if (lane >= lanes) return;
+  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup, step = static_cast<int64_t>(lanes) * row_units;
+  int64_t i0 = tid, s0 = lane * groups + (col >> 5);  // this thread's unit of row r0, and its group
+  f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+  for (int64_t r0 = lane; r0 < rows; r0 += UN * lanes, i0 += UN * step, s0 += UN * lanes * groups) {
+    uint4 gw[UN], zw[UN];
+    uint2 cw[UN];
+    uint32_t byte[UN];
+#pragma unroll
+    for (int k = 0; k < UN; ++k)
+      if (r0 + k * lanes < rows) {
+        gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy) + i0 + k * step);
+        if constexpr (ACT != FSDP_ACT_NONE) {
+          if constexpr (Z8) {
+            cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i0 + k * step);
+            byte[k] = scales[s0 + k * lanes * groups];
+          } else {
+            zw[k] = __ldcs(reinterpret_cast<const uint4*>(z) + i0 + k * step);
+          }
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < UN; ++k)
+      if (r0 + k * lanes < rows) {
+        f2 g[4], v[4];
+        widen8(gw[k], g);
+        if constexpr (ACT != FSDP_ACT_NONE) {
+          if constexpr (Z8) decode8(cw[k], byte[k], v);
+          else widen8(zw[k], v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
+        }
+        if (dz) __stcs(reinterpret_cast<uint4*>(dz) + i0 + k * step, narrow8(g));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], g[j]);
+      }
+  }
+  ulonglong2* out = reinterpret_cast<ulonglong2*>(partial + static_cast<int64_t>(lane) * cols + col);
+  out[0] = make_ulonglong2(sum[0], sum[1]);
+  out[1] = make_ulonglong2(sum[2], sum[3]);
+}
+
+// db = the sum of `lanes` partial sums a column: a block takes 32 columns, 4 a thread; 32 threads share
+// a column (thread y the partials y, y + 32, ..) and are added in order
+__global__ void __launch_bounds__(kThreads) sum_partials_kernel(const float* __restrict__ partial, int lanes,
+                                                                int64_t cols, float* __restrict__ db) {
+  __shared__ float part[32][33];
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 32, col = col0 + x * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < cols) {
+#pragma unroll 4
+    for (int l = y; l < lanes; l += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(partial + l * cols + col);
+      s.x = __fadd_rn(s.x, v.x), s.y = __fadd_rn(s.y, v.y), s.z = __fadd_rn(s.z, v.z), s.w = __fadd_rn(s.w, v.w);
+    }
+  }
+  part[y][4 * x] = s.x, part[y][4 * x + 1] = s.y, part[y][4 * x + 2] = s.z, part[y][4 * x + 3] = s.w;
+  __syncthreads();
+  if (threadIdx.x < 32 && col0 + threadIdx.x < cols) {
+    float t = part[0][threadIdx.x];
+#pragma unroll
+    for (int l = 1; l < 32; ++l) t = __fadd_rn(t, part[l][threadIdx.x]);
+    db[col0 + threadIdx.x] = t;
+  }
+}
+
+// Activation backward with the column sums, without a workspace, for small matrices, where one
+// launch counts more. A cluster of blocks takes a strip of 8 LANES
 // columns, each block a run of its rows: LANES threads across the strip (8 columns each),
 // kThreads / LANES rows at a time, four of a thread's rows in flight. A thread sums its rows in
 // order; a block adds its row lanes in order through shared memory, and block c of the cluster
@@ -219,13 +347,13 @@ __global__ void __launch_bounds__(kThreads, kActBlocks) act_backward_kernel(cons
       for (int k = 0; k < UN; ++k) {
         const int64_t row = r0 + k * RL;
         if (row < last) {
-          t.g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + row * cols + col));
+          t.g[k] = *reinterpret_cast<const uint4*>(dy + row * cols + col);
           if constexpr (ACT != FSDP_ACT_NONE) {
             if constexpr (Z8) {
-              t.c[k] = __ldcs(reinterpret_cast<const uint2*>(codes + row * cols + col));
+              t.c[k] = __ldg(reinterpret_cast<const uint2*>(codes + row * cols + col));
               t.byte[k] = scales[row * groups + (col >> 5)];
             } else {
-              t.z[k] = __ldcs(reinterpret_cast<const uint4*>(z + row * cols + col));
+              t.z[k] = __ldg(reinterpret_cast<const uint4*>(z + row * cols + col));
             }
           }
         }
@@ -244,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, kActBlocks) act_backward_kernel(cons
 #pragma unroll
             for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
           }
-          if (dz) __stcs(reinterpret_cast<uint4*>(dz + row * cols + col), narrow8(g));
+          if (dz) *reinterpret_cast<uint4*>(dz + row * cols + col) = narrow8(g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], g[j]);
         }
@@ -326,9 +454,43 @@ cudaError_t launch_act(const uint16_t* dy, const uint16_t* z, const int8_t* code
   return launch_strips<ACT, Z8, 4>(dy, z, codes, scales, rows, cols, dz, db, st);
 }
 
+// Rows that the sweep takes at a time, and so partial sums a column; 0: the matrix is for the strips.
+// From 2^22 elements and 4096 columns on the sweep wins (8192 x 14336: from 8 bits 97 us against 104,
+// from bf16 107 against 115); narrower rows leave too many partial sums (8192 x 768: 29 against 9),
+// and without an activation, where only dY is read, the strips are level or ahead (40 us against 45).
+int sweep_lanes(int64_t rows, int64_t cols) {
+  if (rows * cols < (int64_t(1) << 22) || cols < 4096) return 0;
+  return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms()) * kSweepBlocks * kThreads / (cols / 8), rows));
+}
+
+template <int ACT, bool Z8>
+cudaError_t launch_sweep(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales, int64_t rows,
+                         int64_t cols, int lanes, uint16_t* dz, float* db, float* partial, cudaStream_t st) {
+  const int64_t threads = lanes * (cols / 8);
+  const cudaError_t e = launch_overlapped(act_backward_sweep_kernel<ACT, Z8>,
+                                          dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)),
+                                          dim3(kThreads), 0, 1, st, dy, z, codes, scales, rows, cols, lanes, dz, partial);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(sum_partials_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(kThreads), 0, 1, st,
+                           partial, lanes, cols, db);
+}
+
 template <int ACT>
 cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales,
-                                int64_t rows, int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
+                                int64_t rows, int64_t cols, uint16_t* dz, float* db, float* partial, cudaStream_t st) {
+  if constexpr (ACT != FSDP_ACT_NONE) {
+    const int lanes = db && partial ? sweep_lanes(rows, cols) : 0;
+    if (lanes && codes) return launch_sweep<ACT, true>(dy, z, codes, scales, rows, cols, lanes, dz, db, partial, st);
+    if (lanes) return launch_sweep<ACT, false>(dy, z, codes, scales, rows, cols, lanes, dz, db, partial, st);
+  }
+  if constexpr (ACT != FSDP_ACT_NONE) {
+    if (!db && (!codes || cols % kCkptGroup == 0)) {
+      const int64_t units = rows * (cols / 8);
+      return launch_overlapped(codes ? act_backward_flat_kernel<ACT, true> : act_backward_flat_kernel<ACT, false>,
+                               dim3(grid_for(units, kFlatBlocks)), dim3(kThreads), 0, 1, st, dy, z, codes, scales, units,
+                               dz);
+    }
+  }
   if constexpr (ACT != FSDP_ACT_NONE)
     if (codes) return launch_act<ACT, true>(dy, z, codes, scales, rows, cols, dz, db, st);
   return launch_act<ACT, false>(dy, z, codes, scales, rows, cols, dz, db, st);
@@ -421,26 +583,42 @@ extern "C" int fsdp_checkpoint8_unpack(const int8_t* codes, const uint8_t* scale
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 
+extern "C" int fsdp_act_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes) {
+  const char* who = "fsdp_act_backward_workspace";
+  if (!bytes) return set_error(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+  const int rc = check_shape(rows, cols, who);
+  if (rc) return rc;
+  *bytes = 4 * static_cast<uint64_t>(sweep_lanes(rows, cols)) * static_cast<uint64_t>(cols);
+  return ZERO_OK;
+}
+
 extern "C" int fsdp_act_backward(const zero_bf16* dY, const zero_bf16* z, const int8_t* z_codes, const uint8_t* z_scales,
-                                 int64_t rows, int64_t cols, int act, zero_bf16* dZ, float* db, zero_stream_t stream) {
+                                 int64_t rows, int64_t cols, int act, zero_bf16* dZ, float* db, void* workspace,
+                                 uint64_t workspace_bytes, zero_stream_t stream) {
   const char* who = "fsdp_act_backward";
   int rc = check_shape(rows, cols, who);
   if (rc) return rc;
   if (!dY) return set_error(ZERO_ERR_INVALID_ARG, "%s: dY is NULL", who);
   if (!dZ && !db) return set_error(ZERO_ERR_INVALID_ARG, "%s: dZ and db are both NULL", who);
   if ((rc = check_kept_activation(z, z_codes, z_scales, act, who))) return rc;
-  if (!aligned16(dY) || !aligned16(dZ) || !aligned16(db))
-    return set_error(ZERO_ERR_INVALID_ARG, "%s: dY, dZ and db must be 16-byte aligned", who);
+  if (!aligned16(dY) || !aligned16(dZ) || !aligned16(db) || !aligned16(workspace))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: dY, dZ, db and workspace must be 16-byte aligned", who);
+  uint64_t need = 0;
+  if (workspace && (rc = fsdp_act_backward_workspace(rows, cols, &need))) return rc;
+  if (workspace && workspace_bytes < need)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: workspace of %llu bytes is below the %llu needed", who,
+                     (unsigned long long)workspace_bytes, (unsigned long long)need);
+  float* partial = static_cast<float*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (act) {
-    case FSDP_ACT_RELU: e = launch_act_backward<FSDP_ACT_RELU>(dY, z, z_codes, z_scales, rows, cols, dZ, db, st); break;
-    case FSDP_ACT_GELU: e = launch_act_backward<FSDP_ACT_GELU>(dY, z, z_codes, z_scales, rows, cols, dZ, db, st); break;
+    case FSDP_ACT_RELU: e = launch_act_backward<FSDP_ACT_RELU>(dY, z, z_codes, z_scales, rows, cols, dZ, db, partial, st); break;
+    case FSDP_ACT_GELU: e = launch_act_backward<FSDP_ACT_GELU>(dY, z, z_codes, z_scales, rows, cols, dZ, db, partial, st); break;
     case FSDP_ACT_GELU_TANH:
-      e = launch_act_backward<FSDP_ACT_GELU_TANH>(dY, z, z_codes, z_scales, rows, cols, dZ, db, st);
+      e = launch_act_backward<FSDP_ACT_GELU_TANH>(dY, z, z_codes, z_scales, rows, cols, dZ, db, partial, st);
       break;
-    case FSDP_ACT_SILU: e = launch_act_backward<FSDP_ACT_SILU>(dY, z, z_codes, z_scales, rows, cols, dZ, db, st); break;
-    default: e = launch_act_backward<FSDP_ACT_NONE>(dY, nullptr, nullptr, nullptr, rows, cols, dZ, db, st); break;
+    case FSDP_ACT_SILU: e = launch_act_backward<FSDP_ACT_SILU>(dY, z, z_codes, z_scales, rows, cols, dZ, db, partial, st); break;
+    default: e = launch_act_backward<FSDP_ACT_NONE>(dY, nullptr, nullptr, nullptr, rows, cols, dZ, db, partial, st); break;
   }
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }

@@ -1042,26 +1042,31 @@ int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char
 // and take one part.
 constexpr int kMaxChunkBlocks = 64;
 
-// Kernel choice, from both kernels timed over 19 shapes (forward, dx, dw; splits 1 to 8): the wide
-// kernel from 34 tiles for its 76 CTA pairs on (36 tiles, 1024 x 2304 from 768: 13.0 us against 13.9; 48
-// tiles, 4096 x 768 from 2304: 20.8 against 27.3), the narrow one below (32 tiles, 512 x 4096 from 4096: 24.3
-// against 29.0) and for up to 128 rows, which leave half of a 256-row tile or more empty. The narrow
-// kernel's splits double while every CTA keeps two blocks and all CTAs are resident at once (two per SM).
+// Kernel choice, from both kernels timed over 20 shapes (forward, dx, dw; splits 1 to 8). The narrow
+// kernel while its 128 x 128 tiles, split in two, are resident at once (two CTAs per SM: up to 38
+// wide tiles; 36 of them, 1000 x 2304 from 768: 11.6 us against 14.8) and for up to 128 rows, which
+// leave half of a 256-row tile or more empty; else the wide one (48 tiles, 4096 x 768 from 2304: 20.3
+// against 25.9). The narrow kernel's splits double while every CTA keeps two blocks and one CTA per
+// SM is not passed, and on to two per SM up to 4 splits, or with 8 blocks left to each (32 tiles of
+// 64 blocks: 8 splits 10.3 us, 4 splits 12.1; 36 tiles of 32 blocks: 12.0 and 9.3).
 struct Choice {
   bool wide;
   int tn, splits;
 };
 Choice choose(int op, int64_t m, int64_t n, int64_t k, bool fp32) {
-  const int64_t wide_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t wide_tiles = ((m + 255) / 256) * ((n + 255) / 256), sms = num_sms();
   const int64_t blocks = (k + BK - 1) / BK, col_tiles = (n + 127) / 128;
   const bool few_rows = op != OP_DW && m <= 128;
   Choice c{true, 128, 1};
-  if ((wide_tiles * 9 >= num_sms() * 2 && !few_rows) || (fp32 && blocks > 8 * kMaxChunkBlocks) || col_tiles > 65535)
-    return c;
+  if ((wide_tiles * 4 > sms && !few_rows) || (fp32 && blocks > 8 * kMaxChunkBlocks) || col_tiles > 65535) return c;
   c.wide = false;
   if (op != OP_DW && m <= 32) c.tn = 32;
   const int64_t tiles = ((m + c.tn - 1) / c.tn) * col_tiles;
-  while (c.splits < 8 && blocks >= 4 * c.splits && tiles * c.splits <= num_sms()) c.splits *= 2;
+  while (c.splits < 8 && blocks >= 4 * c.splits) {
+    const int64_t next = 2 * c.splits, ctas = tiles * next;
+    if (ctas > sms && (ctas > 2 * sms || (next > 4 && blocks < 8 * next))) break;
+    c.splits = static_cast<int>(next);
+  }
   while (fp32 && c.splits < 8 && blocks > static_cast<int64_t>(c.splits) * kMaxChunkBlocks) c.splits *= 2;
   return c;
 }

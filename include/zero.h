@@ -548,12 +548,18 @@ ZERO_API int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[],
                                  const zero_bf16* residual, zero_bf16* Y, zero_bf16* z, int8_t* z_codes,
                                  uint8_t* z_scales, zero_stream_t stream);
 
+/* Bytes of device workspace with which fsdp_act_backward sums db faster over a large matrix (0: none
+ * is used). */
+ZERO_API int fsdp_act_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
+
 /* Backward of the activation and the bias: dZ = bf16(dY act'(Z)), db = sum over the rows of
- * the unrounded dY act'(Z), fp32, in a fixed order (the same bits every call). dY, dZ [rows,
- * cols] bf16, dZ nullable when db is asked for; db [cols] fp32, nullable. With FSDP_ACT_NONE, db is the column sum of
- * dY. The residual's gradient is dY itself. */
+ * the unrounded dY act'(Z), fp32, in a fixed order (the same bits every call with the same
+ * sizes and choice of workspace). dY, dZ [rows, cols] bf16, dZ nullable when db is asked for;
+ * db [cols] fp32, nullable. With FSDP_ACT_NONE, db is the column sum of dY. The residual's
+ * gradient is dY itself. workspace: nullable, else of fsdp_act_backward_workspace() bytes. */
 ZERO_API int fsdp_act_backward(const zero_bf16* dY, const zero_bf16* z, const int8_t* z_codes, const uint8_t* z_scales,
-                               int64_t rows, int64_t cols, int act, zero_bf16* dZ, float* db, zero_stream_t stream);
+                               int64_t rows, int64_t cols, int act, zero_bf16* dZ, float* db, void* workspace,
+                               uint64_t workspace_bytes, zero_stream_t stream);
 
 /* Input gradient: dX = bf16((dZ W) act'(Z) + residual), with Z the kept pre-activation of the
  * layer that produced this layer's input (so dX is that layer's dZ) and residual the gradient

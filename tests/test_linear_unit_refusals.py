@@ -50,10 +50,10 @@ def dw(z, **kw):
 
 
 def actb(z, **kw):
-    a = dict(dy=P, zz=P, zc=None, zs=None, m=4, k=32, act=4, dz=P, db=None)
+    a = dict(dy=P, zz=P, zc=None, zs=None, m=4, k=32, act=4, dz=P, db=None, ws=None, wsb=0)
     a.update(kw)
     return z.library().fsdp_act_backward(a["dy"], a["zz"], a["zc"], a["zs"], a["m"], a["k"], a["act"], a["dz"], a["db"],
-                                         None)
+                                         a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("kw,word", [
@@ -93,7 +93,8 @@ def test_dw_refuses(z, kw, word):
     (dict(m=0), ">= 1"), (dict(k=0), ">= 1"), (dict(k=20), "multiple of 8"), (dict(dy=None), "dY"),
     (dict(dz=None), "both NULL"), (dict(act=5), "act 5"), (dict(zz=None), "kept activation"),
     (dict(zz=None, zs=P), "kept activation"), (dict(dz=P + 8), "16-byte"), (dict(db=P + 4), "16-byte"),
-    (dict(m=1 << 41), "2^40")])
+    (dict(m=1 << 41), "2^40"), (dict(ws=P + 8, wsb=1 << 30), "16-byte"),
+    (dict(m=1 << 20, db=P, ws=P, wsb=64), "workspace of 64")])
 def test_act_backward_refuses(z, kw, word):
     refused(z, actb(z, **kw), word)
 
@@ -112,6 +113,16 @@ def test_pack_refuses(z, args, word):
     ((P, P, 4, 32, 0, P + 2), "16-byte")])
 def test_unpack_refuses(z, args, word):
     refused(z, z.library().fsdp_checkpoint8_unpack(*args, None), word)
+
+
+def test_act_backward_workspace(z):
+    assert z.fsdp_act_backward_workspace(16, 4096) == 0
+    b = z.fsdp_act_backward_workspace(1 << 20, 4096)
+    assert b > 0 and b % (4 * 4096) == 0
+    assert z.fsdp_act_backward_workspace(3, 1 << 21) == 0 or z.fsdp_act_backward_workspace(3, 1 << 21) >= 4 << 21
+    with pytest.raises(z.ZeroError):
+        z.fsdp_act_backward_workspace(4, 20)
+    refused(z, z.library().fsdp_act_backward_workspace(4, 32, None), "NULL")
 
 
 def test_dw_workspace(z):

@@ -208,3 +208,48 @@ def test_dw_workspace_and_streams(z):
     assert all(torch.equal(t, out[0]) for t in out[1:])
     with pytest.raises(z.ZeroError):
         z.fsdp_linear_dw(g, out[0], x8=c, workspace=ws[:-256])
+
+
+@pytest.mark.parametrize("kind", ["z", "z8", "none"])
+@pytest.mark.parametrize("rows,cols", [(4100, 1032), (531, 8200), (9, 524296), (70001, 64)])
+def test_act_backward_large(z, rows, cols, kind):
+    """Matrices past 2^22 elements, whose column sums go through a workspace: the caller's, the
+    allocator's, or none (the strips), in order in each."""
+    act = {"z": "gelu_tanh", "z8": "silu", "none": "none"}[kind]
+    dy, pre = randn(rows, cols, 0.3, 13), randn(rows, cols, 1.5, 14)
+    arg, v = {}, pre.double()
+    if kind == "z":
+        arg = {"z": pre}
+    elif kind == "z8":
+        c = new8(rows, cols)
+        z.fsdp_checkpoint8_pack(pre, *c)
+        arg, v = {"z8": c}, values(z, c)
+    zbuf, dz = guarded(rows, cols, BF, 3.0)
+    bbuf, db = guarded(1, cols, torch.float32, 3.0)
+    z.fsdp_act_backward(dy, dz, db=db[0], act=ACTS[act], **arg)
+    z.zero_device_status()
+    g = dy.double()
+    want = g * dact64(v, act)
+    e = g.abs() * act_err(v, act)[1] + SUM * want.abs()
+    inside(dz, want, e + B16 * (want.abs() + e) + 2.0 ** -133, "dZ")
+    inside(db[0], want.sum(0), e.sum(0) + (rows + 1) * SUM * want.abs().sum(0), "db")
+    assert kept(zbuf, 3.0) and kept(bbuf, 3.0)
+    nbytes = z.fsdp_act_backward_workspace(rows, cols)
+    ws = torch.full((nbytes + 64,), 7, dtype=torch.uint8, device=DEV)
+    db2 = torch.empty(cols, device=DEV)
+    z.fsdp_act_backward(dy, db=db2, act=ACTS[act], workspace=ws[:nbytes] if nbytes else None, **arg)
+    assert torch.equal(db2, db[0]) and bool((ws[nbytes:] == 7).all())
+    # dZ alone, and dZ in dY's place
+    dz2 = torch.empty_like(dz)
+    z.fsdp_act_backward(dy, dz2, act=ACTS[act], **arg)
+    assert torch.equal(dz2, dz)
+    # through the C ABI without a workspace: the strips, another fixed order
+    z.library().fsdp_act_backward(dy.data_ptr(), arg["z"].data_ptr() if "z" in arg else None,
+                                  *([t.data_ptr() for t in arg["z8"]] if "z8" in arg else [None, None]), rows, cols,
+                                  ACTS[act], dz2.data_ptr(), db2.data_ptr(), None, 0,
+                                  torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(dz2, dz)
+    inside(db2, want.sum(0), e.sum(0) + (rows + 1) * SUM * want.abs().sum(0), "db, strips")
+    z.fsdp_act_backward(dy, dy, db=db2, act=ACTS[act], **arg)
+    assert torch.equal(dy, dz) and torch.equal(db2, db[0])
+    z.zero_device_status()

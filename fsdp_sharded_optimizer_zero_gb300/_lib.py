@@ -601,14 +601,44 @@ def fsdp_unit_forward_static_scratch(w_shards, A, Y, Y_bf16=None, stream=None):
 # linear unit with its epilogue, 8-bit activation checkpoints
 # ---------------------------------------------------------------------------------------
 
-def _is(t, shape, dtype, name: str):
-    """Device pointer of a tensor of exactly this shape and dtype (None passes as NULL)."""
+_current_device = torch._C._cuda_getDevice
+
+
+def _is(t, shape, dtype, name, dev: int):
+    """Device pointer of a tensor of exactly this shape and dtype on the current device `dev` (None
+    passes as NULL)."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     p = _dev(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
     return p
+
+
+def _shards(ts, name: str, dev: int):
+    """(count, rows of one shard, columns, pointer array) of bf16 row shards, in one pass: a call with
+    eight shards spends more time here than in the library."""
+    if not ts:
+        raise ValueError(f"{name} is empty")
+    shape = getattr(ts[0], "shape", ())
+    if len(shape) == 2:
+        dtype, ptrs = torch.bfloat16, []
+        try:
+            for t in ts:
+                if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+                    break
+                ptrs.append(t.data_ptr())
+        except AttributeError:
+            pass
+        if len(ptrs) == len(ts):
+            return len(ptrs), shape[0], shape[1], (C.c_void_p * len(ptrs))(*ptrs)
+    rows, cols = _shards_shape(ts, name)  # the refusals, by name
+    return len(ts), rows, cols, _ptr_array(ts, torch.bfloat16, name)
 
 
 def _rows_cols(t, name: str):
@@ -617,29 +647,31 @@ def _rows_cols(t, name: str):
     return int(t.shape[0]), int(t.shape[1])
 
 
-def _kept(pair, shape, name: str):
+def _kept(pair, shape, name: str, dev: int):
     """Pointers of an 8-bit checkpoint (codes, scales) of a [rows, cols] activation."""
     if pair is None:
         return None, None
     codes, scales = pair
     groups = -(-shape[1] // FSDP_CHECKPOINT8_GROUP)
-    return (_is(codes, shape, torch.int8, f"{name}[0] (codes)"),
-            _is(scales, (shape[0], groups), torch.uint8, f"{name}[1] (scales)"))
+    return (_is(codes, shape, torch.int8, (name, 0), dev),
+            _is(scales, (shape[0], groups), torch.uint8, (name, 1), dev))
 
 
 def fsdp_checkpoint8_pack(x, codes, scales, stream=None):
     """codes [rows, cols] int8, scales [rows, ceil(cols / 32)] uint8 = the 8-bit checkpoint of
     x [rows, cols] bf16: value = code * 2^(scale - 127)."""
     rows, cols = _rows_cols(x, "x")
-    pc, ps = _kept((codes, scales), (rows, cols), "checkpoint")
-    _check(_lib.fsdp_checkpoint8_pack(_dev(x, torch.bfloat16, "x"), rows, cols, pc, ps, _stream(stream)))
+    dev = _current_device()
+    pc, ps = _kept((codes, scales), (rows, cols), "checkpoint", dev)
+    _check(_lib.fsdp_checkpoint8_pack(_is(x, (rows, cols), torch.bfloat16, "x", dev), rows, cols, pc, ps, _stream(stream)))
 
 
 def fsdp_checkpoint8_unpack(codes, scales, out, act: int = FSDP_ACT_NONE, stream=None):
     """out [rows, cols] bf16 = act(values of the checkpoint)."""
     rows, cols = _rows_cols(codes, "codes")
-    pc, ps = _kept((codes, scales), (rows, cols), "checkpoint")
-    _check(_lib.fsdp_checkpoint8_unpack(pc, ps, rows, cols, act, _is(out, (rows, cols), torch.bfloat16, "out"),
+    dev = _current_device()
+    pc, ps = _kept((codes, scales), (rows, cols), "checkpoint", dev)
+    _check(_lib.fsdp_checkpoint8_unpack(pc, ps, rows, cols, act, _is(out, (rows, cols), torch.bfloat16, "out", dev),
                                         _stream(stream)))
 
 
@@ -647,14 +679,14 @@ def fsdp_linear_forward(w_shards, X, Y, bias=None, act: int = FSDP_ACT_NONE, res
                         stream=None):
     """Y = bf16(act(X W^T + bias) + residual); z (bf16) or z8 = (codes, scales) receives the
     pre-activation X W^T + bias for the backward."""
-    n = len(w_shards)
-    rs, k = _shards_shape(w_shards, "w_shards")
-    m = _rows_cols(X, "X")[0]
-    r, bf = n * rs, torch.bfloat16
-    pc, ps = _kept(z8, (m, r), "z8")
+    dev, bf = _current_device(), torch.bfloat16
+    n, rs, k, w = _shards(w_shards, "w_shards", dev)
+    m, r = _rows_cols(X, "X")[0], n * rs
+    out = (m, r)
+    pc, ps = _kept(z8, out, "z8", dev)
     _check(_lib.fsdp_linear_forward(
-        n, _ptr_array(w_shards, bf, "w_shards"), r, k, _is(X, (m, k), bf, "X"), m, _is(bias, (r,), bf, "bias"), act,
-        _is(residual, (m, r), bf, "residual"), _is(Y, (m, r), bf, "Y"), _is(z, (m, r), bf, "z"), pc, ps,
+        n, w, r, k, _is(X, (m, k), bf, "X", dev), m, _is(bias, (r,), bf, "bias", dev), act,
+        _is(residual, out, bf, "residual", dev), _is(Y, out, bf, "Y", dev), _is(z, out, bf, "z", dev), pc, ps,
         _stream(stream)))
 
 
@@ -680,28 +712,28 @@ def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT
     (codes, scales). workspace: a uint8 CUDA tensor of fsdp_act_backward_workspace(...) bytes; None
     takes it from PyTorch's allocator for this call where db of a large matrix uses one."""
     rows, cols = _rows_cols(dY, "dY")
-    bf = torch.bfloat16
-    pc, ps = _kept(z8, (rows, cols), "z8")
+    dev, bf = _current_device(), torch.bfloat16
+    pc, ps = _kept(z8, (rows, cols), "z8", dev)
     if workspace is None and db is not None and act and rows * cols >= 1 << 22:
         nbytes = fsdp_act_backward_workspace(rows, cols)
         workspace = _call_workspace(nbytes, dY.device, stream) if nbytes else None
     _check(_lib.fsdp_act_backward(
-        _dev(dY, bf, "dY"), _is(z, (rows, cols), bf, "z"), pc, ps, rows, cols, act, _is(dZ, (rows, cols), bf, "dZ"),
-        _is(db, (cols,), torch.float32, "db"), _dev(workspace, torch.uint8, "workspace"),
+        _is(dY, (rows, cols), bf, "dY", dev), _is(z, (rows, cols), bf, "z", dev), pc, ps, rows, cols, act, _is(dZ, (rows, cols), bf, "dZ", dev),
+        _is(db, (cols,), torch.float32, "db", dev), _dev(workspace, torch.uint8, "workspace"),
         0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 def fsdp_linear_dx(w_shards, dZ, dX, z=None, z8=None, act: int = FSDP_ACT_NONE, residual=None, stream=None):
     """dX = bf16((dZ W) act'(Z) + residual), Z (z or z8) the kept pre-activation of the layer
     that produced this layer's input."""
-    n = len(w_shards)
-    rs, k = _shards_shape(w_shards, "w_shards")
-    m = _rows_cols(dZ, "dZ")[0]
-    r, bf = n * rs, torch.bfloat16
-    pc, ps = _kept(z8, (m, k), "z8")
+    dev, bf = _current_device(), torch.bfloat16
+    n, rs, k, w = _shards(w_shards, "w_shards", dev)
+    m, r = _rows_cols(dZ, "dZ")[0], n * rs
+    out = (m, k)
+    pc, ps = _kept(z8, out, "z8", dev)
     _check(_lib.fsdp_linear_dx(
-        n, _ptr_array(w_shards, bf, "w_shards"), r, k, _is(dZ, (m, r), bf, "dZ"), m, _is(z, (m, k), bf, "z"), pc, ps,
-        act, _is(residual, (m, k), bf, "residual"), _is(dX, (m, k), bf, "dX"), _stream(stream)))
+        n, w, r, k, _is(dZ, (m, r), bf, "dZ", dev), m, _is(z, out, bf, "z", dev), pc, ps, act,
+        _is(residual, out, bf, "residual", dev), _is(dX, out, bf, "dX", dev), _stream(stream)))
 
 
 def fsdp_linear_dw_workspace(m_tokens: int, k_in: int) -> int:
@@ -717,13 +749,13 @@ def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, workspace=None, 
     None takes it from PyTorch's allocator for this call."""
     m, r = _rows_cols(dZ, "dZ")
     k = _rows_cols(dW, "dW")[1]
-    bf = torch.bfloat16
-    pc, ps = _kept(x8, (m, k), "x8")
+    dev, bf = _current_device(), torch.bfloat16
+    pc, ps = _kept(x8, (m, k), "x8", dev)
     wide = dW.dtype == torch.float32
-    pw = _is(dW, (r, k), torch.float32 if wide else bf, "dW")
+    pw = _is(dW, (r, k), torch.float32 if wide else bf, "dW", dev)
     if pc is not None and workspace is None:
         workspace = _call_workspace(fsdp_linear_dw_workspace(m, k), dZ.device, stream)
-    _check(_lib.fsdp_linear_dw(_dev(dZ, bf, "dZ"), _is(x, (m, k), bf, "x"), pc, ps, m, r, k, scale,
+    _check(_lib.fsdp_linear_dw(_is(dZ, (m, r), bf, "dZ", dev), _is(x, (m, k), bf, "x", dev), pc, ps, m, r, k, scale,
                                pw if wide else None, None if wide else pw, _dev(workspace, torch.uint8, "workspace"),
                                0 if workspace is None else workspace.numel(), _stream(stream)))
 

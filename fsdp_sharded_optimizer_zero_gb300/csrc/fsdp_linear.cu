@@ -68,6 +68,59 @@ struct LinearParams {
 };
 
 // ------------------------------------------------------------------------------------
+// waits: bounded as everywhere in the library. The barrier queries suspend the thread for up to 20
+// us: queries that return at once keep their threads issuing, which at the power limit costs clock
+// rate (forward, dx and dw at 8192 tokens, 14336 x 4096: 591, 605 and 555 us, suspended 555, 584 and
+// 540). The global timer is read after 64 queries, not at each miss: a read takes long enough that
+// the MMA thread then runs 10 % behind.
+// ------------------------------------------------------------------------------------
+template <bool CLUSTER>  // CLUSTER: arrivals come from the other CTA of the pair too
+__device__ __forceinline__ bool try_wait_suspended(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+  return done != 0;
+}
+// false: gave up after kWaitTimeoutNs (recorded in the error word) or because another thread of the
+// CTA did
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int code) {
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_suspended<CLUSTER>(bar, parity)) return true;
+    if (*abort) return false;
+    if ((it & 63u) != 0) continue;
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitTimeoutNs) {
+      atomicCAS(&g_zgb_dev_error, 0u, code);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+// one lane of a warp waits, the whole warp gets the result
+__device__ __forceinline__ bool warp_wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int code) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = wait_bounded(bar, parity, abort, code) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// ------------------------------------------------------------------------------------
 // operand copies: what one lane of the producer warp loads for each stage
 // ------------------------------------------------------------------------------------
 struct Copy {
@@ -359,38 +412,6 @@ __device__ __forceinline__ void wide_tile_coords(int tile, int num_m, int num_n,
   nb = in_band / rows;
 }
 
-// A whole warp waits for a finished accumulator. Lane 0 asks the barrier with a suspend time of
-// 20 us, so the warp neither polls beside the producer and the MMA nor wakes late (polling with
-// sleeps of up to 2 us cost 1 us per launch at K = 4096).
-__device__ __forceinline__ bool warp_wait_suspended(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int code) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) {
-    for (unsigned long long t0 = 0;;) {
-      uint32_t done;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(bar), "r"(parity), "r"(20000u)
-          : "memory");
-      if (done) {
-        ok = 1;
-        break;
-      }
-      if (*abort) break;
-      const unsigned long long now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitTimeoutNs) {
-        atomicCAS(&g_zgb_dev_error, 0u, code);
-        *abort = 1;
-        break;
-      }
-    }
-  }
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
 // A 4 KiB staging buffer holds 32 rows x 64 bf16 columns, the 16-byte piece j of row i at slot j ^
 // (i % 8): a thread's own row and the warp's rows in order are both free of bank conflicts.
 // The epilogue moves it to and from global memory with ordinary accesses, eight lanes to a row of
@@ -489,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
           if constexpr (OP == OP_FWD) shard = min(n0 / p.shard_rows, p.n_shards - 1), row = n0 - shard * p.shard_rows;
           for (int kb = 0; kb < num_k; ++kb, ++it) {
             if (it >= static_cast<uint32_t>(C::STAGES) &&
-                !mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty)) {
+                !wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, kErrEmpty)) {
               stop = true;
               break;
             }
@@ -526,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
       for (int kb = 0; kb < num_k; ++kb, ++it) {
         bool ok = true;
         if (it >= static_cast<uint32_t>(C::STAGES))
-          ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
+          ok = wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, kErrEmpty);
         if (!__all_sync(0xffffffffu, ok)) {
           stop = true;
           break;
@@ -547,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
       int never = 0;
       const uint32_t first = it > static_cast<uint32_t>(C::STAGES) ? it - C::STAGES : 0u;
       for (uint32_t j = first; j < it; ++j)
-        mbar_wait_bounded(smem_u32(&empty_bar[j % C::STAGES]), (j / C::STAGES) & 1u, &never, &g_zgb_dev_error, kErrDrain);
+        wait_bounded(smem_u32(&empty_bar[j % C::STAGES]), (j / C::STAGES) & 1u, &never, kErrDrain);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (even CTA) ----------------
@@ -561,14 +582,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
         for (int kb = 0; kb < num_k && !stop; ++i) {  // one accumulator per chunk
           const int kb_end = min(kb + p.chunk_blocks, num_k), kb_first = kb;
           const uint32_t a = i & 1u, u = i >> 1;
-          if (u >= 1 && !mbar_wait_cluster_bounded(smem_u32(&acce_bar[a]), (u - 1) & 1u, abort, &g_zgb_dev_error, kErrAccE)) {
+          if (u >= 1 && !wait_bounded<true>(smem_u32(&acce_bar[a]), (u - 1) & 1u, abort, kErrAccE)) {
             stop = true;
             break;
           }
           tc_fence_after();
           const uint32_t d = tmem_base + a * 256;
           for (; kb < kb_end; ++kb) {
-            if (!mbar_wait_bounded(smem_u32(&full_bar[s]), ph, abort, &g_zgb_dev_error, kErrFull)) {
+            if (!wait_bounded(smem_u32(&full_bar[s]), ph, abort, kErrFull)) {
               stop = true;
               break;
             }
@@ -589,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
       if (*abort && issued) {
         int never = 0;
         umma_commit_pair(smem_u32(&drain_bar), 0x1);
-        mbar_wait_bounded(smem_u32(&drain_bar), 0, &never, &g_zgb_dev_error, kErrDrain);
+        wait_bounded(smem_u32(&drain_bar), 0, &never, kErrDrain);
       }
     }
   } else if (warp < 2 + C::EPI_WARPS) {
@@ -642,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
       }
       for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
         const uint32_t a = i & 1u, u = i >> 1;
-        if (!warp_wait_suspended(smem_u32(&accf_bar[a]), u & 1u, abort, kErrAccF)) {
+        if (!warp_wait_bounded(smem_u32(&accf_bar[a]), u & 1u, abort, kErrAccF)) {
           stop = true;
           break;
         }
@@ -871,7 +892,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
       bool ok = true;
       if (issued >= C::STAGES)
-        ok = mbar_wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, &g_zgb_dev_error, kErrEmpty);
+        ok = wait_bounded(smem_u32(&empty_bar[s]), ph ^ 1u, abort, kErrEmpty);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), C::STAGE);
       if (mine) {
@@ -884,8 +905,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
     if (*abort && lane == 0) {  // copies in flight still write this CTA's shared memory
       int never = 0;
       for (int j = max(0, issued - C::STAGES); j < issued; ++j)
-        mbar_wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never,
-                          &g_zgb_dev_error, kErrDrain);
+wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never, kErrDrain);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -893,7 +913,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       constexpr uint32_t idesc = idesc_bf16_f32(128, TN, P_MN, Q_MN);
       uint32_t s = 0, ph = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(smem_u32(&full_bar[s]), ph, abort, &g_zgb_dev_error, kErrFull)) break;
+        if (!wait_bounded(smem_u32(&full_bar[s]), ph, abort, kErrFull)) break;
         tc_fence_after();
         const uint32_t sp = smem_u32(smem) + s * C::STAGE;
         const uint64_t pd = P_MN ? sw128_mnmajor_desc(sp, kChunk) : sw128_kmajor_desc(sp);
@@ -911,7 +931,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
 
   // the accumulator is complete (or, after an abort, no MMA runs any more)
   int never = 0;
-  mbar_wait_bounded(smem_u32(&acc_bar), 0, &never, &g_zgb_dev_error, kErrAccF);
+  wait_bounded(smem_u32(&acc_bar), 0, &never, kErrAccF);
   __syncthreads();
   tc_fence_after();
   // tensor memory lane l = output column n0 + l, column t = output row m0 + t

@@ -194,7 +194,58 @@ __device__ __forceinline__ void unpack8(const uint4& w, f2* x) {
   x[0] = f2_from_bf16x2(w.x), x[1] = f2_from_bf16x2(w.y), x[2] = f2_from_bf16x2(w.z), x[3] = f2_from_bf16x2(w.w);
 }
 
-// 4 or 8 bytes of codes a column unit of 8, or 16 where rows allow
+// A 4 KiB staging buffer holds 32 rows x 64 bf16 columns, the 16-byte piece j of row i at slot j ^
+// (i % 8): a thread's own row and the warp's rows in order are both free of bank conflicts.
+// The epilogue moves it to and from global memory with ordinary accesses, eight lanes to a row of
+// 128 bytes: bulk copies would need a proxy fence by every thread, which waits for the warp's
+// stores in flight (about 1000 cycles, twice a tile).
+__device__ __forceinline__ uint32_t staged_at(int i, int j) { return static_cast<uint32_t>(i * 128 + ((j ^ (i & 7)) * 16)); }
+// rows r0 .., columns c0 .. c0 + 63 of src [m, n] to the buffer, asynchronously; zeros outside
+__device__ __forceinline__ void stage_load(uint32_t buf, const uint16_t* src, int r0, int c0, int m, int n, int lane) {
+  const int j = lane & 7, col = c0 + 8 * j;
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int i = it * 4 + (lane >> 3);
+    const bool in = r0 + i < m && col < n;
+    const uint16_t* at = in ? src + static_cast<size_t>(r0 + i) * n + col : src;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(buf + staged_at(i, j)), "l"(at), "r"(in ? 16u : 0u)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// the buffer to rows r0 .., columns c0 .. of dst [m, n]
+__device__ __forceinline__ void stage_store(const uint8_t* buf, uint16_t* dst, int r0, int c0, int m, int n, int lane) {
+  const int j = lane & 7, col = c0 + 8 * j, i0 = lane >> 3;  // rows i0, i0 + 4, ..: two alternating slots
+  const int left = col < n ? m - r0 - i0 : 0;
+  uint16_t* to = dst + static_cast<size_t>(r0 + i0) * n + col;
+  const size_t step = static_cast<size_t>(4) * n;
+  const uint8_t *even = buf + staged_at(i0, j), *odd = buf + staged_at(i0 + 4, j);
+#pragma unroll
+  for (int it = 0; it < 8; ++it, to += step) {
+    const uint4 w = *reinterpret_cast<const uint4*>(((it & 1) ? odd : even) + (it >> 1) * 1024);
+    if (4 * it < left) __stcs(reinterpret_cast<uint4*>(to), w);
+  }
+}
+
+// half h of the buffer, 32 columns, from each thread's row, and on to global memory: 64 bytes a row,
+// four lanes to one (the two rows of every eight lanes are four apart: no bank conflicts)
+__device__ __forceinline__ void stage_store_half(uint8_t* buf, const uint4 (&w)[4], int h, uint16_t* dst, int r0, int c0,
+                                                 int m, int n, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = w[j];
+  __syncwarp();
+  const int j = 4 * h + (lane & 3), col = c0 + 8 * j, i0 = ((lane >> 2) & 1) * 4 + (lane >> 3);
+  const int left = col < n ? m - r0 - i0 : 0;
+  uint16_t* to = dst + static_cast<size_t>(r0 + i0) * n + col;
+#pragma unroll
+  for (int it = 0; it < 4; ++it, to += static_cast<size_t>(8) * n) {
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + staged_at(i0, j) + it * 1024);
+    if (8 * it < left) __stcs(reinterpret_cast<uint4*>(to), v);
+  }
+  __syncwarp();
+}
+
+// 32 codes of a row, in accesses of 16 bytes where rows allow, else 8
 __device__ __forceinline__ void load_codes32(const LinearParams& p, size_t at, int col0, uint32_t (&c)[8]) {
   if (col0 + 32 <= p.n && (p.n & 15) == 0) {
 #pragma unroll
@@ -216,12 +267,13 @@ __device__ __forceinline__ void load_codes32(const LinearParams& p, size_t at, i
 // output's values in place. 32 columns are one group of the 8-bit checkpoint: the forward stores
 // its codes and returns its scale byte in `byte`; for dx from 8 bits `byte` is the kept
 // activation's. side: the 32 columns' bf16 words of the tensor read beside the sums (forward: the
-// residual; dx: the kept activation in bf16, or else the residual). zw (forward): the
-// pre-activation in bf16, where it is kept so. bias: the columns' biases in shared memory. Sums
-// past column n are zero.
+// residual; dx: the kept activation in bf16, or else the residual). bias: the columns' biases in
+// shared memory. buf, h: the staging buffer's half through which a bf16 pre-activation leaves.
+// Sums past column n are zero. Called by whole warps, thread `lane` with row r0 + lane.
 template <int OP>
-__device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int col0, const uint4* bias,
-                                           const uint4 (&side)[4], uint4 (&zw)[4], uint32_t& byte, f2 (&v)[16]) {
+__device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int col0, int r0, const uint4* bias,
+                                           const uint4 (&side)[4], uint8_t* buf, int h, int lane, uint32_t& byte,
+                                           f2 (&v)[16]) {
   const size_t at = static_cast<size_t>(row) * p.n + col0;
   const bool live = row < p.m;
   bool side_is_res = p.res != nullptr;
@@ -236,10 +288,12 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
       }
     }
     if (p.z) {
+      uint4 w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        zw[q] = make_uint4(f2_to_bf16x2(v[4 * q]), f2_to_bf16x2(v[4 * q + 1]), f2_to_bf16x2(v[4 * q + 2]),
-                           f2_to_bf16x2(v[4 * q + 3]));
+        w[q] = make_uint4(f2_to_bf16x2(v[4 * q]), f2_to_bf16x2(v[4 * q + 1]), f2_to_bf16x2(v[4 * q + 2]),
+                          f2_to_bf16x2(v[4 * q + 3]));
+      stage_store_half(buf, w, h, p.z, r0, col0 - 32 * h, p.m, p.n, lane);
     }
     if (p.zc) {
       float amax = 0.0f;
@@ -267,9 +321,9 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
         }
       }
     }
-    with_act(p.act, [&](auto a) {
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
+      for (int j = 0; j < 16; ++j) v[j] = act_fwd<decltype(act)::value>(v[j]);
     });
   } else if constexpr (OP == OP_DX) {
     if (p.act != FSDP_ACT_NONE) {
@@ -285,9 +339,9 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
 #pragma unroll
         for (int q = 0; q < 4; ++q) unpack8(side[q], z + 4 * q);
       }
-      with_act(p.act, [&](auto a) {
+      with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], act_grad<decltype(a)::value>(z[j]));
+        for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], act_grad<decltype(act)::value>(z[j]));
       });
     }
   } else {
@@ -412,41 +466,165 @@ __device__ __forceinline__ void wide_tile_coords(int tile, int num_m, int num_n,
   nb = in_band / rows;
 }
 
-// A 4 KiB staging buffer holds 32 rows x 64 bf16 columns, the 16-byte piece j of row i at slot j ^
-// (i % 8): a thread's own row and the warp's rows in order are both free of bank conflicts.
-// The epilogue moves it to and from global memory with ordinary accesses, eight lanes to a row of
-// 128 bytes: bulk copies would need a proxy fence by every thread, which waits for the warp's
-// stores in flight (about 1000 cycles, twice a tile).
-__device__ __forceinline__ uint32_t staged_at(int i, int j) { return static_cast<uint32_t>(i * 128 + ((j ^ (i & 7)) * 16)); }
-// rows r0 .., columns c0 .. c0 + 63 of src [m, n] to the buffer, asynchronously; zeros outside
-__device__ __forceinline__ void stage_load(uint32_t buf, const uint16_t* src, int r0, int c0, int m, int n, int lane) {
-  const int j = lane & 7, col = c0 + 8 * j;
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int i = it * 4 + (lane >> 3);
-    const bool in = r0 + i < m && col < n;
-    const uint16_t* at = in ? src + static_cast<size_t>(r0 + i) * n + col : src;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(buf + staged_at(i, j)), "l"(at), "r"(in ? 16u : 0u)
-                 : "memory");
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// the buffer to rows r0 .., columns c0 .. of dst [m, n]
-__device__ __forceinline__ void stage_store(const uint8_t* buf, uint16_t* dst, int r0, int c0, int m, int n, int lane) {
-  const int j = lane & 7, col = c0 + 8 * j;
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int i = it * 4 + (lane >> 3);
-    const uint4 w = *reinterpret_cast<const uint4*>(buf + staged_at(i, j));
-    if (r0 + i < m && col < n) __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(r0 + i) * n + col), w);
-  }
-}
-
 // fp32 add of a shared-memory box to global memory, in L2
 __device__ __forceinline__ void tma_reduce_add_2d(const void* tmap, int32_t x, int32_t y, uint32_t src_smem) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap),
                "r"(x), "r"(y), "r"(src_smem)
                : "memory");
+}
+
+// The epilogue warps' role. A thread has a row of the tile; a warp's 64-column chunk of bf16 output
+// goes through one of its staging buffers. A bf16 tensor that the epilogue reads beside the sums
+// (residual, kept activation) is loaded into the buffers before the sums are ready, and each thread
+// replaces its row by the output.
+template <int OP>
+__device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* smem, uint32_t tmem_base, uint32_t accf_bar,
+                                              uint32_t acce_bar, volatile int* abort, int warp, int lane, uint32_t rank,
+                                              int pair, int pairs, int num_m, int num_n) {
+  using C = Wide<OP>;
+  const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
+  const int part = (warp - 2) >> 2;  // which of the quarter's warps
+  uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;
+  uint8_t* bias_sm = smem + C::STAGES * C::STAGE + C::EPI;
+  const int groups = (p.n + 31) / 32;
+  const uint16_t* side_src = nullptr;
+  if constexpr (OP != OP_DW) side_src = OP == OP_DX && p.z_in ? p.z_in : p.res;
+  uint32_t i = 0, bias_turn = 0;
+  bool stop = false;
+  for (int tile = pair; tile < num_m * num_n && !stop; tile += pairs, bias_turn ^= 1u) {
+    int mb, nb;
+    wide_tile_coords(tile, num_m, num_n, mb, nb);
+    const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
+    const int c0 = nb * 256 + part * C::EPI_COLS;
+    uint32_t bytes = 0;  // the row's scale bytes of four groups
+    const uint4* bias = nullptr;
+    if constexpr (OP == OP_FWD) {
+      if (p.bias) {
+        // one warp of the four that share these 128 columns copies them; the other half of the
+        // area is the last tile's, so one barrier is enough
+        uint8_t* at = bias_sm + bias_turn * 512u + part * 256u;
+        if (q == 0 && lane < 16) {
+          const int col = c0 + 8 * lane;
+          reinterpret_cast<uint4*>(at)[lane] = col < p.n ? ldg16(p.bias + col) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+        bias = reinterpret_cast<const uint4*>(at);
+      }
+    }
+    if constexpr (OP != OP_DW) {
+      if (side_src)
+        for (int b = 0; b < 2; ++b) stage_load(smem_u32(stage) + 4096u * b, side_src, r0, c0 + 64 * b, p.m, p.n, lane);
+      if (OP == OP_DX && p.zc_in && row < p.m) {
+        const uint8_t* zs = p.zs_in + static_cast<size_t>(row) * groups + (c0 >> 5);
+        if ((groups & 3) == 0) {
+          if (c0 < p.n) bytes = __ldg(reinterpret_cast<const uint32_t*>(zs));
+        } else {
+          for (int g = 0; g < 4; ++g)
+            if (c0 + 32 * g < p.n) bytes |= static_cast<uint32_t>(__ldg(zs + g)) << (8 * g);
+        }
+      }
+    }
+    for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
+      const uint32_t a = i & 1u, u = i >> 1;
+      if (!warp_wait_bounded(accf_bar + 8u * a, u & 1u, abort, kErrAccF)) {
+        stop = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
+      if (OP == OP_DW && p.y32) {
+        if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
+  #pragma unroll 1
+        for (int c = 0; c < C::EPI_COLS; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32cols(taddr + c, r);
+          if (c0 + c >= p.n) continue;
+          const f2 s = f2_both(p.scale);
+          uint8_t* buf = stage + ((c >> 5) & 1) * 4096;
+          if (lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+  #pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<ulonglong2*>(buf + staged_at(lane, j)) =
+                make_ulonglong2(f2_mul(f2_make(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), s),
+                                f2_mul(f2_make(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), s));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
+            else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(buf));
+            bulk_commit_group();
+          }
+        }
+      } else {
+          // 32 columns at a time, rolled: unrolled by two the code is twice as long for the instruction
+        // cache that the producer and MMA loops share (8192 x 2304 from 768: 32.2 us, rolled 30.0). The
+        // activation is a switch in it for the same reason: the role once per activation cost 4096 x
+        // 2304 from 4096 6 %.
+#pragma unroll 1
+        for (int c = 0; c < C::EPI_COLS; c += 32) {
+          const int h = (c >> 5) & 1, col0 = c0 + c;
+          uint8_t* buf = stage + ((c >> 6) & 1) * 4096;
+          if (h == 0) {
+            if (OP != OP_DW && side_src) {
+              if (c == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+              else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncwarp();  // the buffer is loaded, or its last store has read it
+          }
+          uint32_t r[32];
+          tmem_ld_32cols(taddr + c, r);
+          if (col0 >= p.n) continue;  // warp-uniform
+          f2 v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          uint4 w[4];
+          if constexpr (OP == OP_DW) {
+            const f2 s = f2_both(p.scale);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], s);
+          } else {
+            if (side_src) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(buf + staged_at(lane, 4 * h + j));
+            }
+            uint32_t byte = OP == OP_DX ? (bytes >> (c >> 2)) & 0xFFu : 0u;
+            epilogue32<OP>(p, row, col0, r0, bias + (c >> 3), w, buf, h, lane, byte, v);
+            if (OP == OP_FWD) bytes |= byte << (c >> 2);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) =
+                make_uint4(f2_to_bf16x2(v[4 * j]), f2_to_bf16x2(v[4 * j + 1]), f2_to_bf16x2(v[4 * j + 2]),
+                           f2_to_bf16x2(v[4 * j + 3]));
+          if (h == 1 || col0 + 32 >= p.n) {
+            __syncwarp();
+            stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.n, lane);
+          }
+        }
+        __syncwarp();  // before the next tile's loads into the buffers
+        if (OP == OP_FWD && p.zc && row < p.m) {
+          uint8_t* zs = p.zs + static_cast<size_t>(row) * groups + (c0 >> 5);
+          if ((groups & 3) == 0) {
+            if (c0 < p.n) *reinterpret_cast<uint32_t*>(zs) = bytes;
+          } else {
+            for (int g = 0; g < 4; ++g)
+              if (c0 + 32 * g < p.n) zs[g] = static_cast<uint8_t>(bytes >> (8 * g));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      // relaxed: the arrival only says that the tensor-memory loads are done (ordered by the fence
+      // above); a release at cluster scope would wait for every store the epilogue just made
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         mapa_shared(acce_bar + 8u * a, 0))
+                     : "memory");
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // no copy may still write this CTA's shared memory
+  if (lane == 0) bulk_wait_group_all();             // and no store still read it
 }
 
 template <int OP, bool FAST>
@@ -615,158 +793,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
     }
   } else if (warp < 2 + C::EPI_WARPS) {
     // ---------------- epilogue (both CTAs, own 128 rows) ----------------
-    // A thread has a row of the tile; a warp's 64-column chunk of bf16 output goes through one of
-    // its staging buffers. A bf16 tensor that the epilogue reads beside the sums (residual, kept
-    // activation) is loaded into the buffers before the sums are ready, and each thread replaces
-    // its row by the output.
-    const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
-    const int part = (warp - 2) >> 2;  // which of the quarter's warps
-    uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;
-    uint8_t* bias_sm = smem + C::STAGES * C::STAGE + C::EPI;
-    const int groups = (p.n + 31) / 32;
-    const uint16_t* side_src = nullptr;
-    if constexpr (OP != OP_DW) side_src = OP == OP_DX && p.z_in ? p.z_in : p.res;
-    uint32_t i = 0, bias_turn = 0;
-    bool stop = false;
-    for (int tile = pair; tile < tiles && !stop; tile += pairs, bias_turn ^= 1u) {
-      int mb, nb;
-      wide_tile_coords(tile, num_m, num_n, mb, nb);
-      const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
-      const int c0 = nb * 256 + part * C::EPI_COLS;
-      uint32_t bytes = 0;  // the row's scale bytes of four groups
-      const uint4* bias = nullptr;
-      if constexpr (OP == OP_FWD) {
-        if (p.bias) {
-          // one warp of the four that share these 128 columns copies them; the other half of the
-          // area is the last tile's, so one barrier is enough
-          uint8_t* at = bias_sm + bias_turn * 512u + part * 256u;
-          if (q == 0 && lane < 16) {
-            const int col = c0 + 8 * lane;
-            reinterpret_cast<uint4*>(at)[lane] = col < p.n ? ldg16(p.bias + col) : make_uint4(0u, 0u, 0u, 0u);
-          }
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
-          bias = reinterpret_cast<const uint4*>(at);
-        }
-      }
-      if constexpr (OP != OP_DW) {
-        if (side_src)
-          for (int b = 0; b < 2; ++b) stage_load(smem_u32(stage) + 4096u * b, side_src, r0, c0 + 64 * b, p.m, p.n, lane);
-        if (OP == OP_DX && p.zc_in && row < p.m) {
-          const uint8_t* zs = p.zs_in + static_cast<size_t>(row) * groups + (c0 >> 5);
-          if ((groups & 3) == 0) {
-            if (c0 < p.n) bytes = __ldg(reinterpret_cast<const uint32_t*>(zs));
-          } else {
-            for (int g = 0; g < 4; ++g)
-              if (c0 + 32 * g < p.n) bytes |= static_cast<uint32_t>(__ldg(zs + g)) << (8 * g);
-          }
-        }
-      }
-      for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
-        const uint32_t a = i & 1u, u = i >> 1;
-        if (!warp_wait_bounded(smem_u32(&accf_bar[a]), u & 1u, abort, kErrAccF)) {
-          stop = true;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
-        if (OP == OP_DW && p.y32) {
-          if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
-#pragma unroll 1
-          for (int c = 0; c < C::EPI_COLS; c += 32) {
-            uint32_t r[32];
-            tmem_ld_32cols(taddr + c, r);
-            if (c0 + c >= p.n) continue;
-            const f2 s = f2_both(p.scale);
-            uint8_t* buf = stage + ((c >> 5) & 1) * 4096;
-            if (lane == 0) bulk_wait_group_read<1>();
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<ulonglong2*>(buf + staged_at(lane, j)) =
-                  make_ulonglong2(f2_mul(f2_make(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), s),
-                                  f2_mul(f2_make(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), s));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (chunk == 0) tma_store_2d(&p.out, c0 + c, r0, smem_u32(buf));
-              else tma_reduce_add_2d(&p.out, c0 + c, r0, smem_u32(buf));
-              bulk_commit_group();
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < C::EPI_COLS; c += 64) {
-            uint8_t* buf = stage + ((c >> 6) & 1) * 4096;
-            const bool any = c0 + c < p.n;  // warp-uniform
-            if (OP != OP_DW && side_src) {
-              if (c == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
-              else asm volatile("cp.async.wait_group 0;" ::: "memory");
-            }
-            __syncwarp();  // the buffer is loaded, or its last store has read it
-            uint32_t w[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[32];
-              tmem_ld_32cols(taddr + c + 32 * h, r);
-              f2 v[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-              if (any) {
-                uint4 side[4], zw[4];
-                if (OP != OP_DW && side_src) {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) side[j] = *reinterpret_cast<const uint4*>(buf + staged_at(lane, 4 * h + j));
-                }
-                const int g = (c >> 5) + h;
-                uint32_t byte = OP == OP_DX ? (bytes >> (8 * g)) & 0xFFu : 0u;
-                epilogue32<OP>(p, row, c0 + c + 32 * h, bias + 4 * g, side, zw, byte, v);
-                if (OP == OP_FWD) {
-                  bytes |= byte << (8 * g);
-                  if (p.z) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = zw[j];
-                  }
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[16 * h + j] = f2_to_bf16x2(v[j]);
-            }
-            if (!any) continue;
-            if (OP == OP_FWD && p.z) {
-              __syncwarp();
-              stage_store(buf, p.z, r0, c0 + c, p.m, p.n, lane);
-              __syncwarp();
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(buf + staged_at(lane, j)) =
-                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            __syncwarp();
-            stage_store(buf, p.y, r0, c0 + c, p.m, p.n, lane);
-          }
-          __syncwarp();  // before the next tile's loads into the buffers
-          if (OP == OP_FWD && p.zc && row < p.m) {
-            uint8_t* zs = p.zs + static_cast<size_t>(row) * groups + (c0 >> 5);
-            if ((groups & 3) == 0) {
-              if (c0 < p.n) *reinterpret_cast<uint32_t*>(zs) = bytes;
-            } else {
-              for (int g = 0; g < 4; ++g)
-                if (c0 + 32 * g < p.n) zs[g] = static_cast<uint8_t>(bytes >> (8 * g));
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        // relaxed: the arrival only says that the tensor-memory loads are done (ordered by the fence
-        // above); a release at cluster scope would wait for every store the epilogue just made
-        if (lane == 0)
-          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                           mapa_shared(smem_u32(&acce_bar[a]), 0))
-                       : "memory");
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy may still write this CTA's shared memory
-    if (lane == 0) bulk_wait_group_all();             // and no store still read it
+    wide_epilogue<OP>(p, smem, tmem_base, smem_u32(&accf_bar[0]), smem_u32(&acce_bar[0]), abort, warp, lane, rank, pair,
+                      pairs, num_m, num_n);
   }
 
   tc_fence_before();

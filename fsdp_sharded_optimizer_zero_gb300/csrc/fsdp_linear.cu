@@ -371,13 +371,38 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
   }
 }
 
-// narrow kernel: 4 columns of one output row per lane, 32 lanes across 128 columns; the 8 lanes
-// of a group of 32 columns share its scale byte through shuffles. Called by whole warps.
+// narrow kernel: what 4 columns of a row read beside their sums, loaded while the main loop runs.
+// Volatile: the compiler would move the loads down to their use.
 template <int OP>
-__device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int col, f2 (&v)[2]) {
+struct Side4 {
+  uint2 res, z;   // z: bf16, or codes in z.x
+  uint32_t byte;  // the group's scale byte
+  __device__ __forceinline__ void load(const LinearParams& p, int row, int col) {
+    if (OP == OP_DW || row >= p.m || col >= p.n) return;
+    const size_t at = static_cast<size_t>(row) * p.n + col;
+    if (p.res) load8(p.res + at, res);
+    if (OP == OP_DX && p.zc_in) {
+      asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(z.x) : "l"(p.zc_in + at));
+      asm volatile("ld.global.nc.u8 %0, [%1];"
+                   : "=r"(byte)
+                   : "l"(p.zs_in + static_cast<size_t>(row) * ((p.n + 31) / 32) + (col >> 5)));
+    } else if (OP == OP_DX && p.z_in) {
+      load8(p.z_in + at, z);
+    }
+  }
+  static __device__ __forceinline__ void load8(const uint16_t* src, uint2& w) {
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(src));
+  }
+};
+
+// 4 columns of one output row per lane, 32 lanes across 128 columns; the 8 lanes of a group of 32
+// columns share its scale byte through shuffles. bias: the columns' biases (fwd, where there are
+// any). Called by whole warps.
+template <int OP, int ACT>
+__device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int col, uint2 bias, const Side4<OP>& side,
+                                          f2 (&v)[2]) {
   const size_t at = static_cast<size_t>(row) * p.n + col;
   const bool live = row < p.m && col < p.n;
-  const size_t group = static_cast<size_t>(row) * ((p.n + 31) / 32) + (col >> 5);
   if constexpr (OP == OP_DW) {
     v[0] = f2_mul(v[0], f2_both(p.scale)), v[1] = f2_mul(v[1], f2_both(p.scale));
     if (!live) return;
@@ -386,10 +411,7 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
     return;
   }
   if constexpr (OP == OP_FWD) {
-    if (p.bias && live) {
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
-      v[0] = f2_add(v[0], f2_from_bf16x2(b.x)), v[1] = f2_add(v[1], f2_from_bf16x2(b.y));
-    }
+    if (p.bias) v[0] = f2_add(v[0], f2_from_bf16x2(bias.x)), v[1] = f2_add(v[1], f2_from_bf16x2(bias.y));
     if (p.z && live)
       *reinterpret_cast<uint2*>(p.z + at) = make_uint2(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]));
     if (p.zc) {
@@ -402,33 +424,25 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
                                      : ckpt_code4(ckpt_clamped(v[0], byte), ckpt_clamped(v[1], byte), inv);
       if (live) {
         *reinterpret_cast<uint32_t*>(p.zc + at) = w;
-        if ((col & 31) == 0) p.zs[group] = static_cast<uint8_t>(byte);
+        if ((col & 31) == 0)
+          p.zs[static_cast<size_t>(row) * ((p.n + 31) / 32) + (col >> 5)] = static_cast<uint8_t>(byte);
       }
     }
-    with_act(p.act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[j] = act_fwd<decltype(a)::value>(v[j]);
-    });
-  } else if (p.act != FSDP_ACT_NONE && live) {
+    for (int j = 0; j < 2; ++j) v[j] = act_fwd<ACT>(v[j]);
+  } else if (ACT != FSDP_ACT_NONE && live) {
     f2 z[2];
     if (p.zc_in) {
-      const float s = ckpt_scale(__ldg(p.zs_in + group));
-      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.zc_in + at));
-      z[0] = ckpt_values2(c, 0, s), z[1] = ckpt_values2(c, 1, s);
+      const float s = ckpt_scale(side.byte);
+      z[0] = ckpt_values2(side.z.x, 0, s), z[1] = ckpt_values2(side.z.x, 1, s);
     } else {
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.z_in + at));
-      z[0] = f2_from_bf16x2(b.x), z[1] = f2_from_bf16x2(b.y);
+      z[0] = f2_from_bf16x2(side.z.x), z[1] = f2_from_bf16x2(side.z.y);
     }
-    with_act(p.act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) v[j] = f2_mul(v[j], act_grad<decltype(a)::value>(z[j]));
-    });
+    for (int j = 0; j < 2; ++j) v[j] = f2_mul(v[j], act_grad<ACT>(z[j]));
   }
   if (!live) return;
-  if (p.res) {
-    const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.res + at));
-    v[0] = f2_add(v[0], f2_from_bf16x2(b.x)), v[1] = f2_add(v[1], f2_from_bf16x2(b.y));
-  }
+  if (p.res) v[0] = f2_add(v[0], f2_from_bf16x2(side.res.x)), v[1] = f2_add(v[1], f2_from_bf16x2(side.res.y));
   *reinterpret_cast<uint2*>(p.y + at) = make_uint2(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]));
 }
 
@@ -810,9 +824,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
 // narrow kernel
 // ------------------------------------------------------------------------------------
 // One tile per cluster: 128 output columns (the MMA's M side) x TN output rows (its N side, so
-// a few tokens cost a narrow MMA and a small copy). The cluster's CTAs split the K blocks;
-// each leaves its fp32 part in shared memory as [row][128 columns], and CTA c adds the parts of
-// rows c TN / S .. in CTA order and runs the epilogue on them, 4 columns a lane.
+// a few tokens cost a narrow MMA and a small copy). The cluster's CTAs split the K blocks. CTA c
+// finishes rows c TN / S .. of the tile: every CTA stores its fp32 part of them into CTA c's shared
+// memory (as [row][128 columns]; stores to a neighbour need no answer, where loads from it take most
+// of a microsecond), and CTA c adds the parts in CTA order and runs the epilogue, 4 columns a lane.
 //   warp 0      producer: lane i issues the i-th copy of a stage
 //   warp 1      MMA issuer, tensor-memory allocation
 //   all warps   the sum over the parts and the epilogue
@@ -825,45 +840,68 @@ template <int TN> struct Narrow {
   static_assert(STAGES * STAGE >= TN * 128 * 4, "the fp32 part takes the stages' place");
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// The sum of S CTAs' parts (shared-memory address `base` in each) over this CTA's rows, in CTA order,
-// and the epilogue on it: rows warp, warp + 8, .., with eight remote loads of a lane in flight (each
-// takes most of a microsecond).
-template <int OP, int TN, int S>
-__device__ __forceinline__ void add_parts(const LinearParams& p, uint32_t base, int rank, int m0, int n0, int warp,
-                                          int lane) {
-  constexpr int ROWS = TN / S, R = 8 / S;
-  for (int b = warp; b < ROWS; b += 8 * R) {
-    float4 f[R][S];
+// What follows the main loop, for S CTAs to a tile, by all eight warps: the parts to their owners,
+// their sum and the epilogue. `wait` returns once the accumulator is complete.
+template <int OP, int TN, int S, class Wait>
+__device__ __forceinline__ void finish_tile(const LinearParams& p, uint8_t* smem, uint32_t tmem_base, int rank, int m0,
+                                            int n0, int warp, int lane, Wait&& wait) {
+  constexpr int ROWS = TN / S;                         // rows this CTA finishes
+  constexpr int MINE = ROWS < 8 ? 1 : ROWS / 8;        // rows of a warp: warp, warp + 8, ..
+  constexpr int AHEAD = MINE < 8 ? MINE : 8;           // of them, with their side tensors loaded ahead
+  const int col = n0 + lane * 4, row0 = m0 + rank * ROWS;
+  uint2 bias = make_uint2(0u, 0u);
+  if (OP == OP_FWD && p.bias && col < p.n) Side4<OP>::load8(p.bias + col, bias);
+  Side4<OP> side[AHEAD];
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int t = rank * ROWS + b + 8 * j;
+  for (int j = 0; j < AHEAD; ++j)
+    if (warp + 8 * j < ROWS) side[j].load(p, row0 + warp + 8 * j, col);
+
+  wait();
+  __syncthreads();
+  tc_fence_after();
+  if (S > 1) cluster_arrive();  // this CTA's stages are free for the others' parts
+  // tensor memory lane l = output column n0 + l, column t = output row m0 + t
+  const int q = warp & 3, half = warp >> 2;
+  const uint32_t base = smem_u32(smem), taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+  if (S > 1) cluster_wait();
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        f[j][s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (b + 8 * j < ROWS && m0 + t < p.m)
-          f[j][s] = ld_cluster_f4(mapa_shared(base, s) + static_cast<uint32_t>(t * 128 + lane * 4) * 4u);
-      }
-    }
+  for (int t0 = half * 32; t0 < TN; t0 += 64) {
+    uint32_t r[32];
+    tmem_ld_32cols(taddr + t0, r);
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int t = rank * ROWS + b + 8 * j;
-      if (b + 8 * j < ROWS && m0 + t < p.m) {  // the same for the whole warp
-        f2 v[2] = {f2_make(f[j][0].x, f[j][0].y), f2_make(f[j][0].z, f[j][0].w)};
-#pragma unroll
-        for (int s = 1; s < S; ++s)
-          v[0] = f2_add(v[0], f2_make(f[j][s].x, f[j][s].y)), v[1] = f2_add(v[1], f2_make(f[j][s].z, f[j][s].w));
-        epilogue4<OP>(p, m0 + t, n0 + lane * 4, v);
-      }
+    for (int j = 0; j < 32; ++j) {
+      const int t = t0 + j;
+      const uint32_t at = static_cast<uint32_t>(((rank * ROWS + t % ROWS) * 128 + q * 32 + lane) * 4);
+      if (S > 1)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(base, t / ROWS) + at), "r"(r[j]) : "memory");
+      else
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + at), "r"(r[j]) : "memory");
     }
   }
+  tc_fence_before();
+  if (S > 1) cluster_sync_all();  // every part is in its owner's shared memory
+  else __syncthreads();
+  const float4* part = reinterpret_cast<const float4*>(smem);
+  with_act(OP == OP_DW ? FSDP_ACT_NONE : p.act, [&](auto act) {
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      const int t = warp + 8 * j;
+      if (t < ROWS && row0 + t < p.m) {  // the same for the whole warp
+        if (j >= AHEAD) side[j % AHEAD].load(p, row0 + t, col);
+        f2 v[2];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const float4 f = part[(s * ROWS + t) * 32 + lane];
+          const f2 lo = f2_make(f.x, f.y), hi = f2_make(f.z, f.w);
+          v[0] = s == 0 ? lo : f2_add(v[0], lo), v[1] = s == 0 ? hi : f2_add(v[1], hi);
+        }
+        epilogue4<OP, decltype(act)::value>(p, row0 + t, col, bias, side[j % AHEAD], v);
+      }
+    }
+  });
 }
 
 template <int OP, int TN>
@@ -933,7 +971,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
     if (*abort && lane == 0) {  // copies in flight still write this CTA's shared memory
       int never = 0;
       for (int j = max(0, issued - C::STAGES); j < issued; ++j)
-wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never, kErrDrain);
+        wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never, kErrDrain);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -958,32 +996,16 @@ wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::ST
   }
 
   // the accumulator is complete (or, after an abort, no MMA runs any more)
-  int never = 0;
-  wait_bounded(smem_u32(&acc_bar), 0, &never, kErrAccF);
-  __syncthreads();
-  tc_fence_after();
-  // tensor memory lane l = output column n0 + l, column t = output row m0 + t
-  float* part = reinterpret_cast<float*>(smem);
-  {
-    const int q = warp & 3, half = warp >> 2;
-    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    for (int t0 = half * 32; t0 < TN; t0 += 64) {
-      uint32_t r[32];
-      tmem_ld_32cols(taddr + t0, r);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) part[(t0 + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
-    }
-  }
-  tc_fence_before();
-  cluster_sync_all();  // every CTA's part is in its shared memory
-  const uint32_t base = smem_u32(smem);
+  const auto wait = [&] {
+    int never = 0;
+    wait_bounded(smem_u32(&acc_bar), 0, &never, kErrAccF);
+  };
   switch (splits) {
-    case 1: add_parts<OP, TN, 1>(p, base, rank, m0, n0, warp, lane); break;
-    case 2: add_parts<OP, TN, 2>(p, base, rank, m0, n0, warp, lane); break;
-    case 4: add_parts<OP, TN, 4>(p, base, rank, m0, n0, warp, lane); break;
-    default: add_parts<OP, TN, 8>(p, base, rank, m0, n0, warp, lane); break;
+    case 1: finish_tile<OP, TN, 1>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
+    case 2: finish_tile<OP, TN, 2>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
+    case 4: finish_tile<OP, TN, 4>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
+    default: finish_tile<OP, TN, 8>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
   }
-  cluster_sync_all();  // no CTA leaves while its part is read
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);

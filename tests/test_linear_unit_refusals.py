@@ -93,10 +93,17 @@ def test_dw_refuses(z, kw, word):
     (dict(m=0), ">= 1"), (dict(k=0), ">= 1"), (dict(k=20), "multiple of 8"), (dict(dy=None), "dY"),
     (dict(dz=None), "both NULL"), (dict(act=5), "act 5"), (dict(zz=None), "kept activation"),
     (dict(zz=None, zs=P), "kept activation"), (dict(dz=P + 8), "16-byte"), (dict(db=P + 4), "16-byte"),
-    (dict(m=1 << 41), "2^40"), (dict(ws=P + 8, wsb=1 << 30), "16-byte"),
-    (dict(m=1 << 20, db=P, ws=P, wsb=64), "workspace of 64")])
+    (dict(m=1 << 41), "2^40"), (dict(ws=P + 8, wsb=1 << 30), "16-byte")])
 def test_act_backward_refuses(z, kw, word):
     refused(z, actb(z, **kw), word)
+
+
+def test_act_backward_refuses_a_small_workspace(z):
+    m, k = 1 << 20, 4096
+    need = C.c_uint64()
+    assert z.library().fsdp_act_backward_workspace(m, k, C.byref(need)) == 0
+    assert need.value > 64  # else the call would be accepted, and launched
+    refused(z, actb(z, m=m, k=k, db=P, ws=P, wsb=64), "workspace of 64")
 
 
 @pytest.mark.parametrize("args,word", [

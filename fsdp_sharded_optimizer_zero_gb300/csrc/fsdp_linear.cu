@@ -834,7 +834,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
 template <int TN> struct Narrow {
   static constexpr uint32_t QB = TN * BK * 2;               // the row-side operand of a stage
   static constexpr uint32_t STAGE = kHalf + QB;
-  static constexpr int STAGES = TN == 128 ? 3 : 5;  // two CTAs per SM
+  static constexpr int STAGES = TN == 128 ? 3 : TN == 64 ? 4 : 5;  // two CTAs per SM
   static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
   static constexpr uint32_t TMEM_COLS = TN;
   static_assert(STAGES * STAGE >= TN * 128 * 4, "the fp32 part takes the stages' place");
@@ -944,6 +944,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   wait_for_prior_grids();
   const uint32_t tmem_base = tmem_base_sh;
 
+  int issued = 0;  // K blocks, warp 0
   if (warp == 0) {
     Copy c;
     int i = lane;
@@ -954,7 +955,6 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
     else i -= k_copies(&p.a, i, m0, kb0, kHalf, c);
     const bool mine = i < 0;
     uint32_t s = 0, ph = 0;
-    int issued = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
       bool ok = true;
       if (issued >= C::STAGES)
@@ -967,11 +967,6 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       }
       __syncwarp();
       if (++s == C::STAGES) s = 0, ph ^= 1u;
-    }
-    if (*abort && lane == 0) {  // copies in flight still write this CTA's shared memory
-      int never = 0;
-      for (int j = max(0, issued - C::STAGES); j < issued; ++j)
-        wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never, kErrDrain);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -999,12 +994,16 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   const auto wait = [&] {
     int never = 0;
     wait_bounded(smem_u32(&acc_bar), 0, &never, kErrAccF);
+    if (*abort && warp == 0)  // copies in flight still write this CTA's shared memory
+      for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+        wait_bounded(smem_u32(&full_bar[j % C::STAGES]), static_cast<uint32_t>(j / C::STAGES) & 1u, &never, kErrDrain);
   };
   switch (splits) {
     case 1: finish_tile<OP, TN, 1>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
     case 2: finish_tile<OP, TN, 2>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
     case 4: finish_tile<OP, TN, 4>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
-    default: finish_tile<OP, TN, 8>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait); break;
+    default:  // 128-row tiles are split in 8 only for long fp32 weight gradients
+      if constexpr (TN != 128 || OP == OP_DW) finish_tile<OP, TN, 8>(p, smem, tmem_base, rank, m0, n0, warp, lane, wait);
   }
   if (warp == 1) {
     tc_fence_after();
@@ -1112,13 +1111,20 @@ int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char
 // and take one part.
 constexpr int kMaxChunkBlocks = 64;
 
-// Kernel choice, from both kernels timed over 20 shapes (forward, dx, dw; splits 1 to 8). The narrow
-// kernel while its 128 x 128 tiles, split in two, are resident at once (two CTAs per SM: up to 38
-// wide tiles; 36 of them, 1000 x 2304 from 768: 11.6 us against 14.8) and for up to 128 rows, which
-// leave half of a 256-row tile or more empty; else the wide one (48 tiles, 4096 x 768 from 2304: 20.3
-// against 25.9). The narrow kernel's splits double while every CTA keeps two blocks and one CTA per
-// SM is not passed, and on to two per SM up to 4 splits, or with 8 blocks left to each (32 tiles of
-// 64 blocks: 8 splits 10.3 us, 4 splits 12.1; 36 tiles of 32 blocks: 12.0 and 9.3).
+// Kernel choice, from both kernels timed over 35 shapes (forward, dx, dw; every tile height and
+// split), repeated calls in a graph. The narrow kernel while its 128 x 128 tiles, split in two, are
+// resident at once (two CTAs per SM: up to 38 wide tiles; 36 of them, 1024 x 2304 from 768: 9.9 us
+// against 11.6) and for up to 128 rows, which leave half of a 256-row tile or more empty; else the
+// wide one (48 tiles, 4096 x 768 from 768: 11.9 against 14.4).
+//   splits: doubled while every CTA keeps two K blocks and the CTAs are resident at once, beyond
+// one CTA per SM only if three blocks are left to each (72 tiles of 8 blocks: 2 splits 5.3 us, 4
+// splits 6.2; of 32 blocks: 9.3 and 8.1).
+//   rows of a tile: 32 for up to 32 rows (16 x 768 from 768: 4.8 us). A tile of 64 rows passes on half
+// of what one of 128 does and needs fewer splits for as many CTAs, but loads the column side for 64
+// rows only. So 64 if that leaves 4 splits or more (dW 768 x 768 from 4096: 10.9 us, 128 rows with 8
+// splits 14.2, with 4 12.3), or if it loads at most 240 KB per SM more (1024 x 2304 from 768, 182
+// KB: 9.9 us against 11.5; dW 2304 x 768 from 1500, 273 KB: 11.4 against 11.0; from 2048, 364 KB: 14.2
+// against 12.5).
 struct Choice {
   bool wide;
   int tn, splits;
@@ -1130,13 +1136,24 @@ Choice choose(int op, int64_t m, int64_t n, int64_t k, bool fp32) {
   Choice c{true, 128, 1};
   if ((wide_tiles * 4 > sms && !few_rows) || (fp32 && blocks > 8 * kMaxChunkBlocks) || col_tiles > 65535) return c;
   c.wide = false;
-  if (op != OP_DW && m <= 32) c.tn = 32;
-  const int64_t tiles = ((m + c.tn - 1) / c.tn) * col_tiles;
-  while (c.splits < 8 && blocks >= 4 * c.splits) {
-    const int64_t next = 2 * c.splits, ctas = tiles * next;
-    if (ctas > sms && (ctas > 2 * sms || (next > 4 && blocks < 8 * next))) break;
-    c.splits = static_cast<int>(next);
-  }
+  const int64_t tiles64 = ((m + 63) / 64) * col_tiles, tiles128 = ((m + 127) / 128) * col_tiles;
+  const auto splits_of = [&](int64_t tiles) {
+    int splits = 1;
+    while (splits < 8 && blocks >= 4 * splits) {
+      const int64_t next = 2 * splits, ctas = tiles * next;
+      if (ctas > sms && (ctas > 2 * sms || blocks < 3 * next)) break;
+      splits = static_cast<int>(next);
+    }
+    return splits;
+  };
+  const int64_t kb = BK * 2 * (128 + 64) / 1024, kb128 = BK * 2 * (128 + 128) / 1024;  // KB of a stage
+  if (op != OP_DW && m <= 32)
+    c.tn = 32, c.splits = splits_of(col_tiles);
+  else if (tiles64 <= 2 * sms &&
+           (splits_of(tiles64) >= 4 || blocks * (tiles64 * kb - tiles128 * kb128) <= 240 * sms))
+    c.tn = 64, c.splits = splits_of(tiles64);
+  else
+    c.splits = splits_of(tiles128);
   while (fp32 && c.splits < 8 && blocks > static_cast<int64_t>(c.splits) * kMaxChunkBlocks) c.splits *= 2;
   return c;
 }
@@ -1189,6 +1206,7 @@ int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who)
   }
   if constexpr (OP != OP_DW)
     if (c.tn == 32) return launch_narrow<OP, 32>(p, c.splits, st, who);
+  if (c.tn == 64) return launch_narrow<OP, 64>(p, c.splits, st, who);
   return launch_narrow<OP, 128>(p, c.splits, st, who);
 }
 

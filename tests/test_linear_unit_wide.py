@@ -106,10 +106,7 @@ def forward_case(i):
     return act, ("z", "z8", "none")[i % 3], i % 2 == 0, i % 4 in (0, 3)
 
 
-@pytest.mark.parametrize("i", range(24))
-def test_forward(z, i):
-    m, r, k, n = SHAPES[i % len(SHAPES)]
-    act, kind, has_bias, has_res = forward_case(i // len(SHAPES) + i)
+def check_forward(z, m, r, k, n, act, kind, has_bias, has_res):
     x, w = randn(m, k, 1.0, 1), randn(r, k, 0.04, 2)
     bias = randn(1, r, 0.5, 3)[0].contiguous() if has_bias else None
     res = randn(m, r, 2.0, 4) if has_res else None
@@ -144,10 +141,13 @@ def test_forward(z, i):
     assert torch.equal(again, y)
 
 
-@pytest.mark.parametrize("i", range(16))
-def test_dx(z, i):
+@pytest.mark.parametrize("i", range(24))
+def test_forward(z, i):
     m, r, k, n = SHAPES[i % len(SHAPES)]
-    act, _, has_res, bits8 = forward_case(i // len(SHAPES) + i)
+    check_forward(z, m, r, k, n, *forward_case(i // len(SHAPES) + i))
+
+
+def check_dx(z, m, r, k, n, act, has_res, bits8):
     g, w, pre = randn(m, r, 0.3, 5), randn(r, k, 0.04, 6), randn(m, k, 1.5, 7)
     res = randn(m, k, 0.5, 8) if has_res else None
     c = new8(m, k)
@@ -168,10 +168,14 @@ def test_dx(z, i):
     assert kept(buf, 3.0)
 
 
-@pytest.mark.parametrize("wide", [True, False])
-@pytest.mark.parametrize("m,r,k", [(300, 2312, 1096), (1, 2304, 1544), (4097, 1544, 2312), (9001, 2560, 1160),
-                                   (5000, 2048, 2048), (65, 2048, 2112)])
-def test_dw(z, m, r, k, wide):
+@pytest.mark.parametrize("i", range(16))
+def test_dx(z, i):
+    m, r, k, n = SHAPES[i % len(SHAPES)]
+    act, _, has_res, bits8 = forward_case(i // len(SHAPES) + i)
+    check_dx(z, m, r, k, n, act, has_res, bits8)
+
+
+def check_dw(z, m, r, k, wide):
     """fp32 results over more than 4096 tokens are summed in parts: their error stays below the
     4096-term bound (4097 2^-23 of the magnitudes) plus a rounding per part."""
     g, x = randn(m, r, 0.3, 9), randn(m, k, 1.0, 10)
@@ -186,6 +190,13 @@ def test_dw(z, m, r, k, wide):
         e = (terms + 1 + m // 4096) * SUM * mag + SUM * want.abs()
         inside(dw, want, e if wide else e + B16 * (want.abs() + e), "dW")
         assert kept(buf, 3.0)
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("m,r,k", [(300, 2312, 1096), (1, 2304, 1544), (4097, 1544, 2312), (9001, 2560, 1160),
+                                   (5000, 2048, 2048), (65, 2048, 2112)])
+def test_dw(z, m, r, k, wide):
+    check_dw(z, m, r, k, wide)
 
 
 def test_dw_workspace_and_streams(z):

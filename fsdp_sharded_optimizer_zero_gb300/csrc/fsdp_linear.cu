@@ -277,6 +277,17 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
   const size_t at = static_cast<size_t>(row) * p.n + col0;
   const bool live = row < p.m;
   bool side_is_res = p.res != nullptr;
+  // dx: a residual beside a bf16 kept activation, which has the staging buffers: on its way while the
+  // activation's derivative is computed
+  const bool own_res = OP == OP_DX && p.res && p.z_in;
+  uint4 res[4];
+  if (own_res) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      res[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && col0 + 8 * q < p.n) res[q] = ldg16(p.res + at + 8 * q);
+    }
+  }
   if constexpr (OP == OP_FWD) {
     if (p.bias) {
 #pragma unroll
@@ -350,23 +361,14 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
     for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], s);
   }
   if constexpr (OP != OP_DW) {
-    if (side_is_res) {
+    if (side_is_res || own_res) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f2 r[4];
-        unpack8(side[q], r);
+        unpack8(own_res ? res[q] : side[q], r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
       }
-    } else if (OP == OP_DX && p.res && live) {  // beside a bf16 kept activation, which has the staging buffers
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (col0 + 8 * q < p.n) {
-          f2 r[4];
-          unpack8(ldg16(p.res + at + 8 * q), r);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
-        }
     }
   }
 }
@@ -571,7 +573,7 @@ __device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* sm
           }
         }
       } else {
-          // 32 columns at a time, rolled: unrolled by two the code is twice as long for the instruction
+        // 32 columns at a time, rolled: unrolled by two the code is twice as long for the instruction
         // cache that the producer and MMA loops share (8192 x 2304 from 768: 32.2 us, rolled 30.0). The
         // activation is a switch in it for the same reason: the role once per activation cost 4096 x
         // 2304 from 4096 6 %.

@@ -5,10 +5,8 @@
 //   unpack   act(code * 2^(byte - 127)) -> bf16
 //   act_backward   dZ = bf16(dY act'(Z)), db = column sums of dY act'(Z) in fp32
 //
-// Widths that are multiples of 32 have no partial group, so a checkpoint is flat: pack and
-// unpack walk it 8 elements a lane (four lanes to a group) without knowing rows. Other
-// widths go row by row, a warp to four rows; the
-// last group of a row may then have fewer than four lanes with data, the others hold zeros.
+// A thread has 8 columns, four threads a group; where the last group of a row is cut short, its
+// threads past the row hold zeros.
 #include <algorithm>
 
 #include "linear_math.cuh"
@@ -46,184 +44,148 @@ __device__ __forceinline__ float amax8(const f2 (&v)[4]) {
   return m;
 }
 
-constexpr int kFlatBlocks = 32;  // blocks per SM of the flat kernels
-constexpr int kFlat = 3;  // units a thread has in flight in the flat kernels
+// ------------------------------------------------------------------------------------
+// one sweep over memory: pack, unpack, activation backward without column sums
+// ------------------------------------------------------------------------------------
+constexpr int kWalkBlocks = 32;  // blocks per SM
+constexpr int kWalk = 3;         // units a thread has in flight
 
-// flat: units of 8 elements, four lanes to a group; every access of a warp is contiguous
-__global__ void __launch_bounds__(kThreads) ckpt8_pack_flat_kernel(const uint16_t* __restrict__ x, int64_t units,
-                                                                   int8_t* __restrict__ codes,
-                                                                   uint8_t* __restrict__ scales) {
+// A matrix as units of 8 columns, four to a group of the checkpoint, walked by all threads together:
+// a warp's accesses are contiguous. FLAT: widths of whole groups, rows need not be known (also where
+// there is no checkpoint). Otherwise a row has units up to the end of its last group, those past its
+// columns without data, and a thread steps by whole rows and units instead of dividing.
+struct WalkDims {
+  int64_t rows, cols, units;        // units: of a row, or (flat) of the matrix
+  int64_t step_rows, step_units;    // a step of all threads
+};
+template <bool FLAT>
+struct Walk {
+  int64_t row, unit;
+  __device__ __forceinline__ explicit Walk(const WalkDims& d) {
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;  // below 2^31
+    row = 0, unit = i;
+    if (!FLAT && d.units <= unit) {
+      row = i / static_cast<uint32_t>(d.units);
+      unit = i - static_cast<uint32_t>(row) * static_cast<uint32_t>(d.units);
+    }
+  }
+  // the four units of a group are there together, though some may have no data
+  __device__ __forceinline__ bool there(const WalkDims& d) const { return FLAT ? unit < d.units : row < d.rows; }
+  __device__ __forceinline__ bool data(const WalkDims& d) const { return there(d) && (FLAT || 8 * unit < d.cols); }
+  __device__ __forceinline__ int64_t at(const WalkDims& d) const { return FLAT ? 8 * unit : row * d.cols + 8 * unit; }
+  __device__ __forceinline__ int64_t group(const WalkDims& d) const {
+    return FLAT ? unit >> 2 : row * (d.units >> 2) + (unit >> 2);
+  }
+  __device__ __forceinline__ void step(const WalkDims& d) {
+    unit += d.step_units;
+    if constexpr (!FLAT) {
+      row += d.step_rows;
+      if (unit >= d.units) unit -= d.units, ++row;
+    }
+  }
+};
+
+template <bool FLAT>
+__global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __restrict__ x, const WalkDims d,
+                                                              int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   allow_next_grid();
+  Walk<FLAT> w(d);
   wait_for_prior_grids();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += kFlat * stride) {
-    uint4 w[kFlat];
+  while (w.there(d)) {
+    uint4 in[kWalk];
+    Walk<FLAT> a = w;
 #pragma unroll
-    for (int k = 0; k < kFlat; ++k) {
-      const int64_t i = i0 + k * stride;
-      w[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < units) w[k] = __ldcs(reinterpret_cast<const uint4*>(x) + i);
+    for (int k = 0; k < kWalk; ++k, a.step(d)) {
+      in[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.data(d)) in[k] = __ldcs(reinterpret_cast<const uint4*>(x + a.at(d)));
     }
 #pragma unroll
-    for (int k = 0; k < kFlat; ++k) {
-      const int64_t i = i0 + k * stride;
+    for (int k = 0; k < kWalk; ++k, w.step(d)) {
       f2 v[4];
-      widen8(w[k], v);
+      widen8(in[k], v);
       float amax = amax8(v);
-      // units and stride are multiples of 4: a group's lanes are in the loop together
+      // units and steps are multiples of 4: a group's lanes are in the loop together
       const uint32_t four = 0xFu << (threadIdx.x & 28u);
       amax = max_nan(amax, __shfl_xor_sync(four, amax, 1));
       amax = max_nan(amax, __shfl_xor_sync(four, amax, 2));
       const uint32_t byte = ckpt_byte(amax);
       const uint2 c = encode8(v, byte);
-      if (i < units) {
-        reinterpret_cast<uint2*>(codes)[i] = c;
-        if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(byte);
+      if (w.data(d)) {
+        *reinterpret_cast<uint2*>(codes + w.at(d)) = c;
+        if ((w.unit & 3) == 0) scales[w.group(d)] = static_cast<uint8_t>(byte);
       }
     }
   }
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(kThreads) ckpt8_unpack_flat_kernel(const int8_t* __restrict__ codes,
-                                                                     const uint8_t* __restrict__ scales,
-                                                                     int64_t units, uint16_t* __restrict__ out) {
+template <int ACT, bool FLAT>
+__global__ void __launch_bounds__(kThreads) ckpt8_unpack_kernel(const int8_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ scales, const WalkDims d,
+                                                                uint16_t* __restrict__ out) {
   allow_next_grid();
+  Walk<FLAT> w(d);
   wait_for_prior_grids();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += kFlat * stride) {
-    uint2 w[kFlat];
-    uint32_t byte[kFlat];
+  while (w.there(d)) {
+    uint2 in[kWalk];
+    uint32_t byte[kWalk];
+    Walk<FLAT> a = w;
 #pragma unroll
-    for (int k = 0; k < kFlat; ++k) {
-      const int64_t i = i0 + k * stride;
-      if (i < units) {
-        w[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i);
-        byte[k] = scales[i >> 2];
+    for (int k = 0; k < kWalk; ++k, a.step(d)) {
+      if (a.data(d)) {
+        in[k] = __ldcs(reinterpret_cast<const uint2*>(codes + a.at(d)));
+        byte[k] = scales[a.group(d)];
       }
     }
 #pragma unroll
-    for (int k = 0; k < kFlat; ++k) {
-      const int64_t i = i0 + k * stride;
-      if (i < units) {
+    for (int k = 0; k < kWalk; ++k, w.step(d)) {
+      if (w.data(d)) {
         f2 v[4];
-        decode8(w[k], byte[k], v);
+        decode8(in[k], byte[k], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = act_fwd<ACT>(v[j]);
-        __stcs(reinterpret_cast<uint4*>(out) + i, narrow8(v));
+        __stcs(reinterpret_cast<uint4*>(out + w.at(d)), narrow8(v));
       }
     }
   }
 }
 
-// row by row: warp w takes rows 4 w .. 4 w + 3, lane l the columns 8 (l + 32 c)
-constexpr int kRows = 4;
-__global__ void __launch_bounds__(kThreads) ckpt8_pack_rows_kernel(const uint16_t* __restrict__ x, int64_t rows,
-                                                                   int64_t cols, int8_t* __restrict__ codes,
-                                                                   uint8_t* __restrict__ scales) {
-  allow_next_grid();
-  wait_for_prior_grids();
-  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t r0 = kRows * (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)); r0 < rows;
-       r0 += kRows * warps)
-    for (int64_t u0 = 0; u0 < 4 * groups; u0 += 32) {
-      const int64_t col = (u0 + lane) * 8;
-      uint4 w[kRows];
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        w[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (r0 + k < rows && col < cols) w[k] = __ldcs(reinterpret_cast<const uint4*>(x + (r0 + k) * cols + col));
-      }
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        f2 v[4];
-        widen8(w[k], v);
-        float amax = amax8(v);
-        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const uint32_t byte = ckpt_byte(amax);
-        const uint2 c = encode8(v, byte);
-        if (r0 + k < rows && col < cols) {
-          *reinterpret_cast<uint2*>(codes + (r0 + k) * cols + col) = c;
-          if ((lane & 3) == 0) scales[(r0 + k) * groups + (col >> 5)] = static_cast<uint8_t>(byte);
-        }
-      }
-    }
-}
-
-template <int ACT>
-__global__ void __launch_bounds__(kThreads) ckpt8_unpack_rows_kernel(const int8_t* __restrict__ codes,
-                                                                     const uint8_t* __restrict__ scales, int64_t rows,
-                                                                     int64_t cols, uint16_t* __restrict__ out) {
-  allow_next_grid();
-  wait_for_prior_grids();
-  const int64_t groups = (cols + kCkptGroup - 1) / kCkptGroup;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t r0 = kRows * (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)); r0 < rows;
-       r0 += kRows * warps)
-    for (int64_t col = lane * 8; col < cols; col += 256) {
-      uint2 w[kRows];
-      uint32_t byte[kRows];
-#pragma unroll
-      for (int k = 0; k < kRows; ++k)
-        if (r0 + k < rows) {
-          w[k] = __ldcs(reinterpret_cast<const uint2*>(codes + (r0 + k) * cols + col));
-          byte[k] = scales[(r0 + k) * groups + (col >> 5)];
-        }
-#pragma unroll
-      for (int k = 0; k < kRows; ++k)
-        if (r0 + k < rows) {
-          f2 v[4];
-          decode8(w[k], byte[k], v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = act_fwd<ACT>(v[j]);
-          __stcs(reinterpret_cast<uint4*>(out + (r0 + k) * cols + col), narrow8(v));
-        }
-    }
-}
-
-// Activation backward without column sums: flat, as pack and unpack (8 bits: widths that are
-// multiples of 32). One sweep over memory: 8192 x 14336 from 8 bits 91 us, 106 us in the strips below.
-template <int ACT, bool Z8>
-__global__ void __launch_bounds__(kThreads) act_backward_flat_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
+// Activation backward without column sums. 8192 x 14336 from 8 bits 91 us, 106 us in the strips below.
+template <int ACT, bool Z8, bool FLAT>
+__global__ void __launch_bounds__(kThreads) act_backward_walk_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
                                                                      const int8_t* __restrict__ codes,
-                                                                     const uint8_t* __restrict__ scales, int64_t units,
-                                                                     uint16_t* dz) {
+                                                                     const uint8_t* __restrict__ scales,
+                                                                     const WalkDims d, uint16_t* dz) {
   constexpr int UN = 2;
   allow_next_grid();
+  Walk<FLAT> w(d);
   wait_for_prior_grids();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i0 < units; i0 += UN * stride) {
+  while (w.there(d)) {
     uint4 gw[UN], zw[UN];
     uint2 cw[UN];
     uint32_t byte[UN];
+    Walk<FLAT> a = w;
 #pragma unroll
-    for (int k = 0; k < UN; ++k) {
-      const int64_t i = i0 + k * stride;
-      if (i < units) {
-        gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy) + i);
+    for (int k = 0; k < UN; ++k, a.step(d)) {
+      if (a.data(d)) {
+        gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy + a.at(d)));
         if constexpr (Z8) {
-          cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i);
-          byte[k] = scales[i >> 2];
+          cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes + a.at(d)));
+          byte[k] = scales[a.group(d)];
         } else {
-          zw[k] = __ldcs(reinterpret_cast<const uint4*>(z) + i);
+          zw[k] = __ldcs(reinterpret_cast<const uint4*>(z + a.at(d)));
         }
       }
     }
 #pragma unroll
-    for (int k = 0; k < UN; ++k) {
-      const int64_t i = i0 + k * stride;
-      if (i < units) {
+    for (int k = 0; k < UN; ++k, w.step(d)) {
+      if (w.data(d)) {
         f2 g[4], v[4];
         widen8(gw[k], g);
         if constexpr (Z8) decode8(cw[k], byte[k], v);
         else widen8(zw[k], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
-        __stcs(reinterpret_cast<uint4*>(dz) + i, narrow8(g));
+        __stcs(reinterpret_cast<uint4*>(dz + w.at(d)), narrow8(g));
       }
     }
   }
@@ -418,6 +380,20 @@ unsigned int grid_for(int64_t threads, int blocks_per_sm) {
   return static_cast<unsigned int>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms()) * blocks_per_sm));
 }
 
+// a walk over a [rows, cols] matrix, with its checkpoint's groups or without
+struct Walking {
+  bool flat;
+  unsigned int blocks;
+  WalkDims d;
+  Walking(int64_t rows, int64_t cols, bool groups) {
+    flat = !groups || cols % kCkptGroup == 0;
+    const int64_t row_units = flat ? cols / 8 : (cols + kCkptGroup - 1) / kCkptGroup * 4;
+    blocks = grid_for(rows * row_units, kWalkBlocks);
+    const int64_t step = static_cast<int64_t>(blocks) * kThreads;
+    d = {rows, cols, flat ? rows * row_units : row_units, flat ? 0 : step / row_units, flat ? step : step % row_units};
+  }
+};
+
 template <int ACT, bool Z8, int LANES>
 cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales,
                           int64_t rows, int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
@@ -484,11 +460,12 @@ cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, const int
     if (lanes) return launch_sweep<ACT, false>(dy, z, codes, scales, rows, cols, lanes, dz, db, partial, st);
   }
   if constexpr (ACT != FSDP_ACT_NONE) {
-    if (!db && (!codes || cols % kCkptGroup == 0)) {
-      const int64_t units = rows * (cols / 8);
-      return launch_overlapped(codes ? act_backward_flat_kernel<ACT, true> : act_backward_flat_kernel<ACT, false>,
-                               dim3(grid_for(units, kFlatBlocks)), dim3(kThreads), 0, 1, st, dy, z, codes, scales, units,
-                               dz);
+    if (!db) {
+      const Walking w(rows, cols, codes != nullptr);
+      const auto kernel = !codes ? act_backward_walk_kernel<ACT, false, true>
+                          : w.flat ? act_backward_walk_kernel<ACT, true, true>
+                                   : act_backward_walk_kernel<ACT, true, false>;
+      return launch_overlapped(kernel, dim3(w.blocks), dim3(kThreads), 0, 1, st, dy, z, codes, scales, w.d, dz);
     }
   }
   if constexpr (ACT != FSDP_ACT_NONE)
@@ -497,25 +474,17 @@ cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, const int
 }
 
 cudaError_t launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, uint8_t* scales, cudaStream_t st) {
-  if (cols % kCkptGroup == 0) {
-    const int64_t units = rows * (cols / 8);
-    return launch_overlapped(ckpt8_pack_flat_kernel, dim3(grid_for(units, kFlatBlocks)), dim3(kThreads), 0, 1, st, x,
-                             units, codes, scales);
-  }
-  return launch_overlapped(ckpt8_pack_rows_kernel, dim3(grid_for((rows + kRows - 1) / kRows * 32, 8)), dim3(kThreads), 0,
-                           1, st, x, rows, cols, codes, scales);
+  const Walking w(rows, cols, true);
+  return launch_overlapped(w.flat ? ckpt8_pack_kernel<true> : ckpt8_pack_kernel<false>, dim3(w.blocks), dim3(kThreads),
+                           0, 1, st, x, w.d, codes, scales);
 }
 
 template <int ACT>
 cudaError_t launch_unpack(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, uint16_t* out,
                           cudaStream_t st) {
-  if (cols % kCkptGroup == 0) {
-    const int64_t units = rows * (cols / 8);
-    return launch_overlapped(ckpt8_unpack_flat_kernel<ACT>, dim3(grid_for(units, kFlatBlocks)), dim3(kThreads), 0, 1, st,
-                             codes, scales, units, out);
-  }
-  return launch_overlapped(ckpt8_unpack_rows_kernel<ACT>, dim3(grid_for((rows + kRows - 1) / kRows * 32, 8)),
-                           dim3(kThreads), 0, 1, st, codes, scales, rows, cols, out);
+  const Walking w(rows, cols, true);
+  return launch_overlapped(w.flat ? ckpt8_unpack_kernel<ACT, true> : ckpt8_unpack_kernel<ACT, false>, dim3(w.blocks),
+                           dim3(kThreads), 0, 1, st, codes, scales, w.d, out);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

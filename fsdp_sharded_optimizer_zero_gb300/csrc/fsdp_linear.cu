@@ -10,10 +10,10 @@
 // MN-major tiles. Two kernels:
 //   linear_wide_kernel    256 x 256 output tiles on CTA pairs (tcgen05.mma.cta_group::2),
 //                         persistent, the epilogue of one tile beside the main loop of the next;
-//   linear_narrow_kernel  128 output columns x TN output rows per CTA, the contraction split
-//                         over the CTAs of a cluster, which add their parts through
-//                         distributed shared memory in a fixed order. For outputs of too few
-//                         256 x 256 tiles to fill the GPU.
+//   linear_narrow_kernel  128 output columns x TN output rows per tile, the contraction split
+//                         over the CTAs of a cluster, whose parts meet in distributed shared
+//                         memory and are added in a fixed order. For outputs of too few 256 x
+//                         256 tiles to fill the GPU.
 // All sums are fp32 in tensor memory; every output is rounded once. Every mbarrier wait is
 // bounded: after one gives up the CTA's roles leave their loops, copies and MMAs in flight
 // are waited for, and zero_device_status reports it.
@@ -457,6 +457,15 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
 //   warp 0       producer: lane i issues the i-th copy of a stage (TMA), both CTAs
 //   warp 1       MMA issuer (even CTA), tensor-memory allocation
 //   then 8 (dw: 4) epilogue warps, two (one) per tensor-memory lane quarter, sharing its columns
+// What bounds it: at 8192 tokens, 14336 x 4096, tensor work at the power limit (forward with bias,
+// SiLU and 8-bit Z 512-610 us by the board's temperature, 1.58-1.88 PFLOP/s; alone and cool 505 us,
+// tensor pipe 86 % active; dx with the derivative from 8 bits 507; dW 490 us, 93 %). The pair tile
+// is the least that an SM's reads from L2 can feed: 32 KB per 64 contraction elements, about 51
+// bytes a clock at the measured tensor rate, near the most an SM reads. At 768 contraction elements
+// a tile's products take 4 us and its epilogue up to 6 (GELU with 8-bit Z; the eight warps issue in
+// 36 % of the cycles, stalled mostly on fixed latencies), so the epilogue bounds it: 8192 x 2304
+// from 768 24.0 us bare, 30.1 with both. Sixteen epilogue warps have 112 registers and spill: 36.1.
+// Loading the next 32 sums ahead of their use needs 64 registers more than there are: 38.5.
 // FAST: every operand of a stage is one copy (W's shards of whole 128-row, dx: 64-row blocks, MN-
 // major widths of whole 64-column chunks), issued by one lane; otherwise lane i of the producer
 // warp issues the i-th of up to 18.
@@ -833,6 +842,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
 //   warp 0      producer: lane i issues the i-th copy of a stage
 //   warp 1      MMA issuer, tensor-memory allocation
 //   all warps   the sum over the parts and the epilogue
+// What bounds it: launch, first loads and the exchange of the parts, about 4.5 us of every call (one
+// token, 2304 from 768: 4.8 us, of which reading the weights takes 0.5); then the weights' bytes (one
+// token, 4096 from 4096: 9.9 us; 14336 from 4096: 23.0 us, 5.1 TB/s), and with many rows the reads from
+// L2, 24 KB per 64 contraction elements of a 128 x 64 tile (2041 x 768 from 768: 9.2 us).
 template <int TN> struct Narrow {
   static constexpr uint32_t QB = TN * BK * 2;               // the row-side operand of a stage
   static constexpr uint32_t STAGE = kHalf + QB;

@@ -714,11 +714,12 @@ def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT
     rows, cols = _rows_cols(dY, "dY")
     dev, bf = _current_device(), torch.bfloat16
     pc, ps = _kept(z8, (rows, cols), "z8", dev)
-    if workspace is None and db is not None and act and rows * cols >= 1 << 22:
+    if workspace is None and db is not None and act and rows * cols > 1 << 24:
         nbytes = fsdp_act_backward_workspace(rows, cols)
         workspace = _call_workspace(nbytes, dY.device, stream) if nbytes else None
     _check(_lib.fsdp_act_backward(
-        _is(dY, (rows, cols), bf, "dY", dev), _is(z, (rows, cols), bf, "z", dev), pc, ps, rows, cols, act, _is(dZ, (rows, cols), bf, "dZ", dev),
+        _is(dY, (rows, cols), bf, "dY", dev), _is(z, (rows, cols), bf, "z", dev), pc, ps, rows, cols, act,
+        _is(dZ, (rows, cols), bf, "dZ", dev),
         _is(db, (cols,), torch.float32, "db", dev), _dev(workspace, torch.uint8, "workspace"),
         0 if workspace is None else workspace.numel(), _stream(stream)))
 

@@ -85,6 +85,8 @@ struct Walk {
   }
 };
 
+// Bound by HBM: 8192 x 14336 54-59 us, 6.0-6.6 TB/s (with the codes written); 8192 x 14344, groups cut
+// short, 69 us; 33 x 1160 2.8 us, a launch.
 template <bool FLAT>
 __global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __restrict__ x, const WalkDims d,
                                                               int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -118,6 +120,8 @@ __global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __
   }
 }
 
+// Bound by HBM: 8192 x 14336 55 us, 6.5 TB/s; 8192 x 14344 59 us. With erf's GELU by arithmetic (its
+// polynomial): 84 us.
 template <int ACT, bool FLAT>
 __global__ void __launch_bounds__(kThreads) ckpt8_unpack_kernel(const int8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, const WalkDims d,
@@ -217,13 +221,11 @@ __global__ void __launch_bounds__(kThreads, kSweepBlocks) act_backward_sweep_ker
     for (int k = 0; k < UN; ++k)
       if (r0 + k * lanes < rows) {
         gw[k] = __ldcs(reinterpret_cast<const uint4*>(dy) + i0 + k * step);
-        if constexpr (ACT != FSDP_ACT_NONE) {
-          if constexpr (Z8) {
-            cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i0 + k * step);
-            byte[k] = scales[s0 + k * lanes * groups];
-          } else {
-            zw[k] = __ldcs(reinterpret_cast<const uint4*>(z) + i0 + k * step);
-          }
+        if constexpr (Z8) {
+          cw[k] = __ldcs(reinterpret_cast<const uint2*>(codes) + i0 + k * step);
+          byte[k] = scales[s0 + k * lanes * groups];
+        } else {
+          zw[k] = __ldcs(reinterpret_cast<const uint4*>(z) + i0 + k * step);
         }
       }
 #pragma unroll
@@ -231,12 +233,10 @@ __global__ void __launch_bounds__(kThreads, kSweepBlocks) act_backward_sweep_ker
       if (r0 + k * lanes < rows) {
         f2 g[4], v[4];
         widen8(gw[k], g);
-        if constexpr (ACT != FSDP_ACT_NONE) {
-          if constexpr (Z8) decode8(cw[k], byte[k], v);
-          else widen8(zw[k], v);
+        if constexpr (Z8) decode8(cw[k], byte[k], v);
+        else widen8(zw[k], v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
-        }
+        for (int j = 0; j < 4; ++j) g[j] = f2_mul(g[j], act_grad<ACT>(v[j]));
         if (dz) __stcs(reinterpret_cast<uint4*>(dz) + i0 + k * step, narrow8(g));
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], g[j]);
@@ -274,9 +274,8 @@ __global__ void __launch_bounds__(kThreads) sum_partials_kernel(const float* __r
   }
 }
 
-// Activation backward with the column sums, without a workspace, for small matrices, where one
-// launch counts more. A cluster of blocks takes a strip of 8 LANES
-// columns, each block a run of its rows: LANES threads across the strip (8 columns each),
+// Activation backward with the column sums, without a workspace, for smaller matrices, where one
+// launch counts more. A cluster of blocks takes a strip of 8 LANES columns, each block a run of its rows: LANES threads across the strip (8 columns each),
 // kThreads / LANES rows at a time, four of a thread's rows in flight. A thread sums its rows in
 // order; a block adds its row lanes in order through shared memory, and block c of the cluster
 // the columns c, c + blocks, .. of all blocks' sums, in block order: the same bits every call, and no
@@ -394,21 +393,69 @@ struct Walking {
   }
 };
 
+// Clusters of 1 .. 8 blocks of one kernel that are resident at once, asked for once per device
+class ResidentClusters {
+ public:
+  template <class... P>
+  cudaError_t get(void (*kernel)(P...), const int** per_size) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int* known = known_[dev & 63];
+    *per_size = known;
+    return once_.run(dev, [&] {
+      for (unsigned int n = 1; n <= 8; ++n) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n), cfg.blockDim = dim3(kThreads);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = n, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr, cfg.numAttrs = 1;
+        const cudaError_t q = cudaOccupancyMaxActiveClusters(&known[n], kernel, &cfg);
+        if (q != cudaSuccess) return q;
+      }
+      return cudaSuccess;
+    });
+  }
+
+ private:
+  OncePerDevice once_;
+  int known_[64][9] = {};
+};
+
+struct Strips {
+  int lanes = 0, blocks = 1;
+  double score = 0.0;
+};
+// `best`, or strips of 8 LANES columns with n blocks across the rows (one cluster: at most 8; no fewer
+// than four rows a thread), whichever scores higher: the share of the GPU's block slots that work over
+// the waves taken, less for larger clusters, whose sums take longer to meet, and for narrower strips,
+// whose rows are shorter runs of memory (32 columns: 64 bytes). Measured against a strip width by
+// thresholds of the columns: column sums of 8192 x 4096 alone 10.4 us, 20.1 (32 columns); 8192 x 6144
+// 16.9, 21.0 (256 columns); from 8 bits 16384 x 1536 33.5, 47.1 (clusters of 6, of which 46 and not 50
+// are resident); 400 x 10240 7.8, 12.3; level where the threshold was right (8192 x 14336 40).
+template <int ACT, bool Z8, int LANES>
+cudaError_t consider_strips(int64_t rows, int64_t cols, Strips* best) {
+  static ResidentClusters resident;
+  const int* per_size = nullptr;
+  const cudaError_t e = resident.get(act_backward_kernel<ACT, Z8, LANES>, &per_size);
+  if (e != cudaSuccess) return e;
+  constexpr int RL = kThreads / LANES, STRIP = 8 * LANES;
+  constexpr double WIDE = LANES == 32 ? 1.2 : LANES == 16 ? 1.1 : LANES == 8 ? 1.0 : 0.9;
+  const int64_t strips = (cols + STRIP - 1) / STRIP;
+  for (int n = 1; n <= 8 && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
+    const int64_t waves = (strips + per_size[n] - 1) / std::max(per_size[n], 1);
+    const double busy = static_cast<double>(strips * n) / (static_cast<double>(waves) * num_sms() * kActBlocks);
+    const double score = busy * (1.0 - 0.03 * n) * WIDE;
+    if (score > best->score) best->score = score, best->lanes = LANES, best->blocks = n;
+  }
+  return cudaSuccess;
+}
+
 template <int ACT, bool Z8, int LANES>
 cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales,
-                          int64_t rows, int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
-  constexpr int RL = kThreads / LANES, STRIP = 8 * LANES;
-  // Blocks across the rows, no fewer than four rows a thread: the count (one cluster: at most 8)
-  // whose blocks fill their last wave best (8192 x 14336, 56 strips: 5 blocks, one wave of 280 where 304
-  // fit, 109 us).
-  const int64_t strips_all = (cols + STRIP - 1) / STRIP, resident = static_cast<int64_t>(num_sms()) * kActBlocks;
-  int blocks = 1;
-  double best = 0.0;
-  for (int n = 1; n <= 8 && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
-    const int64_t total = strips_all * n, waves = (total + resident - 1) / resident;
-    const double fill = static_cast<double>(total) / static_cast<double>(waves * resident);
-    if (fill > best + 0.01) best = fill, blocks = n;
-  }
+                          int64_t rows, int64_t cols, int blocks, uint16_t* dz, float* db, cudaStream_t st) {
+  constexpr int STRIP = 8 * LANES;
   const int64_t per = (rows + blocks - 1) / blocks;
   // strips in launches of at most 65535 (the grid's y limit)
   for (int64_t s0 = 0, strips = (cols + STRIP - 1) / STRIP; s0 < strips; s0 += 65535) {
@@ -421,21 +468,30 @@ cudaError_t launch_strips(const uint16_t* dy, const uint16_t* z, const int8_t* c
   return cudaSuccess;
 }
 
-// Strips of 128 columns (a row of a strip is two lines of dY) where their blocks fill the GPU;
-// narrower ones, down to 32 columns (one group), for narrow matrices
 template <int ACT, bool Z8>
 cudaError_t launch_act(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales, int64_t rows,
                        int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
-  if (cols > 4096) return launch_strips<ACT, Z8, 32>(dy, z, codes, scales, rows, cols, dz, db, st);
-  return launch_strips<ACT, Z8, 4>(dy, z, codes, scales, rows, cols, dz, db, st);
+  Strips s;
+  cudaError_t e;
+  if ((e = consider_strips<ACT, Z8, 32>(rows, cols, &s)) != cudaSuccess) return e;
+  if ((e = consider_strips<ACT, Z8, 16>(rows, cols, &s)) != cudaSuccess) return e;
+  if ((e = consider_strips<ACT, Z8, 8>(rows, cols, &s)) != cudaSuccess) return e;
+  if ((e = consider_strips<ACT, Z8, 4>(rows, cols, &s)) != cudaSuccess) return e;
+  switch (s.lanes) {
+    case 32: return launch_strips<ACT, Z8, 32>(dy, z, codes, scales, rows, cols, s.blocks, dz, db, st);
+    case 16: return launch_strips<ACT, Z8, 16>(dy, z, codes, scales, rows, cols, s.blocks, dz, db, st);
+    case 8: return launch_strips<ACT, Z8, 8>(dy, z, codes, scales, rows, cols, s.blocks, dz, db, st);
+    default: return launch_strips<ACT, Z8, 4>(dy, z, codes, scales, rows, cols, s.blocks, dz, db, st);
+  }
 }
 
 // Rows that the sweep takes at a time, and so partial sums a column; 0: the matrix is for the strips.
-// From 2^22 elements and 4096 columns on the sweep wins (8192 x 14336: from 8 bits 97 us against 104,
-// from bf16 107 against 115); narrower rows leave too many partial sums (8192 x 768: 29 against 9),
-// and without an activation, where only dY is read, the strips are level or ahead (40 us against 45).
+// Past 2^24 elements and from 2048 columns on the sweep wins (from 8 bits 8192 x 14336: 107 us against
+// 114, 8192 x 3584 32 against 34, 16384 x 2304 41 against 43; level at 4096 x 4096; 1024 x 8192 13.0
+// against 10.9; 32768 x 1024 level). Without an activation, where only dY is read, the strips are ahead
+// (8192 x 14336 40 us against 45).
 int sweep_lanes(int64_t rows, int64_t cols) {
-  if (rows * cols < (int64_t(1) << 22) || cols < 4096) return 0;
+  if (rows * cols <= (int64_t(1) << 24) || cols < 2048) return 0;
   return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms()) * kSweepBlocks * kThreads / (cols / 8), rows));
 }
 

@@ -47,8 +47,9 @@ __device__ __forceinline__ float amax8(const f2 (&v)[4]) {
 // ------------------------------------------------------------------------------------
 // one sweep over memory: pack, unpack, activation backward without column sums
 // ------------------------------------------------------------------------------------
-constexpr int kWalkBlocks = 32;  // blocks per SM
-constexpr int kWalk = 3;         // units a thread has in flight
+constexpr int kWalkBlocks = 48;  // blocks per SM at most; 32 and 16: pack 8192 x 14336 57.4 and 62 us, 56.1
+// units a thread has in flight (4 and 3: pack 8192 x 14336 56.1 and 58.9 us, 8192 x 14344 77.8 and 70.9)
+__host__ __device__ constexpr int walk_units(bool flat) { return flat ? 4 : 3; }
 
 // A matrix as units of 8 columns, four to a group of the checkpoint, walked by all threads together:
 // a warp's accesses are contiguous. FLAT: widths of whole groups, rows need not be known (also where
@@ -85,24 +86,26 @@ struct Walk {
   }
 };
 
-// Bound by HBM: 8192 x 14336 54-59 us, 6.0-6.6 TB/s (with the codes written); 8192 x 14344, groups cut
-// short, 69 us; 33 x 1160 2.8 us, a launch.
+// Bound by HBM: 8192 x 14336 56 us, 6.4 TB/s (with the codes written); 8192 x 14344, groups cut
+// short, 71 us; 33 x 1160 2.8 us, a launch.
 template <bool FLAT>
 __global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __restrict__ x, const WalkDims d,
                                                               int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   allow_next_grid();
   Walk<FLAT> w(d);
   wait_for_prior_grids();
+  constexpr int UN = walk_units(FLAT);
   while (w.there(d)) {
-    uint4 in[kWalk];
+    uint4 in[UN];
     Walk<FLAT> a = w;
 #pragma unroll
-    for (int k = 0; k < kWalk; ++k, a.step(d)) {
+    for (int k = 0; k < UN; ++k, a.step(d)) {
       in[k] = make_uint4(0u, 0u, 0u, 0u);
       if (a.data(d)) in[k] = __ldcs(reinterpret_cast<const uint4*>(x + a.at(d)));
     }
 #pragma unroll
-    for (int k = 0; k < kWalk; ++k, w.step(d)) {
+    for (int k = 0; k < UN; ++k, w.step(d)) {
+      if (!w.there(d)) return;
       f2 v[4];
       widen8(in[k], v);
       float amax = amax8(v);
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __
   }
 }
 
-// Bound by HBM: 8192 x 14336 55 us, 6.5 TB/s; 8192 x 14344 59 us. With erf's GELU by arithmetic (its
+// Bound by HBM: 8192 x 14336 54 us, 6.6 TB/s; 8192 x 14344 59 us. With erf's GELU by arithmetic (its
 // polynomial): 84 us.
 template <int ACT, bool FLAT>
 __global__ void __launch_bounds__(kThreads) ckpt8_unpack_kernel(const int8_t* __restrict__ codes,
@@ -129,19 +132,20 @@ __global__ void __launch_bounds__(kThreads) ckpt8_unpack_kernel(const int8_t* __
   allow_next_grid();
   Walk<FLAT> w(d);
   wait_for_prior_grids();
+  constexpr int UN = walk_units(FLAT);
   while (w.there(d)) {
-    uint2 in[kWalk];
-    uint32_t byte[kWalk];
+    uint2 in[UN];
+    uint32_t byte[UN];
     Walk<FLAT> a = w;
 #pragma unroll
-    for (int k = 0; k < kWalk; ++k, a.step(d)) {
+    for (int k = 0; k < UN; ++k, a.step(d)) {
       if (a.data(d)) {
         in[k] = __ldcs(reinterpret_cast<const uint2*>(codes + a.at(d)));
         byte[k] = scales[a.group(d)];
       }
     }
 #pragma unroll
-    for (int k = 0; k < kWalk; ++k, w.step(d)) {
+    for (int k = 0; k < UN; ++k, w.step(d)) {
       if (w.data(d)) {
         f2 v[4];
         decode8(in[k], byte[k], v);
@@ -387,7 +391,10 @@ struct Walking {
   Walking(int64_t rows, int64_t cols, bool groups) {
     flat = !groups || cols % kCkptGroup == 0;
     const int64_t row_units = flat ? cols / 8 : (cols + kCkptGroup - 1) / kCkptGroup * 4;
-    blocks = grid_for(rows * row_units, kWalkBlocks);
+    // one unit a thread until there are four blocks per SM, then as many as a thread has in flight (more
+    // blocks that use part of it: pack 4096 x 4096 8.2 -> 12.9 us)
+    const int64_t units = rows * row_units;
+    blocks = std::max(grid_for(units, 4), grid_for(units / walk_units(flat), kWalkBlocks));
     const int64_t step = static_cast<int64_t>(blocks) * kThreads;
     d = {rows, cols, flat ? rows * row_units : row_units, flat ? 0 : step / row_units, flat ? step : step % row_units};
   }
@@ -397,10 +404,7 @@ struct Walking {
 class ResidentClusters {
  public:
   template <class... P>
-  cudaError_t get(void (*kernel)(P...), const int** per_size) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+  cudaError_t get(int dev, void (*kernel)(P...), const int** per_size) {
     int* known = known_[dev & 63];
     *per_size = known;
     return once_.run(dev, [&] {
@@ -425,7 +429,7 @@ class ResidentClusters {
 
 struct Strips {
   int lanes = 0, blocks = 1;
-  double score = 0.0;
+  float score = 0.0f;
 };
 // `best`, or strips of 8 LANES columns with n blocks across the rows (one cluster: at most 8; no fewer
 // than four rows a thread), whichever scores higher: the share of the GPU's block slots that work over
@@ -435,18 +439,18 @@ struct Strips {
 // 16.9, 21.0 (256 columns); from 8 bits 16384 x 1536 33.5, 47.1 (clusters of 6, of which 46 and not 50
 // are resident); 400 x 10240 7.8, 12.3; level where the threshold was right (8192 x 14336 40).
 template <int ACT, bool Z8, int LANES>
-cudaError_t consider_strips(int64_t rows, int64_t cols, Strips* best) {
+cudaError_t consider_strips(int dev, int slots, int64_t rows, int64_t cols, Strips* best) {
   static ResidentClusters resident;
   const int* per_size = nullptr;
-  const cudaError_t e = resident.get(act_backward_kernel<ACT, Z8, LANES>, &per_size);
+  const cudaError_t e = resident.get(dev, act_backward_kernel<ACT, Z8, LANES>, &per_size);
   if (e != cudaSuccess) return e;
   constexpr int RL = kThreads / LANES, STRIP = 8 * LANES;
-  constexpr double WIDE = LANES == 32 ? 1.2 : LANES == 16 ? 1.1 : LANES == 8 ? 1.0 : 0.9;
+  constexpr float WIDE = LANES == 32 ? 1.2f : LANES == 16 ? 1.1f : LANES == 8 ? 1.0f : 0.9f;
   const int64_t strips = (cols + STRIP - 1) / STRIP;
   for (int n = 1; n <= 8 && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
     const int64_t waves = (strips + per_size[n] - 1) / std::max(per_size[n], 1);
-    const double busy = static_cast<double>(strips * n) / (static_cast<double>(waves) * num_sms() * kActBlocks);
-    const double score = busy * (1.0 - 0.03 * n) * WIDE;
+    const float busy = static_cast<float>(strips * n) / static_cast<float>(waves * slots);
+    const float score = busy * (1.0f - 0.03f * n) * WIDE;
     if (score > best->score) best->score = score, best->lanes = LANES, best->blocks = n;
   }
   return cudaSuccess;
@@ -472,11 +476,14 @@ template <int ACT, bool Z8>
 cudaError_t launch_act(const uint16_t* dy, const uint16_t* z, const int8_t* codes, const uint8_t* scales, int64_t rows,
                        int64_t cols, uint16_t* dz, float* db, cudaStream_t st) {
   Strips s;
-  cudaError_t e;
-  if ((e = consider_strips<ACT, Z8, 32>(rows, cols, &s)) != cudaSuccess) return e;
-  if ((e = consider_strips<ACT, Z8, 16>(rows, cols, &s)) != cudaSuccess) return e;
-  if ((e = consider_strips<ACT, Z8, 8>(rows, cols, &s)) != cudaSuccess) return e;
-  if ((e = consider_strips<ACT, Z8, 4>(rows, cols, &s)) != cudaSuccess) return e;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int slots = num_sms() * kActBlocks;
+  if ((e = consider_strips<ACT, Z8, 32>(dev, slots, rows, cols, &s)) != cudaSuccess) return e;
+  if ((e = consider_strips<ACT, Z8, 16>(dev, slots, rows, cols, &s)) != cudaSuccess) return e;
+  if ((e = consider_strips<ACT, Z8, 8>(dev, slots, rows, cols, &s)) != cudaSuccess) return e;
+  if ((e = consider_strips<ACT, Z8, 4>(dev, slots, rows, cols, &s)) != cudaSuccess) return e;
   switch (s.lanes) {
     case 32: return launch_strips<ACT, Z8, 32>(dy, z, codes, scales, rows, cols, s.blocks, dz, db, st);
     case 16: return launch_strips<ACT, Z8, 16>(dy, z, codes, scales, rows, cols, s.blocks, dz, db, st);

@@ -491,6 +491,11 @@ __device__ __forceinline__ void wide_tile_coords(int tile, int num_m, int num_n,
   nb = in_band / rows;
 }
 
+// a box of global memory to L2
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y) : "memory");
+}
+
 // fp32 add of a shared-memory box to global memory, in L2
 __device__ __forceinline__ void tma_reduce_add_2d(const void* tmap, int32_t x, int32_t y, uint32_t src_smem) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap),
@@ -842,9 +847,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
 //   warp 0      producer: lane i issues the i-th copy of a stage
 //   warp 1      MMA issuer, tensor-memory allocation
 //   all warps   the sum over the parts and the epilogue
-// What bounds it: launch, first loads and the exchange of the parts, about 4.5 us of every call (one
-// token, 2304 from 768: 4.8 us, of which reading the weights takes 0.5); then the weights' bytes (one
-// token, 4096 from 4096: 9.9 us; 14336 from 4096: 23.0 us, 5.1 TB/s), and with many rows the reads from
+// What bounds it: launch, first loads and the exchange of the parts, about 4 us of every call (one
+// token, 2304 from 768: 4.4 us, of which reading the weights takes 0.5); then the weights' bytes (one
+// token, 4096 from 4096: 9.2 us; 14336 from 4096: 22.9 us, 5.1 TB/s), and with many rows the reads from
 // L2, 24 KB per 64 contraction elements of a 128 x 64 tile (2041 x 768 from 768: 9.2 us).
 template <int TN> struct Narrow {
   static constexpr uint32_t QB = TN * BK * 2;               // the row-side operand of a stage
@@ -956,10 +961,10 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   allow_next_grid();
-  wait_for_prior_grids();
   const uint32_t tmem_base = tmem_base_sh;
 
   int issued = 0;  // K blocks, warp 0
+  if (warp != 0) wait_for_prior_grids();
   if (warp == 0) {
     Copy c;
     int i = lane;
@@ -969,6 +974,19 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
     if constexpr (Q_MN) i -= mn_copies(&p.a, TN / 64, i, m0, kb0, kHalf, c);
     else i -= k_copies(&p.a, i, m0, kb0, kHalf, c);
     const bool mine = i < 0;
+    if (mine) {
+      // While the stream's earlier kernels finish: the copy's map (dW 2304 x 768 from 1024 tokens 8.5 -> 7.6
+      // us), and, where W is read by one row of tiles, its first stages to L2, which an earlier kernel's
+      // writes to W reach too (one token, repeated calls: 2304 from 768 4.9 -> 4.4 us, 4096 from 4096 10.0
+      // -> 9.2; by sixteen rows of tiles 1003 x 1160 from 520 10.1 -> 11.1, so not there).
+      prefetch_tmap(c.map);
+      if (OP != OP_DW && gridDim.z == 1 && c.dst < kHalf) {
+        Copy ahead = c;
+        for (int kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb, copy_advance(p, ahead))
+          tma_prefetch_2d(ahead.map, ahead.x, ahead.y);
+      }
+    }
+    wait_for_prior_grids();
     uint32_t s = 0, ph = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++issued) {
       bool ok = true;

@@ -850,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
 // What bounds it: launch, first loads and the exchange of the parts, about 4 us of every call (one
 // token, 2304 from 768: 4.4 us, of which reading the weights takes 0.5); then the weights' bytes (one
 // token, 4096 from 4096: 9.2 us; 14336 from 4096: 22.9 us, 5.1 TB/s), and with many rows the reads from
-// L2, 24 KB per 64 contraction elements of a 128 x 64 tile (2041 x 768 from 768: 9.2 us).
+// L2, 24 KB per 64 contraction elements of a 128 x 64 tile (2041 x 768 from 768: 7.0 us).
 template <int TN> struct Narrow {
   static constexpr uint32_t QB = TN * BK * 2;               // the row-side operand of a stage
   static constexpr uint32_t STAGE = kHalf + QB;

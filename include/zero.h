@@ -512,8 +512,9 @@ ZERO_API int fsdp_unit_forward_static_scratch(int n_ranks, const zero_bf16* cons
  * codes: it reads back as NaN throughout.
  *
  * Activations: the FSDP_ACT_* values; RELU's derivative at 0 is 0, GELU is x Phi(x), GELU_TANH
- * its tanh form, SILU x / (1 + exp(-x)). They and their derivatives are computed in fp32 (relative error of a few 2^-20)
- * from the fp32 sum or the kept activation, with one rounding to the output's type.
+ * its tanh form, SILU x / (1 + exp(-x)). They and their derivatives are computed in fp32
+ * (relative error of a few 2^-20) from the fp32 sum or the kept activation, with one rounding
+ * to the output's type.
  *
  * Calls take every m_tokens / rows >= 1; widths (rows_out, k_in, cols) are multiples of 8,
  * every buffer is 16-byte aligned, row-major and contiguous, and W is held as n_ranks (1..16)

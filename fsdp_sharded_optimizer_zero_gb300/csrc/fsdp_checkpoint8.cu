@@ -448,7 +448,8 @@ cudaError_t consider_strips(int dev, int slots, int64_t rows, int64_t cols, Stri
   constexpr float WIDE = LANES == 32 ? 1.2f : LANES == 16 ? 1.1f : LANES == 8 ? 1.0f : 0.9f;
   const int64_t strips = (cols + STRIP - 1) / STRIP;
   for (int n = 1; n <= 8 && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
-    const int64_t waves = (strips + per_size[n] - 1) / std::max(per_size[n], 1);
+    if (per_size[n] < 1) continue;
+    const int64_t waves = (strips + per_size[n] - 1) / per_size[n];
     const float busy = static_cast<float>(strips * n) / static_cast<float>(waves * slots);
     const float score = busy * (1.0f - 0.03f * n) * WIDE;
     if (score > best->score) best->score = score, best->lanes = LANES, best->blocks = n;

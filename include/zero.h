@@ -554,8 +554,8 @@ ZERO_API int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[],
 ZERO_API int fsdp_act_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
 
 /* Backward of the activation and the bias: dZ = bf16(dY act'(Z)), db = sum over the rows of
- * the unrounded dY act'(Z), fp32, in a fixed order (the same bits every call with the same
- * sizes and choice of workspace). dY, dZ [rows, cols] bf16, dZ nullable when db is asked for;
+ * the unrounded dY act'(Z), fp32, in a fixed order (the same bits every call on one
+ * device with the same sizes and choice of workspace). dY, dZ [rows, cols] bf16, dZ nullable when db is asked for;
  * db [cols] fp32, nullable. With FSDP_ACT_NONE, db is the column sum of dY. The residual's
  * gradient is dY itself. workspace: nullable, else of fsdp_act_backward_workspace() bytes. */
 ZERO_API int fsdp_act_backward(const zero_bf16* dY, const zero_bf16* z, const int8_t* z_codes, const uint8_t* z_scales,

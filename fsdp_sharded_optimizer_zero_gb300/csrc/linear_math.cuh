@@ -87,35 +87,36 @@ __device__ __forceinline__ f2 sigmoid256(f2 m) {
   return f2_make(ra, rb);
 }
 
-// Phi(x), the normal distribution function, and e = exp(-x^2 / 2), which the density shares.
-// For a = |x|: 1 - Phi(a) = e / 2 * erfcx(a / sqrt 2), and erfcx(a / sqrt 2) = t P(t) with t = 1 / (1 +
-// 0.36 a), P of degree 8, fitted here for the least largest relative error over 0 <= a <= 40
-// (weighted least squares, weights iterated): 9.1e-8. So the lower tail keeps its relative
-// precision, at one exponential and one reciprocal.
-__device__ __forceinline__ f2 normal_cdf(f2 x, f2& e) {
-  float a, b, ta, tb, ea, eb;
-  f2_split(x, a, b);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ta) : "f"(__fmaf_rn(fabsf(a), 0.36f, 1.0f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(tb) : "f"(__fmaf_rn(fabsf(b), 0.36f, 1.0f)));
+// Phi(a) - 1 for a = |x| held to 60 (where it is 0), and e = exp(-a^2 / 2), which the density shares.
+// 1 - Phi(a) = e / 2 * erfcx(a / sqrt 2), and erfcx(a / sqrt 2) = t P(t) with t = 1 / (1 + 0.36 a), P of
+// degree 8 (here times -1/2), fitted here for the least largest relative error over 0 <= a <= 40
+// (weighted least squares, weights iterated): 9.1e-8. So the tail keeps its relative precision, at
+// one exponential and one reciprocal.
+__device__ __forceinline__ f2 normal_tail(f2 a, f2& e) {
+  float u, v, ta, tb, ea, eb;
+  f2_split(f2_fma(a, f2_both(0.36f), f2_both(1.0f)), u, v);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ta) : "f"(u));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(tb) : "f"(v));
   const f2 t = f2_make(ta, tb);
-  f2_split(f2_mul(f2_mul(x, x), f2_both(-kHalfLog2e)), ea, eb);
+  f2_split(f2_mul(f2_mul(a, a), f2_both(-kHalfLog2e)), ea, eb);
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ea) : "f"(ea));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(eb) : "f"(eb));
   e = f2_make(ea, eb);
-  f2 p = f2_both(-0.060481980f);
-  p = f2_fma(p, t, f2_both(0.27903997f));
-  p = f2_fma(p, t, f2_both(-0.44723977f));
-  p = f2_fma(p, t, f2_both(0.21477633f));
-  p = f2_fma(p, t, f2_both(-0.00079324538f));
-  p = f2_fma(p, t, f2_both(0.19208115f));
-  p = f2_fma(p, t, f2_both(0.24801837f));
-  p = f2_fma(p, t, f2_both(0.28736386f));
-  p = f2_fma(p, t, f2_both(0.28723533f));
-  const f2 q = f2_mul(f2_mul(p, t), f2_mul(e, f2_both(0.5f)));
-  float qa, qb, ua, ub;
-  f2_split(q, qa, qb);
-  f2_split(f2_fma(q, f2_both(-1.0f), f2_both(1.0f)), ua, ub);
-  return f2_make(a < 0.0f ? qa : ua, b < 0.0f ? qb : ub);
+  f2 p = f2_both(-0.5f * -0.060481980f);
+  p = f2_fma(p, t, f2_both(-0.5f * 0.27903997f));
+  p = f2_fma(p, t, f2_both(-0.5f * -0.44723977f));
+  p = f2_fma(p, t, f2_both(-0.5f * 0.21477633f));
+  p = f2_fma(p, t, f2_both(-0.5f * -0.00079324538f));
+  p = f2_fma(p, t, f2_both(-0.5f * 0.19208115f));
+  p = f2_fma(p, t, f2_both(-0.5f * 0.24801837f));
+  p = f2_fma(p, t, f2_both(-0.5f * 0.28736386f));
+  p = f2_fma(p, t, f2_both(-0.5f * 0.28723533f));
+  return f2_mul(f2_mul(p, t), e);
+}
+__device__ __forceinline__ f2 abs_to_60(f2 x) {
+  float a, b;
+  f2_split(x, a, b);
+  return f2_make(fminf(fabsf(a), 60.0f), fminf(fabsf(b), 60.0f));
 }
 
 // act(x). The tanh form of GELU uses (1 + tanh u) / 2 = 1 / (1 + exp(-2u)): one exponential,
@@ -128,9 +129,12 @@ __device__ __forceinline__ f2 act_fwd(f2 x) {
     f2_split(x, a, b);
     return f2_make(a < 0.0f ? 0.0f : a, b < 0.0f ? 0.0f : b);  // NaN stays
   }
-  if constexpr (ACT == FSDP_ACT_GELU) {
+  if constexpr (ACT == FSDP_ACT_GELU) {  // max(x, 0) - |x| (1 - Phi(|x|)); a NaN comes through the maximum
+    float a, b;
     f2 e;
-    return f2_mul(x, normal_cdf(x, e));
+    f2_split(x, a, b);
+    const f2 m = abs_to_60(x);
+    return f2_fma(m, normal_tail(m, e), f2_make(max_nan(a, 0.0f), max_nan(b, 0.0f)));
   }
   if constexpr (ACT == FSDP_ACT_GELU_TANH) {
     const f2 w = f2_fma(f2_mul(x, x), f2_both(-kGeluA * kGeluB * kHalfLog2e), f2_both(-kGeluA * kHalfLog2e));
@@ -150,9 +154,13 @@ __device__ __forceinline__ f2 act_grad(f2 x) {
     return f2_make(a > 0.0f ? 1.0f : a != a ? a : 0.0f, b > 0.0f ? 1.0f : b != b ? b : 0.0f);
   }
   if constexpr (ACT == FSDP_ACT_GELU) {  // Phi(x) + x phi(x)
+    float a, b, qa, qb, ua, ub;
     f2 e;
-    const f2 cdf = normal_cdf(x, e);
-    return f2_fma(f2_mul(x, e), f2_both(kInvSqrt2Pi), cdf);
+    const f2 q = normal_tail(abs_to_60(x), e);
+    f2_split(q, qa, qb);
+    f2_split(f2_add(q, f2_both(1.0f)), ua, ub);
+    f2_split(x, a, b);
+    return f2_fma(f2_mul(x, e), f2_both(kInvSqrt2Pi), f2_make(a < 0.0f ? -qa : ua, b < 0.0f ? -qb : ub));
   }
   if constexpr (ACT == FSDP_ACT_GELU_TANH) {
     // s + x s (1 - s) du with du = A (1 + 3 B x^2). Past |x| = 100 s is 0 or 1: holding x^2

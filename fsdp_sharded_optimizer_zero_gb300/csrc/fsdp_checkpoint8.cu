@@ -494,12 +494,12 @@ cudaError_t launch_act(const uint16_t* dy, const uint16_t* z, const int8_t* code
 }
 
 // Rows that the sweep takes at a time, and so partial sums a column; 0: the matrix is for the strips.
-// Past 2^24 elements and from 2048 columns on the sweep wins (from 8 bits 8192 x 14336: 107 us against
-// 114, 8192 x 3584 32 against 34, 16384 x 2304 41 against 43; level at 4096 x 4096; 1024 x 8192 13.0
-// against 10.9; 32768 x 1024 level). Without an activation, where only dY is read, the strips are ahead
+// Past 2^24 elements and from 1024 columns on the sweep wins (from 8 bits 8192 x 14336: 107 us against
+// 114, 8192 x 3584 32 against 34, 16384 x 1536 29.4 against 33.3, with GELU 34 against 50; level at 4096 x
+// 4096 and 32768 x 1024; 1024 x 8192 12.3 against 10.7). Without an activation, where only dY is read, the strips are ahead
 // (8192 x 14336 40 us against 45).
 int sweep_lanes(int64_t rows, int64_t cols) {
-  if (rows * cols <= (int64_t(1) << 24) || cols < 2048) return 0;
+  if (rows * cols <= (int64_t(1) << 24) || cols < 1024) return 0;
   return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms()) * kSweepBlocks * kThreads / (cols / 8), rows));
 }
 

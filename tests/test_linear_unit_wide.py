@@ -223,9 +223,9 @@ def test_dw_workspace_and_streams(z):
 
 @pytest.mark.parametrize("kind", ["z", "z8", "none"])
 @pytest.mark.parametrize("rows,cols", [(4100, 1032), (531, 8200), (9, 524296), (70001, 64), (4106, 4104),
-                                       (8200, 2056), (33, 524296), (16385, 1536), (401, 10248)])
+                                       (8200, 2056), (33, 524296), (16385, 1536), (401, 10248), (16401, 1032)])
 def test_act_backward_large(z, rows, cols, kind):
-    """Large matrices: past 2^24 elements, from 2048 columns on, the column sums go through a workspace,
+    """Large matrices: past 2^24 elements, from 1024 columns on, the column sums go through a workspace,
     the caller's or the allocator's; without one, and else, they are summed in strips of any width."""
     act = {"z": "gelu_tanh", "z8": "silu", "none": "none"}[kind]
     dy, pre = randn(rows, cols, 0.3, 13), randn(rows, cols, 1.5, 14)

@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(kThreads) sum_partials_kernel(const float* __r
 }
 
 // Activation backward with the column sums, without a workspace, for smaller matrices, where one
-// launch counts more. A cluster of blocks takes a strip of 8 LANES columns, each block a run of its rows: LANES threads across the strip (8 columns each),
+// launch counts more. A cluster of blocks takes a strip of 8 LANES columns, each block a run of its
+// rows: LANES threads across the strip (8 columns each),
 // kThreads / LANES rows at a time, four of a thread's rows in flight. A thread sums its rows in
 // order; a block adds its row lanes in order through shared memory, and block c of the cluster
 // the columns c, c + blocks, .. of all blocks' sums, in block order: the same bits every call, and no
@@ -400,7 +401,8 @@ struct Walking {
   }
 };
 
-// Clusters of 1 .. 8 blocks of one kernel that are resident at once, asked for once per device
+constexpr int kMaxCluster = 16;  // blocks; more than 8 a kernel has to allow
+// Clusters of 1 .. kMaxCluster blocks of one kernel that are resident at once, asked for once per device
 class ResidentClusters {
  public:
   template <class... P>
@@ -408,15 +410,16 @@ class ResidentClusters {
     int* known = known_[dev & 63];
     *per_size = known;
     return once_.run(dev, [&] {
-      for (unsigned int n = 1; n <= 8; ++n) {
+      cudaError_t q = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (q != cudaSuccess) return q;
+      for (unsigned int n = 1; n <= kMaxCluster; ++n) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n), cfg.blockDim = dim3(kThreads);
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = n, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr, cfg.numAttrs = 1;
-        const cudaError_t q = cudaOccupancyMaxActiveClusters(&known[n], kernel, &cfg);
-        if (q != cudaSuccess) return q;
+        if ((q = cudaOccupancyMaxActiveClusters(&known[n], kernel, &cfg)) != cudaSuccess) return q;
       }
       return cudaSuccess;
     });
@@ -424,20 +427,21 @@ class ResidentClusters {
 
  private:
   OncePerDevice once_;
-  int known_[64][9] = {};
+  int known_[64][kMaxCluster + 1] = {};
 };
 
 struct Strips {
   int lanes = 0, blocks = 1;
   float score = 0.0f;
 };
-// `best`, or strips of 8 LANES columns with n blocks across the rows (one cluster: at most 8; no fewer
-// than four rows a thread), whichever scores higher: the share of the GPU's block slots that work over
+// `best`, or strips of 8 LANES columns with n blocks across the rows (one cluster; no fewer than four
+// rows a thread), whichever scores higher: the share of the GPU's block slots that work over
 // the waves taken, less for larger clusters, whose sums take longer to meet, and for narrower strips,
 // whose rows are shorter runs of memory (32 columns: 64 bytes). Measured against a strip width by
 // thresholds of the columns: column sums of 8192 x 4096 alone 10.4 us, 20.1 (32 columns); 8192 x 6144
 // 16.9, 21.0 (256 columns); from 8 bits 16384 x 1536 33.5, 47.1 (clusters of 6, of which 46 and not 50
-// are resident); 400 x 10240 7.8, 12.3; level where the threshold was right (8192 x 14336 40).
+// are resident); 400 x 10240 7.8, 12.3; level where the threshold was right (8192 x 14336 40). Clusters of
+// up to 16 against up to 8: 9879 x 544 with GELU 11.6, 15.5; 16384 x 512 with SiLU 11.4, 14.6.
 template <int ACT, bool Z8, int LANES>
 cudaError_t consider_strips(int dev, int slots, int64_t rows, int64_t cols, Strips* best) {
   static ResidentClusters resident;
@@ -447,7 +451,7 @@ cudaError_t consider_strips(int dev, int slots, int64_t rows, int64_t cols, Stri
   constexpr int RL = kThreads / LANES, STRIP = 8 * LANES;
   constexpr float WIDE = LANES == 32 ? 1.2f : LANES == 16 ? 1.1f : LANES == 8 ? 1.0f : 0.9f;
   const int64_t strips = (cols + STRIP - 1) / STRIP;
-  for (int n = 1; n <= 8 && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
+  for (int n = 1; n <= kMaxCluster && (n == 1 || rows > static_cast<int64_t>(n - 1) * RL * 4); ++n) {
     if (per_size[n] < 1) continue;
     const int64_t waves = (strips + per_size[n] - 1) / per_size[n];
     const float busy = static_cast<float>(strips * n) / static_cast<float>(waves * slots);

@@ -46,12 +46,15 @@ constexpr unsigned int kErrAccF = (5u << 8) | 4u;   // epilogue waiting for a fi
 constexpr unsigned int kErrDrain = (5u << 8) | 5u;  // waiting for copies or MMAs in flight
 
 struct LinearParams {
-  CUtensorMap w[kGemmMaxPieces];  // fwd, dx: the row shards of W, boxes of 64 columns x w_box rows
+  // fwd, dx: the row shards of W, boxes of 64 columns x w_box rows; where they are cut to fit (w_levels > 1),
+  // again with boxes of 4 w_box, 16 w_box rows
+  CUtensorMap w[kGemmMaxPieces];
   CUtensorMap a;                  // fwd: X, dx: dZ (K-major, box 64 x 128 or TN rows); dw: dZ (MN-major, box 64 x 64)
   CUtensorMap b;                  // dw: X (MN-major, box 64 x 64)
   CUtensorMap out;                // wide kernel, fp32 dW: the output, boxes of 32 columns x 32 rows
   int m, n, k;                    // the product: out [m, n], contraction over k
   int n_shards, shard_rows;       // fwd, dx
+  int w_levels;
   int w_box, w_box_log;           // rows of W per copy: the largest power of two <= 128 (fwd) or 64 (dx) that divides shard_rows
   const uint16_t *bias, *res;     // fwd: bias; fwd, dx: residual
   int act;
@@ -130,15 +133,49 @@ struct Copy {
   bool k_major;   // x advances with K, y otherwise
   bool w_rows;    // y walks W's rows through the shards (dx)
   int shard;
+  // W cut to fit: shard and row are where the K block's rows (dx) or the tile's columns (fwd) start
+  int row, piece;
+  uint32_t base;
 };
-__device__ __forceinline__ void copy_advance(const LinearParams& p, Copy& c) {
+// W cut to fit: copy number c.piece of ROWS rows from row c.row of shard c.shard, each as high as the
+// shard allows of w_box, 4 w_box, .., ROWS; false if there are fewer. Rows past the last one count to
+// the last shard, past its end (they read zeros).
+template <int ROWS>
+__device__ __forceinline__ bool w_piece(const LinearParams& p, Copy& c) {
+  int shard = c.shard, y = c.row, at = 0, level = p.w_levels - 1;
+  const auto box = [&](int l) { return min(p.w_box << (2 * l), ROWS); };
+  if (shard + 1 == p.n_shards || p.shard_rows - y >= ROWS) {
+    at = c.piece * box(level), y += at;
+  } else {
+    for (int i = c.piece; at < ROWS; --i) {
+      const bool last = shard + 1 == p.n_shards;
+      const int left = last ? ROWS - at : min(ROWS - at, p.shard_rows - y);
+      for (level = p.w_levels - 1; level > 0 && box(level) > left;) --level;
+      if (i == 0) break;
+      at += box(level), y += box(level);
+      if (!last && y >= p.shard_rows) y = 0, ++shard;
+    }
+  }
+  if (at >= ROWS) return false;
+  c.map = &p.w[level * p.n_shards + shard];
+  c.y = y, c.dst = c.base + static_cast<uint32_t>(at) * 128u;
+  return true;
+}
+// to the next K block; false: this lane has nothing to copy for it
+template <bool CUT>
+__device__ __forceinline__ bool copy_advance(const LinearParams& p, Copy& c) {
   if (c.k_major) {
     c.x += BK;
+  } else if (CUT && c.w_rows) {
+    c.row += BK;
+    while (c.row >= p.shard_rows && c.shard + 1 < p.n_shards) c.row -= p.shard_rows, ++c.shard;
+    return w_piece<BK>(p, c);
   } else {
     c.y += BK;
     if (c.w_rows)
       while (c.y >= p.shard_rows && c.shard + 1 < p.n_shards) c.y -= p.shard_rows, ++c.shard, ++c.map;
   }
+  return true;
 }
 // the shard that holds row `row` of W; rows past the last one stay in the last shard, past
 // its end (they read zeros)
@@ -147,42 +184,65 @@ __device__ __forceinline__ void copy_seek(const LinearParams& p, Copy& c, int ro
   c.map = &p.w[c.shard];
   c.y = row - c.shard * p.shard_rows;
 }
-// copies of W (fwd): 128 output columns from n0, K-major, 128 / w_box copies of w_box rows
-__device__ __forceinline__ int w_copies_k_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c) {
+// copies of W (fwd): 128 output columns from n0, K-major, 128 / w_box copies of w_box rows, or (CUT) up to
+// as many lanes with `has` true
+template <bool CUT>
+__device__ __forceinline__ int w_copies_k_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c,
+                                                bool& has) {
   const int count = 128 >> p.w_box_log;
   if (i >= 0 && i < count) {
     c.k_major = true, c.w_rows = false;
-    copy_seek(p, c, n0 + i * p.w_box);
     c.x = kb0 * BK;
-    c.dst = dst + static_cast<uint32_t>(i * p.w_box) * 128u;
+    if constexpr (CUT) {
+      copy_seek(p, c, n0);
+      c.row = c.y, c.piece = i, c.base = dst;
+      has = w_piece<128>(p, c);
+    } else {
+      copy_seek(p, c, n0 + i * p.w_box);
+      c.dst = dst + static_cast<uint32_t>(i * p.w_box) * 128u;
+      has = true;
+    }
   }
   return count;
 }
 // copies of W (dx): 128 output columns from n0, MN-major: two chunks of 64 columns, the 64 rows
-// of a K block in 64 / w_box copies each
-__device__ __forceinline__ int w_copies_mn_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c) {
+// of a K block in 64 / w_box copies each, or (CUT) up to as many
+template <bool CUT>
+__device__ __forceinline__ int w_copies_mn_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c,
+                                                 bool& has) {
   const int per = 64 >> p.w_box_log, count = 2 * per;
   if (i >= 0 && i < count) {
     const int chunk = i / per, sub = i - chunk * per;
     c.k_major = false, c.w_rows = true;
-    copy_seek(p, c, kb0 * BK + sub * p.w_box);
     c.x = n0 + 64 * chunk;
-    c.dst = dst + static_cast<uint32_t>(chunk) * kChunk + static_cast<uint32_t>(sub * p.w_box) * 128u;
+    dst += static_cast<uint32_t>(chunk) * kChunk;
+    if constexpr (CUT) {
+      copy_seek(p, c, kb0 * BK);
+      c.row = c.y, c.piece = sub, c.base = dst;
+      has = w_piece<BK>(p, c);
+    } else {
+      copy_seek(p, c, kb0 * BK + sub * p.w_box);
+      c.dst = dst + static_cast<uint32_t>(sub * p.w_box) * 128u;
+      has = true;
+    }
   }
   return count;
 }
 // an MN-major operand in one piece: `chunks` chunks of 64 columns from c0
-__device__ __forceinline__ int mn_copies(const CUtensorMap* map, int chunks, int i, int c0, int kb0, uint32_t dst, Copy& c) {
+__device__ __forceinline__ int mn_copies(const CUtensorMap* map, int chunks, int i, int c0, int kb0, uint32_t dst, Copy& c,
+                                         bool& has) {
   if (i >= 0 && i < chunks) {
     c.map = map, c.k_major = false, c.w_rows = false, c.shard = 0;
     c.x = c0 + 64 * i, c.y = kb0 * BK;
     c.dst = dst + static_cast<uint32_t>(i) * kChunk;
+    has = true;
   }
   return chunks;
 }
 // a K-major operand in one piece: one box of rows from r0
-__device__ __forceinline__ int k_copies(const CUtensorMap* map, int i, int r0, int kb0, uint32_t dst, Copy& c) {
-  if (i == 0) c.map = map, c.k_major = true, c.w_rows = false, c.shard = 0, c.x = kb0 * BK, c.y = r0, c.dst = dst;
+__device__ __forceinline__ int k_copies(const CUtensorMap* map, int i, int r0, int kb0, uint32_t dst, Copy& c, bool& has) {
+  if (i == 0)
+    c.map = map, c.k_major = true, c.w_rows = false, c.shard = 0, c.x = kb0 * BK, c.y = r0, c.dst = dst, has = true;
   return 1;
 }
 
@@ -466,9 +526,12 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
 // 36 % of the cycles, stalled mostly on fixed latencies), so the epilogue bounds it: 8192 x 2304
 // from 768 24.0 us bare, 30.1 with both. Sixteen epilogue warps have 112 registers and spill: 36.1.
 // Loading the next 32 sums ahead of their use needs 64 registers more than there are: 38.5.
-// FAST: every operand of a stage is one copy (W's shards of whole 128-row, dx: 64-row blocks, MN-
-// major widths of whole 64-column chunks), issued by one lane; otherwise lane i of the producer
-// warp issues the i-th of up to 18.
+// COPIES_ONE: every operand of a stage is one copy (W's shards of whole 128-row, dx: 64-row blocks,
+// MN-major widths of whole 64-column chunks), issued by one lane. COPIES_EQUAL: lane i of the
+// producer warp issues the i-th of a few; COPIES_CUT: W's shards end at multiples of 8 or 16 rows only, and
+// its copies are cut to fit (4096 x 3480 from 4096, five shards: 87 us, in equal copies of 8 rows 139; dx
+// 130 and 186; one shard 63 and 73). Where equal copies have 32 rows or more they are faster, above all
+// for dx, whose cuts change from K block to K block (4096 x 768 from 2304, eight shards: 20, cut 27).
 template <int OP> struct Wide {
   static constexpr int EPI_WARPS = OP == OP_DW ? 4 : 8;     // dw's epilogue is a scale and a store
   static constexpr int EPI_COLS = 1024 / EPI_WARPS;         // output columns of one epilogue warp
@@ -657,7 +720,8 @@ __device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* sm
   if (lane == 0) bulk_wait_group_all();             // and no store still read it
 }
 
-template <int OP, bool FAST>
+enum { COPIES_EQUAL, COPIES_ONE, COPIES_CUT };
+template <int OP, int COPIES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1)
     linear_wide_kernel(const __grid_constant__ LinearParams p) {
   using C = Wide<OP>;
@@ -708,7 +772,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
     // ---------------- producer (both CTAs) ----------------
     uint32_t it = 0, s = 0, ph = 0;  // K blocks issued; their stage and its phase parity
     bool stop = false;
-    if constexpr (FAST) {
+    if constexpr (COPIES == COPIES_ONE) {
       if (lane == 0) {
         for (int tile = pair; tile < tiles && !stop; tile += pairs) {
           int mb, nb;
@@ -746,12 +810,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
       const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
       Copy c;
       int i = lane;
-      if constexpr (A_MN) i -= mn_copies(&p.a, 2, i, m0, 0, 0, c);
-      else i -= k_copies(&p.a, i, m0, 0, 0, c);
-      if constexpr (OP == OP_FWD) i -= w_copies_k_major(p, i, n0, 0, kHalf, c);
-      else if constexpr (OP == OP_DX) i -= w_copies_mn_major(p, i, n0, 0, kHalf, c);
-      else i -= mn_copies(&p.b, 2, i, n0, 0, kHalf, c);
-      const bool mine = i < 0;
+      bool has = false;  // a copy of this K block
+      constexpr bool CUT = COPIES == COPIES_CUT;
+      if constexpr (A_MN) i -= mn_copies(&p.a, 2, i, m0, 0, 0, c, has);
+      else i -= k_copies(&p.a, i, m0, 0, 0, c, has);
+      if constexpr (OP == OP_FWD) i -= w_copies_k_major<CUT>(p, i, n0, 0, kHalf, c, has);
+      else if constexpr (OP == OP_DX) i -= w_copies_mn_major<CUT>(p, i, n0, 0, kHalf, c, has);
+      else i -= mn_copies(&p.b, 2, i, n0, 0, kHalf, c, has);
+      const bool mine = CUT && OP == OP_DX ? i < 0 : has;
       for (int kb = 0; kb < num_k; ++kb, ++it) {
         bool ok = true;
         if (it >= static_cast<uint32_t>(C::STAGES))
@@ -763,9 +829,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1
         if (rank == 0 && lane == 0)
           mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 4 * kHalf);
         if (mine) {
-          tma_load_2d_pair(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y,
-                           mapa_shared(smem_u32(&full_bar[s]), 0));
-          copy_advance(p, c);
+          if (!(CUT && OP == OP_DX) || has)
+            tma_load_2d_pair(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y,
+                             mapa_shared(smem_u32(&full_bar[s]), 0));
+          has = copy_advance<CUT>(p, c);
         }
         __syncwarp();
         if (++s == C::STAGES) s = 0, ph ^= 1u;
@@ -924,7 +991,7 @@ __device__ __forceinline__ void finish_tile(const LinearParams& p, uint8_t* smem
   });
 }
 
-template <int OP, int TN>
+template <int OP, int TN, bool CUT>
 __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_constant__ LinearParams p) {
   using C = Narrow<TN>;
   constexpr bool P_MN = OP != OP_FWD, Q_MN = OP == OP_DW;  // P: the column side, Q: the row side
@@ -968,22 +1035,24 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
   if (warp == 0) {
     Copy c;
     int i = lane;
-    if constexpr (OP == OP_FWD) i -= w_copies_k_major(p, i, n0, kb0, 0, c);
-    else if constexpr (OP == OP_DX) i -= w_copies_mn_major(p, i, n0, kb0, 0, c);
-    else i -= mn_copies(&p.b, 2, i, n0, kb0, 0, c);
-    if constexpr (Q_MN) i -= mn_copies(&p.a, TN / 64, i, m0, kb0, kHalf, c);
-    else i -= k_copies(&p.a, i, m0, kb0, kHalf, c);
-    const bool mine = i < 0;
+    bool has = false;  // a copy of this K block
+    if constexpr (OP == OP_FWD) i -= w_copies_k_major<CUT>(p, i, n0, kb0, 0, c, has);
+    else if constexpr (OP == OP_DX) i -= w_copies_mn_major<CUT>(p, i, n0, kb0, 0, c, has);
+    else i -= mn_copies(&p.b, 2, i, n0, kb0, 0, c, has);
+    if constexpr (Q_MN) i -= mn_copies(&p.a, TN / 64, i, m0, kb0, kHalf, c, has);
+    else i -= k_copies(&p.a, i, m0, kb0, kHalf, c, has);
+    const bool mine = CUT && OP == OP_DX ? i < 0 : has;
     if (mine) {
       // While the stream's earlier kernels finish: the copy's map (dW 2304 x 768 from 1024 tokens 8.5 -> 7.6
       // us), and, where W is read by one row of tiles, its first stages to L2, which an earlier kernel's
       // writes to W reach too (one token, repeated calls: 2304 from 768 4.9 -> 4.4 us, 4096 from 4096 10.0
       // -> 9.2; by sixteen rows of tiles 1003 x 1160 from 520 10.1 -> 11.1, so not there).
-      prefetch_tmap(c.map);
-      if (OP != OP_DW && gridDim.z == 1 && c.dst < kHalf) {
+      if (has) prefetch_tmap(c.map);
+      if (OP != OP_DW && gridDim.z == 1 && (!has || c.dst < kHalf)) {
         Copy ahead = c;
-        for (int kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb, copy_advance(p, ahead))
-          tma_prefetch_2d(ahead.map, ahead.x, ahead.y);
+        bool some = has;
+        for (int kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb, some = copy_advance<CUT>(p, ahead))
+          if (some) tma_prefetch_2d(ahead.map, ahead.x, ahead.y);
       }
     }
     wait_for_prior_grids();
@@ -995,8 +1064,9 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), C::STAGE);
       if (mine) {
-        tma_load_2d(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y, smem_u32(&full_bar[s]));
-        copy_advance(p, c);
+        if (!(CUT && OP == OP_DX) || has)
+          tma_load_2d(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y, smem_u32(&full_bar[s]));
+        has = copy_advance<CUT>(p, c);
       }
       __syncwarp();
       if (++s == C::STAGES) s = 0, ph ^= 1u;
@@ -1108,30 +1178,30 @@ int set_smem(OncePerDevice& once, K kernel, uint32_t bytes, const char* who) {
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 
-template <int OP, bool FAST>
+template <int OP, int COPIES>
 int launch_wide(const LinearParams& p, cudaStream_t st, const char* who) {
   using C = Wide<OP>;
   static OncePerDevice once;
-  int rc = set_smem(once, linear_wide_kernel<OP, FAST>, C::SMEM, who);
+  int rc = set_smem(once, linear_wide_kernel<OP, COPIES>, C::SMEM, who);
   if (rc) return rc;
   const int64_t tiles = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + 255) / 256);
   if (tiles > INT32_MAX / 2)
     return set_error(ZERO_ERR_UNSUPPORTED, "%s: an output of %d x %d is more than 2^30 tiles", who, p.m, p.n);
   const unsigned int pairs = static_cast<unsigned int>(std::min<int64_t>(tiles, std::max(1, num_sms() / 2)));
   const cudaError_t e =
-      launch_overlapped(linear_wide_kernel<OP, FAST>, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, 1, st, p);
+      launch_overlapped(linear_wide_kernel<OP, COPIES>, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, 1, st, p);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 
-template <int OP, int TN>
+template <int OP, int TN, bool CUT>
 int launch_narrow(const LinearParams& p, int splits, cudaStream_t st, const char* who) {
   using C = Narrow<TN>;
   static OncePerDevice once;
-  int rc = set_smem(once, linear_narrow_kernel<OP, TN>, C::SMEM, who);
+  int rc = set_smem(once, linear_narrow_kernel<OP, TN, CUT>, C::SMEM, who);
   if (rc) return rc;
   const dim3 grid(static_cast<unsigned>(splits), static_cast<unsigned>((p.n + 127) / 128),
                   static_cast<unsigned>((p.m + TN - 1) / TN));
-  const cudaError_t e = launch_overlapped(linear_narrow_kernel<OP, TN>, grid, dim3(256), C::SMEM,
+  const cudaError_t e = launch_overlapped(linear_narrow_kernel<OP, TN, CUT>, grid, dim3(256), C::SMEM,
                                           static_cast<unsigned>(splits), st, p);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
@@ -1225,22 +1295,33 @@ int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who)
     // one shard: rows past the last are zeros in any box, so it may be whole
     p.w_box = p.n_shards == 1 ? most : std::min(p.shard_rows & -p.shard_rows, most);
     for (p.w_box_log = 3; (1 << p.w_box_log) < p.w_box;) ++p.w_box_log;
+    // copies below 32 rows keep the producer behind: as many as fit in a copy of 4, 16 times the rows
+    p.w_levels = 1;
+    if (p.w_box < 32)
+      while ((p.w_levels + 1) * p.n_shards <= kGemmMaxPieces && (p.w_box << (2 * (p.w_levels - 1))) < most) ++p.w_levels;
     fast = fast && p.w_box == most && (OP == OP_FWD || p.n % 64 == 0);
     const int64_t w_cols = OP == OP_FWD ? p.k : p.n;
-    for (int s = 0; s < p.n_shards; ++s) {
-      rc = OP == OP_DX && fast ? encode_mn(&p.w[s], o.w[s], p.shard_rows, w_cols, who)
-                               : encode(&p.w[s], o.w[s], p.shard_rows, w_cols, 64, p.w_box, false, who);
+    for (int i = 0; i < p.w_levels * p.n_shards; ++i) {
+      const int s = i % p.n_shards, box = std::min(p.w_box << (2 * (i / p.n_shards)), most);
+      rc = OP == OP_DX && fast ? encode_mn(&p.w[i], o.w[s], p.shard_rows, w_cols, who)
+                               : encode(&p.w[i], o.w[s], p.shard_rows, w_cols, 64, box, false, who);
       if (rc) return rc;
     }
   }
-  if (c.wide) {
-    if (fp32 && (rc = encode(&p.out, p.y32, p.m, p.n, 32, 32, true, who))) return rc;
-    return fast ? launch_wide<OP, true>(p, st, who) : launch_wide<OP, false>(p, st, who);
-  }
+  if (c.wide && fp32 && (rc = encode(&p.out, p.y32, p.m, p.n, 32, 32, true, who))) return rc;
   if constexpr (OP != OP_DW)
-    if (c.tn == 32) return launch_narrow<OP, 32>(p, c.splits, st, who);
-  if (c.tn == 64) return launch_narrow<OP, 64>(p, c.splits, st, who);
-  return launch_narrow<OP, 128>(p, c.splits, st, who);
+    if (p.w_levels > 1) {
+      if (c.wide) return launch_wide<OP, COPIES_CUT>(p, st, who);
+      if (c.tn == 32) return launch_narrow<OP, 32, true>(p, c.splits, st, who);
+      if (c.tn == 64) return launch_narrow<OP, 64, true>(p, c.splits, st, who);
+      return launch_narrow<OP, 128, true>(p, c.splits, st, who);
+    }
+  if (c.wide)
+    return fast ? launch_wide<OP, COPIES_ONE>(p, st, who) : launch_wide<OP, COPIES_EQUAL>(p, st, who);
+  if constexpr (OP != OP_DW)
+    if (c.tn == 32) return launch_narrow<OP, 32, false>(p, c.splits, st, who);
+  if (c.tn == 64) return launch_narrow<OP, 64, false>(p, c.splits, st, who);
+  return launch_narrow<OP, 128, false>(p, c.splits, st, who);
 }
 
 int check_sizes(int64_t m, int64_t r, int64_t k, const char* who) {

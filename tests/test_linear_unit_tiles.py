@@ -27,6 +27,12 @@ SHAPES = [
     (1700, 2312, 776, 1),  # dx: 128 x 2
     (1150, 904, 5128, 1),  # 128 x 4
     (1150, 5128, 904, 1),  # dx: 128 x 4
+    # copies of W cut to the shards' ends (shards of a multiple of 8 or 16 rows)
+    (1700, 760, 2312, 5),  # 128 x 2
+    (1700, 2280, 776, 5),  # dx: 128 x 2
+    (2100, 1680, 520, 7),
+    (300, 192, 392, 8),
+    (5, 240, 1032, 6),
 ]
 
 

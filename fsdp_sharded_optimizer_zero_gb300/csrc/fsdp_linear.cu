@@ -583,6 +583,11 @@ __device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* sm
   const uint16_t* side_src = nullptr;
   if constexpr (OP != OP_DW) side_src = OP == OP_DX && p.z_in ? p.z_in : p.res;
   uint32_t i = 0, bias_turn = 0;
+  // fp32 dW: bulk stores this warp has made. The two buffers alternate over all of them, across tiles: a
+  // buffer is written again once all stores but the newest, which reads the other one, have read theirs.
+  // Counted by a tile's own columns, two stores in a row would leave from buffer 0 where a tile at the
+  // right edge has an odd number of 32-column blocks.
+  uint32_t stores = 0;
   bool stop = false;
   for (int tile = pair; tile < num_m * num_n && !stop; tile += pairs, bias_turn ^= 1u) {
     int mb, nb;
@@ -633,7 +638,7 @@ __device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* sm
           tmem_ld_32cols(taddr + c, r);
           if (c0 + c >= p.n) continue;
           const f2 s = f2_both(p.scale);
-          uint8_t* buf = stage + ((c >> 5) & 1) * 4096;
+          uint8_t* buf = stage + (stores++ & 1u) * 4096u;
           if (lane == 0) bulk_wait_group_read<1>();
           __syncwarp();
   #pragma unroll

@@ -691,13 +691,16 @@ def fsdp_linear_forward(w_shards, X, Y, bias=None, act: int = FSDP_ACT_NONE, res
 
 
 def _call_workspace(nbytes: int, device, stream):
-    """Device memory for one call on `stream`, from PyTorch's allocator; not reused before that
-    stream is done with it."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream
-                         else stream or torch.cuda.default_stream())
-    return ws
+    """Device memory for one call on `stream`, from PyTorch's allocator as that stream's own. A block of
+    the current stream's, freed in Python, may still be in use by that stream's queued work, which another
+    stream does not wait for; one of `stream`'s is reused in the order of `stream`, before and after."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def fsdp_act_backward_workspace(rows: int, cols: int) -> int:

@@ -566,6 +566,22 @@ __device__ __forceinline__ void tma_reduce_add_2d(const void* tmap, int32_t x, i
                : "memory");
 }
 
+// A barrier of 128 threads (whole warps): whether any of them says `mine`. Warps of a role meet only at
+// barriers that tell all of them when one gave up a wait, so that they leave together: one whose query of
+// the same barrier succeeded a moment later would else wait here for a warp that has left.
+__device__ __forceinline__ bool any_of_128(int id, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(mine ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
+
 // The epilogue warps' role. A thread has a row of the tile; a warp's 64-column chunk of bf16 output
 // goes through one of its staging buffers. A bf16 tensor that the epilogue reads beside the sums
 // (residual, kept activation) is loaded into the buffers before the sums are ready, and each thread
@@ -588,8 +604,9 @@ __device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* sm
   // Counted by a tile's own columns, two stores in a row would leave from buffer 0 where a tile at the
   // right edge has an odd number of 32-column blocks.
   uint32_t stores = 0;
-  bool stop = false;
-  for (int tile = pair; tile < num_m * num_n && !stop; tile += pairs, bias_turn ^= 1u) {
+  const bool shared_bias = OP == OP_FWD && p.bias;
+  bool stop = false;  // this warp gave up a wait
+  for (int tile = pair; tile < num_m * num_n && (shared_bias || !stop); tile += pairs, bias_turn ^= 1u) {
     int mb, nb;
     wide_tile_coords(tile, num_m, num_n, mb, nb);
     const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
@@ -597,15 +614,16 @@ __device__ __forceinline__ void wide_epilogue(const LinearParams& p, uint8_t* sm
     uint32_t bytes = 0;  // the row's scale bytes of four groups
     const uint4* bias = nullptr;
     if constexpr (OP == OP_FWD) {
-      if (p.bias) {
+      if (shared_bias) {
         // one warp of the four that share these 128 columns copies them; the other half of the
-        // area is the last tile's, so one barrier is enough
+        // area is the last tile's, so one barrier is enough. Every warp comes to it at every tile until
+        // all leave, one that has given up without the rest of its tile
         uint8_t* at = bias_sm + bias_turn * 512u + part * 256u;
         if (q == 0 && lane < 16) {
           const int col = c0 + 8 * lane;
           reinterpret_cast<uint4*>(at)[lane] = col < p.n ? ldg16(p.bias + col) : make_uint4(0u, 0u, 0u, 0u);
         }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+        if (any_of_128(1 + part, stop)) break;
         bias = reinterpret_cast<const uint4*>(at);
       }
     }

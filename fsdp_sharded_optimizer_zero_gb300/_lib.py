@@ -163,9 +163,24 @@ def _check(rc: int):
         raise ZeroError(rc, _lib.zero_last_error().decode(errors="replace"))
 
 
+# torch.cuda.current_device() and current_stream().cuda_stream without the objects they build and the
+# initialisation they look after (a CUDA tensor has seen to it). The names they use for it are private: a
+# PyTorch that lacks them, as one without CUDA does, takes the public way.
+def _device():
+    """Index of the current device; None where it cannot be told: no tensor is on that, and _dev refuses
+    by name."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        return None
+
+
 def _stream(stream) -> int:
-    if stream is None:  # the raw handle of torch.cuda.current_stream(), without building its object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -176,7 +191,7 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
         return None
     # the common case in a few attribute reads: a call with eight shards checks fifteen tensors
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
-            and t.get_device() == torch._C._cuda_getDevice()):
+            and t.get_device() == _device()):
         return t.data_ptr()
     if isinstance(name, tuple):  # element of a list, named only when it is refused
         name = "%s[%d]" % name
@@ -195,7 +210,7 @@ def _dev(t: torch.Tensor, dtype, name: str) -> int:
 
 
 def _ptr_array(ts, dtype, name):
-    dev = torch._C._cuda_getDevice()
+    dev = _device()
     return (C.c_void_p * len(ts))(*[
         t.data_ptr() if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.get_device() == dev
                          and t.is_contiguous())
@@ -601,9 +616,6 @@ def fsdp_unit_forward_static_scratch(w_shards, A, Y, Y_bf16=None, stream=None):
 # linear unit with its epilogue, 8-bit activation checkpoints
 # ---------------------------------------------------------------------------------------
 
-_current_device = torch._C._cuda_getDevice
-
-
 def _is(t, shape, dtype, name, dev: int):
     """Device pointer of a tensor of exactly this shape and dtype on the current device `dev` (None
     passes as NULL)."""
@@ -661,7 +673,7 @@ def fsdp_checkpoint8_pack(x, codes, scales, stream=None):
     """codes [rows, cols] int8, scales [rows, ceil(cols / 32)] uint8 = the 8-bit checkpoint of
     x [rows, cols] bf16: value = code * 2^(scale - 127)."""
     rows, cols = _rows_cols(x, "x")
-    dev = _current_device()
+    dev = _device()
     pc, ps = _kept((codes, scales), (rows, cols), "checkpoint", dev)
     _check(_lib.fsdp_checkpoint8_pack(_is(x, (rows, cols), torch.bfloat16, "x", dev), rows, cols, pc, ps, _stream(stream)))
 
@@ -669,7 +681,7 @@ def fsdp_checkpoint8_pack(x, codes, scales, stream=None):
 def fsdp_checkpoint8_unpack(codes, scales, out, act: int = FSDP_ACT_NONE, stream=None):
     """out [rows, cols] bf16 = act(values of the checkpoint)."""
     rows, cols = _rows_cols(codes, "codes")
-    dev = _current_device()
+    dev = _device()
     pc, ps = _kept((codes, scales), (rows, cols), "checkpoint", dev)
     _check(_lib.fsdp_checkpoint8_unpack(pc, ps, rows, cols, act, _is(out, (rows, cols), torch.bfloat16, "out", dev),
                                         _stream(stream)))
@@ -679,7 +691,7 @@ def fsdp_linear_forward(w_shards, X, Y, bias=None, act: int = FSDP_ACT_NONE, res
                         stream=None):
     """Y = bf16(act(X W^T + bias) + residual); z (bf16) or z8 = (codes, scales) receives the
     pre-activation X W^T + bias for the backward."""
-    dev, bf = _current_device(), torch.bfloat16
+    dev, bf = _device(), torch.bfloat16
     n, rs, k, w = _shards(w_shards, "w_shards", dev)
     m, r = _rows_cols(X, "X")[0], n * rs
     out = (m, r)
@@ -715,7 +727,7 @@ def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT
     (codes, scales). workspace: a uint8 CUDA tensor of fsdp_act_backward_workspace(...) bytes; None
     takes it from PyTorch's allocator for this call where db of a large matrix uses one."""
     rows, cols = _rows_cols(dY, "dY")
-    dev, bf = _current_device(), torch.bfloat16
+    dev, bf = _device(), torch.bfloat16
     pc, ps = _kept(z8, (rows, cols), "z8", dev)
     if workspace is None and db is not None and act and rows * cols > 1 << 24:
         nbytes = fsdp_act_backward_workspace(rows, cols)
@@ -730,7 +742,7 @@ def fsdp_act_backward(dY, dZ=None, db=None, z=None, z8=None, act: int = FSDP_ACT
 def fsdp_linear_dx(w_shards, dZ, dX, z=None, z8=None, act: int = FSDP_ACT_NONE, residual=None, stream=None):
     """dX = bf16((dZ W) act'(Z) + residual), Z (z or z8) the kept pre-activation of the layer
     that produced this layer's input."""
-    dev, bf = _current_device(), torch.bfloat16
+    dev, bf = _device(), torch.bfloat16
     n, rs, k, w = _shards(w_shards, "w_shards", dev)
     m, r = _rows_cols(dZ, "dZ")[0], n * rs
     out = (m, k)
@@ -753,7 +765,7 @@ def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, workspace=None, 
     None takes it from PyTorch's allocator for this call."""
     m, r = _rows_cols(dZ, "dZ")
     k = _rows_cols(dW, "dW")[1]
-    dev, bf = _current_device(), torch.bfloat16
+    dev, bf = _device(), torch.bfloat16
     pc, ps = _kept(x8, (m, k), "x8", dev)
     wide = dW.dtype == torch.float32
     pw = _is(dW, (r, k), torch.float32 if wide else bf, "dW", dev)

@@ -635,7 +635,7 @@ def _is(t, shape, dtype, name, dev: int):
 def _shards(ts, name: str, dev: int):
     """(count, rows of one shard, columns, pointer array) of bf16 row shards, in one pass: a call with
     eight shards spends more time here than in the library."""
-    if not ts:
+    if not len(ts):  # a list of shards, or a tensor of them
         raise ValueError(f"{name} is empty")
     shape = getattr(ts[0], "shape", ())
     if len(shape) == 2:

@@ -334,6 +334,7 @@ template <int OP>
 __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int col0, int r0, const uint4* bias,
                                            const uint4 (&side)[4], uint8_t* buf, int h, int lane, uint32_t& byte,
                                            f2 (&v)[16]) {
+  static_assert(OP != OP_DW, "a weight gradient is only scaled, by its caller");
   const size_t at = static_cast<size_t>(row) * p.n + col0;
   const bool live = row < p.m;
   bool side_is_res = p.res != nullptr;
@@ -396,7 +397,7 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = act_fwd<decltype(act)::value>(v[j]);
     });
-  } else if constexpr (OP == OP_DX) {
+  } else {
     if (p.act != FSDP_ACT_NONE) {
       f2 z[16];
       if (p.zc_in) {
@@ -415,20 +416,14 @@ __device__ __forceinline__ void epilogue32(const LinearParams& p, int row, int c
         for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], act_grad<decltype(act)::value>(z[j]));
       });
     }
-  } else {
-    const f2 s = f2_both(p.scale);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], s);
   }
-  if constexpr (OP != OP_DW) {
-    if (side_is_res || own_res) {
+  if (side_is_res || own_res) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f2 r[4];
-        unpack8(own_res ? res[q] : side[q], r);
+    for (int q = 0; q < 4; ++q) {
+      f2 r[4];
+      unpack8(own_res ? res[q] : side[q], r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
-      }
+      for (int j = 0; j < 4; ++j) v[4 * q + j] = f2_add(v[4 * q + j], r[j]);
     }
   }
 }

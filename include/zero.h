@@ -508,13 +508,18 @@ ZERO_API int fsdp_unit_forward_static_scratch(int n_ranks, const zero_bf16* cons
  * least with amax / 2^(byte - 127) < 127.5 (amax: the group's largest magnitude), kept in
  * 1..248; code = the nearest integer (ties to even) to x / 2^(byte - 127), in [-127, 127]. So
  * |x - value| <= 2^(byte - 127) / 2 <= amax / 127.5 (where 2^-127 is larger: 2^-127), and
- * every value is exact in bf16. A group that holds an infinity or a NaN has byte 255 and zero
- * codes: it reads back as NaN throughout.
+ * every value is exact in bf16. Only a magnitude past 127.5 * 2^121, which fp32 has and bf16 has
+ * not, is held to the largest value 127 * 2^121, off by less than 2^121 (byte 248). A group that
+ * holds an infinity or a NaN has byte 255 and zero codes: it reads back as NaN throughout.
  *
  * Activations: the FSDP_ACT_* values; RELU's derivative at 0 is 0, GELU is x Phi(x), GELU_TANH
- * its tanh form, SILU x / (1 + exp(-x)). They and their derivatives are computed in fp32
- * (relative error of a few 2^-20) from the fp32 sum or the kept activation, with one rounding
- * to the output's type.
+ * its tanh form, SILU x / (1 + exp(-x)). They and their derivatives are computed in fp32 from
+ * the fp32 sum or the kept activation, with one rounding to the output's type (none on the way
+ * into db). A value is x g(x), with the gate g = 1 / (1 + exp(-a)), a = x (SILU) or 1.596 x +
+ * 0.0714 x^3 (GELU_TANH), or g = Phi(x), a = x^2 / 2 (GELU). With |a| counted to 90, before that
+ * rounding a value is off by at most 2^-20 + |a| 2^-22 of itself (x >= 0: 2^-19), and a
+ * derivative, which crosses 0, by (2^-20 + |a| 2^-22) (1 + 3 |a|) g (x >= 0: 2^-17). Magnitudes
+ * below 2^-115 may be lost. RELU is exact.
  *
  * Calls take every m_tokens / rows >= 1; widths (rows_out, k_in, cols) are multiples of 8,
  * every buffer is 16-byte aligned, row-major and contiguous, and W is held as n_ranks (1..16)
@@ -543,7 +548,11 @@ ZERO_API int fsdp_checkpoint8_unpack(const int8_t* codes, const uint8_t* scales,
  * residual [m_tokens, rows_out] (nullable), Y [m_tokens, rows_out], all bf16.
  * What the backward needs of Z, optionally: z [m_tokens, rows_out] bf16, or its 8-bit
  * checkpoint z_codes / z_scales, taken from the fp32 Z (not both). The sum over k_in is an
- * fp32 sum of exact bf16 products in an unspecified order (bound as fsdp_unit_forward). */
+ * fp32 sum of exact bf16 products in an unspecified order (bound as fsdp_unit_forward), to which
+ * the tensor cores add with truncation. So a code may be one off where Z lies near the middle
+ * between two, the oftener the longer the sum: over thousands of tokens the values read back are
+ * off by 1.3e-4 of their norm at k_in 768, 3.1e-4 at 4096 and 5.9e-4 at 14336 (from a sum rounded
+ * to nearest: 0.5e-4, 1.1e-4, 1.6e-4) beside the 8e-3 that the coding itself is off by. */
 ZERO_API int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t k_in,
                                  const zero_bf16* X, int64_t m_tokens, const zero_bf16* bias, int act,
                                  const zero_bf16* residual, zero_bf16* Y, zero_bf16* z, int8_t* z_codes,
@@ -554,10 +563,11 @@ ZERO_API int fsdp_linear_forward(int n_ranks, const zero_bf16* const w_shards[],
 ZERO_API int fsdp_act_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
 
 /* Backward of the activation and the bias: dZ = bf16(dY act'(Z)), db = sum over the rows of
- * the unrounded dY act'(Z), fp32, in a fixed order (the same bits every call on one
- * device with the same sizes and choice of workspace). dY, dZ [rows, cols] bf16, dZ nullable when db is asked for;
- * db [cols] fp32, nullable. With FSDP_ACT_NONE, db is the column sum of dY. The residual's
- * gradient is dY itself. workspace: nullable, else of fsdp_act_backward_workspace() bytes. */
+ * the unrounded dY act'(Z), fp32 (each term as near as act' is, above), in a fixed order (the
+ * same bits every call on one device with the same sizes and choice of workspace). dY, dZ
+ * [rows, cols] bf16, dZ nullable when db is asked for; db [cols] fp32, nullable. With
+ * FSDP_ACT_NONE, db is the column sum of dY. The residual's gradient is dY itself. workspace:
+ * nullable, else of fsdp_act_backward_workspace() bytes. */
 ZERO_API int fsdp_act_backward(const zero_bf16* dY, const zero_bf16* z, const int8_t* z_codes, const uint8_t* z_scales,
                                int64_t rows, int64_t cols, int act, zero_bf16* dZ, float* db, void* workspace,
                                uint64_t workspace_bytes, zero_stream_t stream);

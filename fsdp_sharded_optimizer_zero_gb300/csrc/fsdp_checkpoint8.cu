@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(const uint16_t* __
   }
 }
 
-// Bound by HBM: 8192 x 14336 54 us, 6.6 TB/s; 8192 x 14344 59 us. With erf's GELU by arithmetic (its
-// polynomial): 74 us.
+// Bound by HBM: 8192 x 14336 54 us, 6.6 TB/s; 8192 x 14344 59 us. With erf's GELU by its instructions (the
+// polynomial; 70 % of the issue slots, half of the DRAM rate): 74-77 us.
 template <int ACT, bool FLAT>
 __global__ void __launch_bounds__(kThreads) ckpt8_unpack_kernel(const int8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, const WalkDims d,

@@ -513,8 +513,8 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
 //   warp 1       MMA issuer (even CTA), tensor-memory allocation
 //   then 8 (dw: 4) epilogue warps, two (one) per tensor-memory lane quarter, sharing its columns
 // What bounds it: at 8192 tokens, 14336 x 4096, tensor work at the power limit (forward with bias,
-// SiLU and 8-bit Z 512-610 us by the board's temperature, 1.58-1.88 PFLOP/s; alone and cool 505 us,
-// tensor pipe 86 % active; dx with the derivative from 8 bits 507; dW 490 us, 93 %). The pair tile
+// SiLU and 8-bit Z 512-656 us by the board's temperature, 1.47-1.88 PFLOP/s; alone and cool 505-516 us,
+// tensor pipe 86-88 % active; dx with the derivative from 8 bits 507; dW 490 us, 93-97 %, to fp32 515). The pair tile
 // is the least that an SM's reads from L2 can feed: 32 KB per 64 contraction elements, about 51
 // bytes a clock at the measured tensor rate, near the most an SM reads. At 768 contraction elements
 // a tile's products take 4 us and its epilogue up to 6 (GELU with 8-bit Z; the eight warps issue in

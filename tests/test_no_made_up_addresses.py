@@ -46,5 +46,6 @@ def test_skipped_where_there_is_a_gpu(name, others):
 
 
 def test_others_are_not():
+    assert counts(True, __file__) == (3, 0)  # whose parameters name them
     run, skipped = counts(True, "tests/test_capi_host.py", "tests/test_binding_checks.py")
     assert run > 10 and skipped == 1

@@ -39,6 +39,10 @@ EXPORTS = (
     "fsdp_checkpoint8_pack", "fsdp_checkpoint8_unpack", "fsdp_linear_forward", "fsdp_act_backward",
     "fsdp_act_backward_workspace", "fsdp_linear_dx",
     "fsdp_linear_dw", "fsdp_linear_dw_workspace",
+    "fsdp_embedding_forward", "fsdp_embedding_backward", "fsdp_embedding_backward_workspace",
+    "fsdp_layernorm_forward", "fsdp_layernorm_backward", "fsdp_layernorm_backward_workspace",
+    "fsdp_vocab_loss_forward", "fsdp_vocab_loss_forward_workspace", "fsdp_vocab_loss_backward",
+    "fsdp_vocab_loss_backward_workspace",
     "zero_last_error", "zero_device_status", "zero_selftest_bounded_wait", "zero_set_fused_kernel", "zero_set_gemm_kernel", "zero_version",
 )
 
@@ -146,6 +150,17 @@ def _load():
         "fsdp_linear_dx": (I, [I, PP, I64, I64, VP, I64, VP, VP, VP, I, VP, VP, VP]),
         "fsdp_linear_dw": (I, [VP, VP, VP, VP, I64, I64, I64, C.c_float, VP, VP, VP, U64, VP]),
         "fsdp_linear_dw_workspace": (I, [I64, I64, C.POINTER(U64)]),
+        "fsdp_embedding_forward": (I, [I, PP, I64, I64, I64, VP, I, I64, C.c_float, VP, VP]),
+        "fsdp_embedding_backward": (I, [VP, VP, I, I64, I64, I64, I64, C.c_float, I, VP, VP, VP, U64, VP]),
+        "fsdp_embedding_backward_workspace": (I, [I64, I64, I64, C.POINTER(U64)]),
+        "fsdp_layernorm_forward": (I, [VP, I64, I64, VP, VP, C.c_float, VP, VP, VP, VP]),
+        "fsdp_layernorm_backward": (I, [VP, VP, VP, VP, I64, I64, VP, VP, VP, VP, VP, VP, U64, VP]),
+        "fsdp_layernorm_backward_workspace": (I, [I64, I64, C.POINTER(U64)]),
+        "fsdp_vocab_loss_forward": (I, [I, PP, I64, I64, I64, VP, I64, VP, I, VP, VP, VP, VP, U64, VP]),
+        "fsdp_vocab_loss_forward_workspace": (I, [I64, I64, C.POINTER(U64)]),
+        "fsdp_vocab_loss_backward": (I, [I, PP, I64, I64, I64, VP, I64, VP, I, VP, VP, VP, C.c_float, VP, VP, I64, VP,
+                                         U64, VP]),
+        "fsdp_vocab_loss_backward_workspace": (I, [I64, I64, I64, I64, C.POINTER(U64)]),
         "zero_set_gemm_kernel": (I, [I]),
         "zero_version": (I, []),
     }
@@ -774,6 +789,144 @@ def fsdp_linear_dw(dZ, dW, x=None, x8=None, scale: float = 1.0, workspace=None, 
     _check(_lib.fsdp_linear_dw(_is(dZ, (m, r), bf, "dZ", dev), _is(x, (m, k), bf, "x", dev), pc, ps, m, r, k, scale,
                                pw if wide else None, None if wide else pw, _dev(workspace, torch.uint8, "workspace"),
                                0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------
+# token embedding, layer norm, loss over the vocabulary
+# ---------------------------------------------------------------------------------------
+
+def _ids(t, name: str, dev: int):
+    """(count, pointer, bytes of one) of a 1-D tensor of int32 or int64 tokens."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D tensor")
+    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be torch.int32 or torch.int64 (got {t.dtype})")
+    m = t.shape[0]
+    return m, _is(t, (m,), t.dtype, name, dev), 8 if t.dtype is torch.int64 else 4
+
+
+def _space(workspace, nbytes, device, stream):
+    """(tensor to keep, pointer, bytes) of a call's workspace: the caller's, or one taken for this call."""
+    if workspace is None:
+        workspace = _call_workspace(nbytes(), device, stream)
+    return workspace, _dev(workspace, torch.uint8, "workspace"), workspace.numel()
+
+
+def _bytes(fn, *args) -> int:
+    b = C.c_uint64()
+    _check(fn(*args, C.byref(b)))
+    return b.value
+
+
+def fsdp_embedding_forward(e_shards, tokens, Y, vocab=None, scale: float = 1.0, stream=None):
+    """Y [m, cols] = bf16(scale * E[tokens]); E as its row shards, tokens [m] int32 or int64. vocab: the
+    table's rows that are not padding (None: all); a token outside 0..vocab-1 gives zeros."""
+    dev = _device()
+    n, rs, k, e = _shards(e_shards, "e_shards", dev)
+    m, ids, width = _ids(tokens, "tokens", dev)
+    _check(_lib.fsdp_embedding_forward(n, e, n * rs, n * rs if vocab is None else vocab, k, ids, width, m, scale,
+                                       _is(Y, (m, k), torch.bfloat16, "Y", dev), _stream(stream)))
+
+
+def fsdp_embedding_backward_workspace(m_tokens: int, vocab: int, cols: int) -> int:
+    """Workspace bytes of fsdp_embedding_backward."""
+    return _bytes(_lib.fsdp_embedding_backward_workspace, m_tokens, vocab, cols)
+
+
+def fsdp_embedding_backward(dY, tokens, dE, vocab=None, scale: float = 1.0, accumulate: bool = False, workspace=None,
+                            stream=None):
+    """dE [rows, cols] (fp32 or bf16) = scale * the sums of dY's rows by their tokens, zeros in the other
+    rows; with accumulate added to what dE holds. workspace: a uint8 CUDA tensor of
+    fsdp_embedding_backward_workspace(...) bytes; None takes it from PyTorch's allocator for this call."""
+    dev = _device()
+    m, ids, width = _ids(tokens, "tokens", dev)
+    rows, k = _rows_cols(dE, "dE")
+    vocab = rows if vocab is None else vocab
+    dy = _is(dY, (m, k), torch.bfloat16, "dY", dev)
+    wide = dE.dtype == torch.float32
+    de = _is(dE, (rows, k), torch.float32 if wide else torch.bfloat16, "dE", dev)
+    workspace, ws, nbytes = _space(workspace, lambda: fsdp_embedding_backward_workspace(m, vocab, k), dY.device, stream)
+    _check(_lib.fsdp_embedding_backward(dy, ids, width, m, rows, vocab, k, scale, 1 if accumulate else 0,
+                                        de if wide else None, None if wide else de, ws, nbytes, _stream(stream)))
+
+
+def fsdp_layernorm_forward(X, Y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None, stream=None):
+    """Y = bf16((X - mean) * rstd * gamma + beta) over the columns; mean, rstd [rows] fp32 receive the
+    statistics for the backward."""
+    rows, cols = _rows_cols(X, "X")
+    dev, bf, f32 = _device(), torch.bfloat16, torch.float32
+    _check(_lib.fsdp_layernorm_forward(
+        _is(X, (rows, cols), bf, "X", dev), rows, cols, _is(gamma, (cols,), bf, "gamma", dev),
+        _is(beta, (cols,), bf, "beta", dev), eps, _is(Y, (rows, cols), bf, "Y", dev),
+        _is(mean, (rows,), f32, "mean", dev), _is(rstd, (rows,), f32, "rstd", dev), _stream(stream)))
+
+
+def fsdp_layernorm_backward_workspace(rows: int, cols: int) -> int:
+    """Workspace bytes with which fsdp_layernorm_backward sums dgamma and dbeta."""
+    return _bytes(_lib.fsdp_layernorm_backward_workspace, rows, cols)
+
+
+def fsdp_layernorm_backward(dY, X, mean, rstd, dX, gamma=None, residual=None, dgamma=None, dbeta=None, workspace=None,
+                            stream=None):
+    """dX of the layer norm (+ residual, the gradient that reaches X past it), dgamma and dbeta [cols] fp32.
+    workspace (with dgamma or dbeta): a uint8 CUDA tensor of fsdp_layernorm_backward_workspace(...)
+    bytes; None takes it from PyTorch's allocator for this call."""
+    rows, cols = _rows_cols(X, "X")
+    dev, bf, f32 = _device(), torch.bfloat16, torch.float32
+    shape = (rows, cols)
+    px = _is(X, shape, bf, "X", dev)
+    ws, nbytes = None, 0
+    if workspace is not None or dgamma is not None or dbeta is not None:
+        workspace, ws, nbytes = _space(workspace, lambda: fsdp_layernorm_backward_workspace(rows, cols), X.device, stream)
+    _check(_lib.fsdp_layernorm_backward(
+        _is(dY, shape, bf, "dY", dev), px, _is(mean, (rows,), f32, "mean", dev), _is(rstd, (rows,), f32, "rstd", dev),
+        rows, cols, _is(gamma, (cols,), bf, "gamma", dev), _is(residual, shape, bf, "residual", dev),
+        _is(dX, shape, bf, "dX", dev), _is(dgamma, (cols,), f32, "dgamma", dev), _is(dbeta, (cols,), f32, "dbeta", dev),
+        ws, nbytes, _stream(stream)))
+
+
+def fsdp_vocab_loss_forward_workspace(m_tokens: int, vocab: int) -> int:
+    """Workspace bytes of fsdp_vocab_loss_forward."""
+    return _bytes(_lib.fsdp_vocab_loss_forward_workspace, m_tokens, vocab)
+
+
+def fsdp_vocab_loss_forward(w_shards, X, labels, loss, lse, total=None, vocab=None, workspace=None, stream=None):
+    """loss [m] fp32 = the softmax cross entropy of X W^T against labels [m] (int32 or int64), lse [m] its
+    log-sum-exp, total [2] = (sum of the losses, counted tokens). W as its row shards; vocab: its rows that
+    are not padding (None: all). A label outside 0..vocab-1 is not counted and has loss 0."""
+    dev, f32 = _device(), torch.float32
+    n, rs, k, w = _shards(w_shards, "w_shards", dev)
+    m, ids, width = _ids(labels, "labels", dev)
+    vocab = n * rs if vocab is None else vocab
+    x = _is(X, (m, k), torch.bfloat16, "X", dev)
+    workspace, ws, nbytes = _space(workspace, lambda: fsdp_vocab_loss_forward_workspace(m, vocab), X.device, stream)
+    _check(_lib.fsdp_vocab_loss_forward(n, w, n * rs, vocab, k, x, m, ids, width, _is(loss, (m,), f32, "loss", dev),
+                                        _is(lse, (m,), f32, "lse", dev), _is(total, (2,), f32, "total", dev), ws, nbytes,
+                                        _stream(stream)))
+
+
+def fsdp_vocab_loss_backward_workspace(m_tokens: int, vocab: int, k_in: int, piece: int = 0) -> int:
+    """Workspace bytes of fsdp_vocab_loss_backward."""
+    return _bytes(_lib.fsdp_vocab_loss_backward_workspace, m_tokens, vocab, k_in, piece)
+
+
+def fsdp_vocab_loss_backward(w_shards, X, labels, lse, dX, dW, vocab=None, dloss=None, total=None, scale: float = 1.0,
+                             piece: int = 0, workspace=None, stream=None):
+    """dX [m, k] and dW [rows, k] (bf16; either may be None) of the sum over the counted tokens of scale *
+    dloss[i] / total[1] * loss[i]; dloss (fp32 [m]) and total (of the forward: the gradient of the mean)
+    are 1 where None. piece: columns of the vocabulary at a time (a multiple of 256; 0: chosen)."""
+    dev, bf, f32 = _device(), torch.bfloat16, torch.float32
+    n, rs, k, w = _shards(w_shards, "w_shards", dev)
+    m, ids, width = _ids(labels, "labels", dev)
+    rows = n * rs
+    vocab = rows if vocab is None else vocab
+    x = _is(X, (m, k), bf, "X", dev)
+    workspace, ws, nbytes = _space(workspace, lambda: fsdp_vocab_loss_backward_workspace(m, vocab, k, piece), X.device,
+                                   stream)
+    _check(_lib.fsdp_vocab_loss_backward(
+        n, w, rows, vocab, k, x, m, ids, width, _is(lse, (m,), f32, "lse", dev), _is(dloss, (m,), f32, "dloss", dev),
+        _is(total, (2,), f32, "total", dev), scale, _is(dX, (m, k), bf, "dX", dev), _is(dW, (rows, k), bf, "dW", dev),
+        piece, ws, nbytes, _stream(stream)))
 
 
 def zero_device_status(stream=None):

@@ -1,0 +1,534 @@
+// The loss over the vocabulary on the 5th-generation tensor cores: softmax cross entropy of the logits
+// Z = X W^T, W the output layer held as row shards, without keeping Z.
+//
+//   forward   lse_i = log sum_v exp Z_iv, loss_i = lse_i - Z_i[label]: each 256 x 256 tile of Z leaves, per
+//             row and 128 columns, its maximum and the sum of exponentials below it (2 fp32), joined after
+//   backward  in pieces of the vocabulary: Z again from X and the piece of W, dZ = (exp(Z - lse) - onehot) w
+//             in bf16, then the piece's rows of dW = dZ^T X, and dX += dZ W
+//
+// The products run in linear_wide_kernel; what is here are its epilogues and the joining passes. Softmax
+// statistics and all sums are fp32. dZ is rounded to bf16, as the gradient of a linear unit's output is
+// everywhere in the library: the tensor cores multiply bf16, and its gradients are bf16.
+#include "linear_wide.cuh"
+
+namespace zgb {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct VocabParams : LinearParams {
+  int w_row0;              // the row of W where this launch's columns (dx: contraction) begin
+  int splits, slot_rows;   // dx: parts of the contraction, each its own [slot_rows, n] of y32
+  bool add;                // dx: to what y32 holds
+  int vocab;
+  int cols, ld;            // dlogits: columns of y to write (the rest of n is none), and its row distance
+  const void* labels;
+  int labels_wide;         // 8-byte labels
+  float2* part;            // lse: [2 ceil(n / 256)][m]: base-2 maximum, sum of 2^(z log2 e - maximum)
+  float* z_label;          // lse: [m]
+  const float *lse, *dloss, *total;
+  float gscale;
+};
+
+template <> struct Wide<OP_LSE> {
+  using Params = VocabParams;
+  static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr uint32_t STAGE = 2 * kHalf, SMEM = STAGES * STAGE + 1024;
+};
+template <> struct Wide<OP_DLOGITS> {
+  using Params = VocabParams;
+  static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 5, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr uint32_t STAGE = 2 * kHalf, EPI = EPI_WARPS * 8192u, SMEM = STAGES * STAGE + EPI + 1024;
+};
+template <> struct Wide<OP_DX_SPLIT> {
+  using Params = VocabParams;
+  static constexpr int EPI_WARPS = 4, EPI_COLS = 256, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr uint32_t STAGE = 2 * kHalf, EPI = EPI_WARPS * 8192u, SMEM = STAGES * STAGE + EPI + 1024;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// label i, or -1 where it is none (outside 0 .. vocab - 1): the token is not counted
+__device__ __forceinline__ int label_at(const void* labels, int wide, int64_t i, int vocab) {
+  const int64_t t = wide ? __ldg(static_cast<const long long*>(labels) + i) : __ldg(static_cast<const int*>(labels) + i);
+  return t >= 0 && t < vocab ? static_cast<int>(t) : -1;
+}
+__device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < __int_as_float(0x7f800000) ? x : 0.0f; }
+
+// A row's running maximum (times log2 e) and sum of 2^(z log2 e - maximum). An infinite maximum is
+// subtracted as 0: -inf throughout leaves the sum 0, +inf makes it infinite, and NaN stays.
+struct Softmax {
+  float top, sum;
+  __device__ __forceinline__ void join(float top2, float sum2) {
+    const float t = max_nan(top, top2), r = finite_or_0(t);
+    const float a = sum == 0.0f ? 0.0f : __fmul_rn(sum, exp2_fast(__fsub_rn(finite_or_0(top), r)));
+    const float b = sum2 == 0.0f ? 0.0f : __fmul_rn(sum2, exp2_fast(__fsub_rn(finite_or_0(top2), r)));
+    top = t;
+    sum = __fadd_rn(a, b);
+  }
+};
+
+// The epilogue warps' role: as in the linear unit, a thread has a row of the tile and a warp 32 rows.
+template <int OP>
+__device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p, uint8_t* smem, uint32_t tmem_base,
+                                              uint32_t accf_bar, uint32_t acce_bar, volatile int* abort, int warp,
+                                              int lane, uint32_t rank, int pair, int pairs, int num_m, int num_n) {
+  using C = Wide<OP>;
+  const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
+  const int part = (warp - 2) >> 2;  // which of the quarter's warps
+  uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;  // (not OP_LSE)
+  uint32_t i = 0, stores = 0;
+  float gscale = p.gscale;
+  if (OP == OP_DLOGITS && p.total) gscale = __fdiv_rn(gscale, fmaxf(p.total[1], 1.0f));
+  const int tiles = num_m * num_n, items = wide_items<OP>(p, tiles);
+  for (int item = pair; item < items; item += pairs, ++i) {
+    const int part_k = OP == OP_DX_SPLIT ? item / tiles : 0;
+    int mb, nb;
+    wide_tile_coords(item - part_k * tiles, num_m, num_n, mb, nb);
+    const int r0 = mb * 256 + static_cast<int>(rank) * 128 + q * 32, row = r0 + lane;
+    const int c0 = nb * 256 + part * C::EPI_COLS;
+    // while the products run: the row's label, as a column of this launch
+    int target = -1;
+    bool counted = false;
+    float lse2 = 0.0f, weight = 0.0f;
+    if (OP != OP_DX_SPLIT && row < p.m) {
+      const int label = label_at(p.labels, p.labels_wide, row, p.vocab);
+      counted = label >= 0;
+      target = counted ? label - p.w_row0 : -1;
+      if (OP == OP_DLOGITS && counted) {
+        lse2 = __fmul_rn(__ldg(p.lse + row), kLog2e);
+        weight = p.dloss ? __fmul_rn(__ldg(p.dloss + row), gscale) : gscale;
+      }
+    }
+    const uint32_t a = i & 1u, u = i >> 1;
+    if (!warp_wait_bounded(accf_bar + 8u * a, u & 1u, abort, kErrAccF)) break;
+    tc_fence_after();
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
+    if constexpr (OP == OP_DX_SPLIT) {
+      if (p.y32) {
+        if (r0 < p.m) store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, 1.0f, p.add, stage, stores, lane);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < C::EPI_COLS; c += 32) {
+          const int h = (c >> 5) & 1, col0 = c0 + c;
+          uint8_t* buf = stage + ((c >> 6) & 1) * 4096;
+          if (h == 0) __syncwarp();  // the buffer's last store has read it
+          uint32_t r[32];
+          tmem_ld_32cols(taddr + c, r);
+          if (col0 >= p.n) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) =
+                make_uint4(pack_bf16x2(__uint_as_float(r[8 * j]), __uint_as_float(r[8 * j + 1])),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 2]), __uint_as_float(r[8 * j + 3])),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 4]), __uint_as_float(r[8 * j + 5])),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 6]), __uint_as_float(r[8 * j + 7])));
+          if (h == 1 || col0 + 32 >= p.n) {
+            __syncwarp();
+            stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.n, p.n, lane);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if constexpr (OP == OP_LSE) {
+      Softmax s{__int_as_float(0xff800000), 0.0f};
+#pragma unroll 1
+      for (int c = 0; c < C::EPI_COLS; c += 32) {
+        const int col0 = c0 + c;
+        uint32_t r[32];
+        tmem_ld_32cols(taddr + c, r);
+        if (col0 >= p.n) continue;  // warp-uniform
+        if (static_cast<uint32_t>(target - col0) < 32u) {
+          float z = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z = target - col0 == j ? __uint_as_float(r[j]) : z;
+          p.z_label[row] = z;
+        }
+        if (col0 + 32 > p.n) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = col0 + j < p.n ? r[j] : 0xff800000u;
+        }
+        float top = __uint_as_float(r[0]);
+#pragma unroll
+        for (int j = 1; j < 32; ++j) top = max_nan(top, __uint_as_float(r[j]));
+        top = __fmul_rn(top, kLog2e);
+        const f2 base = f2_both(-finite_or_0(top));
+        f2 sum = 0ull;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float x, y;
+          f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), base), x, y);
+          sum = f2_add(sum, f2_make(exp2_fast(x), exp2_fast(y)));
+        }
+        float x, y;
+        f2_split(sum, x, y);
+        s.join(top, __fadd_rn(x, y));
+      }
+      if (row < p.m && c0 < p.n) p.part[static_cast<size_t>(nb * 2 + part) * p.m + row] = make_float2(s.top, s.sum);
+    }
+    if constexpr (OP == OP_DLOGITS) {
+#pragma unroll 1
+      for (int c = 0; c < C::EPI_COLS; c += 32) {
+        const int h = (c >> 5) & 1, col0 = c0 + c;
+        uint8_t* buf = stage + ((c >> 6) & 1) * 4096;
+        if (h == 0) __syncwarp();  // the buffer's last store has read it
+        uint32_t r[32];
+        tmem_ld_32cols(taddr + c, r);
+        if (col0 >= p.cols) continue;  // warp-uniform
+        const bool ragged = col0 + 32 > p.n;
+        const bool hit = static_cast<uint32_t>(target - col0) < 32u;
+        uint4 w[4];
+        uint32_t* word = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float x, y;
+          f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), f2_both(-lse2)), x, y);
+          f2_split(f2_mul(f2_make(exp2_fast(x), exp2_fast(y)), f2_both(weight)), x, y);
+          if (hit) {
+            if (target - col0 == j) x = __fsub_rn(x, weight);
+            if (target - col0 == j + 1) y = __fsub_rn(y, weight);
+          }
+          if (!counted) x = y = 0.0f;  // whatever the logits are
+          if (ragged) {
+            if (col0 + j >= p.n) x = 0.0f;
+            if (col0 + j + 1 >= p.n) y = 0.0f;
+          }
+          word[j >> 1] = pack_bf16x2(x, y);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = w[j];
+        if (h == 1 || col0 + 32 >= p.cols) {
+          __syncwarp();
+          stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.cols, p.ld, lane);
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    // relaxed: the arrival only says that the tensor-memory loads are done (ordered by the fence above)
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(acce_bar + 8u * a, 0))
+                   : "memory");
+  }
+  if (lane == 0) bulk_wait_group_all();  // no store still reads shared memory
+}
+
+// lse and loss from the parts of a row: a block takes 32 rows, its warps the parts in turn
+constexpr int kThreads = 256;
+__global__ void __launch_bounds__(kThreads) join_parts_kernel(const float2* __restrict__ part, int parts, int m,
+                                                              const float* __restrict__ z_label, const void* labels, int wide,
+                                                              int vocab, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 meet[kThreads / 32][32];
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  Softmax s{__int_as_float(0xff800000), 0.0f};
+  if (row < m)
+#pragma unroll 4
+    for (int i = warp; i < parts; i += kThreads / 32) {
+      const float2 v = part[static_cast<size_t>(i) * m + row];
+      s.join(v.x, v.y);
+    }
+  meet[warp][lane] = make_float2(s.top, s.sum);
+  __syncthreads();
+  if (warp == 0 && row < m) {
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) s.join(meet[w][lane].x, meet[w][lane].y);
+    const float l = __fmul_rn(__fadd_rn(finite_or_0(s.top), log2f(s.sum)), kLn2);
+    lse[row] = l;
+    loss[row] = label_at(labels, wide, row, vocab) < 0 ? 0.0f : __fsub_rn(l, z_label[row]);
+  }
+}
+
+// total[0] = the sum of the losses, total[1] = the counted tokens, by one block in a fixed order; a thread
+// keeps what its additions round off
+__global__ void __launch_bounds__(1024) total_kernel(const float* __restrict__ loss, int m, const void* labels, int wide,
+                                                     int vocab, float* __restrict__ total) {
+  __shared__ float2 meet[32];
+  allow_next_grid();
+  wait_for_prior_grids();
+  float sum = 0.0f, lost = 0.0f;
+  int count = 0;
+  for (int64_t i = threadIdx.x; i < m; i += 1024) {
+    const float x = __fsub_rn(loss[i], lost), t = __fadd_rn(sum, x);
+    lost = __fsub_rn(__fsub_rn(t, sum), x);
+    sum = t;
+    count += label_at(labels, wide, i, vocab) >= 0 ? 1 : 0;
+  }
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+    count += __shfl_xor_sync(0xffffffffu, count, d);
+  }
+  if (lane == 0) meet[threadIdx.x >> 5] = make_float2(sum, __int_as_float(count));
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    sum = meet[lane].x, count = __float_as_int(meet[lane].y);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+      count += __shfl_xor_sync(0xffffffffu, count, d);
+    }
+    if (lane == 0) total[0] = sum, total[1] = static_cast<float>(count);
+  }
+}
+
+// dX = bf16 of the sum of `slots` parts, in order
+__global__ void __launch_bounds__(kThreads) sum_slots_kernel(const float* __restrict__ slot, int slots, int64_t slot_elems,
+                                                             int64_t n8, uint16_t* __restrict__ dx) {
+  allow_next_grid();
+  wait_for_prior_grids();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    f2 v[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 4
+    for (int s = 0; s < slots; ++s) {
+      const ulonglong2* a = reinterpret_cast<const ulonglong2*>(slot + s * slot_elems + 8 * i);
+      const ulonglong2 x = a[0], y = a[1];
+      v[0] = f2_add(v[0], x.x), v[1] = f2_add(v[1], x.y), v[2] = f2_add(v[2], y.x), v[3] = f2_add(v[3], y.y);
+    }
+    reinterpret_cast<uint4*>(dx)[i] =
+        make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------
+uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
+
+// W as the launches see it: the shards that hold rows of the vocabulary
+struct Weights {
+  int n, shard_rows;
+  const uint16_t* w[kGemmMaxPieces];
+};
+
+template <int OP>
+int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t st, const char* who) {
+  p.shard_rows = w.shard_rows;
+  p.chunks = 1, p.chunk_blocks = INT32_MAX / 2;
+  int rc;
+  if ((rc = encode_w(p, w.n, w.w, p.vocab, OP != OP_DX_SPLIT, &one_copy, who))) return rc;
+  if (p.w_levels > 1) return launch_wide<OP, COPIES_CUT>(p, st, who);
+  return one_copy ? launch_wide<OP, COPIES_ONE>(p, st, who) : launch_wide<OP, COPIES_EQUAL>(p, st, who);
+}
+
+// The backward's pieces and its workspace: dZ of a piece [m, ld], and where dX is summed in parts, those.
+// The default piece is as much of the vocabulary as a dZ of kPieceBytes holds: each piece is three launches,
+// and more of them than one share dX through memory.
+constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
+struct BackwardPlan {
+  int64_t piece, pieces, ld, slot_rows;
+  int splits;      // of dX's contraction over a piece
+  bool slots;      // dX is summed in slots, else written by the product
+  uint64_t dz_bytes, bytes;
+  BackwardPlan(int64_t m, int64_t vocab, int64_t k, int64_t asked) {
+    piece = asked;
+    if (piece == 0) {
+      const int64_t most = std::max<int64_t>(256, static_cast<int64_t>(kPieceBytes / (2 * static_cast<uint64_t>(m))) / 256 * 256);
+      const int64_t n = (vocab + most - 1) / most;
+      piece = ((vocab + n - 1) / n + 255) / 256 * 256;
+    }
+    pieces = (vocab + piece - 1) / piece;
+    ld = std::min(piece, (vocab + 63) / 64 * 64);
+    // splits: each pair of SMs takes whole (tile, part) items, so the time is the rounds times a part's K
+    // blocks, and the parts' way through memory (256 KB a tile and part, out and in, against 0.34 us a block)
+    const int64_t tiles = ((m + 255) / 256) * ((k + 255) / 256), pairs = std::max(1, num_sms() / 2);
+    const int64_t blocks = (std::min(piece, vocab) + BK - 1) / BK;
+    slot_rows = (m + 31) / 32 * 32;
+    double best = 0.0;
+    splits = 1;
+    for (int s = 1; s <= 32 && s <= blocks && s * slot_rows <= INT32_MAX; ++s) {
+      const int64_t rounds = (tiles * s + pairs - 1) / pairs;
+      const double t = static_cast<double>(rounds) * (static_cast<double>((blocks + s - 1) / s) + 4.0) +
+                       (s > 1 || pieces > 1 ? 0.25 * static_cast<double>(tiles * (s + 0.5)) + 8.0 : 0.0);
+      if (s == 1 || t < best) best = t, splits = s;
+    }
+    slots = splits > 1 || pieces > 1;
+    dz_bytes = up256(2 * static_cast<uint64_t>(m) * static_cast<uint64_t>(ld));
+    bytes = dz_bytes + (slots ? up256(4 * static_cast<uint64_t>(splits) * static_cast<uint64_t>(slot_rows) * static_cast<uint64_t>(k)) : 0);
+  }
+};
+
+int check_sizes(int64_t m, int64_t rows, int64_t vocab, int64_t k, int label_bytes, const char* who) {
+  const int64_t most = 1 << 30;
+  if (m < 1 || rows < 1 || k < 1 || m > most || rows > most || k > most)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: m_tokens, rows_out and k_in must be in 1..2^30", who);
+  if (k % 8) return set_error(ZERO_ERR_INVALID_ARG, "%s: k_in %lld must be a multiple of 8 (16-byte rows)", who, (long long)k);
+  if (vocab < 1 || vocab > rows)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: vocab %lld outside 1..%lld (the rows of W)", who, (long long)vocab, (long long)rows);
+  if (label_bytes != 4 && label_bytes != 8)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: label_bytes %d is not 4 or 8", who, label_bytes);
+  if (((m + 255) / 256) * ((vocab + 255) / 256) > (1 << 30))
+    return set_error(ZERO_ERR_UNSUPPORTED, "%s: logits of %lld x %lld are more than 2^30 tiles", who, (long long)m, (long long)vocab);
+  return ZERO_OK;
+}
+
+int check_shards(Weights* out, int n, const zero_bf16* const w_shards[], int64_t rows, int64_t vocab, const char* who) {
+  if (n < 1 || n > kGemmMaxPieces)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: n_ranks %d outside 1..%d", who, n, kGemmMaxPieces);
+  if (rows % n || (rows / n) % 8)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: rows_out / n_ranks (%lld / %d) must be a multiple of 8", who, (long long)rows, n);
+  if (!w_shards) return set_error(ZERO_ERR_INVALID_ARG, "%s: w_shards is NULL", who);
+  for (int q = 0; q < n; ++q) {
+    if (!w_shards[q]) return set_error(ZERO_ERR_INVALID_ARG, "%s: w_shards[%d] is NULL (missing rank)", who, q);
+    if (!aligned16(w_shards[q]))
+      return set_error(ZERO_ERR_INVALID_ARG, "%s: w_shards[%d] must be 16-byte aligned", who, q);
+    out->w[q] = w_shards[q];
+  }
+  out->shard_rows = static_cast<int>(rows / n);
+  out->n = static_cast<int>((vocab + out->shard_rows - 1) / out->shard_rows);
+  return ZERO_OK;
+}
+
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+
+}  // namespace
+
+unsigned int fsdp_vocab_loss_read_clear_error() {
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_zgb_dev_error, sizeof(v)) != cudaSuccess) return 0xffffffffu;
+  if (v) cudaMemcpyToSymbol(g_zgb_dev_error, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace zgb
+
+using namespace zgb;
+
+extern "C" int fsdp_vocab_loss_forward_workspace(int64_t m_tokens, int64_t vocab, uint64_t* bytes) {
+  const char* who = "fsdp_vocab_loss_forward_workspace";
+  if (!bytes) return set_error(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+  const int rc = check_sizes(m_tokens, vocab, vocab, 8, 4, who);
+  if (rc) return rc;
+  const uint64_t m = static_cast<uint64_t>(m_tokens), parts = 2 * ((static_cast<uint64_t>(vocab) + 255) / 256);
+  *bytes = up256(8 * parts * m) + up256(4 * m);
+  return ZERO_OK;
+}
+
+extern "C" int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
+                                       int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
+                                       int label_bytes, float* loss, float* lse, float* total, void* workspace,
+                                       uint64_t workspace_bytes, zero_stream_t stream) {
+  const char* who = "fsdp_vocab_loss_forward";
+  int rc;
+  if ((rc = check_sizes(m_tokens, rows_out, vocab, k_in, label_bytes, who))) return rc;
+  Weights w;
+  if ((rc = check_shards(&w, n_ranks, w_shards, rows_out, vocab, who))) return rc;
+  if (!X || !labels || !loss || !lse) return set_error(ZERO_ERR_INVALID_ARG, "%s: X, labels, loss or lse is NULL", who);
+  if (!aligned16(X) || !aligned16(workspace))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: X and workspace must be 16-byte aligned", who);
+  if (!aligned(labels, label_bytes) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(total, 4))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: labels, loss, lse and total must be aligned to their elements", who);
+  uint64_t need = 0;
+  if ((rc = fsdp_vocab_loss_forward_workspace(m_tokens, vocab, &need))) return rc;
+  if (!workspace || workspace_bytes < need)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: workspace of %llu bytes is below the %llu needed", who,
+                     workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)need);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  VocabParams p;
+  memset(static_cast<void*>(&p), 0, sizeof(p));
+  p.m = static_cast<int>(m_tokens), p.n = static_cast<int>(vocab), p.k = static_cast<int>(k_in);
+  p.vocab = p.n, p.labels = labels, p.labels_wide = label_bytes == 8;
+  const int parts = 2 * ((p.n + 255) / 256);
+  // a last tile of up to 128 columns has one part
+  const int used = parts - ((p.n + 127) / 128 % 2);
+  p.part = static_cast<float2*>(workspace);
+  p.z_label = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256(8 * static_cast<uint64_t>(parts) * p.m));
+  if ((rc = encode(&p.a, X, p.m, p.k, p.k, BK, 128, false, who))) return rc;
+  if ((rc = launch_product<OP_LSE>(p, w, true, st, who))) return rc;
+  cudaError_t e = launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>((p.m + 31) / 32)), dim3(kThreads), 0, 1, st,
+                                    p.part, used, p.m, p.z_label, labels, p.labels_wide, p.vocab, loss, lse);
+  if (e == cudaSuccess && total)
+    e = launch_overlapped(total_kernel, dim3(1), dim3(1024), 0, 1, st, loss, p.m, labels, p.labels_wide, p.vocab, total);
+  return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
+namespace {
+int check_piece(int64_t piece, const char* who) {
+  if (piece < 0 || piece % 256 || piece > (1 << 30))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: piece %lld must be 0 or a multiple of 256 up to 2^30", who, (long long)piece);
+  return ZERO_OK;
+}
+}  // namespace
+
+extern "C" int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab, int64_t k_in, int64_t piece,
+                                                  uint64_t* bytes) {
+  const char* who = "fsdp_vocab_loss_backward_workspace";
+  if (!bytes) return set_error(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+  int rc;
+  if ((rc = check_sizes(m_tokens, vocab, vocab, k_in, 4, who)) || (rc = check_piece(piece, who))) return rc;
+  *bytes = BackwardPlan(m_tokens, vocab, k_in, piece).bytes;
+  return ZERO_OK;
+}
+
+extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
+                                        int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
+                                        int label_bytes, const float* lse, const float* dloss, const float* total,
+                                        float scale, zero_bf16* dX, zero_bf16* dW, int64_t piece, void* workspace,
+                                        uint64_t workspace_bytes, zero_stream_t stream) {
+  const char* who = "fsdp_vocab_loss_backward";
+  int rc;
+  if ((rc = check_sizes(m_tokens, rows_out, vocab, k_in, label_bytes, who)) || (rc = check_piece(piece, who))) return rc;
+  Weights w;
+  if ((rc = check_shards(&w, n_ranks, w_shards, rows_out, vocab, who))) return rc;
+  if (!X || !labels || !lse) return set_error(ZERO_ERR_INVALID_ARG, "%s: X, labels or lse is NULL", who);
+  if (!dX && !dW) return set_error(ZERO_ERR_INVALID_ARG, "%s: dX and dW are both NULL", who);
+  if (!(scale - scale == 0.0f)) return set_error(ZERO_ERR_INVALID_ARG, "%s: scale must be finite", who);
+  if (!aligned16(X) || !aligned16(dX) || !aligned16(dW) || !aligned16(workspace))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: X, dX, dW and workspace must be 16-byte aligned", who);
+  if (!aligned(labels, label_bytes) || !aligned(lse, 4) || !aligned(dloss, 4) || !aligned(total, 4))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: labels, lse, dloss and total must be aligned to their elements", who);
+  const BackwardPlan plan(m_tokens, vocab, k_in, piece);
+  if (!workspace || workspace_bytes < plan.bytes)
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: workspace of %llu bytes is below the %llu needed", who,
+                     workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)plan.bytes);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint16_t* dz = static_cast<uint16_t*>(workspace);
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.dz_bytes);
+  const int m = static_cast<int>(m_tokens), k = static_cast<int>(k_in), ld = static_cast<int>(plan.ld);
+  cudaError_t e = cudaSuccess;
+  if (dW && rows_out > vocab)  // the padding's rows
+    e = cudaMemsetAsync(dW + vocab * k_in, 0, static_cast<size_t>(rows_out - vocab) * static_cast<size_t>(k_in) * 2, st);
+  if (e != cudaSuccess) return set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  for (int64_t c0 = 0; c0 < vocab; c0 += plan.piece) {
+    const int cols = static_cast<int>(std::min(plan.piece, vocab - c0));
+    VocabParams p;
+    memset(static_cast<void*>(&p), 0, sizeof(p));
+    p.m = m, p.n = cols, p.k = k;
+    p.w_row0 = static_cast<int>(c0), p.vocab = static_cast<int>(vocab);
+    p.cols = (cols + 7) / 8 * 8, p.ld = ld, p.y = dz;
+    p.labels = labels, p.labels_wide = label_bytes == 8;
+    p.lse = lse, p.dloss = dloss, p.total = total, p.gscale = scale;
+    if ((rc = encode(&p.a, X, m, k, k, BK, 128, false, who))) return rc;
+    if ((rc = launch_product<OP_DLOGITS>(p, w, true, st, who))) return rc;
+    if (dW && (rc = launch_linear_dw(dz, ld, X, m, cols, k, dW + c0 * k_in, st, who))) return rc;
+    if (!dX) continue;
+    VocabParams d;
+    memset(static_cast<void*>(&d), 0, sizeof(d));
+    d.m = m, d.n = k, d.k = cols;
+    d.w_row0 = p.w_row0, d.vocab = p.vocab;
+    // a shorter last piece may have fewer K blocks than there are parts: a part has one at least
+    d.splits = static_cast<int>(std::min<int64_t>(plan.splits, (cols + BK - 1) / BK));
+    d.slot_rows = static_cast<int>(plan.slot_rows), d.add = c0 > 0;
+    if (plan.slots) d.y32 = slots;
+    else d.y = dX;
+    if ((rc = encode(&d.a, dz, m, cols, ld, BK, 128, false, who))) return rc;
+    if (plan.slots && (rc = encode(&d.out, slots, plan.splits * plan.slot_rows, k, k, 32, 32, true, who))) return rc;
+    if ((rc = launch_product<OP_DX_SPLIT>(d, w, true, st, who))) return rc;
+  }
+  if (dX && plan.slots) {
+    const int64_t n8 = m_tokens * k_in / 8;
+    const int64_t blocks = std::min<int64_t>((n8 + kThreads - 1) / kThreads, static_cast<int64_t>(num_sms()) * 16);
+    e = launch_overlapped(sum_slots_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, 1, st, slots, plan.splits,
+                          plan.slot_rows * k_in, n8, dX);
+  }
+  return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}

@@ -180,6 +180,9 @@ unsigned int fsdp_linear_read_clear_error();
 int launch_linear_dw(const uint16_t* dZ, int64_t ldz, const uint16_t* x, int64_t m_tokens, int64_t rows_out, int64_t k_in,
                      uint16_t* dW, cudaStream_t st, const char* who);
 
+// ---- loss over the vocabulary (fsdp_vocab_loss.cu) ----
+unsigned int fsdp_vocab_loss_read_clear_error();
+
 // ---- errors (capi.cu) ----
 int set_error(int code, const char* fmt, ...);
 // Adam hyper-parameters and step validated as the step calls do (ZERO_ERR_INVALID_ARG)

@@ -596,6 +596,91 @@ ZERO_API int fsdp_linear_dw(const zero_bf16* dZ, const zero_bf16* x, const int8_
                             zero_bf16* dW_bf16, void* workspace, uint64_t workspace_bytes, zero_stream_t stream);
 
 /* ------------------------------------------------------------------------------------ */
+/* Token embedding, layer norm, loss over the vocabulary                                  */
+/* ------------------------------------------------------------------------------------ */
+/* What a language model has around its linear units. Widths (cols, k_in) are multiples of 8; bf16
+ * buffers and workspaces are 16-byte aligned, others aligned to their elements; all are row-major and
+ * contiguous. Anything else is ZERO_ERR_INVALID_ARG and launches nothing. Outputs may not overlap inputs
+ * unless it says so. Every call takes any m_tokens / rows >= 1, allocates nothing, reads no argument back
+ * to the host (it may be captured in a graph) and gives the same bits every time on one device: no
+ * atomics on floating-point values.
+ *
+ * Tokens and labels are 4- or 8-byte signed integers (token_bytes, label_bytes). One outside 0..vocab-1
+ * is none (padding, -100): its embedding is zeros and it has no gradient; it is not counted in the loss.
+ * A table or output layer [rows, k] is held as n_ranks (1..16) row shards of rows / n_ranks rows; rows
+ * from vocab on pad the shards: they are never read, and gradients give them zeros. */
+
+/* Y[i] = bf16(scale * E[tokens[i]]), [m_tokens, cols]. E [rows, cols] bf16 as its row shards. cols is at
+ * most 2^20. */
+ZERO_API int fsdp_embedding_forward(int n_ranks, const zero_bf16* const e_shards[], int64_t rows, int64_t vocab,
+                                    int64_t cols, const void* tokens, int token_bytes, int64_t m_tokens, float scale,
+                                    zero_bf16* Y, zero_stream_t stream);
+
+/* Bytes of device workspace fsdp_embedding_backward needs. */
+ZERO_API int fsdp_embedding_backward_workspace(int64_t m_tokens, int64_t vocab, int64_t cols, uint64_t* bytes);
+
+/* dE[v] = scale * sum of dY[i] over the i with tokens[i] = v: fp32 sums in a fixed order, [rows, cols] in
+ * fp32 (dE) or bf16 (dE_bf16), one of the two. Every row is written, those of no token with zeros; with
+ * accumulate (not 0) the rows of the batch's tokens are added to instead (rounded once) and the others left
+ * as they are: the gradient of a table that is also the output layer. workspace: of
+ * fsdp_embedding_backward_workspace() bytes. */
+ZERO_API int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, int token_bytes, int64_t m_tokens,
+                                     int64_t rows, int64_t vocab, int64_t cols, float scale, int accumulate, float* dE,
+                                     zero_bf16* dE_bf16, void* workspace, uint64_t workspace_bytes, zero_stream_t stream);
+
+/* Layer norm over the columns of X [rows, cols] bf16: mean = sum x / cols, rstd = 1 / sqrt(sum (x -
+ * mean)^2 / cols + eps), Y = bf16((x - mean) * rstd * gamma + beta). gamma, beta [cols] bf16, nullable (1
+ * and 0). mean, rstd [rows] fp32, what the backward needs: both or neither. eps >= 0. fp32 throughout. */
+ZERO_API int fsdp_layernorm_forward(const zero_bf16* X, int64_t rows, int64_t cols, const zero_bf16* gamma,
+                                    const zero_bf16* beta, float eps, zero_bf16* Y, float* mean, float* rstd,
+                                    zero_stream_t stream);
+
+/* Bytes of device workspace fsdp_layernorm_backward needs for dgamma and dbeta. */
+ZERO_API int fsdp_layernorm_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
+
+/* With h = (x - mean) * rstd and g = dY * gamma: dX = bf16(rstd * (g - sum g / cols - h * sum (g h) / cols) +
+ * residual), dgamma = sum over the rows of dY h, dbeta = sum over the rows of dY. dY, dX, residual [rows,
+ * cols] bf16; residual (nullable): the gradient that reaches X past the norm. dgamma, dbeta [cols] fp32,
+ * nullable; with either, workspace of fsdp_layernorm_backward_workspace() bytes (else it may be NULL). dX
+ * may be dY or residual. */
+ZERO_API int fsdp_layernorm_backward(const zero_bf16* dY, const zero_bf16* X, const float* mean, const float* rstd,
+                                     int64_t rows, int64_t cols, const zero_bf16* gamma, const zero_bf16* residual,
+                                     zero_bf16* dX, float* dgamma, float* dbeta, void* workspace,
+                                     uint64_t workspace_bytes, zero_stream_t stream);
+
+/* Bytes of device workspace fsdp_vocab_loss_forward needs: about m_tokens * vocab / 16. */
+ZERO_API int fsdp_vocab_loss_forward_workspace(int64_t m_tokens, int64_t vocab, uint64_t* bytes);
+
+/* Softmax cross entropy of the logits Z = X W^T over the first vocab rows of W, without keeping Z: lse[i] =
+ * log(sum over v of exp Z[i][v]), loss[i] = lse[i] - Z[i][labels[i]] (0 where the label is none), fp32
+ * [m_tokens]. total (nullable, 2 fp32): the sum of the losses and the number of counted tokens; their
+ * quotient is the mean loss. X [m_tokens, k_in], W [rows_out, k_in] bf16 as row shards of a multiple of 8
+ * rows. Z is an fp32 sum of exact bf16 products (bound as fsdp_unit_forward), exponentials are fp32 within
+ * 2^-21 of themselves. */
+ZERO_API int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
+                                     int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
+                                     int label_bytes, float* loss, float* lse, float* total, void* workspace,
+                                     uint64_t workspace_bytes, zero_stream_t stream);
+
+/* Bytes of device workspace fsdp_vocab_loss_backward needs: dZ of one piece, 2 * m_tokens * piece, and
+ * fp32 sums of dX where they are made in parts. piece: columns of the vocabulary at a time, a multiple of
+ * 256; 0: as many as a dZ of 2^30 bytes holds. */
+ZERO_API int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab, int64_t k_in, int64_t piece,
+                                                uint64_t* bytes);
+
+/* Gradients of sum over the counted tokens of w[i] loss[i], w[i] = scale * dloss[i] / max(total[1], 1), with
+ * dloss (fp32 [m_tokens]) and total (as the forward wrote it) nullable, then 1: dZ = (exp(Z - lse) -
+ * onehot(label)) w, computed piece by piece from X and W again and rounded to bf16; dX = bf16(dZ W)
+ * [m_tokens, k_in] and dW = bf16(dZ^T X) [rows_out, k_in], one of them nullable. A token that is not
+ * counted has zeros in dZ and dX whatever its logits, but its row of X enters dW's product, times zero: it
+ * has to be finite. The result's bits depend on piece through the rounding of fp32 sums only. */
+ZERO_API int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
+                                      int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
+                                      int label_bytes, const float* lse, const float* dloss, const float* total,
+                                      float scale, zero_bf16* dX, zero_bf16* dW, int64_t piece, void* workspace,
+                                      uint64_t workspace_bytes, zero_stream_t stream);
+
+/* ------------------------------------------------------------------------------------ */
 /* status                                                                                */
 /* ------------------------------------------------------------------------------------ */
 

@@ -4,9 +4,12 @@
 //   backward  h = (x - mean) rstd, g = dy gamma: dx = rstd (g - sum g / n - h sum (g h) / n) + residual,
 //             dgamma = sum over the rows of dy h, dbeta = sum over the rows of dy
 //
-// A row stays in registers between the passes over it: it is read once. W warps share a row, each lane
-// U pieces of 8 columns; wider rows (more than 16 warps' worth) take a block that reads them again from
-// L2. All arithmetic is fp32, every output rounded once.
+// A row stays on the SM between the passes over it: it is read once. W warps share a row, each lane U
+// pieces of 8 columns; wider rows (more than 16 warps' worth) take a block that reads them again from L2.
+// Beside HBM the issue of instructions bounds these kernels (67 % of the cycles with W at run time and a
+// row widened anew for each pass): so W and U are compile-time, rows that fill their lanes have kernels without
+// bounds (FULL), and what is widened or multiplied once stays in registers. All arithmetic is fp32, every output
+// rounded once.
 #include <algorithm>
 
 #include "linear_math.cuh"
@@ -15,8 +18,7 @@ namespace zgb {
 namespace {
 
 constexpr int kMaxWarps = 16;               // of a row held in registers
-constexpr int kMaxPieces = 4;               // of a lane
-constexpr int kWidest = kMaxWarps * kMaxPieces * 256;
+constexpr int kWidest = kMaxWarps * 4 * 256;  // columns of four pieces a lane
 constexpr int kWideThreads = 512;           // block of the kernels for wider rows
 
 __device__ __forceinline__ void widen8(const uint4& w, f2 (&x)[4]) {
@@ -40,203 +42,329 @@ __device__ __forceinline__ uint4 param8(const uint16_t* p, int64_t col, bool in,
 }
 constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 1.0
 
-// sums over the warps of a row (W consecutive warps of the block), given to all their threads
-template <int W, int N>
-struct RowSum {
-  float part[2][kMaxWarps][N];
-};
-template <int W, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], RowSum<W, N>& s, int& turn) {
+__device__ __forceinline__ float warp_sum(float v, int lanes = 32) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1)
+    if (d < lanes) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+// Two values of each warp of a row, given to the row's W warps: lane w has those of its warp w (0 past the
+// last). `turn` alternates: the half written now was last read before the barrier ahead of this one.
+template <int N>
+struct RowMeet {
+  float2 of[2][N][kMaxWarps];
+};
+template <int W, int N>
+__device__ __forceinline__ void row_meet(float (&a)[N], float (&b)[N], RowMeet<N>& s, int& turn, int first) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], d));
-  if constexpr (W > 1) {
-    const int warp = threadIdx.x >> 5, first = warp & ~(W - 1);
-    if ((threadIdx.x & 31) == 0)
+    for (int i = 0; i < N; ++i) s.of[turn][i][threadIdx.x >> 5] = make_float2(a[i], b[i]);
+  // where a block has several groups, the row's warps alone: every one of them takes as many rows
+  if constexpr (W >= 8) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + first / W), "n"(32 * W) : "memory");
 #pragma unroll
-      for (int i = 0; i < N; ++i) s.part[turn][warp][i] = v[i];
-    __syncthreads();  // the other half was last read before the barrier ahead of this one
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float t = s.part[turn][first][i];
-#pragma unroll
-      for (int w = 1; w < W; ++w) t = __fadd_rn(t, s.part[turn][first + w][i]);
-      v[i] = t;
-    }
-    turn ^= 1;
+  for (int i = 0; i < N; ++i) {
+    const float2 v = lane < W ? s.of[turn][i][first + lane] : make_float2(0.0f, 0.0f);
+    a[i] = v.x, b[i] = v.y;
   }
+  turn ^= 1;
+}
+// of lanes 0 .. 15, given to all (lanes 16 .. 31 hold zeros)
+__device__ __forceinline__ float low_lanes_sum(float v) { return __shfl_sync(0xffffffffu, warp_sum(v, kMaxWarps), 0); }
+
+// A thread's place: W warps to a row, PER rows of a block at a time; piece u of the thread's is the 8 columns from
+// col0 + 256 W u
+__host__ __device__ constexpr int rows_of_block(int w) { return w >= 8 ? 1 : 8 / w; }
+__host__ __device__ constexpr int threads_of_block(int w) { return 32 * w * rows_of_block(w); }
+template <int W>
+struct Place {
+  static constexpr int PER = rows_of_block(W), STRIDE = W * 256;
+  int first, group, col0;
+  __device__ __forceinline__ Place() {
+    const int warp = threadIdx.x >> 5;
+    group = warp / W, first = group * W;
+    col0 = ((warp - first) * 32 + (threadIdx.x & 31)) * 8;
+  }
+};
+// columns of warp w of a row; 0 past the last warp
+template <int W, int U, bool FULL>
+__device__ __forceinline__ float own_columns(int w, int cols) {
+  if (w >= W) return 0.0f;
+  if (FULL) return 256.0f * U;
+  int n = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) n += min(max(cols - (u * W + w) * 256, 0), 256);
+  return static_cast<float>(n);
 }
 
-__host__ __device__ constexpr int block_threads(int w) { return w == 16 ? 512 : 256; }
-
-template <int W, int U>
-__global__ void __launch_bounds__(block_threads(W)) norm_forward_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
-                                                            const uint16_t* __restrict__ gamma,
-                                                            const uint16_t* __restrict__ beta, float eps, float inv_n,
-                                                            uint16_t* __restrict__ y, float* __restrict__ mean,
-                                                            float* __restrict__ rstd) {
-  constexpr int PER = block_threads(W) / 32 / W;  // rows of a block at a time
-  __shared__ RowSum<W, 1> sums;
+// A block takes R rows in each of its groups of W warps: the rows' loads and reductions are in flight together,
+// and share gamma and beta.
+template <int W, int U, int R, bool FULL>
+__global__ void __launch_bounds__(threads_of_block(W), (U * R > 4 ? 768 : 1024) / threads_of_block(W)) norm_forward_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int cols, const uint16_t* __restrict__ gamma, const uint16_t* __restrict__ beta,
+    float eps, float inv_n, uint16_t* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
+  __shared__ RowMeet<R> sums;
   allow_next_grid();
-  wait_for_prior_grids();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col0 = ((warp % W) * 32 + lane) * 8;
+  const Place<W> at;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * at.PER + at.group) * R;
+  const uint16_t* xr = x + row0 * cols + at.col0;
+  const auto in = [&](int u) { return FULL || at.col0 + u * at.STRIDE < cols; };
   int turn = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * PER;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * PER; r0 < rows; r0 += step) {
-    const int64_t row = r0 + warp / W;
-    const bool there = row < rows;
-    uint4 in[U];
+  wait_for_prior_grids();
+  uint4 w[R][U];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      in[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (there && col0 + u * W * 256 < cols) in[u] = __ldcs(reinterpret_cast<const uint4*>(x + row * cols + col0 + u * W * 256));
+      w[i][u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row0 + i < rows && in(u))
+        w[i][u] = __ldcs(reinterpret_cast<const uint4*>(xr + static_cast<int64_t>(i) * cols + u * at.STRIDE));
     }
-    float s[1] = {0.0f};
+  // each warp's mean and squares about it, joined: with m_w, q_w and n_w the mean, squares and columns of warp w,
+  // the row's squares about its mean are sum q_w + n_w (m_w - mean)^2
+  const float inv_own = W == 1 ? inv_n : __fdiv_rn(1.0f, fmaxf(own_columns<W, U, FULL>((threadIdx.x >> 5) - at.first, cols), 1.0f));
+  f2 v[R][U][4];
+  float sum[R], sq[R], mu[R];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      f2 v[4];
-      widen8(in[u], v);
-      s[0] = __fadd_rn(s[0], f2_sum(f2_sum4(v)));
+  for (int i = 0; i < R; ++i) {
+    f2 t = 0ull;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {  // zeros past the row
+      widen8(w[i][u], v[i][u]);
+      t = f2_add(t, f2_sum4(v[i][u]));
     }
-    row_sum<W, 1>(s, sums, turn);
-    const float mu = __fmul_rn(s[0], inv_n);
-    s[0] = 0.0f;
+    sum[i] = f2_sum(t);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) sum[i] = warp_sum(sum[i]), mu[i] = __fmul_rn(sum[i], inv_own);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    f2 t[2] = {0ull, 0ull};
+    const f2 m = f2_both(-mu[i]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (col0 + u * W * 256 >= cols) continue;
-      f2 v[4];
-      widen8(in[u], v);
+      if (!in(u)) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = f2_add(v[j], f2_both(-mu)), v[j] = f2_mul(v[j], v[j]);
-      s[0] = __fadd_rn(s[0], f2_sum(f2_sum4(v)));
+      for (int j = 0; j < 4; ++j) {
+        const f2 c = f2_add(v[i][u][j], m);
+        t[j & 1] = f2_fma(c, c, t[j & 1]);
+      }
     }
-    row_sum<W, 1>(s, sums, turn);
-    const float r = reciprocal_root(__fadd_rn(__fmul_rn(s[0], inv_n), eps));
-    if (!there) continue;
-    if (lane == 0 && warp % W == 0 && mean) mean[row] = mu, rstd[row] = r;
+    sq[i] = f2_sum(f2_add(t[0], t[1]));
+  }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int col = col0 + u * W * 256;
-      if (col >= cols) continue;
-      f2 v[4], g[4], b[4];
-      widen8(in[u], v);
-      widen8(param8(gamma, col, true, kOnes), g);
-      widen8(param8(beta, col, true, 0u), b);
+  for (int i = 0; i < R; ++i) sq[i] = warp_sum(sq[i]);
+  if constexpr (W > 1) {
+    row_meet<W>(sum, sq, sums, turn, at.first);
+    const float theirs = own_columns<W, U, FULL>(threadIdx.x & 31, cols), inv_theirs = __fdiv_rn(1.0f, fmaxf(theirs, 1.0f));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = f2_fma(f2_mul(f2_add(v[j], f2_both(-mu)), f2_both(r)), g[j], b[j]);
-      __stcs(reinterpret_cast<uint4*>(y + row * cols + col), narrow8(v));
+    for (int i = 0; i < R; ++i) {
+      mu[i] = __fmul_rn(low_lanes_sum(sum[i]), inv_n);
+      const float off = __fsub_rn(__fmul_rn(sum[i], inv_theirs), mu[i]);
+      sq[i] = low_lanes_sum(__fmaf_rn(__fmul_rn(theirs, off), off, sq[i]));
+    }
+  }
+  float r[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    r[i] = reciprocal_root(__fadd_rn(__fmul_rn(sq[i], inv_n), eps));
+    if (at.col0 == 0 && mean && row0 + i < rows) mean[row0 + i] = mu[i], rstd[row0 + i] = r[i];
+  }
+  uint16_t* yr = y + row0 * cols + at.col0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!in(u)) continue;
+    f2 g[4], b[4];
+    widen8(param8(gamma, at.col0 + u * at.STRIDE, true, kOnes), g);
+    widen8(param8(beta, at.col0 + u * at.STRIDE, true, 0u), b);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (row0 + i >= rows) continue;
+      const f2 m = f2_both(-mu[i]), k = f2_both(r[i]);
+      f2 o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = f2_fma(f2_mul(f2_add(v[i][u][j], m), k), g[j], b[j]);
+      __stcs(reinterpret_cast<uint4*>(yr + static_cast<int64_t>(i) * cols + u * at.STRIDE), narrow8(o));
     }
   }
 }
 
-// Backward. partial: nullable, [blocks][2][cols]: a block's sums of dy h and dy over its rows.
-template <int W, int U>
-__global__ void __launch_bounds__(block_threads(W)) norm_backward_kernel(
-    const uint16_t* dy, const uint16_t* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
-    int64_t rows, int cols, const uint16_t* __restrict__ gamma, float inv_n, const uint16_t* residual, uint16_t* dx,
-    float* __restrict__ partial) {
-  constexpr int PER = block_threads(W) / 32 / W;
-  __shared__ RowSum<W, 2> sums;
-  __shared__ __align__(16) float meet[PER > 1 ? 2 * W * U * 256 : 4];
+// What a thread of the backward reads, STAGES - 1 rounds ahead of its use, through its own slots of shared memory: x,
+// dy and the residual, U pieces of 16 bytes of each for R rows, none of another thread's, so that nothing but
+// the thread's own copies is waited for.
+template <int W, int U, int R, int BLOCKS>
+struct Ahead {
+  static constexpr int THREADS = threads_of_block(W);
+  static constexpr uint32_t STAGE = 3 * U * R * 16u * THREADS;
+  static constexpr int FIT = 216 * 1024 / BLOCKS / STAGE, STAGES = FIT < 4 ? FIT : 4;
+  static_assert(STAGES >= 2, "one round in use, one on its way");
+  static constexpr uint32_t BYTES = STAGES * STAGE;
+  uint4* mine;  // this thread's slots, THREADS apart
+  __device__ __forceinline__ uint4* slot(int stage, int t, int u, int i) const {
+    return mine + (((stage * 3 + t) * U + u) * R + i) * THREADS;
+  }
+  static __device__ __forceinline__ void load(uint4* to, const uint16_t* from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16u : 0u) : "memory");
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory"); }
+};
+
+// Backward. partial: nullable, [blocks][2][cols]: a block's sums of dy h and dy over its rows. A group of W warps
+// takes R rows a round, whose reductions are in flight together. h and g are made again for the second pass: keeping
+// them takes 32 registers a row, and two rows a round are worth more (32768 x 768 with residual: one row, kept,
+// 38.6 us; two rows, kept, at half the warps 39.7; two rows, made again 36.6. 8192 x 4096: 47.2, 46.2, 46.4).
+template <int W, int U, int R, int BLOCKS, bool FULL>
+__global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
+    norm_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ x, const float* __restrict__ mean,
+                         const float* __restrict__ rstd, int64_t rows, int cols, const uint16_t* __restrict__ gamma,
+                         float inv_n, const uint16_t* residual, uint16_t* dx, float* __restrict__ partial) {
+  using Ring = Ahead<W, U, R, BLOCKS>;
+  constexpr int STAGES = Ring::STAGES, PER = Place<W>::PER, STRIDE = Place<W>::STRIDE;
+  extern __shared__ uint4 ring_mem[];
+  __shared__ RowMeet<R> sums;
   allow_next_grid();
+  const Place<W> at;
+  const Ring ring{ring_mem + threadIdx.x};
+  const auto in = [&](int u) { return FULL || at.col0 + u * STRIDE < cols; };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * PER * R, first = static_cast<int64_t>(blockIdx.x) * PER * R;
+  const auto load = [&](int64_t row0, int stage) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const bool there = row0 + i < rows;
+      const int64_t base = there ? (row0 + i) * cols + at.col0 : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool some = there && in(u);
+        const int64_t j = some ? base + u * STRIDE : 0;  // a place in the tensors, where nothing is read
+        ring.load(ring.slot(stage, 0, u, i), x + j, some);
+        ring.load(ring.slot(stage, 1, u, i), dy + j, some);
+        if (residual) ring.load(ring.slot(stage, 2, u, i), residual + j, some);
+      }
+    }
+    ring.commit();
+  };
   wait_for_prior_grids();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col0 = ((warp % W) * 32 + lane) * 8;
+  int turn = 0, stage = 0;
+  const int64_t mine = first + at.group * R;
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) load(mine + i * step, i);
   uint4 gw[U];
   f2 dg[U][4], db[U][4];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    gw[u] = param8(gamma, col0 + u * W * 256, col0 + u * W * 256 < cols, kOnes);
+    gw[u] = param8(gamma, at.col0 + u * STRIDE, in(u), kOnes);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[u][j] = db[u][j] = 0ull;
   }
-  int turn = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * PER;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * PER; r0 < rows; r0 += step) {
-    const int64_t row = r0 + warp / W;
-    const bool there = row < rows;
-    uint4 xw[U], yw[U];
+  // the rows' statistics, one round ahead
+  const auto stat = [&](const float* from, int64_t row) { return row < rows ? __ldg(from + row) : 0.0f; };
+  float next_mu[R], next_r[R];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      xw[u] = yw[u] = make_uint4(0u, 0u, 0u, 0u);
-      const int col = col0 + u * W * 256;
-      if (there && col < cols) {
-        xw[u] = __ldcs(reinterpret_cast<const uint4*>(x + row * cols + col));
-        yw[u] = __ldcs(reinterpret_cast<const uint4*>(dy + row * cols + col));
-      }
+  for (int i = 0; i < R; ++i) next_mu[i] = stat(mean, mine + i), next_r[i] = stat(rstd, mine + i);
+  for (int64_t r0 = first; r0 < rows; r0 += step) {
+    const int64_t row0 = r0 + at.group * R;
+    f2 mu[R], r[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      mu[i] = f2_both(-next_mu[i]), r[i] = f2_both(next_r[i]);
+      next_mu[i] = stat(mean, row0 + i + step), next_r[i] = stat(rstd, row0 + i + step);
     }
-    const float mu = there ? mean[row] : 0.0f, r = there ? rstd[row] : 0.0f;
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (col0 + u * W * 256 >= cols) continue;
-      f2 h[4], g[4], d[4];
-      widen8(xw[u], h);
-      widen8(yw[u], d);
+    load(row0 + (STAGES - 1) * step, (stage + STAGES - 1) % STAGES);
+    ring.wait();
+    float s0[R], s1[R];
+    // h and g of piece u of row i; returns dy
+    const auto make = [&](int u, int i, f2 (&h)[4], f2 (&g)[4], f2 (&d)[4]) {
+      widen8(*ring.slot(stage, 0, u, i), h);
+      widen8(*ring.slot(stage, 1, u, i), d);
       widen8(gw[u], g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = f2_mul(f2_add(h[j], f2_both(-mu)), f2_both(r));
-        dg[u][j] = f2_fma(d[j], h[j], dg[u][j]);
-        db[u][j] = f2_add(db[u][j], d[j]);
-        g[j] = f2_mul(g[j], d[j]);
-        h[j] = f2_mul(g[j], h[j]);
-      }
-      s[0] = __fadd_rn(s[0], f2_sum(f2_sum4(g)));
-      s[1] = __fadd_rn(s[1], f2_sum(f2_sum4(h)));
-    }
-    row_sum<W, 2>(s, sums, turn);
-    if (!there) continue;
-    const f2 a = f2_both(__fmul_rn(s[0], inv_n)), b = f2_both(-__fmul_rn(s[1], inv_n));
+      for (int j = 0; j < 4; ++j) h[j] = f2_mul(f2_add(h[j], mu[i]), r[i]), g[j] = f2_mul(g[j], d[j]);
+    };
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int col = col0 + u * W * 256;
-      if (col >= cols) continue;
-      f2 h[4], g[4], d[4], e[4];
-      widen8(xw[u], h);
-      widen8(yw[u], d);
-      widen8(gw[u], g);
-      const uint4 rw = residual ? __ldcs(reinterpret_cast<const uint4*>(residual + row * cols + col)) : make_uint4(0u, 0u, 0u, 0u);
-      widen8(rw, e);
+    for (int i = 0; i < R; ++i) {
+      f2 t0 = 0ull, t1 = 0ull;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = f2_mul(f2_add(h[j], f2_both(-mu)), f2_both(r));
-        const f2 t = f2_fma(h[j], b, f2_add(f2_mul(g[j], d[j]), f2_mul(a, f2_both(-1.0f))));
-        e[j] = residual ? f2_fma(t, f2_both(r), e[j]) : f2_mul(t, f2_both(r));
+      for (int u = 0; u < U; ++u) {
+        f2 h[4], g[4], d[4];
+        make(u, i, h, g, d);
+        // past the row (and the rows) dy is 0, and so is its part in each sum
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dg[u][j] = f2_fma(d[j], h[j], dg[u][j]);
+          db[u][j] = f2_add(db[u][j], d[j]);
+          t1 = f2_fma(g[j], h[j], t1);
+        }
+        t0 = f2_add(t0, f2_sum4(g));
       }
-      __stcs(reinterpret_cast<uint4*>(dx + row * cols + col), narrow8(e));
+      s0[i] = f2_sum(t0), s1[i] = f2_sum(t1);
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i) s0[i] = warp_sum(s0[i]), s1[i] = warp_sum(s1[i]);
+    if constexpr (W > 1) {
+      row_meet<W>(s0, s1, sums, turn, at.first);
+#pragma unroll
+      for (int i = 0; i < R; ++i) s0[i] = low_lanes_sum(s0[i]), s1[i] = low_lanes_sum(s1[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (row0 + i >= rows) continue;
+      const f2 a = f2_both(-__fmul_rn(s0[i], inv_n)), b = f2_both(-__fmul_rn(s1[i], inv_n));
+      uint16_t* to = dx + (row0 + i) * cols + at.col0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!in(u)) continue;
+        f2 h[4], g[4], d[4], t[4];
+        make(u, i, h, g, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = f2_fma(h[j], b, f2_add(g[j], a));
+        if (residual) {
+          f2 e[4];
+          widen8(*ring.slot(stage, 2, u, i), e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[j] = f2_fma(t[j], r[i], e[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[j] = f2_mul(t[j], r[i]);
+        }
+        __stcs(reinterpret_cast<uint4*>(to + u * STRIDE), narrow8(t));
+      }
+    }
+    stage = (stage + 1) % STAGES;
   }
   if (!partial) return;
-  // the block's row groups meet in shared memory, one after the other
+  asm volatile("cp.async.wait_all;" ::: "memory");
   float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
   if constexpr (PER > 1) {
-    constexpr int WIDTH = W * U * 256;
+    // the block's row groups meet in the ring's memory, one after the other
+    constexpr int WIDTH = U * STRIDE;
+    static_assert(2 * WIDTH * 4 <= Ring::BYTES, "the sums take the ring's place");
+    float* meet = reinterpret_cast<float*>(ring_mem);
+    __syncthreads();
     for (int g = 0; g < PER; ++g) {
-      if (warp / W == g) {
+      if (at.group == g) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            f2* a = reinterpret_cast<f2*>(meet + col0 + u * W * 256) + j;
-            f2* b = reinterpret_cast<f2*>(meet + WIDTH + col0 + u * W * 256) + j;
+            f2* a = reinterpret_cast<f2*>(meet + at.col0 + u * STRIDE) + j;
+            f2* b = reinterpret_cast<f2*>(meet + WIDTH + at.col0 + u * STRIDE) + j;
             *a = g == 0 ? dg[u][j] : f2_add(*a, dg[u][j]);
             *b = g == 0 ? db[u][j] : f2_add(*b, db[u][j]);
           }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x * 4; c < cols; c += blockDim.x * 4) {
+    for (int c = threadIdx.x * 4; c < cols; c += static_cast<int>(blockDim.x) * 4) {
       *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(meet + c);
       *reinterpret_cast<float4*>(out + cols + c) = *reinterpret_cast<const float4*>(meet + WIDTH + c);
     }
   } else {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int col = col0 + u * W * 256;
-      if (col >= cols) continue;
+      if (!in(u)) continue;
+      const int col = at.col0 + u * STRIDE;
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
         *reinterpret_cast<ulonglong2*>(out + col + 2 * j) = make_ulonglong2(dg[u][j], dg[u][j + 1]);
@@ -247,18 +375,18 @@ __global__ void __launch_bounds__(block_threads(W)) norm_backward_kernel(
 }
 
 // dgamma, dbeta = the sums of `parts` partial sums a column: a block takes 32 of the 2 cols columns, 4 a
-// thread; 32 threads share a column (thread y the partials y, y + 32, ..) and are added in order
-__global__ void __launch_bounds__(256) norm_params_kernel(const float* __restrict__ partial, int parts, int64_t cols,
+// thread; 64 threads share a column (thread y the partials y, y + 64, ..) and are added in order
+__global__ void __launch_bounds__(512) norm_params_kernel(const float* __restrict__ partial, int parts, int64_t cols,
                                                           float* __restrict__ dgamma, float* __restrict__ dbeta) {
-  __shared__ float part[32][33];
+  __shared__ float part[64][33];
   allow_next_grid();
   wait_for_prior_grids();
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 32, col = col0 + x * 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < 2 * cols) {
-#pragma unroll 4
-    for (int l = y; l < parts; l += 32) {
+#pragma unroll 8
+    for (int l = y; l < parts; l += 64) {
       const float4 v = *reinterpret_cast<const float4*>(partial + l * 2 * cols + col);
       s.x = __fadd_rn(s.x, v.x), s.y = __fadd_rn(s.y, v.y), s.z = __fadd_rn(s.z, v.z), s.w = __fadd_rn(s.w, v.w);
     }
@@ -269,7 +397,7 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const float* __restric
   if (threadIdx.x < 32 && c < 2 * cols) {
     float t = part[0][threadIdx.x];
 #pragma unroll
-    for (int l = 1; l < 32; ++l) t = __fadd_rn(t, part[l][threadIdx.x]);
+    for (int l = 1; l < 64; ++l) t = __fadd_rn(t, part[l][threadIdx.x]);
     float* out = c < cols ? dgamma : dbeta;
     if (out) out[c < cols ? c : c - cols] = t;
   }
@@ -412,56 +540,75 @@ __global__ void __launch_bounds__(256) norm_columns_wide_kernel(const uint16_t* 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-// Warps of a row (0: wider than the registers) and pieces of a lane. The fewest warps whose lanes hold the
-// row in kMaxPieces pieces, so that most rows' sums stay inside a warp; more where there are few rows.
+// f(integral constants W, U) for rows of P pieces of 256 columns
+template <int W, int U>
 struct Shape {
-  int warps, pieces;
+  static constexpr int warps = W, pieces = U;
 };
-Shape shape_of(int64_t rows, int64_t cols) {
-  if (cols > kWidest) return {0, 0};
-  int w = 1;
-  while (w * kMaxPieces * 256 < cols) w *= 2;
-  const int64_t warps = static_cast<int64_t>(num_sms()) * 16;
-  while (w < kMaxWarps && w * 256 < cols && rows * w * 2 <= warps) w *= 2;
-  return {w, static_cast<int>((cols + w * 256 - 1) / (w * 256))};
+int pieces_of(int64_t cols) { return static_cast<int>((cols + 255) / 256); }
+bool few_rows(int64_t rows, int64_t cols) { return rows * pieces_of(cols) <= static_cast<int64_t>(num_sms()) * 16; }
+// forward: two or three pieces a lane; one where there are few rows, whose latency counts
+template <class F>
+auto with_forward_shape(int64_t rows, int64_t cols, F&& f) {
+  const int p = pieces_of(cols);
+  if (few_rows(rows, cols)) {
+    if (p <= 1) return f(Shape<1, 1>{});
+    if (p <= 4) return f(Shape<4, 1>{});
+    if (p <= 8) return f(Shape<8, 1>{});
+    if (p <= 16) return f(Shape<16, 1>{});
+  }
+  if (p <= 1) return f(Shape<1, 1>{});
+  if (p <= 2) return f(Shape<1, 2>{});
+  if (p <= 3) return f(Shape<1, 3>{});
+  if (p <= 4) return f(Shape<2, 2>{});
+  if (p <= 6) return f(Shape<2, 3>{});
+  if (p <= 8) return f(Shape<4, 2>{});
+  if (p <= 9) return f(Shape<3, 3>{});
+  if (p <= 12) return f(Shape<4, 3>{});
+  if (p <= 16) return f(Shape<8, 2>{});
+  if (p <= 24) return f(Shape<8, 3>{});
+  if (p <= 32) return f(Shape<8, 4>{});
+  if (p <= 48) return f(Shape<16, 3>{});
+  return f(Shape<16, 4>{});
 }
-int64_t rows_at_once(int w) { return block_threads(w) / 32 / w; }
+// backward: two pieces a lane and rounds of two rows, as far as sixteen warps reach; 512 threads on an SM
+template <int W, int U>
+struct BackwardShape {
+  static constexpr int warps = W, pieces = U, rows = U <= 2 ? 2 : 1;
+  static constexpr int blocks = threads_of_block(W) > 256 ? 1 : 512 / threads_of_block(W);
+};
+template <class F>
+auto with_backward_shape(int64_t cols, F&& f) {
+  const int p = pieces_of(cols);
+  if (p <= 1) return f(BackwardShape<1, 1>{});
+  if (p <= 2) return f(BackwardShape<1, 2>{});
+  if (p <= 4) return f(BackwardShape<2, 2>{});
+  if (p <= 6) return f(BackwardShape<3, 2>{});
+  if (p <= 8) return f(BackwardShape<4, 2>{});
+  if (p <= 10) return f(BackwardShape<5, 2>{});
+  if (p <= 12) return f(BackwardShape<6, 2>{});
+  if (p <= 16) return f(BackwardShape<8, 2>{});
+  if (p <= 20) return f(BackwardShape<10, 2>{});
+  if (p <= 24) return f(BackwardShape<12, 2>{});
+  if (p <= 32) return f(BackwardShape<16, 2>{});
+  if (p <= 48) return f(BackwardShape<16, 3>{});
+  return f(BackwardShape<16, 4>{});
+}
 
 // blocks of the backward kernel, and so partial sums a column
-constexpr int kBackwardBlocks = 2;  // per SM
-int backward_blocks(int64_t rows, int64_t cols) {
-  const Shape s = shape_of(rows, cols);
-  const int64_t most = static_cast<int64_t>(num_sms()) * kBackwardBlocks;
-  if (s.warps == 0) return static_cast<int>(std::min<int64_t>(rows, 64));
-  const int64_t per = rows_at_once(s.warps);
-  return static_cast<int>(std::min<int64_t>((rows + per - 1) / per, s.warps == 16 ? most / 2 : most));
-}
-
-// f(integral constants W, U)
-template <int W, class F>
-cudaError_t with_pieces(int pieces, F&& f) {
-  switch (pieces) {
-    case 1: return f(ActTag<W>{}, ActTag<1>{});
-    case 2: return f(ActTag<W>{}, ActTag<2>{});
-    case 3: return f(ActTag<W>{}, ActTag<3>{});
-    default: return f(ActTag<W>{}, ActTag<4>{});
-  }
-}
-template <class F>
-cudaError_t with_shape(const Shape& s, F&& f) {
-  switch (s.warps) {
-    case 1: return with_pieces<1>(s.pieces, f);
-    case 2: return with_pieces<2>(s.pieces, f);
-    case 4: return with_pieces<4>(s.pieces, f);
-    case 8: return with_pieces<8>(s.pieces, f);
-    default: return with_pieces<16>(s.pieces, f);
-  }
+int64_t backward_blocks(int64_t rows, int64_t cols) {
+  if (cols > kWidest) return std::min<int64_t>(rows, 64);
+  return with_backward_shape(cols, [&](auto shape) {
+    using S = decltype(shape);
+    constexpr int PER = rows_of_block(S::warps) * S::rows;
+    return std::min<int64_t>((rows + PER - 1) / PER, static_cast<int64_t>(num_sms()) * S::blocks);
+  });
 }
 
 int check_shape(int64_t rows, int64_t cols, const char* who) {
-  if (rows < 1 || cols < 1 || rows > (int64_t(1) << 40) || cols > (1 << 30) || rows > (int64_t(1) << 61) / cols)
-    return set_error(ZERO_ERR_INVALID_ARG, "%s: rows %lld and cols %lld must be >= 1 (at most 2^40 and 2^30)", who,
-                     (long long)rows, (long long)cols);
+  if (rows < 1 || cols < 1 || rows > (1 << 30) || cols > (1 << 30))
+    return set_error(ZERO_ERR_INVALID_ARG, "%s: rows %lld and cols %lld must be in 1..2^30", who, (long long)rows,
+                     (long long)cols);
   if (cols % 8)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: cols %lld must be a multiple of 8 (16-byte rows)", who, (long long)cols);
   return ZERO_OK;
@@ -489,19 +636,17 @@ extern "C" int fsdp_layernorm_forward(const zero_bf16* X, int64_t rows, int64_t 
     return set_error(ZERO_ERR_INVALID_ARG, "%s: mean and rstd must be 4-byte aligned", who);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const float inv_n = 1.0f / static_cast<float>(cols);
-  const Shape s = shape_of(rows, cols);
   cudaError_t e;
-  if (s.warps == 0) {
+  if (cols > kWidest) {
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * 4));
     e = launch_overlapped(norm_forward_wide_kernel, dim3(grid), dim3(kWideThreads), 0, 1, st, X, rows, cols, gamma, beta,
                           eps, inv_n, Y, mean, rstd);
   } else {
-    const int64_t per = rows_at_once(s.warps);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((rows + per - 1) / per, static_cast<int64_t>(num_sms()) * 64));
-    e = with_shape(s, [&](auto w, auto u) {
-      constexpr int W = decltype(w)::value, U = decltype(u)::value;
-      return launch_overlapped(norm_forward_kernel<W, U>, dim3(grid), dim3(block_threads(W)), 0, 1, st, X, rows,
-                               static_cast<int>(cols), gamma, beta, eps, inv_n, Y, mean, rstd);
+    e = with_forward_shape(rows, cols, [&](auto shape) {
+      constexpr int W = decltype(shape)::warps, U = decltype(shape)::pieces, R = (U == 1 && W > 1) || U == 4 || W == 16 ? 1 : 2, PER = rows_of_block(W) * R;
+      const auto kernel = cols == W * U * 256 ? norm_forward_kernel<W, U, R, true> : norm_forward_kernel<W, U, R, false>;
+      return launch_overlapped(kernel, dim3(static_cast<unsigned>((rows + PER - 1) / PER)), dim3(threads_of_block(W)), 0, 1, st, X,
+                               rows, static_cast<int>(cols), gamma, beta, eps, inv_n, Y, mean, rstd);
     });
   }
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
@@ -542,26 +687,38 @@ extern "C" int fsdp_layernorm_backward(const zero_bf16* dY, const zero_bf16* X, 
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const float inv_n = 1.0f / static_cast<float>(cols);
-  const Shape s = shape_of(rows, cols);
-  const int blocks = backward_blocks(rows, cols);
+  const int64_t blocks = backward_blocks(rows, cols);
   cudaError_t e = cudaSuccess;
-  if (s.warps == 0) {
+  if (cols > kWidest) {
     if (params)  // before dX, which may be dY
-      e = launch_overlapped(norm_columns_wide_kernel, dim3(static_cast<unsigned>((cols + 2047) / 2048), blocks), dim3(256), 0,
-                            1, st, dY, X, mean, rstd, rows, cols, partial);
+      e = launch_overlapped(norm_columns_wide_kernel,
+                            dim3(static_cast<unsigned>((cols + 2047) / 2048), static_cast<unsigned>(blocks)), dim3(256), 0, 1, st,
+                            dY, X, mean, rstd, rows, cols, partial);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * 4));
     if (e == cudaSuccess)
       e = launch_overlapped(norm_backward_wide_kernel, dim3(grid), dim3(kWideThreads), 0, 1, st, dY, X, mean, rstd, rows,
                             cols, gamma, inv_n, residual, dX);
   } else {
-    e = with_shape(s, [&](auto w, auto u) {
-      constexpr int W = decltype(w)::value, U = decltype(u)::value;
-      return launch_overlapped(norm_backward_kernel<W, U>, dim3(static_cast<unsigned>(blocks)), dim3(block_threads(W)), 0, 1,
-                               st, dY, X, mean, rstd, rows, static_cast<int>(cols), gamma, inv_n, residual, dX, partial);
+    e = with_backward_shape(cols, [&](auto shape) {
+      using S = decltype(shape);
+      constexpr int W = S::warps, U = S::pieces, R = S::rows;
+      constexpr uint32_t smem = Ahead<W, U, R, S::blocks>::BYTES;
+      static OncePerDevice once[2];
+      const bool full = cols == W * U * 256;
+      const auto kernel = full ? norm_backward_kernel<W, U, R, S::blocks, true> : norm_backward_kernel<W, U, R, S::blocks, false>;
+      int dev = 0;
+      cudaError_t q = cudaGetDevice(&dev);
+      if (q == cudaSuccess)
+        q = once[full].run(dev, [&] {
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        });
+      if (q != cudaSuccess) return q;
+      return launch_overlapped(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads_of_block(W)), smem, 1, st, dY, X, mean,
+                               rstd, rows, static_cast<int>(cols), gamma, inv_n, residual, dX, partial);
     });
   }
   if (e == cudaSuccess && params)
-    e = launch_overlapped(norm_params_kernel, dim3(static_cast<unsigned>((2 * cols + 31) / 32)), dim3(256), 0, 1, st, partial,
-                          blocks, cols, dgamma, dbeta);
+    e = launch_overlapped(norm_params_kernel, dim3(static_cast<unsigned>((2 * cols + 31) / 32)), dim3(512), 0, 1, st, partial,
+                          static_cast<int>(blocks), cols, dgamma, dbeta);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }

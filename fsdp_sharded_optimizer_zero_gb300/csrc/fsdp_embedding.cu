@@ -230,10 +230,11 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const SortPass p
 // ------------------------------------------------------------------------------------
 // sums over the ordered positions
 // ------------------------------------------------------------------------------------
-// A warp takes a run of kRun ordered positions and 256 columns. The stretches of one token that lie inside
+// A warp takes a run of RUN ordered positions and 256 columns. The stretches of one token that lie inside
 // the run are finished; the one that goes on at its end (and came from ahead or not) leaves its fp32 sum in
 // `open`, slot 1, and one that came from ahead and ends here in slot 0.
-constexpr int kRun = 32;
+constexpr int kShortRun = 16, kLongRun = 32;
+int run_of(int64_t m) { return m <= kRankMost ? kShortRun : kLongRun; }
 struct SumArgs {
   Sorted s;
   int64_t m;
@@ -270,14 +271,15 @@ __device__ __forceinline__ void put_row(const SumArgs& p, int key, int64_t col, 
   }
 }
 
+template <int RUN>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(const SumArgs p) {
   allow_next_grid();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31;
-  const int64_t runs = (p.m + kRun - 1) / kRun, items = runs * p.slices, step = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t runs = (p.m + RUN - 1) / RUN, items = runs * p.slices, step = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items; item += step) {
-    const int64_t run = item / p.slices, col = (item - run * p.slices) * 256 + lane * 8, first = run * kRun;
-    const int count = static_cast<int>(min(p.m - first, static_cast<int64_t>(kRun)));
+    const int64_t run = item / p.slices, col = (item - run * p.slices) * 256 + lane * 8, first = run * RUN;
+    const int count = static_cast<int>(min(p.m - first, static_cast<int64_t>(RUN)));
     const int key = lane < count ? p.s.key[first + lane] : kNone;
     const int at = lane < count ? p.s.order[first + lane] : 0;
     const int before = first > 0 ? p.s.key[first - 1] : -1, after = first + count < p.m ? p.s.key[first + count] : -1;
@@ -292,7 +294,8 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(const SumArgs p) {
         to[0] = make_ulonglong2(sum[0], sum[1]), to[1] = make_ulonglong2(sum[2], sum[3]);
       }
     };
-    constexpr int AHEAD = 8;
+    // all rows of the run are on their way before the first is used
+    constexpr int AHEAD = RUN < 16 ? RUN : 16;
     for (int j0 = 0; j0 < count && now != kNone; j0 += AHEAD) {
       uint4 w[AHEAD];
 #pragma unroll
@@ -312,9 +315,8 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(const SumArgs p) {
         }
         f2 v[4];
         widen8(w[j], v);
-        if (j0 + j < count)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[i] = f2_add(sum[i], v[i]);
+        for (int i = 0; i < 4; ++i) sum[i] = f2_add(sum[i], v[i]);  // zeros past the run
       }
     }
     if (now == kNone) continue;
@@ -326,29 +328,30 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(const SumArgs p) {
 
 // The tokens whose stretch crosses from one run into the next: a block takes a boundary where a stretch
 // crosses for the first time and 256 columns, its warps consecutive parts of the runs it touches.
+template <int RUN>
 __global__ void __launch_bounds__(kThreads) sum_crossing_kernel(const SumArgs p) {
   __shared__ f2 part[kWarps][32][4];
   allow_next_grid();
   wait_for_prior_grids();
-  const int64_t b = blockIdx.x + 1, first = b * kRun;  // between runs b - 1 and b
-  const int key = p.s.key[first];
-  if (key == kNone || p.s.key[first - 1] != key) return;
-  if (b > 1 && p.s.key[first - kRun - 1] == key) return;  // it crossed before
-  // the last run it touches: keys are in order
-  int64_t lo = b, hi = (p.m - 1) / kRun;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) / 2;
-    if (p.s.key[mid * kRun] == key) lo = mid;
-    else hi = mid - 1;
+  const int64_t b = blockIdx.x + 1, first = b * RUN, runs = (p.m + RUN - 1) / RUN;  // between runs b - 1 and b
+  const int key = p.s.key[first], before = p.s.key[first - 1], earlier = b > 1 ? p.s.key[first - RUN - 1] : -1;
+  // which of the next runs begin with the key, 256 at a time: keys are in order
+  int64_t last = b;
+  for (int64_t r0 = b + 1;; r0 += kThreads) {
+    const int64_t r = r0 + threadIdx.x;
+    const bool same = r < runs && p.s.key[r * RUN] == key;
+    if (r0 == b + 1 && (key == kNone || before != key || earlier == key)) return;  // none crosses here, or crossed before
+    const int n = __syncthreads_count(same);
+    last += n;
+    if (n < kThreads) break;
   }
-  const int64_t last = lo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
   const bool in = col < p.cols;
   const int64_t parts = last - b + 2, from = b - 1 + parts * warp / kWarps, to = b - 1 + parts * (warp + 1) / kWarps;
   f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
   if (in)
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t r = from; r < to; ++r) {
       // it goes on behind every run but the last, where it left its sum as one that ends there
       const ulonglong2* a = reinterpret_cast<const ulonglong2*>(p.open + (r * 2 + (r < last ? 1 : 0)) * p.cols + col);
@@ -410,7 +413,7 @@ struct BackwardSpace {
       if (passes > 1) key[1] = take(4 * static_cast<uint64_t>(m)), order[1] = take(4 * static_cast<uint64_t>(m));
       count = take(4 * static_cast<uint64_t>(sort_blocks) * kDigits);
     }
-    open = take(8 * static_cast<uint64_t>((m + kRun - 1) / kRun) * static_cast<uint64_t>(cols));
+    open = take(8 * static_cast<uint64_t>((m + run_of(m) - 1) / run_of(m)) * static_cast<uint64_t>(cols));
   }
 };
 
@@ -510,16 +513,18 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
         e = launch_overlapped(sort_scatter_kernel, dim3(static_cast<unsigned>(sp.sort_blocks)), dim3(kThreads), 0, 1, st, p);
     }
   }
-  const int64_t runs = (m_tokens + kRun - 1) / kRun, slices = (cols + 255) / 256;
+  const int run = run_of(m_tokens);
+  const int64_t runs = (m_tokens + run - 1) / run, slices = (cols + 255) / 256;
   SumArgs a;
   a.s = sorted, a.m = m_tokens, a.dy = dY, a.cols = cols, a.slices = static_cast<int>(slices), a.scale = scale;
   a.de32 = dE, a.de16 = dE_bf16, a.add = accumulate != 0, a.open = reinterpret_cast<float*>(ws + sp.open);
   if (e == cudaSuccess) {
     const int64_t blocks = std::min<int64_t>((runs * slices + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms()) * 64);
-    e = launch_overlapped(sum_runs_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, 1, st, a);
+    e = launch_overlapped(run == kShortRun ? sum_runs_kernel<kShortRun> : sum_runs_kernel<kLongRun>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, 1, st, a);
   }
   if (e == cudaSuccess && runs > 1)
-    e = launch_overlapped(sum_crossing_kernel, dim3(static_cast<unsigned>(runs - 1), static_cast<unsigned>(slices)), dim3(kThreads),
+    e = launch_overlapped(run == kShortRun ? sum_crossing_kernel<kShortRun> : sum_crossing_kernel<kLongRun>,
+                          dim3(static_cast<unsigned>(runs - 1), static_cast<unsigned>(slices)), dim3(kThreads),
                           0, 1, st, a);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }

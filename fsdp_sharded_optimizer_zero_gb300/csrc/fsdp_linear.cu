@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       if (OP != OP_DW && gridDim.z == 1 && (!has || c.dst < kHalf)) {
         Copy ahead = c;
         bool some = has;
-        for (int kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb, some = copy_advance<CUT>(p, ahead))
+        for (int kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb, some = copy_advance<CUT>(p, ahead, some))
           if (some) tma_prefetch_2d(ahead.map, ahead.x, ahead.y);
       }
     }
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(256, 2) linear_narrow_kernel(const __grid_cons
       if (mine) {
         if (!(CUT && OP == OP_DX) || has)
           tma_load_2d(smem_u32(smem) + s * C::STAGE + c.dst, c.map, c.x, c.y, smem_u32(&full_bar[s]));
-        has = copy_advance<CUT>(p, c);
+        has = copy_advance<CUT>(p, c, has);
       }
       __syncwarp();
       if (++s == C::STAGES) s = 0, ph ^= 1u;
@@ -635,6 +635,8 @@ Choice choose(int op, int64_t m, int64_t n, int64_t k, bool fp32) {
   return c;
 }
 
+constexpr int kCutFrom = 32;  // copies of W below 32 rows keep the producer behind
+
 // the product's operands as the entry points get them
 struct Operands {
   int n_shards;
@@ -661,7 +663,8 @@ int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who)
       return rc;
   } else {
     if ((rc = encode(&p.a, o.a, p.m, p.k, o.lda, BK, c.wide ? 128 : c.tn, false, who))) return rc;
-    if ((rc = encode_w(p, o.n_shards, o.w, static_cast<int64_t>(o.n_shards) * p.shard_rows, OP == OP_FWD, &fast, who)))
+    if ((rc = encode_w(p, o.n_shards, o.w, static_cast<int64_t>(o.n_shards) * p.shard_rows, OP == OP_FWD, kCutFrom, &fast,
+                       who)))
       return rc;
   }
   if (c.wide && fp32 && (rc = encode(&p.out, p.y32, p.m, p.n, p.n, 32, 32, true, who))) return rc;

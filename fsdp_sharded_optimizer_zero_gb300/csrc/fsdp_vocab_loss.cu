@@ -26,6 +26,7 @@ struct VocabParams : LinearParams {
   const void* labels;
   int labels_wide;         // 8-byte labels
   float2* part;            // lse: [2 ceil(n / 256)][m]: base-2 maximum, sum of 2^(z log2 e - maximum)
+  unsigned int* ticket;    // lse: set to 0 for the kernel that joins the parts
   float* z_label;          // lse: [m]
   const float *lse, *dloss, *total;
   float gscale;
@@ -59,16 +60,22 @@ __device__ __forceinline__ int label_at(const void* labels, int wide, int64_t i,
 }
 __device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < __int_as_float(0x7f800000) ? x : 0.0f; }
 
-// A row's running maximum (times log2 e) and sum of 2^(z log2 e - maximum). An infinite maximum is
-// subtracted as 0: -inf throughout leaves the sum 0, +inf makes it infinite, and NaN stays.
+// A row's maximum (times log2 e) and sum of 2^(z log2 e - maximum). An infinite maximum is subtracted as 0: -inf
+// throughout leaves the sum 0, +inf makes it infinite, and NaN stays.
 struct Softmax {
   float top, sum;
-  __device__ __forceinline__ void join(float top2, float sum2) {
-    const float t = max_nan(top, top2), r = finite_or_0(t);
-    const float a = sum == 0.0f ? 0.0f : __fmul_rn(sum, exp2_fast(__fsub_rn(finite_or_0(top), r)));
-    const float b = sum2 == 0.0f ? 0.0f : __fmul_rn(sum2, exp2_fast(__fsub_rn(finite_or_0(top2), r)));
+  template <int N>
+  __device__ __forceinline__ void join(const float2 (&v)[N]) {
+    float t = top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t = max_nan(t, v[i].x);
+    const float r = finite_or_0(t);
+    // a sum of 0 has no terms: its maximum says nothing
+    const auto scaled = [&](float s, float m) { return s == 0.0f ? 0.0f : __fmul_rn(s, exp2_fast(__fsub_rn(finite_or_0(m), r))); };
+    sum = scaled(sum, top);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum = __fadd_rn(sum, scaled(v[i].y, v[i].x));
     top = t;
-    sum = __fadd_rn(a, b);
   }
 };
 
@@ -83,6 +90,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;  // (not OP_LSE)
   uint32_t i = 0, stores = 0;
   float gscale = p.gscale;
+  if (OP == OP_LSE && pair == 0 && rank == 0 && warp == 2 && lane == 0) *p.ticket = 0u;
   if (OP == OP_DLOGITS && p.total) gscale = __fdiv_rn(gscale, fmaxf(p.total[1], 1.0f));
   const int tiles = num_m * num_n, items = wide_items<OP>(p, tiles);
   for (int item = pair; item < items; item += pairs, ++i) {
@@ -167,7 +175,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
         }
         float x, y;
         f2_split(sum, x, y);
-        s.join(top, __fadd_rn(x, y));
+        s.join({make_float2(top, __fadd_rn(x, y))});
       }
       if (row < p.m && c0 < p.n) p.part[static_cast<size_t>(nb * 2 + part) * p.m + row] = make_float2(s.top, s.sum);
     }
@@ -180,28 +188,33 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
         uint32_t r[32];
         tmem_ld_32cols(taddr + c, r);
         if (col0 >= p.cols) continue;  // warp-uniform
-        const bool ragged = col0 + 32 > p.n;
-        const bool hit = static_cast<uint32_t>(target - col0) < 32u;
+        // few instructions a pair: what concerns single elements (the label's, those past the vocabulary) is
+        // put right in the packed words and in the buffer
         uint4 w[4];
         uint32_t* word = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
           float x, y;
           f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), f2_both(-lse2)), x, y);
-          f2_split(f2_mul(f2_make(exp2_fast(x), exp2_fast(y)), f2_both(weight)), x, y);
-          if (hit) {
-            if (target - col0 == j) x = __fsub_rn(x, weight);
-            if (target - col0 == j + 1) y = __fsub_rn(y, weight);
-          }
-          if (!counted) x = y = 0.0f;  // whatever the logits are
-          if (ragged) {
-            if (col0 + j >= p.n) x = 0.0f;
-            if (col0 + j + 1 >= p.n) y = 0.0f;
-          }
-          word[j >> 1] = pack_bf16x2(x, y);
+          word[j >> 1] = f2_to_bf16x2(f2_mul(f2_make(exp2_fast(x), exp2_fast(y)), f2_both(weight)));
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) word[j] = counted ? word[j] : 0u;  // whatever the logits are
+        if (col0 + 32 > p.n) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            word[j] = col0 + 2 * j >= p.n ? 0u : col0 + 2 * j + 1 >= p.n ? word[j] & 0xFFFFu : word[j];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = w[j];
+        const int at = target - col0;
+        if (static_cast<uint32_t>(at) < 32u) {
+          float z = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z = at == j ? __uint_as_float(r[j]) : z;
+          const float v = __fsub_rn(__fmul_rn(exp2_fast(__fmaf_rn(z, kLog2e, -lse2)), weight), weight);
+          *reinterpret_cast<uint16_t*>(buf + staged_at(lane, 4 * h + (at >> 3)) + 2 * (at & 7)) = f32_to_bf16_bits(v);
+        }
         if (h == 1 || col0 + 32 >= p.cols) {
           __syncwarp();
           stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.cols, p.ld, lane);
@@ -219,65 +232,87 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   if (lane == 0) bulk_wait_group_all();  // no store still reads shared memory
 }
 
-// lse and loss from the parts of a row: a block takes 32 rows, its warps the parts in turn
+// lse and loss from the parts of a row: a block takes 32 rows, its warps the parts in turn, kAtOnce of them in
+// flight; their largest maximum is found first. With total, a block also leaves its rows' sum of losses and count,
+// and the block that comes last (a ticket, left at 0 by the product before) adds them, in the order of the
+// blocks.
 constexpr int kThreads = 256;
-__global__ void __launch_bounds__(kThreads) join_parts_kernel(const float2* __restrict__ part, int parts, int m,
-                                                              const float* __restrict__ z_label, const void* labels, int wide,
-                                                              int vocab, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 meet[kThreads / 32][32];
+constexpr int kJoinWarps = 16, kAtOnce = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const float2* __restrict__ part, int parts, int m,
+                                                                     const float* __restrict__ z_label, const void* labels,
+                                                                     int wide, int vocab, float* __restrict__ loss,
+                                                                     float* __restrict__ lse, float2* __restrict__ block_total,
+                                                                     unsigned int* ticket, float* __restrict__ total) {
+  __shared__ float2 meet[kJoinWarps][32];
+  __shared__ bool last;
   allow_next_grid();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  Softmax s{__int_as_float(0xff800000), 0.0f};
+  const float none = __int_as_float(0xff800000);
+  Softmax s{none, 0.0f};
   if (row < m)
-#pragma unroll 4
-    for (int i = warp; i < parts; i += kThreads / 32) {
-      const float2 v = part[static_cast<size_t>(i) * m + row];
-      s.join(v.x, v.y);
+    for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kAtOnce) {
+      float2 v[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * kJoinWarps;
+        v[j] = i < parts ? part[static_cast<size_t>(i) * m + row] : make_float2(none, 0.0f);
+      }
+      s.join(v);
     }
   meet[warp][lane] = make_float2(s.top, s.sum);
   __syncthreads();
-  if (warp == 0 && row < m) {
+  if (warp == 0) {
+    float2 v[kJoinWarps];
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) s.join(meet[w][lane].x, meet[w][lane].y);
-    const float l = __fmul_rn(__fadd_rn(finite_or_0(s.top), log2f(s.sum)), kLn2);
-    lse[row] = l;
-    loss[row] = label_at(labels, wide, row, vocab) < 0 ? 0.0f : __fsub_rn(l, z_label[row]);
+    for (int w = 0; w < kJoinWarps; ++w) v[w] = meet[w][lane];
+    s = {none, 0.0f};
+    s.join(v);
+    float mine = 0.0f;
+    int count = 0;
+    if (row < m) {
+      const float l = __fmul_rn(__fadd_rn(finite_or_0(s.top), log2f(s.sum)), kLn2);
+      count = label_at(labels, wide, row, vocab) >= 0 ? 1 : 0;
+      mine = count ? __fsub_rn(l, z_label[row]) : 0.0f;
+      lse[row] = l, loss[row] = mine;
+    }
+    if (total) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        mine = __fadd_rn(mine, __shfl_xor_sync(0xffffffffu, mine, d));
+        count += __shfl_xor_sync(0xffffffffu, count, d);
+      }
+      if (lane == 0) {
+        block_total[blockIdx.x] = make_float2(mine, __int_as_float(count));
+        __threadfence();
+        last = atomicAdd(ticket, 1u) + 1u == gridDim.x;
+      }
+    }
   }
-}
-
-// total[0] = the sum of the losses, total[1] = the counted tokens, by one block in a fixed order; a thread
-// keeps what its additions round off
-__global__ void __launch_bounds__(1024) total_kernel(const float* __restrict__ loss, int m, const void* labels, int wide,
-                                                     int vocab, float* __restrict__ total) {
-  __shared__ float2 meet[32];
-  allow_next_grid();
-  wait_for_prior_grids();
-  float sum = 0.0f, lost = 0.0f;
+  if (!total) return;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float sum = 0.0f, lost = 0.0f;  // a thread keeps what its additions round off
   int count = 0;
-  for (int64_t i = threadIdx.x; i < m; i += 1024) {
-    const float x = __fsub_rn(loss[i], lost), t = __fadd_rn(sum, x);
+  for (int64_t i = threadIdx.x; i < gridDim.x; i += 32 * kJoinWarps) {
+    const float2 v = __ldcg(block_total + i);
+    const float x = __fsub_rn(v.x, lost), t = __fadd_rn(sum, x);
     lost = __fsub_rn(__fsub_rn(t, sum), x);
     sum = t;
-    count += label_at(labels, wide, i, vocab) >= 0 ? 1 : 0;
+    count += __float_as_int(v.y);
   }
-  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
     count += __shfl_xor_sync(0xffffffffu, count, d);
   }
-  if (lane == 0) meet[threadIdx.x >> 5] = make_float2(sum, __int_as_float(count));
+  if (lane == 0) meet[0][warp] = make_float2(sum, __int_as_float(count));
   __syncthreads();
-  if (threadIdx.x < 32) {
-    sum = meet[lane].x, count = __float_as_int(meet[lane].y);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-      count += __shfl_xor_sync(0xffffffffu, count, d);
-    }
-    if (lane == 0) total[0] = sum, total[1] = static_cast<float>(count);
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kJoinWarps; ++w) sum = __fadd_rn(sum, meet[0][w].x), count += __float_as_int(meet[0][w].y);
+    total[0] = sum, total[1] = static_cast<float>(count);
   }
 }
 
@@ -315,7 +350,9 @@ int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t
   p.shard_rows = w.shard_rows;
   p.chunks = 1, p.chunk_blocks = INT32_MAX / 2;
   int rc;
-  if ((rc = encode_w(p, w.n, w.w, p.vocab, OP != OP_DX_SPLIT, &one_copy, who))) return rc;
+  // a vocabulary's shards are long: copies as high as they can be, cut at the few places where a shard ends
+  const bool fwd = OP != OP_DX_SPLIT;
+  if ((rc = encode_w(p, w.n, w.w, p.vocab, fwd, fwd ? 128 : BK, &one_copy, who))) return rc;
   if (p.w_levels > 1) return launch_wide<OP, COPIES_CUT>(p, st, who);
   return one_copy ? launch_wide<OP, COPIES_ONE>(p, st, who) : launch_wide<OP, COPIES_EQUAL>(p, st, who);
 }
@@ -403,13 +440,27 @@ unsigned int fsdp_vocab_loss_read_clear_error() {
 
 using namespace zgb;
 
+// The forward's workspace: the parts of each row, the labels' logits, the blocks' totals and their ticket
+namespace {
+struct ForwardSpace {
+  int parts;
+  uint64_t z_label, totals, ticket, bytes;
+  ForwardSpace(int64_t m, int64_t vocab) {
+    parts = static_cast<int>((vocab + 127) / 128);  // 128 columns each
+    z_label = up256(8 * static_cast<uint64_t>(parts) * static_cast<uint64_t>(m));
+    totals = z_label + up256(4 * static_cast<uint64_t>(m));
+    ticket = totals + up256(8 * static_cast<uint64_t>((m + 31) / 32));
+    bytes = ticket + 256;
+  }
+};
+}  // namespace
+
 extern "C" int fsdp_vocab_loss_forward_workspace(int64_t m_tokens, int64_t vocab, uint64_t* bytes) {
   const char* who = "fsdp_vocab_loss_forward_workspace";
   if (!bytes) return set_error(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
   const int rc = check_sizes(m_tokens, vocab, vocab, 8, 4, who);
   if (rc) return rc;
-  const uint64_t m = static_cast<uint64_t>(m_tokens), parts = 2 * ((static_cast<uint64_t>(vocab) + 255) / 256);
-  *bytes = up256(8 * parts * m) + up256(4 * m);
+  *bytes = ForwardSpace(m_tokens, vocab).bytes;
   return ZERO_OK;
 }
 
@@ -427,27 +478,25 @@ extern "C" int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_sha
     return set_error(ZERO_ERR_INVALID_ARG, "%s: X and workspace must be 16-byte aligned", who);
   if (!aligned(labels, label_bytes) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(total, 4))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: labels, loss, lse and total must be aligned to their elements", who);
-  uint64_t need = 0;
-  if ((rc = fsdp_vocab_loss_forward_workspace(m_tokens, vocab, &need))) return rc;
-  if (!workspace || workspace_bytes < need)
+  const ForwardSpace sp(m_tokens, vocab);
+  if (!workspace || workspace_bytes < sp.bytes)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: workspace of %llu bytes is below the %llu needed", who,
-                     workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)need);
+                     workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)sp.bytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   VocabParams p;
   memset(static_cast<void*>(&p), 0, sizeof(p));
   p.m = static_cast<int>(m_tokens), p.n = static_cast<int>(vocab), p.k = static_cast<int>(k_in);
   p.vocab = p.n, p.labels = labels, p.labels_wide = label_bytes == 8;
-  const int parts = 2 * ((p.n + 255) / 256);
-  // a last tile of up to 128 columns has one part
-  const int used = parts - ((p.n + 127) / 128 % 2);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.part = static_cast<float2*>(workspace);
-  p.z_label = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256(8 * static_cast<uint64_t>(parts) * p.m));
+  p.z_label = reinterpret_cast<float*>(ws + sp.z_label);
+  p.ticket = reinterpret_cast<unsigned int*>(ws + sp.ticket);
   if ((rc = encode(&p.a, X, p.m, p.k, p.k, BK, 128, false, who))) return rc;
   if ((rc = launch_product<OP_LSE>(p, w, true, st, who))) return rc;
-  cudaError_t e = launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>((p.m + 31) / 32)), dim3(kThreads), 0, 1, st,
-                                    p.part, used, p.m, p.z_label, labels, p.labels_wide, p.vocab, loss, lse);
-  if (e == cudaSuccess && total)
-    e = launch_overlapped(total_kernel, dim3(1), dim3(1024), 0, 1, st, loss, p.m, labels, p.labels_wide, p.vocab, total);
+  const cudaError_t e =
+      launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>((m_tokens + 31) / 32)), dim3(32 * kJoinWarps), 0, 1, st, p.part,
+                        sp.parts, p.m, p.z_label, labels, p.labels_wide, p.vocab, loss, lse,
+                        reinterpret_cast<float2*>(ws + sp.totals), p.ticket, total);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 

@@ -32,6 +32,22 @@ __device__ __forceinline__ int token_at(const void* tokens, int wide, int64_t i,
   return t >= 0 && t < vocab ? static_cast<int>(t) : -1;
 }
 
+// tokens i0, i0 + 32, .. below m (-1 behind), all on their way at once: a branch on their width at each would wait for
+// one after the other
+template <int N>
+__device__ __forceinline__ void tokens_at(const void* tokens, int wide, int64_t i0, int64_t m, int vocab, int (&t)[N]) {
+  int64_t raw[N];
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) raw[j] = i0 + 32 * j < m ? __ldg(static_cast<const long long*>(tokens) + i0 + 32 * j) : -1;
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) raw[j] = i0 + 32 * j < m ? __ldg(static_cast<const int*>(tokens) + i0 + 32 * j) : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) t[j] = raw[j] >= 0 && raw[j] < vocab ? static_cast<int>(raw[j]) : -1;
+}
+
 // A warp takes up to 1024 columns of a token's row at a time: four pieces of 8 columns a lane, in flight together.
 constexpr int kPieces = 4;
 __global__ void __launch_bounds__(kThreads) embedding_forward_kernel(const __grid_constant__ TableShards e, int shard_rows,
@@ -74,54 +90,129 @@ struct Sorted {
   int* order;  // [m] their positions
 };
 
-__device__ __forceinline__ int key_at(const void* tokens, int wide, int64_t i, int vocab) {
-  const int t = token_at(tokens, wide, i, vocab);
-  return t < 0 ? kNone : t;
-}
-
 // zeros to `n16` pieces of 16 bytes, by block `block` of `blocks`
 __device__ __forceinline__ void fill_zeros(uint4* out, int64_t n16, int64_t block, int64_t blocks) {
-  for (int64_t i = block * kThreads + threadIdx.x; i < n16; i += blocks * kThreads) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < n16; i += blocks * blockDim.x) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
 }
 
-// Up to kRankMost positions: a position's place is the number of smaller keys and of equal ones ahead of it,
-// counted over all keys, kRankSplit threads to a position. m^2 comparisons, but one launch, and beside it the
-// rest of the blocks fill dE with zeros.
-constexpr int kRankMost = 16384;
-constexpr int kRankSplit = 8;
-constexpr int kRankTile = 2048;  // keys in shared memory at a time
-__global__ void __launch_bounds__(kThreads) rank_kernel(const void* tokens, int wide, int m, int vocab, Sorted s,
-                                                        int rank_blocks, uint4* zero, int64_t zero16) {
-  __shared__ int keys[kRankTile];
+// A stable radix sort, a digit of kDigitBits a pass from the lowest. A warp has a run of words, a round of 32 after
+// the other, and finds each word's place among its own of the same digit (returned): the words ahead of it in its
+// round, and those of earlier rounds, which next[digit] counts. The lanes of the same digit are found by a vote
+// for each of its bits: matching any value at once takes longer the more values there are, up to 0.6 us a round.
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+template <int ROUNDS>
+__device__ __forceinline__ void places_in_warp(const int (&digit)[ROUNDS], int rounds, int* next, int (&place)[ROUNDS]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    if (r >= rounds) break;  // the same for the whole warp
+    uint32_t same = __ballot_sync(0xffffffffu, digit[r] >= 0);  // a digit of -1: no word
+#pragma unroll
+    for (int bit = 0; bit < kDigitBits; ++bit) {
+      const bool one = (digit[r] >> bit) & 1;
+      const uint32_t ones = __ballot_sync(0xffffffffu, one);
+      same &= one ? ones : ~ones;
+    }
+    const int ahead = __popc(same & ((1u << lane) - 1u));
+    int at = 0;
+    if (digit[r] >= 0) at = next[digit[r]];
+    __syncwarp();
+    if (digit[r] >= 0 && ahead == 0) next[digit[r]] = at + __popc(same);
+    __syncwarp();
+    place[r] = at + ahead;
+  }
+}
+
+// Up to kBlockMost positions, of a vocabulary whose tokens leave room for a position in 32 bits: one block sorts
+// words of token and position in shared memory, 4 to 8 us, while the others fill dE with zeros. (Counting the
+// smaller words for each position takes m^2 comparisons, 47 us at 16384; passes of several launches, below,
+// about 20.)
+constexpr int kPositionBits = 14, kBlockMost = 1 << kPositionBits;
+constexpr int kBlockThreads = 1024, kBlockWarps = kBlockThreads / 32, kBlockRounds = kBlockMost / kBlockThreads;
+constexpr uint32_t kBlockSmem = kBlockMost * 4 + kBlockWarps * kDigits * 4;
+bool by_one_block(int64_t m, int64_t vocab) { return m <= kBlockMost && vocab < (int64_t(1) << (32 - kPositionBits)); }
+__global__ void __launch_bounds__(kBlockThreads) sort_block_kernel(const void* tokens, int wide, int m, int vocab, int passes,
+                                                                   Sorted s, uint4* zero, int64_t zero16) {
+  extern __shared__ uint32_t sort_mem[];
+  __shared__ int warp_sum[kBlockWarps];
   allow_next_grid();
   wait_for_prior_grids();
-  if (static_cast<int>(blockIdx.x) >= rank_blocks) {
-    fill_zeros(zero, zero16, blockIdx.x - rank_blocks, gridDim.x - rank_blocks);
+  if (blockIdx.x != 0) {
+    fill_zeros(zero, zero16, blockIdx.x - 1, gridDim.x - 1);
     return;
   }
-  const int i = (static_cast<int>(blockIdx.x) * kThreads + static_cast<int>(threadIdx.x)) / kRankSplit;
-  const int part = threadIdx.x % kRankSplit;
-  const int mine = i < m ? key_at(tokens, wide, i, vocab) : kNone;
-  int count = 0;
-  for (int t0 = 0; t0 < m; t0 += kRankTile) {
+  uint32_t* words = sort_mem;
+  int* next = reinterpret_cast<int*>(sort_mem + kBlockMost);  // [warp][digit]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rounds = (m + kBlockThreads - 1) / kBlockThreads, first = warp * rounds * 32 + lane;
+  uint32_t word[kBlockRounds];
+  {
+    int t[kBlockRounds];
+    tokens_at(tokens, wide, first, min(m, first - lane + rounds * 32), vocab, t);
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r)  // none: behind every token
+      word[r] = (static_cast<uint32_t>(t[r] < 0 ? vocab : t[r]) << kPositionBits) | static_cast<uint32_t>(first + r * 32);
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = kPositionBits + pass * kDigitBits;
+    for (int d = tid; d < kBlockWarps * kDigits; d += kBlockThreads) next[d] = 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < kRankTile; j += kThreads) keys[j] = t0 + j < m ? key_at(tokens, wide, t0 + j, vocab) : kNone;
+    int digit[kBlockRounds], place[kBlockRounds];
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r)
+      digit[r] = r < rounds && first + r * 32 < m ? static_cast<int>((word[r] >> shift) & (kDigits - 1)) : -1;
+    places_in_warp(digit, rounds, next + warp * kDigits, place);
     __syncthreads();
-    const int last = min(kRankTile, m - t0);
-    for (int j = part; j < last; j += kRankSplit) {
-      const int k = keys[j];
-      count += (k < mine || (k == mine && t0 + j < i)) ? 1 : 0;
+    // where each warp's words of a digit begin: over the warps (a thread a digit), then over the digits
+    int all = 0;
+    if (tid < kDigits) {
+#pragma unroll 8
+      for (int w = 0; w < kBlockWarps; ++w) {
+        const int n = next[w * kDigits + tid];
+        next[w * kDigits + tid] = all;
+        all += n;
+      }
     }
+    int run = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int t = __shfl_up_sync(0xffffffffu, run, d);
+      if (lane >= d) run += t;
+    }
+    if (lane == 31) warp_sum[warp] = run;
+    __syncthreads();
+    int* start = reinterpret_cast<int*>(words);  // the words are in registers: their place holds the digits' starts
+    if (tid < kDigits) {
+      int ahead = run - all;
+      for (int w = 0; w < warp; ++w) ahead += warp_sum[w];
+      start[tid] = ahead;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r)
+      if (digit[r] >= 0) place[r] += next[warp * kDigits + digit[r]] + start[digit[r]];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r)
+      if (digit[r] >= 0) words[place[r]] = word[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r)
+      if (digit[r] >= 0) word[r] = words[first + r * 32];
+    __syncthreads();
   }
 #pragma unroll
-  for (int d = 1; d < kRankSplit; d *= 2) count += __shfl_xor_sync(0xffffffffu, count, d);
-  if (i < m && part == 0) s.key[count] = mine, s.order[count] = i;
+  for (int r = 0; r < kBlockRounds; ++r) {
+    const int i = first + r * 32;
+    if (r < rounds && i < m) {
+      const int t = static_cast<int>(word[r] >> kPositionBits);
+      s.key[i] = t == vocab ? kNone : t, s.order[i] = static_cast<int>(word[r] & (kBlockMost - 1));
+    }
+  }
 }
 
-// More positions: a radix sort, a digit of kDigitBits a pass from the lowest, each pass stable. Block b has the
-// positions from b kSortTile on, a warp a run of them.
-constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int kSortTile = 4096, kSortRun = kSortTile / kWarps;
+// More positions: three launches a pass. Block b has the positions from b kSortTile on, a warp a run of them.
+constexpr int kSortTile = 4096, kSortRun = kSortTile / kWarps, kSortRounds = kSortRun / 32;
 struct SortPass {
   const void* tokens;  // first pass: the tokens themselves; else null
   int wide, vocab, shift;
@@ -130,12 +221,22 @@ struct SortPass {
   int blocks;
   int* count;  // [kDigits][blocks], then the places where they begin
 };
-__device__ __forceinline__ int sort_key(const SortPass& p, int64_t i) {
-  return p.tokens ? key_at(p.tokens, p.wide, i, p.vocab) : p.in.key[i];
-}
 // positions without a token have the digits of `vocab`, which no token has: behind the others
 __device__ __forceinline__ int sort_digit(const SortPass& p, int key) {
   return (min(key, p.vocab) >> p.shift) & (kDigits - 1);
+}
+// the keys of a lane's positions of its warp's run, all on their way at once
+__device__ __forceinline__ void load_keys(const SortPass& p, int64_t first, int (&key)[kSortRounds], int (&digit)[kSortRounds]) {
+  if (p.tokens) {
+    tokens_at(p.tokens, p.wide, first, p.m, p.vocab, key);
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) key[r] = key[r] < 0 ? kNone : key[r];
+  } else {
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) key[r] = first + r * 32 < p.m ? p.in.key[first + r * 32] : kNone;
+  }
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) digit[r] = first + r * 32 < p.m ? sort_digit(p, key[r]) : -1;
 }
 
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(const SortPass p, uint4* zero, int64_t zero16) {
@@ -146,11 +247,13 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const SortPass p, 
     fill_zeros(zero, zero16, blockIdx.x - p.blocks, gridDim.x - p.blocks);
     return;
   }
+  int key[kSortRounds], digit[kSortRounds];
+  load_keys(p, static_cast<int64_t>(blockIdx.x) * kSortTile + (threadIdx.x >> 5) * kSortRun + (threadIdx.x & 31), key, digit);
   for (int d = threadIdx.x; d < kDigits; d += kThreads) count[d] = 0;
   __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile;
-  for (int j = threadIdx.x; j < kSortTile; j += kThreads)
-    if (first + j < p.m) atomicAdd(&count[sort_digit(p, sort_key(p, first + j))], 1);
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r)
+    if (digit[r] >= 0) atomicAdd(&count[digit[r]], 1);
   __syncthreads();
   for (int d = threadIdx.x; d < kDigits; d += kThreads) p.count[static_cast<int64_t>(d) * p.blocks + blockIdx.x] = count[d];
 }
@@ -189,15 +292,22 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int* count, int64_t n) 
 }
 
 __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const SortPass p) {
-  __shared__ int next[kWarps][kDigits];  // per warp: counts, then where its next position of a digit goes
+  __shared__ int next[kWarps][kDigits];  // per warp: counts, then where its words of a digit begin
   allow_next_grid();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile + warp * kSortRun + lane;
+  int key[kSortRounds], digit[kSortRounds], order[kSortRounds], place[kSortRounds];
+  load_keys(p, first, key, digit);
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) order[r] = static_cast<int>(first + r * 32);
+  if (!p.tokens) {
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) order[r] = first + r * 32 < p.m ? p.in.order[first + r * 32] : 0;
+  }
   for (int d = threadIdx.x; d < kWarps * kDigits; d += kThreads) (&next[0][0])[d] = 0;
   __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile + warp * kSortRun;
-  for (int j = lane; j < kSortRun; j += 32)
-    if (first + j < p.m) atomicAdd(&next[warp][sort_digit(p, sort_key(p, first + j))], 1);
+  places_in_warp(digit, kSortRounds, next[warp], place);
   __syncthreads();
   for (int d = threadIdx.x; d < kDigits; d += kThreads) {
     int at = p.count[static_cast<int64_t>(d) * p.blocks + blockIdx.x];
@@ -209,32 +319,24 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const SortPass p
     }
   }
   __syncthreads();
-  for (int j = lane; j < kSortRun; j += 32) {  // the same number of rounds for every lane
-    const bool there = first + j < p.m;
-    const int key = there ? sort_key(p, first + j) : 0;
-    const int digit = there ? sort_digit(p, key) : kDigits;  // those past the end among themselves
-    const uint32_t same = __match_any_sync(0xffffffffu, digit);
-    const int ahead = __popc(same & ((1u << lane) - 1u));
-    int at = 0;
-    if (there) at = next[warp][digit] + ahead;
-    __syncwarp();
-    if (there && ahead == 0) next[warp][digit] += __popc(same);
-    __syncwarp();
-    if (there) {
-      p.out.key[at] = key;
-      p.out.order[at] = p.tokens ? static_cast<int>(first + j) : p.in.order[first + j];
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r)
+    if (digit[r] >= 0) {
+      const int at = next[warp][digit[r]] + place[r];
+      p.out.key[at] = key[r], p.out.order[at] = order[r];
     }
-  }
 }
 
 // ------------------------------------------------------------------------------------
 // sums over the ordered positions
 // ------------------------------------------------------------------------------------
-// A warp takes a run of RUN ordered positions and 256 columns. The stretches of one token that lie inside
+// A warp takes a run of kRun ordered positions and 256 columns. The stretches of one token that lie inside
 // the run are finished; the one that goes on at its end (and came from ahead or not) leaves its fp32 sum in
-// `open`, slot 1, and one that came from ahead and ends here in slot 0.
-constexpr int kShortRun = 16, kLongRun = 32;
-int run_of(int64_t m) { return m <= kRankMost ? kShortRun : kLongRun; }
+// `open`, slot 1, and one that came from ahead and ends here in slot 0. All rows of the run are on their way at
+// once, each lane's 16 bytes of each through its own slots of shared memory, so that the loop over them is
+// rolled (with the rows in registers and the loop unrolled, its end of a stretch 17 times in the code, 65536
+// positions of 768 columns took 33 us).
+constexpr int kRun = 16, kRunWarps = 8;
 struct SumArgs {
   Sorted s;
   int64_t m;
@@ -271,102 +373,136 @@ __device__ __forceinline__ void put_row(const SumArgs& p, int key, int64_t col, 
   }
 }
 
-template <int RUN>
-__global__ void __launch_bounds__(kThreads) sum_runs_kernel(const SumArgs p) {
+__global__ void __launch_bounds__(32 * kRunWarps) sum_runs_kernel(const SumArgs p) {
+  extern __shared__ uint4 run_mem[];
   allow_next_grid();
   wait_for_prior_grids();
-  const int lane = threadIdx.x & 31;
-  const int64_t runs = (p.m + RUN - 1) / RUN, items = runs * p.slices, step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items; item += step) {
-    const int64_t run = item / p.slices, col = (item - run * p.slices) * 256 + lane * 8, first = run * RUN;
-    const int count = static_cast<int>(min(p.m - first, static_cast<int64_t>(RUN)));
-    const int key = lane < count ? p.s.key[first + lane] : kNone;
-    const int at = lane < count ? p.s.order[first + lane] : 0;
-    const int before = first > 0 ? p.s.key[first - 1] : -1, after = first + count < p.m ? p.s.key[first + count] : -1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* rows = run_mem + warp * kRun * 32 + lane;  // 32 apart
+  const int64_t runs = (p.m + kRun - 1) / kRun, items = runs * p.slices, step = static_cast<int64_t>(gridDim.x) * kRunWarps;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRunWarps + warp; item < items; item += step) {
+    const int64_t run = item / p.slices, col = (item - run * p.slices) * 256 + lane * 8, first = run * kRun;
+    // lane j has position first + j's token and place; lane kRun the token behind the run, lane kRun + 1 the one
+    // ahead of it
+    const int64_t i = lane == kRun + 1 ? first - 1 : first + lane;
+    const bool there = lane <= kRun + 1 && i >= 0 && i < p.m;
+    const int key = there ? p.s.key[i] : -1;
+    const int at = there && lane < kRun ? p.s.order[i] : 0;
     const bool in = col < p.cols;
-    f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
-    int now = __shfl_sync(0xffffffffu, key, 0);
-    bool from_ahead = now == before;
-    float* open = p.open + run * 2 * p.cols + col;
-    const auto leave = [&](int slot) {
-      if (in) {
-        ulonglong2* to = reinterpret_cast<ulonglong2*>(open + slot * p.cols);
-        to[0] = make_ulonglong2(sum[0], sum[1]), to[1] = make_ulonglong2(sum[2], sum[3]);
-      }
-    };
-    // all rows of the run are on their way before the first is used
-    constexpr int AHEAD = RUN < 16 ? RUN : 16;
-    for (int j0 = 0; j0 < count && now != kNone; j0 += AHEAD) {
-      uint4 w[AHEAD];
+    // those without a token are behind the others
+    const int real = __popc(__ballot_sync(0xffffffffu, lane < kRun && key >= 0 && key != kNone));
+    const int behind = __shfl_sync(0xffffffffu, key, kRun), before = __shfl_sync(0xffffffffu, key, kRun + 1);
+    if (real == 0) continue;
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const int k = __shfl_sync(0xffffffffu, key, (j0 + j) & 31), pos = __shfl_sync(0xffffffffu, at, (j0 + j) & 31);
-        w[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (j0 + j < count && k != kNone && in) w[j] = __ldg(reinterpret_cast<const uint4*>(p.dy + pos * p.cols + col));
-      }
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const int k = j0 + j < count ? __shfl_sync(0xffffffffu, key, (j0 + j) & 31) : now;
-        if (k != now) {  // the same for the whole warp
-          if (from_ahead) leave(0);
-          else if (in) put_row(p, now, col, sum);
-          sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
-          now = k, from_ahead = false;
-        }
-        f2 v[4];
-        widen8(w[j], v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = f2_add(sum[i], v[i]);  // zeros past the run
-      }
+    for (int j = 0; j < kRun; ++j) {
+      const int pos = __shfl_sync(0xffffffffu, at, j);
+      if (in && j < real)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(rows + j * 32)), "l"(p.dy + pos * p.cols + col)
+                     : "memory");
     }
-    if (now == kNone) continue;
-    if (now == after) leave(1);
-    else if (from_ahead) leave(0);
-    else if (in) put_row(p, now, col, sum);
+    // bit j: a stretch ends with position j of the run
+    const int next = __shfl_down_sync(0xffffffffu, key, 1);
+    const uint32_t ends = __ballot_sync(0xffffffffu, lane < real && (lane + 1 == real || next != key));
+    bool from_ahead = __shfl_sync(0xffffffffu, key, 0) == before;
+    const bool goes_on = real == kRun && __shfl_sync(0xffffffffu, key, kRun - 1) == behind;
+    float* open = p.open + run * 2 * p.cols + col;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 2
+    for (int j = 0; j < real; ++j) {
+      if (in) {
+        f2 v[4];
+        widen8(rows[j * 32], v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = f2_add(sum[k], v[k]);
+      }
+      if (!((ends >> j) & 1u)) continue;  // the same for the whole warp
+      const int token = __shfl_sync(0xffffffffu, key, j);
+      const bool leaves = goes_on && j == kRun - 1;
+      if (in) {
+        if (leaves || from_ahead) {
+          ulonglong2* to = reinterpret_cast<ulonglong2*>(open + (leaves ? p.cols : 0));
+          to[0] = make_ulonglong2(sum[0], sum[1]), to[1] = make_ulonglong2(sum[2], sum[3]);
+        } else {
+          put_row(p, token, col, sum);
+        }
+      }
+      sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
+      from_ahead = false;
+    }
   }
 }
 
-// The tokens whose stretch crosses from one run into the next: a block takes a boundary where a stretch
-// crosses for the first time and 256 columns, its warps consecutive parts of the runs it touches.
-template <int RUN>
-__global__ void __launch_bounds__(kThreads) sum_crossing_kernel(const SumArgs p) {
-  __shared__ f2 part[kWarps][32][4];
+// The tokens whose stretch crosses from one run into the next, 256 columns at a time: where it touches up to
+// kFewRuns runs, by a warp, at the boundary where it crosses first; where it touches more, by a block, at the first of
+// its runs whose number is a multiple of kFewRuns / 2 (it has one that starts with it), the runs shared among its
+// warps, whose sums meet in shared memory. The first few_blocks blocks are of the first kind.
+constexpr int kFewRuns = 16, kCrossThreads = 512, kCrossWarps = kCrossThreads / 32;
+// the sums that runs from .. to - 1 left of a stretch: it goes on behind every run but `last`, where it left its sum
+// as one that ends there
+__device__ __forceinline__ void add_open(const SumArgs& p, int64_t from, int64_t to, int64_t last, int64_t col, f2 (&sum)[4]) {
+  sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
+#pragma unroll 8
+  for (int64_t r = from; r < to; ++r) {
+    const ulonglong2* a = reinterpret_cast<const ulonglong2*>(p.open + (r * 2 + (r < last ? 1 : 0)) * p.cols + col);
+    const ulonglong2 x = a[0], y = a[1];
+    sum[0] = f2_add(sum[0], x.x), sum[1] = f2_add(sum[1], x.y), sum[2] = f2_add(sum[2], y.x), sum[3] = f2_add(sum[3], y.y);
+  }
+}
+__global__ void __launch_bounds__(kCrossThreads) sum_crossing_kernel(const SumArgs p, int64_t few_blocks) {
+  __shared__ f2 part[kCrossWarps][32][4];
   allow_next_grid();
   wait_for_prior_grids();
-  const int64_t b = blockIdx.x + 1, first = b * RUN, runs = (p.m + RUN - 1) / RUN;  // between runs b - 1 and b
-  const int key = p.s.key[first], before = p.s.key[first - 1], earlier = b > 1 ? p.s.key[first - RUN - 1] : -1;
-  // which of the next runs begin with the key, 256 at a time: keys are in order
-  int64_t last = b;
-  for (int64_t r0 = b + 1;; r0 += kThreads) {
-    const int64_t r = r0 + threadIdx.x;
-    const bool same = r < runs && p.s.key[r * RUN] == key;
-    if (r0 == b + 1 && (key == kNone || before != key || earlier == key)) return;  // none crosses here, or crossed before
-    const int n = __syncthreads_count(same);
-    last += n;
-    if (n < kThreads) break;
-  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+  const int64_t runs = (p.m + kRun - 1) / kRun;
+  const int* key = p.s.key;
+  f2 sum[4];
+  if (blockIdx.x < few_blocks) {
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kCrossWarps + warp, b = 1 + item / p.slices;  // between b - 1 and b
+    if (b >= runs) return;
+    const int64_t first = b * kRun, col = (item - (b - 1) * p.slices) * 256 + lane * 8;
+    // whether the runs from b on begin with the token; lanes in order: the first that does not
+    const int64_t r = b + lane;
+    const int mine = r < runs ? key[r * kRun] : -1, token = __shfl_sync(0xffffffffu, mine, 0);
+    const int before = key[first - 1], earlier = b > 1 ? key[first - kRun - 1] : -1;
+    if (token == kNone || before != token || earlier == token) return;  // none crosses here, or it crossed before
+    const uint32_t other = ~__ballot_sync(0xffffffffu, mine == token);
+    const int more = other ? __ffs(other) - 1 : 32;  // runs from b on that it touches
+    if (1 + more > kFewRuns || col >= p.cols) return;
+    add_open(p, b - 1, b + more, b + more - 1, col, sum);
+    put_row(p, token, col, sum);
+    return;
+  }
+  const int64_t item = blockIdx.x - few_blocks, at = item / p.slices * (kFewRuns / 2);  // a run
+  const int64_t col = (item - item / p.slices * p.slices) * 256 + lane * 8;
+  const int token = key[at * kRun];
+  if (token == kNone) return;
+  // the runs ahead that it touches
+  const int64_t r = at - 1 - lane;
+  const uint32_t other = ~__ballot_sync(0xffffffffu, r >= 0 && key[r * kRun + kRun - 1] == token);
+  const int ahead = other ? __ffs(other) - 1 : 32;
+  // that one's, if it begins the run kFewRuns / 2 ahead too: sure where it touches runs before that
+  if (ahead > kFewRuns / 2 || (ahead == kFewRuns / 2 && key[(at - kFewRuns / 2) * kRun] == token)) return;
+  int64_t last = at;
+  for (int64_t r0 = at + 1;; r0 += kCrossThreads) {
+    const int64_t q = r0 + threadIdx.x;
+    const int n = __syncthreads_count(q < runs && key[q * kRun] == token);
+    last += n;
+    if (n < kCrossThreads) break;
+  }
+  const int64_t from = at - ahead, parts = last - from + 1;
+  if (parts <= kFewRuns) return;
   const bool in = col < p.cols;
-  const int64_t parts = last - b + 2, from = b - 1 + parts * warp / kWarps, to = b - 1 + parts * (warp + 1) / kWarps;
-  f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
-  if (in)
-#pragma unroll 8
-    for (int64_t r = from; r < to; ++r) {
-      // it goes on behind every run but the last, where it left its sum as one that ends there
-      const ulonglong2* a = reinterpret_cast<const ulonglong2*>(p.open + (r * 2 + (r < last ? 1 : 0)) * p.cols + col);
-      const ulonglong2 x = a[0], y = a[1];
-      sum[0] = f2_add(sum[0], x.x), sum[1] = f2_add(sum[1], x.y), sum[2] = f2_add(sum[2], y.x), sum[3] = f2_add(sum[3], y.y);
-    }
+  if (in) add_open(p, from + parts * warp / kCrossWarps, from + parts * (warp + 1) / kCrossWarps, last, col, sum);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) part[warp][lane][j] = sum[j];
+  for (int j = 0; j < 4; ++j) part[warp][lane][j] = in ? sum[j] : 0ull;
   __syncthreads();
   if (warp == 0 && in) {
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w)
+    for (int w = 1; w < kCrossWarps; ++w)
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], part[w][lane][j]);
-    put_row(p, key, col, sum);
+    put_row(p, token, col, sum);
   }
 }
 
@@ -380,6 +516,8 @@ int check_sizes(int64_t m, int64_t rows, int64_t vocab, int64_t cols, int token_
   if (m < 1 || rows < 1 || m > most || rows > most)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: m_tokens and rows must be in 1..2^30", who);
   if (cols < 1 || cols > (1 << 20)) return set_error(ZERO_ERR_INVALID_ARG, "%s: cols must be in 1..2^20", who);
+  if (m * cols > (int64_t(1) << 42))
+    return set_error(ZERO_ERR_UNSUPPORTED, "%s: %lld x %lld is more than 2^42 elements", who, (long long)m, (long long)cols);
   if (cols % 8)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: cols %lld must be a multiple of 8 (16-byte rows)", who, (long long)cols);
   if (vocab < 1 || vocab > rows)
@@ -405,15 +543,15 @@ struct BackwardSpace {
     bytes = 0, passes = 0, sort_blocks = 0, count = 0;
     key[0] = key[1] = take(4 * static_cast<uint64_t>(m));
     order[0] = order[1] = take(4 * static_cast<uint64_t>(m));
-    if (m > kRankMost) {
-      int bits = 1;
-      while (bits < 31 && (vocab >> bits) != 0) ++bits;  // of keys 0 .. vocab
-      passes = (bits + kDigitBits - 1) / kDigitBits;
+    int bits = 1;
+    while (bits < 31 && (vocab >> bits) != 0) ++bits;  // of keys 0 .. vocab
+    passes = (bits + kDigitBits - 1) / kDigitBits;
+    if (!by_one_block(m, vocab)) {
       sort_blocks = (m + kSortTile - 1) / kSortTile;
       if (passes > 1) key[1] = take(4 * static_cast<uint64_t>(m)), order[1] = take(4 * static_cast<uint64_t>(m));
       count = take(4 * static_cast<uint64_t>(sort_blocks) * kDigits);
     }
-    open = take(8 * static_cast<uint64_t>((m + run_of(m) - 1) / run_of(m)) * static_cast<uint64_t>(cols));
+    open = take(8 * static_cast<uint64_t>((m + kRun - 1) / kRun) * static_cast<uint64_t>(cols));
   }
 };
 
@@ -488,11 +626,18 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
   const int wide = token_bytes == 8 ? 1 : 0;
   Sorted sorted{ints(sp.key[0]), ints(sp.order[0])};
   cudaError_t e = cudaSuccess;
-  if (sp.passes == 0) {
-    const int64_t rank_blocks = (m_tokens * kRankSplit + kThreads - 1) / kThreads;
-    e = launch_overlapped(rank_kernel, dim3(static_cast<unsigned>(rank_blocks + zero_blocks)), dim3(kThreads), 0, 1, st, tokens,
-                          wide, static_cast<int>(m_tokens), static_cast<int>(vocab), sorted, static_cast<int>(rank_blocks),
-                          zero, zero16);
+  if (by_one_block(m_tokens, vocab)) {
+    static OncePerDevice once;
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+      e = once.run(dev, [] {
+        return cudaFuncSetAttribute(sort_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBlockSmem));
+      });
+    const int64_t fill = std::min<int64_t>((zero16 + 2 * kBlockThreads - 1) / (2 * kBlockThreads), num_sms() - 1);
+    if (e == cudaSuccess)
+      e = launch_overlapped(sort_block_kernel, dim3(static_cast<unsigned>(1 + fill)), dim3(kBlockThreads), kBlockSmem, 1, st, tokens,
+                            wide, static_cast<int>(m_tokens), static_cast<int>(vocab), sp.passes, sorted, zero, zero16);
   } else {
     for (int pass = 0; pass < sp.passes && e == cudaSuccess; ++pass) {
       SortPass p;
@@ -513,18 +658,27 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
         e = launch_overlapped(sort_scatter_kernel, dim3(static_cast<unsigned>(sp.sort_blocks)), dim3(kThreads), 0, 1, st, p);
     }
   }
-  const int run = run_of(m_tokens);
-  const int64_t runs = (m_tokens + run - 1) / run, slices = (cols + 255) / 256;
+  const int64_t runs = (m_tokens + kRun - 1) / kRun, slices = (cols + 255) / 256;
   SumArgs a;
   a.s = sorted, a.m = m_tokens, a.dy = dY, a.cols = cols, a.slices = static_cast<int>(slices), a.scale = scale;
   a.de32 = dE, a.de16 = dE_bf16, a.add = accumulate != 0, a.open = reinterpret_cast<float*>(ws + sp.open);
   if (e == cudaSuccess) {
-    const int64_t blocks = std::min<int64_t>((runs * slices + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms()) * 64);
-    e = launch_overlapped(run == kShortRun ? sum_runs_kernel<kShortRun> : sum_runs_kernel<kLongRun>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, 1, st, a);
+    const int64_t blocks = std::min<int64_t>((runs * slices + kRunWarps - 1) / kRunWarps, static_cast<int64_t>(num_sms()) * 64);
+    constexpr uint32_t smem = kRunWarps * kRun * 512;
+    static OncePerDevice once;
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+      e = once.run(dev, [] {
+        return cudaFuncSetAttribute(sum_runs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      });
+    if (e == cudaSuccess)
+      e = launch_overlapped(sum_runs_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kRunWarps), smem, 1, st, a);
+    if (e == cudaSuccess && runs > 1) {
+      const int64_t few = ((runs - 1) * slices + kCrossWarps - 1) / kCrossWarps;
+      const int64_t many = (runs + kFewRuns / 2 - 1) / (kFewRuns / 2) * slices;
+      e = launch_overlapped(sum_crossing_kernel, dim3(static_cast<unsigned>(few + many)), dim3(kCrossThreads), 0, 1, st, a, few);
+    }
   }
-  if (e == cudaSuccess && runs > 1)
-    e = launch_overlapped(run == kShortRun ? sum_crossing_kernel<kShortRun> : sum_crossing_kernel<kLongRun>,
-                          dim3(static_cast<unsigned>(runs - 1), static_cast<unsigned>(slices)), dim3(kThreads),
-                          0, 1, st, a);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }

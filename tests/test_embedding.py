@@ -127,6 +127,24 @@ def test_backward_sorted_in_passes(z, m, vocab, rows, cols, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [True, False])
+def test_backward_stretches_of_every_length(z, wide):
+    """Tokens that come 1, 2, .. 40 runs of 16 positions often, each with every offset in its run and among the
+    runs, added to a gradient: none is summed twice or left out."""
+    for pad in (0, 1, 15, 16, 100, 255, 256, 257):
+        lengths = [16 * n + d for n in (1, 2, 15, 16, 17, 31, 32, 33, 34, 40, 48) for d in (-1, 0, 1)]
+        t = torch.cat([torch.full((pad,), 0, device=DEV)]
+                      + [torch.full((n,), 1 + i, device=DEV) for i, n in enumerate(lengths)]).long()
+        rows, cols = len(lengths) + 9, 8
+        dy = torch.ones(t.numel(), cols, dtype=BF, device=DEV)
+        de = torch.full((rows, cols), 1.0, dtype=torch.float32 if wide else BF, device=DEV)
+        z.fsdp_embedding_backward(dy, t, de, accumulate=True)
+        want = torch.bincount(t, minlength=rows).double() + 1.0
+        assert torch.equal(de[:, 0].double(), want if wide else want.to(BF).double())
+        assert torch.equal(de, de[:, :1].expand(-1, cols))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m,vocab,rows,cols,kind", [(1003, 1157, 1160, 520, "text"), (20000, 50, 56, 264, "text"), (7, 9, 16, 8, "none")])
 def test_backward_added_to_a_gradient(z, m, vocab, rows, cols, kind):
     check_backward(z, m, vocab, rows, cols, kind, torch.int64, True, scale=3.0, add=True)

@@ -95,131 +95,83 @@ __device__ __forceinline__ void fill_zeros(uint4* out, int64_t n16, int64_t bloc
   for (int64_t i = block * blockDim.x + threadIdx.x; i < n16; i += blocks * blockDim.x) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
 }
 
-// A stable radix sort, a digit of kDigitBits a pass from the lowest. A warp has a run of words, a round of 32 after
-// the other, and finds each word's place among its own of the same digit (returned): the words ahead of it in its
-// round, and those of earlier rounds, which next[digit] counts. The lanes of the same digit are found by a vote
-// for each of its bits: matching any value at once takes longer the more values there are, up to 0.6 us a round.
-constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-template <int ROUNDS>
-__device__ __forceinline__ void places_in_warp(const int (&digit)[ROUNDS], int rounds, int* next, int (&place)[ROUNDS]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r) {
-    if (r >= rounds) break;  // the same for the whole warp
-    uint32_t same = __ballot_sync(0xffffffffu, digit[r] >= 0);  // a digit of -1: no word
-#pragma unroll
-    for (int bit = 0; bit < kDigitBits; ++bit) {
-      const bool one = (digit[r] >> bit) & 1;
-      const uint32_t ones = __ballot_sync(0xffffffffu, one);
-      same &= one ? ones : ~ones;
-    }
-    const int ahead = __popc(same & ((1u << lane) - 1u));
-    int at = 0;
-    if (digit[r] >= 0) at = next[digit[r]];
-    __syncwarp();
-    if (digit[r] >= 0 && ahead == 0) next[digit[r]] = at + __popc(same);
-    __syncwarp();
-    place[r] = at + ahead;
-  }
-}
-
-// Up to kBlockMost positions, of a vocabulary whose tokens leave room for a position in 32 bits: one block sorts
-// words of token and position in shared memory, 4 to 8 us, while the others fill dE with zeros. (Counting the
-// smaller words for each position takes m^2 comparisons, 47 us at 16384; passes of several launches, below,
-// about 20.)
-constexpr int kPositionBits = 14, kBlockMost = 1 << kPositionBits;
-constexpr int kBlockThreads = 1024, kBlockWarps = kBlockThreads / 32, kBlockRounds = kBlockMost / kBlockThreads;
-constexpr uint32_t kBlockSmem = kBlockMost * 4 + kBlockWarps * kDigits * 4;
-bool by_one_block(int64_t m, int64_t vocab) { return m <= kBlockMost && vocab < (int64_t(1) << (32 - kPositionBits)); }
-__global__ void __launch_bounds__(kBlockThreads) sort_block_kernel(const void* tokens, int wide, int m, int vocab, int passes,
-                                                                   Sorted s, uint4* zero, int64_t zero16) {
-  extern __shared__ uint32_t sort_mem[];
-  __shared__ int warp_sum[kBlockWarps];
+// Up to kRankMost positions, of a vocabulary whose tokens leave room for a position in 32 bits: the token and
+// the position beside it in one word, no two alike, so that a position's place is the number of smaller words. A
+// warp counts for four positions, its lanes a share of the words each, four at a time: m^2 comparisons, but one
+// launch, beside whose blocks others fill dE with zeros (4096 positions 5 us, 8192 20; from there on the passes
+// below are faster: 16384 positions 47 us against 15).
+constexpr int kRankBits = 12, kRankMost = 1 << kRankBits;
+constexpr int kRankTile = 2048;  // words in shared memory at a time
+constexpr int kRankEach = 4;     // positions of a warp
+bool ranked(int64_t m, int64_t vocab) { return m <= kRankMost && vocab < (int64_t(1) << (32 - kRankBits)) - 1; }
+__global__ void __launch_bounds__(kThreads) rank_kernel(const void* tokens, int wide, int m, int vocab, Sorted s,
+                                                        int rank_blocks, uint4* zero, int64_t zero16) {
+  __shared__ uint4 words[kRankTile / 4];
   allow_next_grid();
   wait_for_prior_grids();
-  if (blockIdx.x != 0) {
-    fill_zeros(zero, zero16, blockIdx.x - 1, gridDim.x - 1);
+  if (static_cast<int>(blockIdx.x) >= rank_blocks) {
+    fill_zeros(zero, zero16, blockIdx.x - rank_blocks, gridDim.x - rank_blocks);
     return;
   }
-  uint32_t* words = sort_mem;
-  int* next = reinterpret_cast<int*>(sort_mem + kBlockMost);  // [warp][digit]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rounds = (m + kBlockThreads - 1) / kBlockThreads, first = warp * rounds * 32 + lane;
-  uint32_t word[kBlockRounds];
-  {
-    int t[kBlockRounds];
-    tokens_at(tokens, wide, first, min(m, first - lane + rounds * 32), vocab, t);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // none: `vocab`, behind every token
+  const auto word = [&](int t, int i) {
+    return (static_cast<uint32_t>(t < 0 ? vocab : t) << kRankBits) | static_cast<uint32_t>(i);
+  };
+  const int i0 = (static_cast<int>(blockIdx.x) * kWarps + warp) * kRankEach;
+  uint32_t mine[kRankEach];
+  int count[kRankEach];
 #pragma unroll
-    for (int r = 0; r < kBlockRounds; ++r)  // none: behind every token
-      word[r] = (static_cast<uint32_t>(t[r] < 0 ? vocab : t[r]) << kPositionBits) | static_cast<uint32_t>(first + r * 32);
-  }
-  for (int pass = 0; pass < passes; ++pass) {
-    const int shift = kPositionBits + pass * kDigitBits;
-    for (int d = tid; d < kBlockWarps * kDigits; d += kBlockThreads) next[d] = 0;
+  for (int e = 0; e < kRankEach; ++e)
+    mine[e] = i0 + e < m ? word(token_at(tokens, wide, i0 + e, vocab), i0 + e) : 0u, count[e] = 0;
+  for (int t0 = 0; t0 < m; t0 += kRankTile) {
+    constexpr int EACH = kRankTile / kThreads;
+    const int j0 = warp * EACH * 32 + lane;
+    int t[EACH];
+    tokens_at(tokens, wide, t0 + j0, m, vocab, t);
     __syncthreads();
-    int digit[kBlockRounds], place[kBlockRounds];
 #pragma unroll
-    for (int r = 0; r < kBlockRounds; ++r)
-      digit[r] = r < rounds && first + r * 32 < m ? static_cast<int>((word[r] >> shift) & (kDigits - 1)) : -1;
-    places_in_warp(digit, rounds, next + warp * kDigits, place);
-    __syncthreads();
-    // where each warp's words of a digit begin: over the warps (a thread a digit), then over the digits
-    int all = 0;
-    if (tid < kDigits) {
-#pragma unroll 8
-      for (int w = 0; w < kBlockWarps; ++w) {
-        const int n = next[w * kDigits + tid];
-        next[w * kDigits + tid] = all;
-        all += n;
-      }
-    }
-    int run = all;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int t = __shfl_up_sync(0xffffffffu, run, d);
-      if (lane >= d) run += t;
-    }
-    if (lane == 31) warp_sum[warp] = run;
-    __syncthreads();
-    int* start = reinterpret_cast<int*>(words);  // the words are in registers: their place holds the digits' starts
-    if (tid < kDigits) {
-      int ahead = run - all;
-      for (int w = 0; w < warp; ++w) ahead += warp_sum[w];
-      start[tid] = ahead;
+    for (int r = 0; r < EACH; ++r) {
+      const int j = j0 + 32 * r;
+      reinterpret_cast<uint32_t*>(words)[j] = t0 + j < m ? word(t[r], t0 + j) : 0xFFFFFFFFu;  // more than any
     }
     __syncthreads();
+    const int groups = (min(kRankTile, m - t0) + 3) / 4;
+#pragma unroll 4
+    for (int j = lane; j < groups; j += 32) {
+      const uint4 w = words[j];
 #pragma unroll
-    for (int r = 0; r < kBlockRounds; ++r)
-      if (digit[r] >= 0) place[r] += next[warp * kDigits + digit[r]] + start[digit[r]];
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kBlockRounds; ++r)
-      if (digit[r] >= 0) words[place[r]] = word[r];
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kBlockRounds; ++r)
-      if (digit[r] >= 0) word[r] = words[first + r * 32];
-    __syncthreads();
+      for (int e = 0; e < kRankEach; ++e)
+        count[e] += (w.x < mine[e] ? 1 : 0) + (w.y < mine[e] ? 1 : 0) + (w.z < mine[e] ? 1 : 0) + (w.w < mine[e] ? 1 : 0);
+    }
   }
 #pragma unroll
-  for (int r = 0; r < kBlockRounds; ++r) {
-    const int i = first + r * 32;
-    if (r < rounds && i < m) {
-      const int t = static_cast<int>(word[r] >> kPositionBits);
-      s.key[i] = t == vocab ? kNone : t, s.order[i] = static_cast<int>(word[r] & (kBlockMost - 1));
+  for (int e = 0; e < kRankEach; ++e) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) count[e] += __shfl_xor_sync(0xffffffffu, count[e], d);
+    if (i0 + e < m && lane == e) {
+      const int t = static_cast<int>(mine[e] >> kRankBits);
+      s.key[count[e]] = t == vocab ? kNone : t, s.order[count[e]] = i0 + e;
     }
   }
 }
 
-// More positions: three launches a pass. Block b has the positions from b kSortTile on, a warp a run of them.
-constexpr int kSortTile = 4096, kSortRun = kSortTile / kWarps, kSortRounds = kSortRun / 32;
+// More positions: a stable radix sort, a digit of kDigitBits a pass from the lowest, in two or three launches a
+// pass. Block b has the positions from b kSortTile on, a warp a run of them. They are few blocks: the others of each
+// launch fill a share of dE with zeros.
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kSortTile = 2048, kSortRun = kSortTile / kSortWarps, kSortRounds = kSortRun / 32;
 struct SortPass {
   const void* tokens;  // first pass: the tokens themselves; else null
   int wide, vocab, shift;
   Sorted in, out;
   int64_t m;
   int blocks;
-  int* count;  // [kDigits][blocks], then the places where they begin
+  int* count;  // [blocks][kDigits]; scanned: [kDigits][blocks], the places where they begin
+  bool scanned;
+  uint4* zero;  // this launch's share to fill
+  int64_t zero16;
 };
 // positions without a token have the digits of `vocab`, which no token has: behind the others
 __device__ __forceinline__ int sort_digit(const SortPass& p, int key) {
@@ -239,26 +191,29 @@ __device__ __forceinline__ void load_keys(const SortPass& p, int64_t first, int 
   for (int r = 0; r < kSortRounds; ++r) digit[r] = first + r * 32 < p.m ? sort_digit(p, key[r]) : -1;
 }
 
-__global__ void __launch_bounds__(kThreads) sort_count_kernel(const SortPass p, uint4* zero, int64_t zero16) {
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPass p) {
   __shared__ int count[kDigits];
   allow_next_grid();
   wait_for_prior_grids();
   if (static_cast<int>(blockIdx.x) >= p.blocks) {
-    fill_zeros(zero, zero16, blockIdx.x - p.blocks, gridDim.x - p.blocks);
+    fill_zeros(p.zero, p.zero16, blockIdx.x - p.blocks, gridDim.x - p.blocks);
     return;
   }
   int key[kSortRounds], digit[kSortRounds];
   load_keys(p, static_cast<int64_t>(blockIdx.x) * kSortTile + (threadIdx.x >> 5) * kSortRun + (threadIdx.x & 31), key, digit);
-  for (int d = threadIdx.x; d < kDigits; d += kThreads) count[d] = 0;
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < kSortRounds; ++r)
     if (digit[r] >= 0) atomicAdd(&count[digit[r]], 1);
   __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kThreads) p.count[static_cast<int64_t>(d) * p.blocks + blockIdx.x] = count[d];
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads)
+    p.count[p.scanned ? static_cast<int64_t>(d) * p.blocks + blockIdx.x : static_cast<int64_t>(blockIdx.x) * kDigits + d] = count[d];
 }
 
-// exclusive sums over all of count, in place, by one block
+// exclusive sums over all of count, in place, by one block: where there are so many blocks that each of them cannot
+// add up the others' counts itself
+constexpr int kOwnScan = 64;
 __global__ void __launch_bounds__(1024) sort_scan_kernel(int* count, int64_t n) {
   __shared__ int warp_sum[32];
   allow_next_grid();
@@ -291,10 +246,19 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(int* count, int64_t n) 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const SortPass p) {
-  __shared__ int next[kWarps][kDigits];  // per warp: counts, then where its words of a digit begin
+// A warp finds each position's place among its own of the same digit: those ahead of it in its round of 32, and
+// those of earlier rounds, which next[digit] counts. The lanes of the same digit are found by a vote for each of its
+// bits.
+__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortPass p) {
+  static_assert(kDigits == kSortThreads, "a thread a digit");
+  __shared__ int next[kSortWarps][kDigits];  // per warp: counts, then where its positions of a digit go
+  __shared__ int warp_sum[kSortWarps];
   allow_next_grid();
   wait_for_prior_grids();
+  if (static_cast<int>(blockIdx.x) >= p.blocks) {
+    fill_zeros(p.zero, p.zero16, blockIdx.x - p.blocks, gridDim.x - p.blocks);
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile + warp * kSortRun + lane;
   int key[kSortRounds], digit[kSortRounds], order[kSortRounds], place[kSortRounds];
@@ -305,18 +269,55 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const SortPass p
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) order[r] = first + r * 32 < p.m ? p.in.order[first + r * 32] : 0;
   }
-  for (int d = threadIdx.x; d < kWarps * kDigits; d += kThreads) (&next[0][0])[d] = 0;
-  __syncthreads();
-  places_in_warp(digit, kSortRounds, next[warp], place);
-  __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kThreads) {
-    int at = p.count[static_cast<int64_t>(d) * p.blocks + blockIdx.x];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int n = next[w][d];
-      next[w][d] = at;
-      at += n;
+  // where this block's positions of digit threadIdx.x begin
+  int begin = 0;
+  if (p.scanned) {
+    begin = p.count[static_cast<int64_t>(threadIdx.x) * p.blocks + blockIdx.x];
+  } else {
+    int all = 0;
+#pragma unroll 16
+    for (int b = 0; b < p.blocks; ++b) {
+      const int n = p.count[b * kDigits + static_cast<int>(threadIdx.x)];
+      begin += b < static_cast<int>(blockIdx.x) ? n : 0;
+      all += n;
     }
+    int run = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int t = __shfl_up_sync(0xffffffffu, run, d);
+      if (lane >= d) run += t;
+    }
+    if (lane == 31) warp_sum[warp] = run;
+    begin += run - all;
+  }
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) next[w][threadIdx.x] = 0;
+  __syncthreads();
+  if (!p.scanned)
+    for (int w = 0; w < warp; ++w) begin += warp_sum[w];
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    uint32_t same = __ballot_sync(0xffffffffu, digit[r] >= 0);  // a digit of -1: no position
+#pragma unroll
+    for (int bit = 0; bit < kDigitBits; ++bit) {
+      const bool one = (digit[r] >> bit) & 1;
+      const uint32_t ones = __ballot_sync(0xffffffffu, one);
+      same &= one ? ones : ~ones;
+    }
+    const int ahead = __popc(same & ((1u << lane) - 1u));
+    int at = 0;
+    if (digit[r] >= 0) at = next[warp][digit[r]];
+    __syncwarp();
+    if (digit[r] >= 0 && ahead == 0) next[warp][digit[r]] = at + __popc(same);
+    __syncwarp();
+    place[r] = at + ahead;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    const int n = next[w][threadIdx.x];
+    next[w][threadIdx.x] = begin;
+    begin += n;
   }
   __syncthreads();
 #pragma unroll
@@ -330,13 +331,15 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const SortPass p
 // ------------------------------------------------------------------------------------
 // sums over the ordered positions
 // ------------------------------------------------------------------------------------
-// A warp takes a run of kRun ordered positions and 256 columns. The stretches of one token that lie inside
+// A warp takes a run of RUN ordered positions and 256 columns. The stretches of one token that lie inside
 // the run are finished; the one that goes on at its end (and came from ahead or not) leaves its fp32 sum in
 // `open`, slot 1, and one that came from ahead and ends here in slot 0. All rows of the run are on their way at
 // once, each lane's 16 bytes of each through its own slots of shared memory, so that the loop over them is
 // rolled (with the rows in registers and the loop unrolled, its end of a stretch 17 times in the code, 65536
 // positions of 768 columns took 33 us).
-constexpr int kRun = 16, kRunWarps = 8;
+constexpr int kShortRun = 16, kLongRun = 32;
+int run_of(int64_t m) { return m <= 16384 ? kShortRun : kLongRun; }
+__host__ __device__ constexpr int warps_of_run(int run) { return 128 / run; }
 struct SumArgs {
   Sorted s;
   int64_t m;
@@ -373,28 +376,26 @@ __device__ __forceinline__ void put_row(const SumArgs& p, int key, int64_t col, 
   }
 }
 
-__global__ void __launch_bounds__(32 * kRunWarps) sum_runs_kernel(const SumArgs p) {
+template <int RUN>
+__global__ void __launch_bounds__(32 * warps_of_run(RUN)) sum_runs_kernel(const SumArgs p) {
+  constexpr int WARPS = warps_of_run(RUN);
   extern __shared__ uint4 run_mem[];
   allow_next_grid();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint4* rows = run_mem + warp * kRun * 32 + lane;  // 32 apart
-  const int64_t runs = (p.m + kRun - 1) / kRun, items = runs * p.slices, step = static_cast<int64_t>(gridDim.x) * kRunWarps;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRunWarps + warp; item < items; item += step) {
-    const int64_t run = item / p.slices, col = (item - run * p.slices) * 256 + lane * 8, first = run * kRun;
-    // lane j has position first + j's token and place; lane kRun the token behind the run, lane kRun + 1 the one
-    // ahead of it
-    const int64_t i = lane == kRun + 1 ? first - 1 : first + lane;
-    const bool there = lane <= kRun + 1 && i >= 0 && i < p.m;
-    const int key = there ? p.s.key[i] : -1;
-    const int at = there && lane < kRun ? p.s.order[i] : 0;
+  uint4* rows = run_mem + warp * RUN * 32 + lane;  // 32 apart
+  const int64_t runs = (p.m + RUN - 1) / RUN, items = runs * p.slices, step = static_cast<int64_t>(gridDim.x) * WARPS;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * WARPS + warp; item < items; item += step) {
+    const int64_t run = item / p.slices, col = (item - run * p.slices) * 256 + lane * 8, first = run * RUN;
+    const bool there = lane < RUN && first + lane < p.m;
+    const int key = there ? p.s.key[first + lane] : kNone, at = there ? p.s.order[first + lane] : 0;
+    const int before = first > 0 ? p.s.key[first - 1] : -1, behind = first + RUN < p.m ? p.s.key[first + RUN] : -1;
     const bool in = col < p.cols;
     // those without a token are behind the others
-    const int real = __popc(__ballot_sync(0xffffffffu, lane < kRun && key >= 0 && key != kNone));
-    const int behind = __shfl_sync(0xffffffffu, key, kRun), before = __shfl_sync(0xffffffffu, key, kRun + 1);
+    const int real = __popc(__ballot_sync(0xffffffffu, key != kNone));
     if (real == 0) continue;
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
+    for (int j = 0; j < RUN; ++j) {
       const int pos = __shfl_sync(0xffffffffu, at, j);
       if (in && j < real)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(rows + j * 32)), "l"(p.dy + pos * p.cols + col)
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(32 * kRunWarps) sum_runs_kernel(const SumArgs 
     const int next = __shfl_down_sync(0xffffffffu, key, 1);
     const uint32_t ends = __ballot_sync(0xffffffffu, lane < real && (lane + 1 == real || next != key));
     bool from_ahead = __shfl_sync(0xffffffffu, key, 0) == before;
-    const bool goes_on = real == kRun && __shfl_sync(0xffffffffu, key, kRun - 1) == behind;
+    const bool goes_on = real == RUN && __shfl_sync(0xffffffffu, key, RUN - 1) == behind;
     float* open = p.open + run * 2 * p.cols + col;
     asm volatile("cp.async.wait_all;" ::: "memory");
     f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(32 * kRunWarps) sum_runs_kernel(const SumArgs 
       }
       if (!((ends >> j) & 1u)) continue;  // the same for the whole warp
       const int token = __shfl_sync(0xffffffffu, key, j);
-      const bool leaves = goes_on && j == kRun - 1;
+      const bool leaves = goes_on && j == RUN - 1;
       if (in) {
         if (leaves || from_ahead) {
           ulonglong2* to = reinterpret_cast<ulonglong2*>(open + (leaves ? p.cols : 0));
@@ -449,22 +450,23 @@ __device__ __forceinline__ void add_open(const SumArgs& p, int64_t from, int64_t
     sum[0] = f2_add(sum[0], x.x), sum[1] = f2_add(sum[1], x.y), sum[2] = f2_add(sum[2], y.x), sum[3] = f2_add(sum[3], y.y);
   }
 }
+template <int RUN>
 __global__ void __launch_bounds__(kCrossThreads) sum_crossing_kernel(const SumArgs p, int64_t few_blocks) {
   __shared__ f2 part[kCrossWarps][32][4];
   allow_next_grid();
   wait_for_prior_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t runs = (p.m + kRun - 1) / kRun;
+  const int64_t runs = (p.m + RUN - 1) / RUN;
   const int* key = p.s.key;
   f2 sum[4];
   if (blockIdx.x < few_blocks) {
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kCrossWarps + warp, b = 1 + item / p.slices;  // between b - 1 and b
     if (b >= runs) return;
-    const int64_t first = b * kRun, col = (item - (b - 1) * p.slices) * 256 + lane * 8;
+    const int64_t first = b * RUN, col = (item - (b - 1) * p.slices) * 256 + lane * 8;
     // whether the runs from b on begin with the token; lanes in order: the first that does not
     const int64_t r = b + lane;
-    const int mine = r < runs ? key[r * kRun] : -1, token = __shfl_sync(0xffffffffu, mine, 0);
-    const int before = key[first - 1], earlier = b > 1 ? key[first - kRun - 1] : -1;
+    const int mine = r < runs ? key[r * RUN] : -1, token = __shfl_sync(0xffffffffu, mine, 0);
+    const int before = key[first - 1], earlier = b > 1 ? key[first - RUN - 1] : -1;
     if (token == kNone || before != token || earlier == token) return;  // none crosses here, or it crossed before
     const uint32_t other = ~__ballot_sync(0xffffffffu, mine == token);
     const int more = other ? __ffs(other) - 1 : 32;  // runs from b on that it touches
@@ -475,18 +477,18 @@ __global__ void __launch_bounds__(kCrossThreads) sum_crossing_kernel(const SumAr
   }
   const int64_t item = blockIdx.x - few_blocks, at = item / p.slices * (kFewRuns / 2);  // a run
   const int64_t col = (item - item / p.slices * p.slices) * 256 + lane * 8;
-  const int token = key[at * kRun];
+  const int token = key[at * RUN];
   if (token == kNone) return;
   // the runs ahead that it touches
   const int64_t r = at - 1 - lane;
-  const uint32_t other = ~__ballot_sync(0xffffffffu, r >= 0 && key[r * kRun + kRun - 1] == token);
+  const uint32_t other = ~__ballot_sync(0xffffffffu, r >= 0 && key[r * RUN + RUN - 1] == token);
   const int ahead = other ? __ffs(other) - 1 : 32;
   // that one's, if it begins the run kFewRuns / 2 ahead too: sure where it touches runs before that
-  if (ahead > kFewRuns / 2 || (ahead == kFewRuns / 2 && key[(at - kFewRuns / 2) * kRun] == token)) return;
+  if (ahead > kFewRuns / 2 || (ahead == kFewRuns / 2 && key[(at - kFewRuns / 2) * RUN] == token)) return;
   int64_t last = at;
   for (int64_t r0 = at + 1;; r0 += kCrossThreads) {
     const int64_t q = r0 + threadIdx.x;
-    const int n = __syncthreads_count(q < runs && key[q * kRun] == token);
+    const int n = __syncthreads_count(q < runs && key[q * RUN] == token);
     last += n;
     if (n < kCrossThreads) break;
   }
@@ -546,12 +548,12 @@ struct BackwardSpace {
     int bits = 1;
     while (bits < 31 && (vocab >> bits) != 0) ++bits;  // of keys 0 .. vocab
     passes = (bits + kDigitBits - 1) / kDigitBits;
-    if (!by_one_block(m, vocab)) {
+    if (!ranked(m, vocab)) {
       sort_blocks = (m + kSortTile - 1) / kSortTile;
       if (passes > 1) key[1] = take(4 * static_cast<uint64_t>(m)), order[1] = take(4 * static_cast<uint64_t>(m));
       count = take(4 * static_cast<uint64_t>(sort_blocks) * kDigits);
     }
-    open = take(8 * static_cast<uint64_t>((m + kRun - 1) / kRun) * static_cast<uint64_t>(cols));
+    open = take(8 * static_cast<uint64_t>((m + run_of(m) - 1) / run_of(m)) * static_cast<uint64_t>(cols));
   }
 };
 
@@ -626,18 +628,11 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
   const int wide = token_bytes == 8 ? 1 : 0;
   Sorted sorted{ints(sp.key[0]), ints(sp.order[0])};
   cudaError_t e = cudaSuccess;
-  if (by_one_block(m_tokens, vocab)) {
-    static OncePerDevice once;
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-      e = once.run(dev, [] {
-        return cudaFuncSetAttribute(sort_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBlockSmem));
-      });
-    const int64_t fill = std::min<int64_t>((zero16 + 2 * kBlockThreads - 1) / (2 * kBlockThreads), num_sms() - 1);
-    if (e == cudaSuccess)
-      e = launch_overlapped(sort_block_kernel, dim3(static_cast<unsigned>(1 + fill)), dim3(kBlockThreads), kBlockSmem, 1, st, tokens,
-                            wide, static_cast<int>(m_tokens), static_cast<int>(vocab), sp.passes, sorted, zero, zero16);
+  if (ranked(m_tokens, vocab)) {
+    const int64_t rank_blocks = (m_tokens + kRankEach * kWarps - 1) / (kRankEach * kWarps);
+    e = launch_overlapped(rank_kernel, dim3(static_cast<unsigned>(rank_blocks + zero_blocks)), dim3(kThreads), 0, 1, st, tokens,
+                          wide, static_cast<int>(m_tokens), static_cast<int>(vocab), sorted, static_cast<int>(rank_blocks),
+                          zero, zero16);
   } else {
     for (int pass = 0; pass < sp.passes && e == cudaSuccess; ++pass) {
       SortPass p;
@@ -648,37 +643,49 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
       const int to = (sp.passes - 1 - pass) & 1;
       p.in = {ints(sp.key[to ^ 1]), ints(sp.order[to ^ 1])};
       p.out = {ints(sp.key[to]), ints(sp.order[to])};
-      p.count = ints(sp.count);
-      const int64_t more = pass == 0 ? zero_blocks : 0;
-      e = launch_overlapped(sort_count_kernel, dim3(static_cast<unsigned>(sp.sort_blocks + more)), dim3(kThreads), 0, 1, st, p,
-                            zero, zero16);
-      if (e == cudaSuccess)
+      p.count = ints(sp.count), p.scanned = sp.sort_blocks > kOwnScan;
+      // of every four parts of a pass's share of dE, one beside the counts and three beside the placing, which takes
+      // three times as long
+      const auto part = [&](int64_t i) { return zero16 * (4 * pass + i) / (4 * sp.passes); };
+      const auto share = [&](int64_t from, int64_t to) {
+        p.zero = zero + from, p.zero16 = to - from;
+        return static_cast<unsigned>(sp.sort_blocks + std::min<int64_t>((p.zero16 + 4 * kSortThreads - 1) / (4 * kSortThreads),
+                                                                       static_cast<int64_t>(num_sms()) * 4));
+      };
+      const unsigned counting = share(part(0), part(1));
+      e = launch_overlapped(sort_count_kernel, dim3(counting), dim3(kSortThreads), 0, 1, st, p);
+      if (e == cudaSuccess && p.scanned)
         e = launch_overlapped(sort_scan_kernel, dim3(1), dim3(1024), 0, 1, st, p.count, sp.sort_blocks * kDigits);
+      const unsigned placing = share(part(1), part(4));
       if (e == cudaSuccess)
-        e = launch_overlapped(sort_scatter_kernel, dim3(static_cast<unsigned>(sp.sort_blocks)), dim3(kThreads), 0, 1, st, p);
+        e = launch_overlapped(sort_scatter_kernel, dim3(placing), dim3(kSortThreads), 0, 1, st, p);
     }
   }
-  const int64_t runs = (m_tokens + kRun - 1) / kRun, slices = (cols + 255) / 256;
+  const int run = run_of(m_tokens);
+  const int64_t runs = (m_tokens + run - 1) / run, slices = (cols + 255) / 256;
   SumArgs a;
   a.s = sorted, a.m = m_tokens, a.dy = dY, a.cols = cols, a.slices = static_cast<int>(slices), a.scale = scale;
   a.de32 = dE, a.de16 = dE_bf16, a.add = accumulate != 0, a.open = reinterpret_cast<float*>(ws + sp.open);
-  if (e == cudaSuccess) {
-    const int64_t blocks = std::min<int64_t>((runs * slices + kRunWarps - 1) / kRunWarps, static_cast<int64_t>(num_sms()) * 64);
-    constexpr uint32_t smem = kRunWarps * kRun * 512;
+  const auto sums = [&](auto length) {
+    constexpr int RUN = decltype(length)::value, WARPS = warps_of_run(RUN);
+    constexpr uint32_t smem = WARPS * RUN * 512;
+    const int64_t blocks = std::min<int64_t>((runs * slices + WARPS - 1) / WARPS, static_cast<int64_t>(num_sms()) * 64);
     static OncePerDevice once;
     int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-      e = once.run(dev, [] {
-        return cudaFuncSetAttribute(sum_runs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t q = cudaGetDevice(&dev);
+    if (q == cudaSuccess)
+      q = once.run(dev, [] {
+        return cudaFuncSetAttribute(sum_runs_kernel<RUN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       });
-    if (e == cudaSuccess)
-      e = launch_overlapped(sum_runs_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kRunWarps), smem, 1, st, a);
-    if (e == cudaSuccess && runs > 1) {
+    if (q == cudaSuccess)
+      q = launch_overlapped(sum_runs_kernel<RUN>, dim3(static_cast<unsigned>(blocks)), dim3(32 * WARPS), smem, 1, st, a);
+    if (q == cudaSuccess && runs > 1) {
       const int64_t few = ((runs - 1) * slices + kCrossWarps - 1) / kCrossWarps;
       const int64_t many = (runs + kFewRuns / 2 - 1) / (kFewRuns / 2) * slices;
-      e = launch_overlapped(sum_crossing_kernel, dim3(static_cast<unsigned>(few + many)), dim3(kCrossThreads), 0, 1, st, a, few);
+      q = launch_overlapped(sum_crossing_kernel<RUN>, dim3(static_cast<unsigned>(few + many)), dim3(kCrossThreads), 0, 1, st, a, few);
     }
-  }
+    return q;
+  };
+  if (e == cudaSuccess) e = run == kShortRun ? sums(ActTag<kShortRun>{}) : sums(ActTag<kLongRun>{});
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }

@@ -9,6 +9,7 @@ Python or CPU fallback: if the shared library is missing the import fails.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from pathlib import Path
 
@@ -805,17 +806,25 @@ def _ids(t, name: str, dev: int):
     return m, _is(t, (m,), t.dtype, name, dev), 8 if t.dtype is torch.int64 else 4
 
 
-def _space(workspace, nbytes, device, stream):
-    """(tensor to keep, pointer, bytes) of a call's workspace: the caller's, or one taken for this call."""
-    if workspace is None:
-        workspace = _call_workspace(nbytes(), device, stream)
-    return workspace, _dev(workspace, torch.uint8, "workspace"), workspace.numel()
-
-
 def _bytes(fn, *args) -> int:
     b = C.c_uint64()
     _check(fn(*args, C.byref(b)))
     return b.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes_once(name: str, dev: int, *sizes) -> int:
+    """A call's workspace bytes, which follow from its sizes and the device alone."""
+    return _bytes(getattr(_lib, name), *sizes)
+
+
+def _space(workspace, device, stream, name: str, dev: int, *sizes):
+    """(tensor to keep, pointer, bytes) of a call's workspace: the caller's, or one taken for this call."""
+    if workspace is None:
+        nbytes = _bytes_once(name, dev, *sizes)
+        workspace = _call_workspace(nbytes, device, stream)
+        return workspace, workspace.data_ptr(), nbytes
+    return workspace, _dev(workspace, torch.uint8, "workspace"), workspace.numel()
 
 
 def fsdp_embedding_forward(e_shards, tokens, Y, vocab=None, scale: float = 1.0, stream=None):
@@ -845,7 +854,7 @@ def fsdp_embedding_backward(dY, tokens, dE, vocab=None, scale: float = 1.0, accu
     dy = _is(dY, (m, k), torch.bfloat16, "dY", dev)
     wide = dE.dtype == torch.float32
     de = _is(dE, (rows, k), torch.float32 if wide else torch.bfloat16, "dE", dev)
-    workspace, ws, nbytes = _space(workspace, lambda: fsdp_embedding_backward_workspace(m, vocab, k), dY.device, stream)
+    workspace, ws, nbytes = _space(workspace, dE.device, stream, "fsdp_embedding_backward_workspace", dev, m, vocab, k)
     _check(_lib.fsdp_embedding_backward(dy, ids, width, m, rows, vocab, k, scale, 1 if accumulate else 0,
                                         de if wide else None, None if wide else de, ws, nbytes, _stream(stream)))
 
@@ -877,7 +886,7 @@ def fsdp_layernorm_backward(dY, X, mean, rstd, dX, gamma=None, residual=None, dg
     px = _is(X, shape, bf, "X", dev)
     ws, nbytes = None, 0
     if workspace is not None or dgamma is not None or dbeta is not None:
-        workspace, ws, nbytes = _space(workspace, lambda: fsdp_layernorm_backward_workspace(rows, cols), X.device, stream)
+        workspace, ws, nbytes = _space(workspace, X.device, stream, "fsdp_layernorm_backward_workspace", dev, rows, cols)
     _check(_lib.fsdp_layernorm_backward(
         _is(dY, shape, bf, "dY", dev), px, _is(mean, (rows,), f32, "mean", dev), _is(rstd, (rows,), f32, "rstd", dev),
         rows, cols, _is(gamma, (cols,), bf, "gamma", dev), _is(residual, shape, bf, "residual", dev),
@@ -899,7 +908,7 @@ def fsdp_vocab_loss_forward(w_shards, X, labels, loss, lse, total=None, vocab=No
     m, ids, width = _ids(labels, "labels", dev)
     vocab = n * rs if vocab is None else vocab
     x = _is(X, (m, k), torch.bfloat16, "X", dev)
-    workspace, ws, nbytes = _space(workspace, lambda: fsdp_vocab_loss_forward_workspace(m, vocab), X.device, stream)
+    workspace, ws, nbytes = _space(workspace, X.device, stream, "fsdp_vocab_loss_forward_workspace", dev, m, vocab)
     _check(_lib.fsdp_vocab_loss_forward(n, w, n * rs, vocab, k, x, m, ids, width, _is(loss, (m,), f32, "loss", dev),
                                         _is(lse, (m,), f32, "lse", dev), _is(total, (2,), f32, "total", dev), ws, nbytes,
                                         _stream(stream)))
@@ -921,8 +930,8 @@ def fsdp_vocab_loss_backward(w_shards, X, labels, lse, dX, dW, vocab=None, dloss
     rows = n * rs
     vocab = rows if vocab is None else vocab
     x = _is(X, (m, k), bf, "X", dev)
-    workspace, ws, nbytes = _space(workspace, lambda: fsdp_vocab_loss_backward_workspace(m, vocab, k, piece), X.device,
-                                   stream)
+    workspace, ws, nbytes = _space(workspace, X.device, stream, "fsdp_vocab_loss_backward_workspace", dev, m, vocab, k,
+                                   piece)
     _check(_lib.fsdp_vocab_loss_backward(
         n, w, rows, vocab, k, x, m, ids, width, _is(lse, (m,), f32, "lse", dev), _is(dloss, (m,), f32, "dloss", dev),
         _is(total, (2,), f32, "total", dev), scale, _is(dX, (m, k), bf, "dX", dev), _is(dW, (rows, k), bf, "dW", dev),

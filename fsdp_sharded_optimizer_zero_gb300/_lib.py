@@ -921,9 +921,9 @@ def fsdp_vocab_loss_backward_workspace(m_tokens: int, vocab: int, k_in: int, pie
 
 def fsdp_vocab_loss_backward(w_shards, X, labels, lse, dX, dW, vocab=None, dloss=None, total=None, scale: float = 1.0,
                              piece: int = 0, workspace=None, stream=None):
-    """dX [m, k] and dW [rows, k] (bf16; either may be None) of the sum over the counted tokens of scale *
-    dloss[i] / total[1] * loss[i]; dloss (fp32 [m]) and total (of the forward: the gradient of the mean)
-    are 1 where None. piece: columns of the vocabulary at a time (a multiple of 256; 0: chosen)."""
+    """dX [m, k] and dW [rows, k] (bf16; either may be None) of scale / total[1] times the sum over the counted tokens
+    of dloss[i] * loss[i]; total (of the forward: the gradient of the mean) and dloss (fp32 [m], what differs from
+    token to token) are 1 where None. piece: columns of the vocabulary at a time (a multiple of 256; 0: chosen)."""
     dev, bf, f32 = _device(), torch.bfloat16, torch.float32
     n, rs, k, w = _shards(w_shards, "w_shards", dev)
     m, ids, width = _ids(labels, "labels", dev)

@@ -178,7 +178,8 @@ __device__ __forceinline__ void epilogue4(const LinearParams& p, int row, int co
   const size_t at = static_cast<size_t>(row) * p.n + col;
   const bool live = row < p.m && col < p.n;
   if constexpr (OP == OP_DW) {
-    v[0] = f2_mul(v[0], f2_both(p.scale)), v[1] = f2_mul(v[1], f2_both(p.scale));
+    const f2 scale = f2_both(dw_scale(p.scale, p.count));
+    v[0] = f2_mul(v[0], scale), v[1] = f2_mul(v[1], scale);
     if (!live) return;
     if (p.y32) __stcs(reinterpret_cast<ulonglong2*>(p.y32 + at), make_ulonglong2(v[0], v[1]));
     else *reinterpret_cast<uint2*>(p.y + at) = make_uint2(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]));
@@ -238,6 +239,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   if constexpr (OP != OP_DW) side_src = OP == OP_DX && p.z_in ? p.z_in : p.res;
   uint32_t i = 0, bias_turn = 0;
   uint32_t stores = 0;  // fp32 dW: bulk stores this warp has made
+  const float scale = OP == OP_DW ? dw_scale(p.scale, p.count) : 1.0f;
   const bool shared_bias = OP == OP_FWD && p.bias;
   bool stop = false;  // this warp gave up a wait
   for (int tile = pair; tile < num_m * num_n && (shared_bias || !stop); tile += pairs, bias_turn ^= 1u) {
@@ -284,7 +286,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
       if (OP == OP_DW && p.y32) {
         if (chunk > 0 && lane == 0) bulk_wait_group_all();  // this tile's earlier sums are in memory
-        store_sums<C::EPI_COLS>(&p.out, taddr, r0, c0, p.n, p.scale, chunk > 0, stage, stores, lane);
+        store_sums<C::EPI_COLS>(&p.out, taddr, r0, c0, p.n, scale, chunk > 0, stage, stores, lane);
       } else {
         // 32 columns at a time, rolled: unrolled by two the code is twice as long for the instruction
         // cache that the producer and MMA loops share (8192 x 2304 from 768: 32.2 us, rolled 30.0). The
@@ -309,7 +311,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
           for (int j = 0; j < 16; ++j) v[j] = f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
           uint4 w[4];
           if constexpr (OP == OP_DW) {
-            const f2 s = f2_both(p.scale);
+            const f2 s = f2_both(scale);
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = f2_mul(v[j], s);
           } else {
@@ -714,11 +716,11 @@ int check_shards(LinearParams* p, int n, const zero_bf16* const w_shards[], int6
 }  // namespace
 
 int launch_linear_dw(const uint16_t* dZ, int64_t ldz, const uint16_t* x, int64_t m_tokens, int64_t rows_out, int64_t k_in,
-                     uint16_t* dW, cudaStream_t st, const char* who) {
+                     float scale, const float* count, uint16_t* dW, cudaStream_t st, const char* who) {
   LinearParams p;
   memset(&p, 0, sizeof(p));
   p.m = static_cast<int>(rows_out), p.n = static_cast<int>(k_in), p.k = static_cast<int>(m_tokens);
-  p.scale = 1.0f, p.y = dW;
+  p.scale = scale, p.count = count, p.y = dW;
   return launch<OP_DW>(p, Operands{0, nullptr, dZ, ldz, x}, st, who);
 }
 

@@ -4,11 +4,14 @@
 //   forward   lse_i = log sum_v exp Z_iv, loss_i = lse_i - Z_i[label]: each 256 x 256 tile of Z leaves, per
 //             row and 128 columns, its maximum and the sum of exponentials below it (2 fp32), joined after
 //   backward  in pieces of the vocabulary: Z again from X and the piece of W, dZ = (exp(Z - lse) - onehot) w
-//             in bf16, then the piece's rows of dW = dZ^T X, and dX += dZ W
+//             in bf16, then the piece's rows of dW = c dZ^T X, and dX += c dZ W
 //
 // The products run in linear_wide_kernel; what is here are its epilogues and the joining passes. Softmax
 // statistics and all sums are fp32. dZ is rounded to bf16, as the gradient of a linear unit's output is
-// everywhere in the library: the tensor cores multiply bf16, and its gradients are bf16.
+// everywhere in the library: the tensor cores multiply bf16, and its gradients are bf16. The factor c that all tokens
+// share (the loss's scale, one over the count) is left for the fp32 sums: in dZ it would be rounded alike in every
+// label's element, which is about -c, and so bias every gradient by up to 2^-9 (8192 x 32000 from 4096 with c in dZ:
+// 3.7e-3 of the gradients' norm off, now 1.7e-3, the outputs' own rounding).
 #include "linear_wide.cuh"
 
 namespace zgb {
@@ -28,8 +31,7 @@ struct VocabParams : LinearParams {
   float2* part;            // lse: [2 ceil(n / 256)][m]: base-2 maximum, sum of 2^(z log2 e - maximum)
   unsigned int* ticket;    // lse: set to 0 for the kernel that joins the parts
   float* z_label;          // lse: [m]
-  const float *lse, *dloss, *total;
-  float gscale;
+  const float *lse, *dloss;
 };
 
 template <> struct Wide<OP_LSE> {
@@ -89,9 +91,8 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   const int part = (warp - 2) >> 2;  // which of the quarter's warps
   uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;  // (not OP_LSE)
   uint32_t i = 0, stores = 0;
-  float gscale = p.gscale;
+  const float scale = OP == OP_DX_SPLIT ? dw_scale(p.scale, p.count) : 1.0f;
   if (OP == OP_LSE && pair == 0 && rank == 0 && warp == 2 && lane == 0) *p.ticket = 0u;
-  if (OP == OP_DLOGITS && p.total) gscale = __fdiv_rn(gscale, fmaxf(p.total[1], 1.0f));
   const int tiles = num_m * num_n, items = wide_items<OP>(p, tiles);
   for (int item = pair; item < items; item += pairs, ++i) {
     const int part_k = OP == OP_DX_SPLIT ? item / tiles : 0;
@@ -109,7 +110,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       target = counted ? label - p.w_row0 : -1;
       if (OP == OP_DLOGITS && counted) {
         lse2 = __fmul_rn(__ldg(p.lse + row), kLog2e);
-        weight = p.dloss ? __fmul_rn(__ldg(p.dloss + row), gscale) : gscale;
+        weight = p.dloss ? __ldg(p.dloss + row) : 1.0f;
       }
     }
     const uint32_t a = i & 1u, u = i >> 1;
@@ -118,7 +119,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
     if constexpr (OP == OP_DX_SPLIT) {
       if (p.y32) {
-        if (r0 < p.m) store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, 1.0f, p.add, stage, stores, lane);
+        if (r0 < p.m) store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, scale, p.add, stage, stores, lane);
       } else {
 #pragma unroll 1
         for (int c = 0; c < C::EPI_COLS; c += 32) {
@@ -128,13 +129,13 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
           uint32_t r[32];
           tmem_ld_32cols(taddr + c, r);
           if (col0 >= p.n) continue;
+          const auto two = [&](int i) {
+            return f2_to_bf16x2(f2_mul(f2_make(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_both(scale)));
+          };
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) =
-                make_uint4(pack_bf16x2(__uint_as_float(r[8 * j]), __uint_as_float(r[8 * j + 1])),
-                           pack_bf16x2(__uint_as_float(r[8 * j + 2]), __uint_as_float(r[8 * j + 3])),
-                           pack_bf16x2(__uint_as_float(r[8 * j + 4]), __uint_as_float(r[8 * j + 5])),
-                           pack_bf16x2(__uint_as_float(r[8 * j + 6]), __uint_as_float(r[8 * j + 7])));
+                make_uint4(two(8 * j), two(8 * j + 2), two(8 * j + 4), two(8 * j + 6));
           if (h == 1 || col0 + 32 >= p.n) {
             __syncwarp();
             stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.n, p.n, lane);
@@ -543,6 +544,7 @@ extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_sh
   uint16_t* dz = static_cast<uint16_t*>(workspace);
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.dz_bytes);
   const int m = static_cast<int>(m_tokens), k = static_cast<int>(k_in), ld = static_cast<int>(plan.ld);
+  const float* count = total ? total + 1 : nullptr;
   cudaError_t e = cudaSuccess;
   if (dW && rows_out > vocab)  // the padding's rows
     e = cudaMemsetAsync(dW + vocab * k_in, 0, static_cast<size_t>(rows_out - vocab) * static_cast<size_t>(k_in) * 2, st);
@@ -555,15 +557,15 @@ extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_sh
     p.w_row0 = static_cast<int>(c0), p.vocab = static_cast<int>(vocab);
     p.cols = (cols + 7) / 8 * 8, p.ld = ld, p.y = dz;
     p.labels = labels, p.labels_wide = label_bytes == 8;
-    p.lse = lse, p.dloss = dloss, p.total = total, p.gscale = scale;
+    p.lse = lse, p.dloss = dloss;
     if ((rc = encode(&p.a, X, m, k, k, BK, 128, false, who))) return rc;
     if ((rc = launch_product<OP_DLOGITS>(p, w, true, st, who))) return rc;
-    if (dW && (rc = launch_linear_dw(dz, ld, X, m, cols, k, dW + c0 * k_in, st, who))) return rc;
+    if (dW && (rc = launch_linear_dw(dz, ld, X, m, cols, k, scale, count, dW + c0 * k_in, st, who))) return rc;
     if (!dX) continue;
     VocabParams d;
     memset(static_cast<void*>(&d), 0, sizeof(d));
     d.m = m, d.n = k, d.k = cols;
-    d.w_row0 = p.w_row0, d.vocab = p.vocab;
+    d.w_row0 = p.w_row0, d.vocab = p.vocab, d.scale = scale, d.count = count;
     // a shorter last piece may have fewer K blocks than there are parts: a part has one at least
     d.splits = static_cast<int>(std::min<int64_t>(plan.splits, (cols + BK - 1) / BK));
     d.slot_rows = static_cast<int>(plan.slot_rows), d.add = c0 > 0;

@@ -175,10 +175,10 @@ bool fsdp_fused_gather_ok(int n_ranks, int64_t rows_out);
 // act, and the kept activation it reads: bf16 z, or codes and scales (ZERO_ERR_INVALID_ARG)
 int check_kept_activation(const uint16_t* z, const int8_t* codes, const uint8_t* scales, int act, const char* who);
 unsigned int fsdp_linear_read_clear_error();
-// dW [rows_out, k_in] bf16 = dZ^T X, dZ [m_tokens, rows_out] with rows ldz elements apart (a multiple of 8;
-// rows_out need not be one), X [m_tokens, k_in]
+// dW [rows_out, k_in] bf16 = scale / max(*count, 1) dZ^T X (count nullable: scale alone), dZ [m_tokens, rows_out] with
+// rows ldz elements apart (a multiple of 8; rows_out need not be one), X [m_tokens, k_in]
 int launch_linear_dw(const uint16_t* dZ, int64_t ldz, const uint16_t* x, int64_t m_tokens, int64_t rows_out, int64_t k_in,
-                     uint16_t* dW, cudaStream_t st, const char* who);
+                     float scale, const float* count, uint16_t* dW, cudaStream_t st, const char* who);
 
 // ---- loss over the vocabulary (fsdp_vocab_loss.cu) ----
 unsigned int fsdp_vocab_loss_read_clear_error();

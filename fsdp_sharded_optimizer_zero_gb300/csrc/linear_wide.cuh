@@ -59,6 +59,7 @@ struct LinearParams {
   int8_t* zc;                     // fwd: ... in 8 bits
   uint8_t* zs;
   float scale;                    // dw
+  const float* count;             // dw: nullable, what the scale is divided by (1 at least)
   int chunks, chunk_blocks;       // dw, fp32: the contraction in chunks of chunk_blocks K blocks (1 chunk otherwise)
 };
 
@@ -378,6 +379,11 @@ __device__ __forceinline__ bool any_of_128(int id, bool mine) {
       : "r"(id), "r"(mine ? 1u : 0u)
       : "memory");
   return any != 0;
+}
+
+// what a weight gradient's sums are multiplied by
+__device__ __forceinline__ float dw_scale(float scale, const float* count) {
+  return count ? __fdiv_rn(scale, fmaxf(__ldg(count), 1.0f)) : scale;
 }
 
 // fp32 output: this warp's 32 rows (from row `row` of `out`) and COLS columns (from c0, those below n) of

@@ -668,12 +668,13 @@ ZERO_API int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_shard
 ZERO_API int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab, int64_t k_in, int64_t piece,
                                                 uint64_t* bytes);
 
-/* Gradients of sum over the counted tokens of w[i] loss[i], w[i] = scale * dloss[i] / max(total[1], 1), with
+/* Gradients of c times the sum over the counted tokens of dloss[i] loss[i], c = scale / max(total[1], 1), with
  * dloss (fp32 [m_tokens]) and total (as the forward wrote it) nullable, then 1: dZ = (exp(Z - lse) -
- * onehot(label)) w, computed piece by piece from X and W again and rounded to bf16; dX = bf16(dZ W)
- * [m_tokens, k_in] and dW = bf16(dZ^T X) [rows_out, k_in], one of them nullable. A token that is not
- * counted has zeros in dZ and dX whatever its logits, but its row of X enters dW's product, times zero: it
- * has to be finite. The result's bits depend on piece through the rounding of fp32 sums only. */
+ * onehot(label)) dloss, computed piece by piece from X and W again and rounded to bf16; dX = bf16(c dZ W)
+ * [m_tokens, k_in] and dW = bf16(c dZ^T X) [rows_out, k_in], c applied to the fp32 sums, one of the two nullable. (A
+ * factor that all tokens share belongs in scale: in dloss it is rounded alike with every label's element.) A token
+ * that is not counted has zeros in dZ and dX whatever its logits, but its row of X enters dW's product, times zero:
+ * it has to be finite. The result's bits depend on piece through the rounding of fp32 sums only. */
 ZERO_API int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
                                       int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
                                       int label_bytes, const float* lse, const float* dloss, const float* total,

@@ -97,12 +97,8 @@ class Case:
         assert torch.equal(self.forward(z, total=False)[0], loss)
         return loss, lse, total
 
-    def weights(self, scale, dloss, total):
-        w = torch.full((self.m,), float(scale), dtype=torch.float64, device=DEV)
-        if dloss is not None:
-            w = w * dloss.double()
-        if total is not None:
-            w = w / max(1.0, float(total[1]))
+    def weights(self, dloss):
+        w = torch.ones(self.m, dtype=torch.float64, device=DEV) if dloss is None else dloss.double()
         return torch.where(self.real, w, 0.0)
 
     def backward(self, z, lse, scale=1.0, dloss=None, total=None, piece=0, dx=True, dw=True, **kw):
@@ -118,23 +114,23 @@ class Case:
         return dX[:-64].view(self.m, self.k) if dx else None, dW[:-64].view(self.rows, self.k) if dw else None
 
     def check_backward(self, z, lse, dX, dW, scale, dloss, total, pieces):
-        w = self.weights(scale, dloss, total)[:, None]
+        w = self.weights(dloss)[:, None]
+        c = float(scale) / (1.0 if total is None else max(1.0, float(total[1])))  # on the sums: 2 roundings
         p = torch.exp(self.z - lse.double()[:, None])
         hot = torch.zeros_like(p).scatter_(1, self.at[:, None], 1.0) * self.real[:, None]
         dz = (p - hot) * w
-        # z, the argument's roundings (of z, lse and their difference), the exponential, the weight's product,
-        # the weight itself (2 roundings)
+        # z, the argument's roundings (of z, lse and their difference), the exponential, the weight's product
         size = self.z.abs() + lse.double().abs()[:, None] + 1
         e = w.abs() * (p * (self.ez + 4 * U * size + 2.0 ** -20) * 1.1 + 4 * U * hot) + 4 * U * dz.abs()
         lo, hi = ((dz + s * e).float().to(BF).double() for s in (-1.0, 1.0))
         mid, rad = (lo + hi) / 2, (hi - lo) / 2
-        want = mid @ self.w64
-        bound = rad @ self.w64.abs() + (self.vocab + 32 + pieces) * SUM * (mid.abs() @ self.w64.abs())
+        want = c * (mid @ self.w64)
+        bound = abs(c) * (rad @ self.w64.abs() + (self.vocab + 32 + pieces) * SUM * (mid.abs() @ self.w64.abs())) + 3 * U * want.abs()
         if dX is not None:
             inside(dX, want, bound + B16 * (want.abs() + bound), "dX")
             assert not bool(dX[~self.real].any())
-        want = mid.t() @ self.x64
-        bound = rad.t() @ self.x64.abs() + (self.m + 1) * SUM * (mid.abs().t() @ self.x64.abs())
+        want = c * (mid.t() @ self.x64)
+        bound = abs(c) * (rad.t() @ self.x64.abs() + (self.m + 1) * SUM * (mid.abs().t() @ self.x64.abs())) + 3 * U * want.abs()
         if dW is not None:
             inside(dW[:self.vocab], want, bound + B16 * (want.abs() + bound), "dW")
             assert not bool(dW[self.vocab:].any())

@@ -41,8 +41,8 @@ template <> struct Wide<OP_LSE> {
 };
 template <> struct Wide<OP_DLOGITS> {
   using Params = VocabParams;
-  static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 5, THREADS = 32 * (2 + EPI_WARPS);
-  static constexpr uint32_t STAGE = 2 * kHalf, EPI = EPI_WARPS * 8192u, SMEM = STAGES * STAGE + EPI + 1024;
+  static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr uint32_t STAGE = 2 * kHalf, EPI = EPI_WARPS * 4096u, SMEM = STAGES * STAGE + EPI + 1024;
 };
 template <> struct Wide<OP_DX_SPLIT> {
   using Params = VocabParams;
@@ -89,7 +89,8 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   using C = Wide<OP>;
   const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
   const int part = (warp - 2) >> 2;  // which of the quarter's warps
-  uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * 8192u;  // (not OP_LSE)
+  // staging: two buffers of 4 KiB a warp for dX, one for dZ (not OP_LSE)
+  uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * (OP == OP_DLOGITS ? 4096u : 8192u);
   uint32_t i = 0, stores = 0;
   const float scale = OP == OP_DX_SPLIT ? dw_scale(p.scale, p.count) : 1.0f;
   if (OP == OP_LSE && pair == 0 && rank == 0 && warp == 2 && lane == 0) *p.ticket = 0u;
@@ -184,7 +185,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
 #pragma unroll 1
       for (int c = 0; c < C::EPI_COLS; c += 32) {
         const int h = (c >> 5) & 1, col0 = c0 + c;
-        uint8_t* buf = stage + ((c >> 6) & 1) * 4096;
+        uint8_t* buf = stage;
         if (h == 0) __syncwarp();  // the buffer's last store has read it
         uint32_t r[32];
         tmem_ld_32cols(taddr + c, r);

@@ -822,6 +822,8 @@ def _space(workspace, device, stream, name: str, dev: int, *sizes):
     """(tensor to keep, pointer, bytes) of a call's workspace: the caller's, or one taken for this call."""
     if workspace is None:
         nbytes = _bytes_once(name, dev, *sizes)
+        if not nbytes:
+            return None, None, 0
         workspace = _call_workspace(nbytes, device, stream)
         return workspace, workspace.data_ptr(), nbytes
     return workspace, _dev(workspace, torch.uint8, "workspace"), workspace.numel()
@@ -838,7 +840,7 @@ def fsdp_embedding_forward(e_shards, tokens, Y, vocab=None, scale: float = 1.0, 
 
 
 def fsdp_embedding_backward_workspace(m_tokens: int, vocab: int, cols: int) -> int:
-    """Workspace bytes of fsdp_embedding_backward."""
+    """Workspace bytes of fsdp_embedding_backward (0: none is used)."""
     return _bytes(_lib.fsdp_embedding_backward_workspace, m_tokens, vocab, cols)
 
 
@@ -846,7 +848,8 @@ def fsdp_embedding_backward(dY, tokens, dE, vocab=None, scale: float = 1.0, accu
                             stream=None):
     """dE [rows, cols] (fp32 or bf16) = scale * the sums of dY's rows by their tokens, zeros in the other
     rows; with accumulate added to what dE holds. workspace: a uint8 CUDA tensor of
-    fsdp_embedding_backward_workspace(...) bytes; None takes it from PyTorch's allocator for this call."""
+    fsdp_embedding_backward_workspace(...) bytes; None takes it, where one is used, from PyTorch's allocator for
+    this call."""
     dev = _device()
     m, ids, width = _ids(tokens, "tokens", dev)
     rows, k = _rows_cols(dE, "dE")
@@ -871,7 +874,7 @@ def fsdp_layernorm_forward(X, Y, gamma=None, beta=None, eps: float = 1e-5, mean=
 
 
 def fsdp_layernorm_backward_workspace(rows: int, cols: int) -> int:
-    """Workspace bytes with which fsdp_layernorm_backward sums dgamma and dbeta."""
+    """Workspace bytes with which fsdp_layernorm_backward sums dgamma and dbeta (0: none is used)."""
     return _bytes(_lib.fsdp_layernorm_backward_workspace, rows, cols)
 
 

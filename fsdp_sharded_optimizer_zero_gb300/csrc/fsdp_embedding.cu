@@ -3,11 +3,12 @@
 //   forward   Y[i] = scale E[t_i]
 //   backward  dE[v] = scale * sum over i with t_i = v of dY[i], every row of dE (or added to it)
 //
-// The backward orders the positions by token first (stably: the positions of one token stay in order),
-// so that the rows of one token lie one after the other and are summed in registers in a fixed order,
-// without atomics: the same bits every call. Bound by writing dE (8192 tokens of 50257 x 768 fp32: 39 us, 23 of them
-// the 154 MB of dE, beside which the sort runs, then 16 the latency of the two launches that sum) and by the rows of
-// dY (65536 tokens: 65 us, 3.9 TB/s). A token outside 0 .. vocab - 1 is none: zeros, no gradient.
+// The backward brings the rows of one token together, in the order of their positions, and sums them in registers
+// in that order, without atomics: the same bits every call. Up to 4096 tokens each block looks for its rows' tokens
+// itself, in one launch; more are ordered by a stable sort. Bound by writing dE (8192 tokens of 50257 x 768 fp32: 39 us,
+// 23 of them the 154 MB of dE, beside which the sort runs, then 16 the latency of the two launches that sum; 4096
+// tokens 33 us) and by the rows of dY (65536 tokens: 65 us, 3.9 TB/s). A token outside 0 .. vocab - 1 is none:
+// zeros, no gradient.
 #include <algorithm>
 
 #include "linear_math.cuh"
@@ -99,68 +100,7 @@ __device__ __forceinline__ void fill_zeros(uint4* out, int64_t n16, int64_t bloc
   for (int64_t i = block * blockDim.x + threadIdx.x; i < n16; i += blocks * blockDim.x) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
 }
 
-// Up to kRankMost positions, of a vocabulary whose tokens leave room for a position in 32 bits: the token and
-// the position beside it in one word, no two alike, so that a position's place is the number of smaller words. A
-// warp counts for four positions, its lanes a share of the words each, four at a time: m^2 comparisons, but one
-// launch, beside whose blocks others fill dE with zeros (4096 positions 5 us, 8192 20; from there on the passes
-// below are faster: 16384 positions 47 us against 15).
-constexpr int kRankBits = 12, kRankMost = 1 << kRankBits;
-constexpr int kRankTile = 2048;  // words in shared memory at a time
-constexpr int kRankEach = 4;     // positions of a warp
-bool ranked(int64_t m, int64_t vocab) { return m <= kRankMost && vocab < (int64_t(1) << (32 - kRankBits)) - 1; }
-__global__ void __launch_bounds__(kThreads) rank_kernel(const void* tokens, int wide, int m, int vocab, Sorted s,
-                                                        int rank_blocks, uint4* zero, int64_t zero16) {
-  __shared__ uint4 words[kRankTile / 4];
-  allow_next_grid();
-  wait_for_prior_grids();
-  if (static_cast<int>(blockIdx.x) >= rank_blocks) {
-    fill_zeros(zero, zero16, blockIdx.x - rank_blocks, gridDim.x - rank_blocks);
-    return;
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // none: `vocab`, behind every token
-  const auto word = [&](int t, int i) {
-    return (static_cast<uint32_t>(t < 0 ? vocab : t) << kRankBits) | static_cast<uint32_t>(i);
-  };
-  const int i0 = (static_cast<int>(blockIdx.x) * kWarps + warp) * kRankEach;
-  uint32_t mine[kRankEach];
-  int count[kRankEach];
-#pragma unroll
-  for (int e = 0; e < kRankEach; ++e)
-    mine[e] = i0 + e < m ? word(token_at(tokens, wide, i0 + e, vocab), i0 + e) : 0u, count[e] = 0;
-  for (int t0 = 0; t0 < m; t0 += kRankTile) {
-    constexpr int EACH = kRankTile / kThreads;
-    const int j0 = warp * EACH * 32 + lane;
-    int t[EACH];
-    tokens_at(tokens, wide, t0 + j0, m, vocab, t);
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < EACH; ++r) {
-      const int j = j0 + 32 * r;
-      reinterpret_cast<uint32_t*>(words)[j] = t0 + j < m ? word(t[r], t0 + j) : 0xFFFFFFFFu;  // more than any
-    }
-    __syncthreads();
-    const int groups = (min(kRankTile, m - t0) + 3) / 4;
-#pragma unroll 4
-    for (int j = lane; j < groups; j += 32) {
-      const uint4 w = words[j];
-#pragma unroll
-      for (int e = 0; e < kRankEach; ++e)
-        count[e] += (w.x < mine[e] ? 1 : 0) + (w.y < mine[e] ? 1 : 0) + (w.z < mine[e] ? 1 : 0) + (w.w < mine[e] ? 1 : 0);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < kRankEach; ++e) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) count[e] += __shfl_xor_sync(0xffffffffu, count[e], d);
-    if (i0 + e < m && lane == e) {
-      const int t = static_cast<int>(mine[e] >> kRankBits);
-      s.key[count[e]] = t == vocab ? kNone : t, s.order[count[e]] = i0 + e;
-    }
-  }
-}
-
-// More positions: a stable radix sort, a digit of kDigitBits a pass from the lowest, in two or three launches a
+// More than kFewTokens: a stable radix sort, a digit of kDigitBits a pass from the lowest, in two or three launches a
 // pass. Block b has the positions from b kSortTile on, a warp a run of them. They are few blocks: the others of each
 // launch fill a share of dE with zeros.
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
@@ -357,8 +297,8 @@ struct SumArgs {
   float* open;  // [runs][2][cols]
 };
 
-__device__ __forceinline__ void put_row(const SumArgs& p, int key, int64_t col, f2 (&v)[4]) {
-  const int64_t at = static_cast<int64_t>(key) * p.cols + col;
+__device__ __forceinline__ void put_row(const SumArgs& p, int64_t row, int64_t col, f2 (&v)[4]) {
+  const int64_t at = row * p.cols + col;
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = f2_mul(v[j], f2_both(p.scale));
   if (p.de32) {
@@ -377,6 +317,142 @@ __device__ __forceinline__ void put_row(const SumArgs& p, int key, int64_t col, 
       for (int j = 0; j < 4; ++j) v[j] = f2_add(v[j], old[j]);
     }
     *to = narrow8(v);
+  }
+}
+
+// Up to kFewTokens positions: one launch and no workspace. A block has a group of dE's rows; its warps look through
+// all tokens, a share each, for those of its rows. The first blocks have 256 columns too: they keep what they found, in
+// order; a warp takes a row, collects its positions and sums them. The others mark the rows that they found and fill
+// the rest with zeros, whole rows in one sweep (a warp to a row and 256 columns fills half as fast).
+// Rows of more than kFewRows positions are left for all warps together, each a share of the positions, whose sums meet
+// in shared memory, in order. In which order rows are taken changes no result.
+constexpr int kTokenBits = 12, kFewTokens = 1 << kTokenBits, kFewShare = kFewTokens / kWarps, kFewRows = 64;
+constexpr int kFewGroup = 1 << 13;  // rows of a group at most
+// Blocks per SM that sum and that fill, of five that are resident. 50257 x 768 fp32, 4096 and 1000 tokens, and 1003 of
+// 1157 x 520: with 1 and 4 39.1, 26.8 and 7.7 us; 3 and 4 32.8, 28.5 and 7.9; 5 and 8 31.5, 28.7 and 9.0.
+constexpr int kSumBlocks = 3, kFillBlocks = 4;
+struct FewGroups {
+  int sum_blocks, sum_rows, fill_rows;  // blocks that sum, rows of one's group; rows of a block that fills
+};
+__global__ void __launch_bounds__(kThreads) sum_few_kernel(const void* tokens, int wide, int m, int vocab, int64_t rows,
+                                                           const FewGroups groups, const SumArgs p) {
+  __shared__ __align__(16) uint32_t found[kWarps][kFewShare];  // (row of the block's, position), in order; later: its rows
+  __shared__ uint32_t list[kFewTokens];                        // the same, without gaps
+  __shared__ uint16_t at[kWarps][kFewShare];                   // a warp's positions
+  __shared__ uint32_t seen[kFewGroup / 32];                    // a bit a row
+  __shared__ int count[kWarps];
+  __shared__ int many[kFewTokens / kFewRows], n_many, n_rows;
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int block = static_cast<int>(blockIdx.x);
+  const bool fill = block >= groups.sum_blocks;
+  const int group = fill ? block - groups.sum_blocks : block / p.slices, per = fill ? groups.fill_rows : groups.sum_rows;
+  const int64_t row0 = static_cast<int64_t>(group) * per;
+  const int mine_rows = static_cast<int>(min(static_cast<int64_t>(per), rows - row0));
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = threadIdx.x; i < (mine_rows + 31) / 32; i += kThreads) seen[i] = 0u;
+  if (threadIdx.x == 0) n_many = n_rows = 0;
+  __syncthreads();
+  {
+    constexpr int ROUNDS = kFewShare / 32;
+    const int each = (m + kWarps * 32 - 1) / (kWarps * 32) * 32, first = warp * each;
+    int t[ROUNDS], n = 0;
+    tokens_at(tokens, wide, first + lane, min(m, first + each), vocab, t);
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+      const bool mine = t[r] >= row0 && t[r] < row0 + mine_rows;
+      const uint32_t row = mine ? static_cast<uint32_t>(t[r] - row0) : 0u;
+      const uint32_t all = __ballot_sync(0xffffffffu, mine);
+      if (mine) {
+        if (fill) atomicOr(&seen[row >> 5], 1u << (row & 31));
+        else found[warp][n + __popc(all & below)] = (row << kTokenBits) | static_cast<uint32_t>(first + r * 32 + lane);
+      }
+      n += __popc(all);
+    }
+    if (lane == 0) count[warp] = n;
+  }
+  __syncthreads();
+  if (fill) {
+    const int64_t row16 = p.cols * (p.de32 ? 4 : 2) / 16;
+    uint4* out = reinterpret_cast<uint4*>(p.de32 ? static_cast<void*>(p.de32) : p.de16) + row0 * row16;
+    int row = 0;
+    int64_t i = threadIdx.x;  // of the row
+    while (true) {
+      while (i >= row16 && row < mine_rows) i -= row16, ++row;
+      if (row >= mine_rows) return;
+      if (!((seen[row >> 5] >> (row & 31)) & 1u)) __stcs(out + row * row16 + i, make_uint4(0u, 0u, 0u, 0u));
+      i += kThreads;
+    }
+  }
+  const int64_t col = static_cast<int64_t>(block - group * p.slices) * 256 + lane * 8;
+  const bool in = col < p.cols;
+  int ahead = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) ahead += w < warp ? count[w] : 0, all += count[w];
+  if (all == 0) return;
+  for (int i = lane; i < count[warp]; i += 32) list[ahead + i] = found[warp][i];
+  __syncthreads();
+  uint32_t* present = &found[0][0];
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    const uint32_t row = list[i] >> kTokenBits, bit = 1u << (row & 31);
+    if (!(atomicOr(&seen[row >> 5], bit) & bit)) present[atomicAdd(&n_rows, 1)] = row;
+  }
+  __syncthreads();
+  // the positions of `row` among list[from .. to), to this warp's `at` as far as there is room: how many there are
+  const auto collect = [&](uint32_t row, int from, int to, int room) {
+    int n = 0;
+    for (int i0 = from; i0 < to; i0 += 32) {
+      const uint32_t e = i0 + lane < to ? list[i0 + lane] : 0u;
+      const bool mine = i0 + lane < to && (e >> kTokenBits) == row;
+      const uint32_t hits = __ballot_sync(0xffffffffu, mine);
+      const int i = n + __popc(hits & below);
+      if (mine && i < room) at[warp][i] = static_cast<uint16_t>(e & (kFewTokens - 1));
+      n += __popc(hits);
+    }
+    __syncwarp();
+    return n;
+  };
+  const auto sum_rows = [&](int n, f2 (&sum)[4]) {
+    sum[0] = sum[1] = sum[2] = sum[3] = 0ull;
+    if (in)
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        f2 v[4];
+        widen8(__ldg(reinterpret_cast<const uint4*>(p.dy + at[warp][j] * p.cols + col)), v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = f2_add(sum[k], v[k]);
+      }
+    __syncwarp();  // before the next positions
+  };
+  f2 sum[4];
+  for (int i = warp; i < n_rows; i += kWarps) {
+    const uint32_t row = present[i];
+    const int n = collect(row, 0, all, kFewRows);
+    if (n > kFewRows) {
+      if (lane == 0) many[atomicAdd(&n_many, 1)] = static_cast<int>(row);
+      continue;
+    }
+    sum_rows(n, sum);
+    if (in) put_row(p, row0 + row, col, sum);
+  }
+  __syncthreads();
+  f2(*part)[32][4] = reinterpret_cast<f2(*)[32][4]>(present);  // its rows are done with
+  static_assert(sizeof(f2[kWarps][32][4]) <= sizeof(found), "the warps' sums take their place");
+  for (int i = 0; i < n_many; ++i) {
+    const int n = collect(static_cast<uint32_t>(many[i]), all * warp / kWarps, all * (warp + 1) / kWarps, kFewShare);
+    sum_rows(n, sum);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][lane][j] = sum[j];
+    __syncthreads();
+    if (warp == 0 && in) {
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = f2_add(sum[j], part[w][lane][j]);
+      put_row(p, row0 + many[i], col, sum);
+    }
+    __syncthreads();  // before the next row's sums
   }
 }
 
@@ -547,16 +623,16 @@ struct BackwardSpace {
       return at;
     };
     bytes = 0, passes = 0, sort_blocks = 0, count = 0;
+    key[0] = key[1] = order[0] = order[1] = open = 0;
+    if (m <= kFewTokens) return;
     key[0] = key[1] = take(4 * static_cast<uint64_t>(m));
     order[0] = order[1] = take(4 * static_cast<uint64_t>(m));
     int bits = 1;
     while (bits < 31 && (vocab >> bits) != 0) ++bits;  // of keys 0 .. vocab
     passes = (bits + kDigitBits - 1) / kDigitBits;
-    if (!ranked(m, vocab)) {
-      sort_blocks = (m + kSortTile - 1) / kSortTile;
-      if (passes > 1) key[1] = take(4 * static_cast<uint64_t>(m)), order[1] = take(4 * static_cast<uint64_t>(m));
-      count = take(4 * static_cast<uint64_t>(sort_blocks) * kDigits);
-    }
+    sort_blocks = (m + kSortTile - 1) / kSortTile;
+    if (passes > 1) key[1] = take(4 * static_cast<uint64_t>(m)), order[1] = take(4 * static_cast<uint64_t>(m));
+    count = take(4 * static_cast<uint64_t>(sort_blocks) * kDigits);
     open = take(8 * static_cast<uint64_t>((m + run_of(m) - 1) / run_of(m)) * static_cast<uint64_t>(cols));
   }
 };
@@ -620,7 +696,7 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
   if (reinterpret_cast<uintptr_t>(tokens) % token_bytes)
     return set_error(ZERO_ERR_INVALID_ARG, "%s: tokens must be aligned to their %d bytes", who, token_bytes);
   const BackwardSpace sp(m_tokens, vocab, cols);
-  if (!workspace || workspace_bytes < sp.bytes)
+  if (sp.bytes && (!workspace || workspace_bytes < sp.bytes))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: workspace of %llu bytes is below the %llu needed", who,
                      workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)sp.bytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -628,48 +704,54 @@ extern "C" int fsdp_embedding_backward(const zero_bf16* dY, const void* tokens, 
   const auto ints = [&](uint64_t at) { return reinterpret_cast<int*>(ws + at); };
   uint4* zero = reinterpret_cast<uint4*>(dE ? static_cast<void*>(dE) : dE_bf16);
   const int64_t zero16 = accumulate ? 0 : rows * cols * (dE ? 4 : 2) / 16;
-  const int64_t zero_blocks = std::min<int64_t>((zero16 + 4 * kThreads - 1) / (4 * kThreads), static_cast<int64_t>(num_sms()) * 8);
   const int wide = token_bytes == 8 ? 1 : 0;
   Sorted sorted{ints(sp.key[0]), ints(sp.order[0])};
-  cudaError_t e = cudaSuccess;
-  if (ranked(m_tokens, vocab)) {
-    const int64_t rank_blocks = (m_tokens + kRankEach * kWarps - 1) / (kRankEach * kWarps);
-    e = launch_overlapped(rank_kernel, dim3(static_cast<unsigned>(rank_blocks + zero_blocks)), dim3(kThreads), 0, 1, st, tokens,
-                          wide, static_cast<int>(m_tokens), static_cast<int>(vocab), sorted, static_cast<int>(rank_blocks),
-                          zero, zero16);
-  } else {
-    for (int pass = 0; pass < sp.passes && e == cudaSuccess; ++pass) {
-      SortPass p;
-      p.tokens = pass == 0 ? tokens : nullptr;
-      p.wide = wide, p.vocab = static_cast<int>(vocab), p.shift = pass * kDigitBits, p.m = m_tokens;
-      p.blocks = static_cast<int>(sp.sort_blocks);
-      // the last pass ends in the first buffer
-      const int to = (sp.passes - 1 - pass) & 1;
-      p.in = {ints(sp.key[to ^ 1]), ints(sp.order[to ^ 1])};
-      p.out = {ints(sp.key[to]), ints(sp.order[to])};
-      p.count = ints(sp.count), p.scanned = sp.sort_blocks > kOwnScan;
-      // of every four parts of a pass's share of dE, one beside the counts and three beside the placing, which takes
-      // three times as long
-      const auto part = [&](int64_t i) { return zero16 * (4 * pass + i) / (4 * sp.passes); };
-      const auto share = [&](int64_t from, int64_t to) {
-        p.zero = zero + from, p.zero16 = to - from;
-        return static_cast<unsigned>(sp.sort_blocks + std::min<int64_t>((p.zero16 + 4 * kSortThreads - 1) / (4 * kSortThreads),
-                                                                       static_cast<int64_t>(num_sms()) * 4));
-      };
-      const unsigned counting = share(part(0), part(1));
-      e = launch_overlapped(sort_count_kernel, dim3(counting), dim3(kSortThreads), 0, 1, st, p);
-      if (e == cudaSuccess && p.scanned)
-        e = launch_overlapped(sort_scan_kernel, dim3(1), dim3(1024), 0, 1, st, p.count, sp.sort_blocks * kDigits);
-      const unsigned placing = share(part(1), part(4));
-      if (e == cudaSuccess)
-        e = launch_overlapped(sort_scatter_kernel, dim3(placing), dim3(kSortThreads), 0, 1, st, p);
-    }
-  }
-  const int run = run_of(m_tokens);
-  const int64_t runs = (m_tokens + run - 1) / run, slices = (cols + 255) / 256;
+  const int64_t slices = (cols + 255) / 256;
   SumArgs a;
   a.s = sorted, a.m = m_tokens, a.dy = dY, a.cols = cols, a.slices = static_cast<int>(slices), a.scale = scale;
   a.de32 = dE, a.de16 = dE_bf16, a.add = accumulate != 0, a.open = reinterpret_cast<float*>(ws + sp.open);
+  cudaError_t e = cudaSuccess;
+  if (m_tokens <= kFewTokens) {
+    const auto rows_each = [&](int64_t blocks) {
+      return std::min<int64_t>((rows + blocks - 1) / blocks, kFewGroup);
+    };
+    const int64_t sms = num_sms();
+    const int64_t sum_rows = rows_each(std::max<int64_t>(1, std::min(rows, kSumBlocks * sms / slices)));
+    const int64_t fill_rows = rows_each(std::max<int64_t>(1, std::min(std::min(rows, kFillBlocks * sms), zero16 / (2 * kThreads))));
+    const int64_t sum_blocks = (rows + sum_rows - 1) / sum_rows * slices, fill_blocks = zero16 ? (rows + fill_rows - 1) / fill_rows : 0;
+    const FewGroups groups{static_cast<int>(sum_blocks), static_cast<int>(sum_rows), static_cast<int>(fill_rows)};
+    e = launch_overlapped(sum_few_kernel, dim3(static_cast<unsigned>(sum_blocks + fill_blocks)), dim3(kThreads), 0, 1, st, tokens,
+                          wide, static_cast<int>(m_tokens), static_cast<int>(vocab), rows, groups, a);
+    return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  }
+  for (int pass = 0; pass < sp.passes && e == cudaSuccess; ++pass) {
+    SortPass p;
+    p.tokens = pass == 0 ? tokens : nullptr;
+    p.wide = wide, p.vocab = static_cast<int>(vocab), p.shift = pass * kDigitBits, p.m = m_tokens;
+    p.blocks = static_cast<int>(sp.sort_blocks);
+    // the last pass ends in the first buffer
+    const int to = (sp.passes - 1 - pass) & 1;
+    p.in = {ints(sp.key[to ^ 1]), ints(sp.order[to ^ 1])};
+    p.out = {ints(sp.key[to]), ints(sp.order[to])};
+    p.count = ints(sp.count), p.scanned = sp.sort_blocks > kOwnScan;
+    // of every four parts of a pass's share of dE, one beside the counts and three beside the placing, which takes
+    // three times as long
+    const auto part = [&](int64_t i) { return zero16 * (4 * pass + i) / (4 * sp.passes); };
+    const auto share = [&](int64_t from, int64_t to) {
+      p.zero = zero + from, p.zero16 = to - from;
+      return static_cast<unsigned>(sp.sort_blocks + std::min<int64_t>((p.zero16 + 4 * kSortThreads - 1) / (4 * kSortThreads),
+                                                                     static_cast<int64_t>(num_sms()) * 4));
+    };
+    const unsigned counting = share(part(0), part(1));
+    e = launch_overlapped(sort_count_kernel, dim3(counting), dim3(kSortThreads), 0, 1, st, p);
+    if (e == cudaSuccess && p.scanned)
+      e = launch_overlapped(sort_scan_kernel, dim3(1), dim3(1024), 0, 1, st, p.count, sp.sort_blocks * kDigits);
+    const unsigned placing = share(part(1), part(4));
+    if (e == cudaSuccess)
+      e = launch_overlapped(sort_scatter_kernel, dim3(placing), dim3(kSortThreads), 0, 1, st, p);
+  }
+  const int run = run_of(m_tokens);
+  const int64_t runs = (m_tokens + run - 1) / run;
   const auto sums = [&](auto length) {
     constexpr int RUN = decltype(length)::value, WARPS = warps_of_run(RUN);
     constexpr uint32_t smem = WARPS * RUN * 512;

@@ -222,20 +222,31 @@ struct Ahead {
 // 8192 x 8192 83 us, 6.4 TB/s; narrower rows more by the latency of a round's reductions (8192 x 2304 26 us, 4.4
 // TB/s), and past 8192 columns, where a row takes four pieces a lane and a round is one row, by the same (4096 x 14336
 // with residual 94 us, 5.0 TB/s).
-template <int W, int U, int R, int BLOCKS, bool FULL>
-__global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
-    norm_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ x, const float* __restrict__ mean,
-                         const float* __restrict__ rstd, int64_t rows, int cols, const uint16_t* __restrict__ gamma,
-                         float inv_n, const uint16_t* residual, uint16_t* dx, float* __restrict__ partial) {
+struct BackwardArgs {
+  const uint16_t *dy, *x;
+  const float *mean, *rstd;
+  int64_t rows;
+  int cols;
+  const uint16_t* gamma;
+  float inv_n;
+  const uint16_t* residual;
+  uint16_t* dx;
+};
+template <int W, int U, int R, int BLOCKS, bool FULL, bool PARAMS>
+__device__ __forceinline__ void backward_rows(const BackwardArgs& p, int block, int blocks, uint4* ring_mem, float* __restrict__ partial) {
   using Ring = Ahead<W, U, R, BLOCKS>;
   constexpr int STAGES = Ring::STAGES, PER = Place<W>::PER, STRIDE = Place<W>::STRIDE;
-  extern __shared__ uint4 ring_mem[];
   __shared__ RowMeet<R> sums;
-  allow_next_grid();
+  const uint16_t *dy = p.dy, *residual = p.residual;
+  const uint16_t* __restrict__ x = p.x;
+  const float *__restrict__ mean = p.mean, *__restrict__ rstd = p.rstd;
+  const int64_t rows = p.rows;
+  const int cols = p.cols;
+  const float inv_n = p.inv_n;
   const Place<W> at;
   const Ring ring{ring_mem + threadIdx.x};
   const auto in = [&](int u) { return FULL || at.col0 + u * STRIDE < cols; };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * PER * R, first = static_cast<int64_t>(blockIdx.x) * PER * R;
+  const int64_t step = static_cast<int64_t>(blocks) * PER * R, first = static_cast<int64_t>(block) * PER * R;
   const auto load = [&](int64_t row0, int stage) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -252,7 +263,6 @@ __global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
     }
     ring.commit();
   };
-  wait_for_prior_grids();
   int turn = 0, stage = 0;
   const int64_t mine = first + at.group * R;
 #pragma unroll
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
   f2 dg[U][4], db[U][4];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    gw[u] = param8(gamma, at.col0 + u * STRIDE, in(u), kOnes);
+    gw[u] = param8(p.gamma, at.col0 + u * STRIDE, in(u), kOnes);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[u][j] = db[u][j] = 0ull;
   }
@@ -299,8 +309,7 @@ __global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
         // past the row (and the rows) dy is 0, and so is its part in each sum
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          dg[u][j] = f2_fma(d[j], h[j], dg[u][j]);
-          db[u][j] = f2_add(db[u][j], d[j]);
+          if (PARAMS) dg[u][j] = f2_fma(d[j], h[j], dg[u][j]), db[u][j] = f2_add(db[u][j], d[j]);
           t1 = f2_fma(g[j], h[j], t1);
         }
         t0 = f2_add(t0, f2_sum4(g));
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
     for (int i = 0; i < R; ++i) {
       if (row0 + i >= rows) continue;
       const f2 a = f2_both(-__fmul_rn(s0[i], inv_n)), b = f2_both(-__fmul_rn(s1[i], inv_n));
-      uint16_t* to = dx + (row0 + i) * cols + at.col0;
+      uint16_t* to = p.dx + (row0 + i) * cols + at.col0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (!in(u)) continue;
@@ -340,9 +349,9 @@ __global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
     }
     stage = (stage + 1) % STAGES;
   }
-  if (!partial) return;
   asm volatile("cp.async.wait_all;" ::: "memory");
-  float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+  if (!PARAMS || !partial) return;
+  float* out = partial + static_cast<int64_t>(block) * 2 * cols;
   if constexpr (PER > 1) {
     // the block's row groups meet in the ring's memory, one after the other
     constexpr int WIDTH = U * STRIDE;
@@ -378,6 +387,80 @@ __global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
         *reinterpret_cast<ulonglong2*>(out + cols + col + 2 * j) = make_ulonglong2(db[u][j], db[u][j + 1]);
       }
     }
+  }
+}
+
+template <int W, int U, int R, int BLOCKS, bool FULL>
+__global__ void __launch_bounds__(threads_of_block(W), BLOCKS) norm_backward_kernel(const BackwardArgs p, float* __restrict__ partial) {
+  extern __shared__ uint4 ring_mem[];
+  allow_next_grid();
+  wait_for_prior_grids();
+  backward_rows<W, U, R, BLOCKS, FULL, true>(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), ring_mem, partial);
+}
+
+// Few rows: dgamma and dbeta in the same launch and without a workspace. Blocks from row_blocks on take 64 columns each,
+// 8 threads across them, and all rows, which the other blocks have in L2 too; a thread's sums meet the others' in shared
+// memory, in the order of the threads.
+constexpr int kStrip = 64;
+template <int W, int U, int R, int BLOCKS, bool FULL>
+__global__ void __launch_bounds__(threads_of_block(W), BLOCKS)
+    norm_backward_few_kernel(const BackwardArgs p, int row_blocks, float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  extern __shared__ uint4 ring_mem[];
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < row_blocks) {
+    backward_rows<W, U, R, BLOCKS, FULL, false>(p, block, row_blocks, ring_mem, nullptr);
+    return;
+  }
+  constexpr int LANES = kStrip / 8, ROWS = threads_of_block(W) / LANES, AHEAD = 4;
+  static_assert(2 * ROWS * kStrip * 4 <= Ahead<W, U, R, BLOCKS>::BYTES, "the sums fit into the ring's memory");
+  const int row0 = static_cast<int>(threadIdx.x) / LANES, col = (block - row_blocks) * kStrip + (static_cast<int>(threadIdx.x) % LANES) * 8;
+  f2 dg[4] = {0ull, 0ull, 0ull, 0ull}, db[4] = {0ull, 0ull, 0ull, 0ull};
+  if (col < p.cols) {
+    for (int64_t r0 = row0; r0 < p.rows; r0 += AHEAD * ROWS) {
+      uint4 xw[AHEAD], yw[AHEAD];
+      float mu[AHEAD], r[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int64_t row = r0 + i * ROWS;
+        xw[i] = yw[i] = make_uint4(0u, 0u, 0u, 0u);
+        mu[i] = r[i] = 0.0f;
+        if (row < p.rows) {
+          xw[i] = __ldg(reinterpret_cast<const uint4*>(p.x + row * p.cols + col));
+          yw[i] = __ldg(reinterpret_cast<const uint4*>(p.dy + row * p.cols + col));
+          mu[i] = __ldg(p.mean + row), r[i] = __ldg(p.rstd + row);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        f2 h[4], d[4];
+        widen8(xw[i], h);
+        widen8(yw[i], d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dg[j] = f2_fma(d[j], f2_mul(f2_add(h[j], f2_both(-mu[i])), f2_both(r[i])), dg[j]);
+          db[j] = f2_add(db[j], d[j]);
+        }
+      }
+    }
+  }
+  float* meet = reinterpret_cast<float*>(ring_mem);  // [2][ROWS][kStrip]
+  float* mine = meet + row0 * kStrip + (static_cast<int>(threadIdx.x) % LANES) * 8;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f2_split(dg[j], mine[2 * j], mine[2 * j + 1]);
+    f2_split(db[j], mine[ROWS * kStrip + 2 * j], mine[ROWS * kStrip + 2 * j + 1]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kStrip; i += threads_of_block(W)) {
+    const float* part = meet + (i / kStrip) * ROWS * kStrip + i % kStrip;
+    float t = part[0];
+#pragma unroll 8
+    for (int k = 1; k < ROWS; ++k) t = __fadd_rn(t, part[k * kStrip]);
+    float* out = i < kStrip ? dgamma : dbeta;
+    const int c = (block - row_blocks) * kStrip + i % kStrip;
+    if (out && c < p.cols) out[c] = t;
   }
 }
 
@@ -603,6 +686,11 @@ auto with_backward_shape(int64_t cols, F&& f) {
   return f(BackwardShape<16, 4>{});
 }
 
+// dgamma and dbeta in the launch that computes dX: up to 1024 rows. With residual, in one launch and in two: 1 x 4096
+// 2.2 and 4.7 us, 777 x 2304 8.3 and 9.6, 777 x 14336 22 and 31, 1024 x 4096 12.2 and 13.4, 1024 x 2304 12.3 and 10.8,
+// 2048 x 4096 22.4 and 18.0.
+constexpr int64_t kFewRows = 1024;
+bool few_rows_backward(int64_t rows, int64_t cols) { return rows <= kFewRows && cols <= kWidest; }
 // blocks of the backward kernel, and so partial sums a column
 int64_t backward_blocks(int64_t rows, int64_t cols) {
   if (cols > kWidest) return std::min<int64_t>(rows, 64);
@@ -665,7 +753,7 @@ extern "C" int fsdp_layernorm_backward_workspace(int64_t rows, int64_t cols, uin
   if (!bytes) return set_error(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
   const int rc = check_shape(rows, cols, who);
   if (rc) return rc;
-  *bytes = 8 * static_cast<uint64_t>(backward_blocks(rows, cols)) * static_cast<uint64_t>(cols);
+  *bytes = few_rows_backward(rows, cols) ? 0 : 8 * static_cast<uint64_t>(backward_blocks(rows, cols)) * static_cast<uint64_t>(cols);
   return ZERO_OK;
 }
 
@@ -684,8 +772,9 @@ extern "C" int fsdp_layernorm_backward(const zero_bf16* dY, const zero_bf16* X, 
   if (!aligned4(mean) || !aligned4(rstd) || !aligned4(dgamma) || !aligned4(dbeta))
     return set_error(ZERO_ERR_INVALID_ARG, "%s: mean, rstd, dgamma and dbeta must be 4-byte aligned", who);
   const bool params = dgamma || dbeta;
+  const bool few = params && few_rows_backward(rows, cols);
   float* partial = nullptr;
-  if (params) {
+  if (params && !few) {
     uint64_t need = 0;
     if ((rc = fsdp_layernorm_backward_workspace(rows, cols, &need))) return rc;
     if (!workspace || workspace_bytes < need)
@@ -711,21 +800,35 @@ extern "C" int fsdp_layernorm_backward(const zero_bf16* dY, const zero_bf16* X, 
       using S = decltype(shape);
       constexpr int W = S::warps, U = S::pieces, R = S::rows;
       constexpr uint32_t smem = Ahead<W, U, R, S::blocks>::BYTES;
-      static OncePerDevice once[2];
       const bool full = cols == W * U * 256;
-      const auto kernel = full ? norm_backward_kernel<W, U, R, S::blocks, true> : norm_backward_kernel<W, U, R, S::blocks, false>;
-      int dev = 0;
-      cudaError_t q = cudaGetDevice(&dev);
-      if (q == cudaSuccess)
-        q = once[full].run(dev, [&] {
-          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        });
-      if (q != cudaSuccess) return q;
-      return launch_overlapped(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads_of_block(W)), smem, 1, st, dY, X, mean,
-                               rstd, rows, static_cast<int>(cols), gamma, inv_n, residual, dX, partial);
+      const BackwardArgs p{dY, X, mean, rstd, rows, static_cast<int>(cols), gamma, inv_n, residual, dX};
+      const auto go = [&](auto kernel, OncePerDevice& once, int64_t grid, auto... more) {
+        int dev = 0;
+        cudaError_t q = cudaGetDevice(&dev);
+        if (q == cudaSuccess)
+          q = once.run(dev, [&] {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+          });
+        if (q != cudaSuccess) return q;
+        return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads_of_block(W)), smem, 1, st, p, more...);
+      };
+      static OncePerDevice once[4];
+      if (few) {
+        const int64_t strips = (cols + kStrip - 1) / kStrip;
+        const auto launch = [&](int64_t grid, int64_t row_blocks) {
+          const int n = static_cast<int>(row_blocks);
+          return full ? go(norm_backward_few_kernel<W, U, R, S::blocks, true>, once[0], grid, n, dgamma, dbeta)
+                      : go(norm_backward_few_kernel<W, U, R, S::blocks, false>, once[1], grid, n, dgamma, dbeta);
+        };
+        if (dX != dY) return launch(blocks + strips, blocks);
+        const cudaError_t q = launch(strips, 0);  // which read dY, before it is written
+        return q == cudaSuccess ? launch(blocks, blocks) : q;
+      }
+      return full ? go(norm_backward_kernel<W, U, R, S::blocks, true>, once[2], blocks, partial)
+                  : go(norm_backward_kernel<W, U, R, S::blocks, false>, once[3], blocks, partial);
     });
   }
-  if (e == cudaSuccess && params)
+  if (e == cudaSuccess && params && !few)
     e = launch_overlapped(norm_params_kernel, dim3(static_cast<unsigned>((2 * cols + 31) / 32)), dim3(512), 0, 1, st, partial,
                           static_cast<int>(blocks), cols, dgamma, dbeta);
   return e == cudaSuccess ? ZERO_OK : set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));

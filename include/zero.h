@@ -616,7 +616,7 @@ ZERO_API int fsdp_embedding_forward(int n_ranks, const zero_bf16* const e_shards
                                     int64_t cols, const void* tokens, int token_bytes, int64_t m_tokens, float scale,
                                     zero_bf16* Y, zero_stream_t stream);
 
-/* Bytes of device workspace fsdp_embedding_backward needs. */
+/* Bytes of device workspace fsdp_embedding_backward needs (0 for few tokens: then it may be NULL). */
 ZERO_API int fsdp_embedding_backward_workspace(int64_t m_tokens, int64_t vocab, int64_t cols, uint64_t* bytes);
 
 /* dE[v] = scale * sum of dY[i] over the i with tokens[i] = v: fp32 sums in a fixed order, [rows, cols] in
@@ -635,14 +635,14 @@ ZERO_API int fsdp_layernorm_forward(const zero_bf16* X, int64_t rows, int64_t co
                                     const zero_bf16* beta, float eps, zero_bf16* Y, float* mean, float* rstd,
                                     zero_stream_t stream);
 
-/* Bytes of device workspace fsdp_layernorm_backward needs for dgamma and dbeta. */
+/* Bytes of device workspace fsdp_layernorm_backward needs for dgamma and dbeta (0 for few rows). */
 ZERO_API int fsdp_layernorm_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
 
 /* With h = (x - mean) * rstd and g = dY * gamma: dX = bf16(rstd * (g - sum g / cols - h * sum (g h) / cols) +
  * residual), dgamma = sum over the rows of dY h, dbeta = sum over the rows of dY. dY, dX, residual [rows,
  * cols] bf16; residual (nullable): the gradient that reaches X past the norm. dgamma, dbeta [cols] fp32,
- * nullable; with either, workspace of fsdp_layernorm_backward_workspace() bytes (else it may be NULL). dX
- * may be dY or residual. */
+ * nullable; with either, workspace of fsdp_layernorm_backward_workspace() bytes (else, and for 0, it may be
+ * NULL). dX may be dY or residual. */
 ZERO_API int fsdp_layernorm_backward(const zero_bf16* dY, const zero_bf16* X, const float* mean, const float* rstd,
                                      int64_t rows, int64_t cols, const zero_bf16* gamma, const zero_bf16* residual,
                                      zero_bf16* dX, float* dgamma, float* dbeta, void* workspace,

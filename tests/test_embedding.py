@@ -110,7 +110,8 @@ def check_backward(z, m, vocab, rows, cols, kind, dtype, wide, scale=1.0, add=Fa
 @pytest.mark.parametrize("kind", ["uniform", "one", "text", "falling", "none"])
 @pytest.mark.parametrize("m,vocab,rows,cols", [(1, 1, 8, 8), (31, 5, 8, 264), (32, 40, 40, 256), (33, 3, 16, 520), (64, 2, 8, 8),
                                                (65, 1000, 1008, 768), (1003, 1157, 1160, 520), (2048, 60, 64, 1032),
-                                               (8192, 3000, 3008, 264), (16384, 700, 704, 40)])
+                                               (4096, 3000, 3008, 264), (4097, 90, 96, 520), (8192, 3000, 3008, 264),
+                                               (16384, 700, 704, 40), (700, 1200000, 1200000, 8)])
 def test_backward(z, m, vocab, rows, cols, kind):
     check_backward(z, m, vocab, rows, cols, kind, torch.int64, True)
     check_backward(z, m, vocab, rows, cols, kind, torch.int32, False, scale=cols ** 0.5)
@@ -121,7 +122,7 @@ def test_backward(z, m, vocab, rows, cols, kind):
 @pytest.mark.parametrize("m,vocab,rows,cols", [(16385, 50257, 50264, 64), (20000, 1, 8, 264), (40961, 300, 304, 264),
                                                (70001, 600, 600, 520), (33000, 300000, 300000, 8)])
 def test_backward_sorted_in_passes(z, m, vocab, rows, cols, kind):
-    """More tokens than are ordered by counting: one, two and three passes of the sort."""
+    """Tokens that take one, two and three passes of the sort."""
     check_backward(z, m, vocab, rows, cols, kind, torch.int32, True)
     check_backward(z, m, vocab, rows, cols, kind, torch.int64, False)
 
@@ -179,7 +180,7 @@ def test_infinities_stay_with_their_tokens(z):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m", [700, 20000])
+@pytest.mark.parametrize("m", [700, 6000, 20000])
 def test_streams_and_graph(z, m):
     """Another stream than the current one; captured and replayed with other tokens; two graphs that share a
     workspace, one after the other."""

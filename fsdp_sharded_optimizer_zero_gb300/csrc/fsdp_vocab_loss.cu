@@ -14,7 +14,7 @@
 // 3.7e-3 of the gradients' norm off, now 1.7e-3, the outputs' own rounding).
 //
 // Bound by tensor work: forward 8192 x 50257 from 768 346 us (1.83 PFLOP/s; tensor pipe 83 % active), of which joining
-// the parts takes about 10, from 4096 (vocabulary 32000) 1077 us (1.99); gradients 8192 x 32000 from 4096 3.50-3.57 ms
+// the parts takes about 10, from 4096 (vocabulary 32000) 1135 us (1.89); gradients 8192 x 32000 from 4096 3.50-3.57 ms
 // (1.81-1.84, at the power limit 3.97), 8192 x 50257 from 768 1.16-1.18 ms (1.61-1.64: dZ's product 386 us, held up by
 // the 824 MB that it writes, tensor pipe 74 %; dW's 360, dX's 344). Of few tokens: W's bytes, 1 of 50257 x 768 29 us.
 #include "linear_wide.cuh"
@@ -44,6 +44,7 @@ template <> struct Wide<OP_LSE> {
   static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
   static constexpr uint32_t STAGE = 2 * kHalf, SMEM = STAGES * STAGE + 1024;
 };
+template <> struct Wide<OP_LSE_PARTS> : Wide<OP_LSE> {};
 template <> struct Wide<OP_DLOGITS> {
   using Params = VocabParams;
   static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
@@ -98,9 +99,9 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * (OP == OP_DLOGITS ? 4096u : 8192u);
   uint32_t i = 0, stores = 0;
   const float scale = OP == OP_DX_SPLIT ? dw_scale(p.scale, p.count) : 1.0f;
-  if (OP == OP_LSE && pair == 0 && rank == 0 && warp == 2 && lane == 0) *p.ticket = 0u;
+  if (is_lse(OP) && pair == 0 && rank == 0 && warp == 2 && lane == 0) *p.ticket = 0u;
   const int tiles = num_m * num_n, items = wide_items<OP>(p, tiles);
-  for (int item = pair; item < items; item += pairs, ++i) {
+  for (int item = pair; item < items; item += pairs) {
     const int part_k = OP == OP_DX_SPLIT ? item / tiles : 0;
     int mb, nb;
     wide_tile_coords(item - part_k * tiles, num_m, num_n, mb, nb);
@@ -119,7 +120,89 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
         weight = p.dloss ? __ldg(p.dloss + row) : 1.0f;
       }
     }
+    // 32 logits of the row, of columns col0 ..: joined to s
+    Softmax s{__int_as_float(0xff800000), 0.0f};
+    const auto join_32 = [&](int col0, uint32_t (&r)[32]) {
+      if (static_cast<uint32_t>(target - col0) < 32u) {
+        float z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z = target - col0 == j ? __uint_as_float(r[j]) : z;
+        p.z_label[row] = z;
+      }
+      if (col0 + 32 > p.n) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = col0 + j < p.n ? r[j] : 0xff800000u;
+      }
+      float top = __uint_as_float(r[0]);
+#pragma unroll
+      for (int j = 1; j < 32; ++j) top = max_nan(top, __uint_as_float(r[j]));
+      top = __fmul_rn(top, kLog2e);
+      const f2 base = f2_both(-finite_or_0(top));
+      f2 sum = 0ull;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        float x, y;
+        f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), base), x, y);
+        sum = f2_add(sum, f2_make(exp2_fast(x), exp2_fast(y)));
+      }
+      float x, y;
+      f2_split(sum, x, y);
+      s.join({make_float2(top, __fadd_rn(x, y))});
+    };
+    const auto put_part = [&] {
+      if (row < p.m && c0 < p.n) p.part[static_cast<size_t>(nb * 2 + part) * p.m + row] = make_float2(s.top, s.sum);
+    };
+    // relaxed: the arrival only says that the tensor-memory loads are done (ordered by the fence before it)
+    const auto drained = [&](uint32_t a) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(acce_bar + 8u * a, 0))
+                     : "memory");
+    };
+    if constexpr (OP == OP_LSE_PARTS) {
+      // the row's 128 logits, added up part by part with rounding to nearest
+      f2 z[C::EPI_COLS / 2];
+#pragma unroll
+      for (int j = 0; j < C::EPI_COLS / 2; ++j) z[j] = 0ull;
+      bool stop = false;
+#pragma unroll 1
+      for (int chunk = 0; chunk < p.chunks; ++chunk, ++i) {
+        const uint32_t a = i & 1u, u = i >> 1;
+        if (!warp_wait_bounded(accf_bar + 8u * a, u & 1u, abort, kErrAccF)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
+#pragma unroll
+        for (int c = 0; c < C::EPI_COLS; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32cols(taddr + c, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            z[c / 2 + j] = f2_add(z[c / 2 + j], f2_make(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+        }
+        drained(a);
+      }
+      if (stop) break;
+#pragma unroll
+      for (int c = 0; c < C::EPI_COLS; c += 32) {
+        if (c0 + c >= p.n) continue;  // warp-uniform
+        uint32_t r[32];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float x, y;
+          f2_split(z[c / 2 + j], x, y);
+          r[2 * j] = __float_as_uint(x), r[2 * j + 1] = __float_as_uint(y);
+        }
+        join_32(c0 + c, r);
+      }
+      put_part();
+      continue;
+    }
     const uint32_t a = i & 1u, u = i >> 1;
+    ++i;
     if (!warp_wait_bounded(accf_bar + 8u * a, u & 1u, abort, kErrAccF)) break;
     tc_fence_after();
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
@@ -151,40 +234,13 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       }
     }
     if constexpr (OP == OP_LSE) {
-      Softmax s{__int_as_float(0xff800000), 0.0f};
 #pragma unroll 1
       for (int c = 0; c < C::EPI_COLS; c += 32) {
-        const int col0 = c0 + c;
         uint32_t r[32];
         tmem_ld_32cols(taddr + c, r);
-        if (col0 >= p.n) continue;  // warp-uniform
-        if (static_cast<uint32_t>(target - col0) < 32u) {
-          float z = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z = target - col0 == j ? __uint_as_float(r[j]) : z;
-          p.z_label[row] = z;
-        }
-        if (col0 + 32 > p.n) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = col0 + j < p.n ? r[j] : 0xff800000u;
-        }
-        float top = __uint_as_float(r[0]);
-#pragma unroll
-        for (int j = 1; j < 32; ++j) top = max_nan(top, __uint_as_float(r[j]));
-        top = __fmul_rn(top, kLog2e);
-        const f2 base = f2_both(-finite_or_0(top));
-        f2 sum = 0ull;
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float x, y;
-          f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), base), x, y);
-          sum = f2_add(sum, f2_make(exp2_fast(x), exp2_fast(y)));
-        }
-        float x, y;
-        f2_split(sum, x, y);
-        s.join({make_float2(top, __fadd_rn(x, y))});
+        if (c0 + c < p.n) join_32(c0 + c, r);  // warp-uniform
       }
-      if (row < p.m && c0 < p.n) p.part[static_cast<size_t>(nb * 2 + part) * p.m + row] = make_float2(s.top, s.sum);
+      put_part();
     }
     if constexpr (OP == OP_DLOGITS) {
 #pragma unroll 1
@@ -229,12 +285,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       }
       __syncwarp();
     }
-    tc_fence_before();
-    __syncwarp();
-    // relaxed: the arrival only says that the tensor-memory loads are done (ordered by the fence above)
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(acce_bar + 8u * a, 0))
-                   : "memory");
+    drained(a);
   }
   if (lane == 0) bulk_wait_group_all();  // no store still reads shared memory
 }
@@ -346,6 +397,12 @@ __global__ void __launch_bounds__(kThreads) sum_slots_kernel(const float* __rest
 // ------------------------------------------------------------------------------------
 uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 
+// The tensor cores add to an accumulator with truncation, about 2^-24 of it a step and always toward zero. The loss is
+// an fp32 result, so its logits are summed in parts of 16 K blocks (1024 elements), which are added with rounding
+// to nearest: at 8192 elements lse is 6.4e-6 of itself off in one part, 3.3e-7 in eight, at 1024 3.6e-7 (8192 x 32000
+// from 4096: 1077 us in one part, 1135 in four). The backward's logits go into exponentials that are rounded to bf16.
+constexpr int kLsePart = 16;
+
 // W as the launches see it: the shards that hold rows of the vocabulary
 struct Weights {
   int n, shard_rows;
@@ -355,7 +412,9 @@ struct Weights {
 template <int OP>
 int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t st, const char* who) {
   p.shard_rows = w.shard_rows;
-  p.chunks = 1, p.chunk_blocks = INT32_MAX / 2;
+  const int blocks = (p.k + BK - 1) / BK;
+  p.chunk_blocks = OP == OP_LSE_PARTS ? kLsePart : blocks;
+  p.chunks = (blocks + p.chunk_blocks - 1) / p.chunk_blocks;
   int rc;
   // a vocabulary's shards are long: copies as high as they can be, cut at the few places where a shard ends
   const bool fwd = OP != OP_DX_SPLIT;
@@ -499,7 +558,8 @@ extern "C" int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_sha
   p.z_label = reinterpret_cast<float*>(ws + sp.z_label);
   p.ticket = reinterpret_cast<unsigned int*>(ws + sp.ticket);
   if ((rc = encode(&p.a, X, p.m, p.k, p.k, BK, 128, false, who))) return rc;
-  if ((rc = launch_product<OP_LSE>(p, w, true, st, who))) return rc;
+  const bool parts = p.k > kLsePart * BK;
+  if ((rc = parts ? launch_product<OP_LSE_PARTS>(p, w, true, st, who) : launch_product<OP_LSE>(p, w, true, st, who))) return rc;
   const cudaError_t e =
       launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>((m_tokens + 31) / 32)), dim3(32 * kJoinWarps), 0, 1, st, p.part,
                         sp.parts, p.m, p.z_label, labels, p.labels_wide, p.vocab, loss, lse,

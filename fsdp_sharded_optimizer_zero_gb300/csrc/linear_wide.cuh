@@ -21,10 +21,12 @@ namespace {
 
 // The products. What an operation loads: like the forward (both operands K-major, the second W's row
 // shards), like dx (W's shards read MN-major along the contraction) or like dw (both MN-major).
-//   OP_LSE, OP_DLOGITS, OP_DX_SPLIT   the loss over the vocabulary: its forward's and backward's logits,
-//                                     and an input gradient whose contraction is split over pairs
-enum { OP_FWD, OP_DX, OP_DW, OP_LSE, OP_DLOGITS, OP_DX_SPLIT };
-__host__ __device__ constexpr bool loads_as_fwd(int op) { return op == OP_FWD || op == OP_LSE || op == OP_DLOGITS; }
+//   OP_LSE, OP_LSE_PARTS, OP_DLOGITS  the loss over the vocabulary: its forward's logits, summed at once or in parts of
+//                                     the contraction, and its backward's
+//   OP_DX_SPLIT                       an input gradient whose contraction is split over pairs
+enum { OP_FWD, OP_DX, OP_DW, OP_LSE, OP_LSE_PARTS, OP_DLOGITS, OP_DX_SPLIT };
+__host__ __device__ constexpr bool is_lse(int op) { return op == OP_LSE || op == OP_LSE_PARTS; }
+__host__ __device__ constexpr bool loads_as_fwd(int op) { return op == OP_FWD || is_lse(op) || op == OP_DLOGITS; }
 __host__ __device__ constexpr bool loads_as_dx(int op) { return op == OP_DX || op == OP_DX_SPLIT; }
 
 constexpr int BK = 64;                        // contraction elements of one stage (128 bytes of bf16)
@@ -424,11 +426,11 @@ template <int OP>
 __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p, uint8_t* smem, uint32_t tmem_base,
                                               uint32_t accf_bar, uint32_t acce_bar, volatile int* abort, int warp,
                                               int lane, uint32_t rank, int pair, int pairs, int num_m, int num_n);
-// What else the loss over the vocabulary sets: where in W its columns (OP_LSE, OP_DLOGITS) or its
+// What else the loss over the vocabulary sets: where in W its columns (logits) or its
 // contraction (OP_DX_SPLIT) begin, and in how many parts the contraction is summed.
 template <int OP>
 __device__ __forceinline__ int first_w_row(const typename Wide<OP>::Params& p) {
-  if constexpr (OP == OP_LSE || OP == OP_DLOGITS || OP == OP_DX_SPLIT) return p.w_row0;
+  if constexpr (is_lse(OP) || OP == OP_DLOGITS || OP == OP_DX_SPLIT) return p.w_row0;
   return 0;
 }
 // A work item of the persistent loop: an output tile, and (OP_DX_SPLIT) the K blocks of one part

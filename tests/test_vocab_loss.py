@@ -19,7 +19,7 @@ SUM, U, B16 = 2.0 ** -23, 2.0 ** -24, 2.0 ** -8
 SHAPES = [(1, 1, 8, 8, 1), (1, 1000, 1000, 72, 1), (5, 129, 144, 64, 2), (130, 255, 256, 136, 1), (256, 256, 256, 256, 1),
           (300, 257, 264, 264, 1), (257, 513, 640, 520, 5), (1003, 1157, 1160, 520, 5), (64, 5000, 5120, 768, 8),
           (700, 2100, 2560, 328, 4), (31, 1400, 2048, 136, 8), (2049, 3000, 3008, 128, 2), (20, 4100, 4224, 1032, 3),
-          (520, 640, 640, 2056, 16), (4400, 2900, 2944, 192, 1)]
+          (520, 640, 640, 2056, 16), (4400, 2900, 2944, 192, 1), (600, 700, 704, 8200, 2), (300, 5000, 5120, 1096, 8)]
 
 
 @pytest.fixture(scope="module")
@@ -64,15 +64,17 @@ class Case:
         self.x64, self.w64 = self.x.double(), w[:vocab].double()
         self.z = self.x64 @ self.w64.t()
         self.ez = (k + 1) * SUM * (self.x64.abs() @ self.w64.abs().t())
+        # the forward's logits are summed in parts of 1024 products, which are added with rounding to nearest
+        ef = (min(k, 1024) + k // 1024 + 1) / (k + 1) * self.ez
         self.lse = torch.logsumexp(self.z, 1)
         # the sum's terms: exponential 2^-21, its argument 2 U of z and of the maximum (up to z's size), then
         # additions: 16 in a thread's two lanes, 4 groups, and the parts, in eight turns and joined; each join
         # scales by an exponential
         parts = -(-vocab // 128)
         top = self.z.abs().amax(1)
-        self.e_lse = self.ez.amax(1) + 4 * U * (top + 1) + (parts / 8 + 16) * 2.0 ** -20 + 4 * U * self.lse.abs()
+        self.e_lse = ef.amax(1) + 4 * U * (top + 1) + (parts / 8 + 16) * 2.0 ** -20 + 4 * U * self.lse.abs()
         self.loss = torch.where(self.real, self.lse - self.z.gather(1, self.at[:, None])[:, 0], 0.0)
-        self.e_loss = torch.where(self.real, self.e_lse + self.ez.gather(1, self.at[:, None])[:, 0] + U * self.loss.abs(), 0.0)
+        self.e_loss = torch.where(self.real, self.e_lse + ef.gather(1, self.at[:, None])[:, 0] + U * self.loss.abs(), 0.0)
 
     def forward(self, z, total=True, **kw):
         out = [torch.full((self.m + 16,), 3.0, device=DEV) for _ in range(2)] + [torch.full((4,), 3.0, device=DEV)]

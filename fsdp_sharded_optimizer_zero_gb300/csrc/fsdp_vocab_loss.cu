@@ -14,9 +14,9 @@
 // 3.7e-3 of the gradients' norm off, now 1.7e-3, the outputs' own rounding).
 //
 // Bound by tensor work: forward 8192 x 50257 from 768 346 us (1.83 PFLOP/s; tensor pipe 83 % active), of which joining
-// the parts takes about 10, from 4096 (vocabulary 32000) 1135 us (1.89); gradients 8192 x 32000 from 4096 3.50-3.57 ms
-// (1.81-1.84, at the power limit 3.97), 8192 x 50257 from 768 1.16-1.18 ms (1.61-1.64: dZ's product 386 us, held up by
-// the 824 MB that it writes, tensor pipe 74 %; dW's 360, dX's 344). Of few tokens: W's bytes, 1 of 50257 x 768 29 us.
+// the parts takes about 10, from 4096 (vocabulary 32000) 1135 us (1.89); gradients 8192 x 32000 from 4096 3.55 ms
+// (1.82; at the power limit 3.97), 8192 x 50257 from 768 1.16-1.18 ms (1.61-1.64: dZ's product 386 us, held up by the
+// 824 MB that it writes, tensor pipe 74 %; dW's 360, dX's 344). Of few tokens: W's bytes, 1 of 50257 x 768 29 us.
 #include "linear_wide.cuh"
 
 namespace zgb {
@@ -50,6 +50,7 @@ template <> struct Wide<OP_DLOGITS> {
   static constexpr int EPI_WARPS = 8, EPI_COLS = 128, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
   static constexpr uint32_t STAGE = 2 * kHalf, EPI = EPI_WARPS * 4096u, SMEM = STAGES * STAGE + EPI + 1024;
 };
+template <> struct Wide<OP_DLOGITS_PARTS> : Wide<OP_DLOGITS> {};
 template <> struct Wide<OP_DX_SPLIT> {
   using Params = VocabParams;
   static constexpr int EPI_WARPS = 4, EPI_COLS = 256, STAGES = 6, THREADS = 32 * (2 + EPI_WARPS);
@@ -95,8 +96,8 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   using C = Wide<OP>;
   const int q = warp & 3;            // the tensor-memory lane quarter this warp may read
   const int part = (warp - 2) >> 2;  // which of the quarter's warps
-  // staging: two buffers of 4 KiB a warp for dX, one for dZ (not OP_LSE)
-  uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * (OP == OP_DLOGITS ? 4096u : 8192u);
+  // staging: two buffers of 4 KiB a warp for dX, one for dZ (the forward: none)
+  uint8_t* stage = smem + C::STAGES * C::STAGE + static_cast<uint32_t>(warp - 2) * (is_dlogits(OP) ? 4096u : 8192u);
   uint32_t i = 0, stores = 0;
   const float scale = OP == OP_DX_SPLIT ? dw_scale(p.scale, p.count) : 1.0f;
   if (is_lse(OP) && pair == 0 && rank == 0 && warp == 2 && lane == 0) *p.ticket = 0u;
@@ -115,7 +116,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       const int label = label_at(p.labels, p.labels_wide, row, p.vocab);
       counted = label >= 0;
       target = counted ? label - p.w_row0 : -1;
-      if (OP == OP_DLOGITS && counted) {
+      if (is_dlogits(OP) && counted) {
         lse2 = __fmul_rn(__ldg(p.lse + row), kLog2e);
         weight = p.dloss ? __ldg(p.dloss + row) : 1.0f;
       }
@@ -149,6 +150,42 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       f2_split(sum, x, y);
       s.join({make_float2(top, __fadd_rn(x, y))});
     };
+    // ... or written as dZ, at column c of this warp's (the buffer takes two of them)
+    const auto put_32 = [&](int c, uint32_t (&r)[32]) {
+      const int h = (c >> 5) & 1, col0 = c0 + c;
+      uint8_t* buf = stage;
+      // few instructions a pair: what concerns single elements (the label's, those past the vocabulary) is
+      // put right in the packed words and in the buffer
+      uint4 w[4];
+      uint32_t* word = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        float x, y;
+        f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), f2_both(-lse2)), x, y);
+        word[j >> 1] = f2_to_bf16x2(f2_mul(f2_make(exp2_fast(x), exp2_fast(y)), f2_both(weight)));
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) word[j] = counted ? word[j] : 0u;  // whatever the logits are
+      if (col0 + 32 > p.n) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          word[j] = col0 + 2 * j >= p.n ? 0u : col0 + 2 * j + 1 >= p.n ? word[j] & 0xFFFFu : word[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = w[j];
+      const int at = target - col0;
+      if (static_cast<uint32_t>(at) < 32u) {
+        float z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z = at == j ? __uint_as_float(r[j]) : z;
+        const float v = __fsub_rn(__fmul_rn(exp2_fast(__fmaf_rn(z, kLog2e, -lse2)), weight), weight);
+        *reinterpret_cast<uint16_t*>(buf + staged_at(lane, 4 * h + (at >> 3)) + 2 * (at & 7)) = f32_to_bf16_bits(v);
+      }
+      if (h == 1 || col0 + 32 >= p.cols) {
+        __syncwarp();
+        stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.cols, p.ld, lane);
+      }
+    };
     const auto put_part = [&] {
       if (row < p.m && c0 < p.n) p.part[static_cast<size_t>(nb * 2 + part) * p.m + row] = make_float2(s.top, s.sum);
     };
@@ -160,7 +197,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
         asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(acce_bar + 8u * a, 0))
                      : "memory");
     };
-    if constexpr (OP == OP_LSE_PARTS) {
+    if constexpr (OP == OP_LSE_PARTS || OP == OP_DLOGITS_PARTS) {
       // the row's 128 logits, added up part by part with rounding to nearest
       f2 z[C::EPI_COLS / 2];
 #pragma unroll
@@ -188,7 +225,8 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       if (stop) break;
 #pragma unroll
       for (int c = 0; c < C::EPI_COLS; c += 32) {
-        if (c0 + c >= p.n) continue;  // warp-uniform
+        if (is_dlogits(OP) && ((c >> 5) & 1) == 0) __syncwarp();  // the buffer's last store has read it
+        if (c0 + c >= (is_lse(OP) ? p.n : p.cols)) continue;  // warp-uniform
         uint32_t r[32];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -196,9 +234,11 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
           f2_split(z[c / 2 + j], x, y);
           r[2 * j] = __float_as_uint(x), r[2 * j + 1] = __float_as_uint(y);
         }
-        join_32(c0 + c, r);
+        if constexpr (is_lse(OP)) join_32(c0 + c, r);
+        else put_32(c, r);
       }
-      put_part();
+      if constexpr (is_lse(OP)) put_part();
+      else __syncwarp();
       continue;
     }
     const uint32_t a = i & 1u, u = i >> 1;
@@ -245,43 +285,10 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
     if constexpr (OP == OP_DLOGITS) {
 #pragma unroll 1
       for (int c = 0; c < C::EPI_COLS; c += 32) {
-        const int h = (c >> 5) & 1, col0 = c0 + c;
-        uint8_t* buf = stage;
-        if (h == 0) __syncwarp();  // the buffer's last store has read it
+        if (((c >> 5) & 1) == 0) __syncwarp();  // the buffer's last store has read it
         uint32_t r[32];
         tmem_ld_32cols(taddr + c, r);
-        if (col0 >= p.cols) continue;  // warp-uniform
-        // few instructions a pair: what concerns single elements (the label's, those past the vocabulary) is
-        // put right in the packed words and in the buffer
-        uint4 w[4];
-        uint32_t* word = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float x, y;
-          f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), f2_both(-lse2)), x, y);
-          word[j >> 1] = f2_to_bf16x2(f2_mul(f2_make(exp2_fast(x), exp2_fast(y)), f2_both(weight)));
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) word[j] = counted ? word[j] : 0u;  // whatever the logits are
-        if (col0 + 32 > p.n) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            word[j] = col0 + 2 * j >= p.n ? 0u : col0 + 2 * j + 1 >= p.n ? word[j] & 0xFFFFu : word[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + staged_at(lane, 4 * h + j)) = w[j];
-        const int at = target - col0;
-        if (static_cast<uint32_t>(at) < 32u) {
-          float z = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z = at == j ? __uint_as_float(r[j]) : z;
-          const float v = __fsub_rn(__fmul_rn(exp2_fast(__fmaf_rn(z, kLog2e, -lse2)), weight), weight);
-          *reinterpret_cast<uint16_t*>(buf + staged_at(lane, 4 * h + (at >> 3)) + 2 * (at & 7)) = f32_to_bf16_bits(v);
-        }
-        if (h == 1 || col0 + 32 >= p.cols) {
-          __syncwarp();
-          stage_store(buf, p.y, r0, col0 - 32 * h, p.m, p.cols, p.ld, lane);
-        }
+        if (c0 + c < p.cols) put_32(c, r);  // warp-uniform
       }
       __syncwarp();
     }
@@ -400,8 +407,9 @@ uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 // The tensor cores add to an accumulator with truncation, about 2^-24 of it a step and always toward zero. The loss is
 // an fp32 result, so its logits are summed in parts of 16 K blocks (1024 elements), which are added with rounding
 // to nearest: at 8192 elements lse is 6.4e-6 of itself off in one part, 3.3e-7 in eight, at 1024 3.6e-7 (8192 x 32000
-// from 4096: 1077 us in one part, 1135 in four). The backward's logits go into exponentials that are rounded to bf16.
-constexpr int kLsePart = 16;
+// from 4096: 1077 us in one part, 1135 in four). The backward's logits are summed the same way: they have to be the
+// forward's, bit for bit, for exp(Z - lse) to add up to 1, or what is left of a sure token's gradient is wrong.
+constexpr int kPartBlocks = 16;
 
 // W as the launches see it: the shards that hold rows of the vocabulary
 struct Weights {
@@ -413,7 +421,7 @@ template <int OP>
 int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t st, const char* who) {
   p.shard_rows = w.shard_rows;
   const int blocks = (p.k + BK - 1) / BK;
-  p.chunk_blocks = OP == OP_LSE_PARTS ? kLsePart : blocks;
+  p.chunk_blocks = OP == OP_LSE_PARTS || OP == OP_DLOGITS_PARTS ? kPartBlocks : blocks;
   p.chunks = (blocks + p.chunk_blocks - 1) / p.chunk_blocks;
   int rc;
   // a vocabulary's shards are long: copies as high as they can be, cut at the few places where a shard ends
@@ -421,6 +429,11 @@ int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t
   if ((rc = encode_w(p, w.n, w.w, p.vocab, fwd, fwd ? 128 : BK, &one_copy, who))) return rc;
   if (p.w_levels > 1) return launch_wide<OP, COPIES_CUT>(p, st, who);
   return one_copy ? launch_wide<OP, COPIES_ONE>(p, st, who) : launch_wide<OP, COPIES_EQUAL>(p, st, who);
+}
+
+template <int OP, int OP_PARTS>
+int launch_logits(VocabParams& p, const Weights& w, cudaStream_t st, const char* who) {
+  return p.k > kPartBlocks * BK ? launch_product<OP_PARTS>(p, w, true, st, who) : launch_product<OP>(p, w, true, st, who);
 }
 
 // The backward's pieces and its workspace: dZ of a piece [m, ld], and where dX is summed in parts, those.
@@ -558,8 +571,7 @@ extern "C" int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_sha
   p.z_label = reinterpret_cast<float*>(ws + sp.z_label);
   p.ticket = reinterpret_cast<unsigned int*>(ws + sp.ticket);
   if ((rc = encode(&p.a, X, p.m, p.k, p.k, BK, 128, false, who))) return rc;
-  const bool parts = p.k > kLsePart * BK;
-  if ((rc = parts ? launch_product<OP_LSE_PARTS>(p, w, true, st, who) : launch_product<OP_LSE>(p, w, true, st, who))) return rc;
+  if ((rc = launch_logits<OP_LSE, OP_LSE_PARTS>(p, w, st, who))) return rc;
   const cudaError_t e =
       launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>((m_tokens + 31) / 32)), dim3(32 * kJoinWarps), 0, 1, st, p.part,
                         sp.parts, p.m, p.z_label, labels, p.labels_wide, p.vocab, loss, lse,
@@ -625,7 +637,7 @@ extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_sh
     p.labels = labels, p.labels_wide = label_bytes == 8;
     p.lse = lse, p.dloss = dloss;
     if ((rc = encode(&p.a, X, m, k, k, BK, 128, false, who))) return rc;
-    if ((rc = launch_product<OP_DLOGITS>(p, w, true, st, who))) return rc;
+    if ((rc = launch_logits<OP_DLOGITS, OP_DLOGITS_PARTS>(p, w, st, who))) return rc;
     if (dW && (rc = launch_linear_dw(dz, ld, X, m, cols, k, scale, count, dW + c0 * k_in, st, who))) return rc;
     if (!dX) continue;
     VocabParams d;

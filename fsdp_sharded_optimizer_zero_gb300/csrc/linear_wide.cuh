@@ -21,12 +21,14 @@ namespace {
 
 // The products. What an operation loads: like the forward (both operands K-major, the second W's row
 // shards), like dx (W's shards read MN-major along the contraction) or like dw (both MN-major).
-//   OP_LSE, OP_LSE_PARTS, OP_DLOGITS  the loss over the vocabulary: its forward's logits, summed at once or in parts of
-//                                     the contraction, and its backward's
-//   OP_DX_SPLIT                       an input gradient whose contraction is split over pairs
-enum { OP_FWD, OP_DX, OP_DW, OP_LSE, OP_LSE_PARTS, OP_DLOGITS, OP_DX_SPLIT };
+//   OP_LSE, OP_DLOGITS      the loss over the vocabulary: its forward's and backward's logits
+//   OP_LSE_PARTS, OP_DLOGITS_PARTS    the same, their contraction summed in parts
+//   OP_DX_SPLIT             an input gradient whose contraction is split over pairs
+enum { OP_FWD, OP_DX, OP_DW, OP_LSE, OP_LSE_PARTS, OP_DLOGITS, OP_DLOGITS_PARTS, OP_DX_SPLIT };
 __host__ __device__ constexpr bool is_lse(int op) { return op == OP_LSE || op == OP_LSE_PARTS; }
-__host__ __device__ constexpr bool loads_as_fwd(int op) { return op == OP_FWD || is_lse(op) || op == OP_DLOGITS; }
+__host__ __device__ constexpr bool is_dlogits(int op) { return op == OP_DLOGITS || op == OP_DLOGITS_PARTS; }
+__host__ __device__ constexpr bool is_logits(int op) { return is_lse(op) || is_dlogits(op); }
+__host__ __device__ constexpr bool loads_as_fwd(int op) { return op == OP_FWD || is_logits(op); }
 __host__ __device__ constexpr bool loads_as_dx(int op) { return op == OP_DX || op == OP_DX_SPLIT; }
 
 constexpr int BK = 64;                        // contraction elements of one stage (128 bytes of bf16)
@@ -430,7 +432,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
 // contraction (OP_DX_SPLIT) begin, and in how many parts the contraction is summed.
 template <int OP>
 __device__ __forceinline__ int first_w_row(const typename Wide<OP>::Params& p) {
-  if constexpr (is_lse(OP) || OP == OP_DLOGITS || OP == OP_DX_SPLIT) return p.w_row0;
+  if constexpr (is_logits(OP) || OP == OP_DX_SPLIT) return p.w_row0;
   return 0;
 }
 // A work item of the persistent loop: an output tile, and (OP_DX_SPLIT) the K blocks of one part

@@ -670,7 +670,7 @@ ZERO_API int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab,
 
 /* Gradients of c times the sum over the counted tokens of dloss[i] loss[i], c = scale / max(total[1], 1), with
  * dloss (fp32 [m_tokens]) and total (as the forward wrote it) nullable, then 1: dZ = (exp(Z - lse) -
- * onehot(label)) dloss, computed piece by piece from X and W again and rounded to bf16; dX = bf16(c dZ W)
+ * onehot(label)) dloss, computed piece by piece from X and W again (the forward's Z, bit for bit) and rounded to bf16; dX = bf16(c dZ W)
  * [m_tokens, k_in] and dW = bf16(c dZ^T X) [rows_out, k_in], c applied to the fp32 sums, one of the two nullable. (A
  * factor that all tokens share belongs in scale: in dloss it is rounded alike with every label's element.) A token
  * that is not counted has zeros in dZ and dX whatever its logits, but its row of X enters dW's product, times zero:

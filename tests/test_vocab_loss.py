@@ -169,6 +169,34 @@ def test_flat_and_peaked_logits(z, std):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k,piece", [(776, 0), (4104, 0), (8200, 256)])
+def test_what_is_left_of_sure_tokens_adds_up_to_nothing(z, k, piece):
+    """The gradients of a token's logits add up to 0. Column 0 of X is 0 and of W 1, so dX's is their sum: small
+    where the label's probability is near 1, however large the logits, if the backward's logits are the forward's."""
+    m, vocab = 130, 600
+    x = randn(m, k).abs().add(0.5).to(BF)
+    w = (1.0 + 0.01 * randn(vocab, k, key=1)) * (26.0 / (1.3 * k))
+    w[7] *= 40.0 / 26.0
+    w = w.to(BF)
+    x[:, 0], w[:, 0] = 0.0, 1.0
+    labels = torch.full((m,), 7, dtype=torch.int64, device=DEV)
+    loss, lse = torch.empty(m, device=DEV), torch.empty(m, device=DEV)
+    dX = torch.empty(m, k, dtype=BF, device=DEV)
+    z.fsdp_vocab_loss_forward([w], x, labels, loss, lse)
+    z.fsdp_vocab_loss_backward([w], x, labels, lse, dX, None, piece=piece)
+    z.zero_device_status()
+    logits = x.double() @ w.double().t()
+    p = torch.softmax(logits, 1)
+    left = 1.0 - p[:, 7]
+    assert 1e-5 < float(left.min()) and float(left.max()) < 0.05 and float(logits[:, 7].min()) > 30.0
+    # dZ rounded to bf16, the label's and the others'; lse as in Case (without its logits' sums: they are the same
+    # here), then the argument's roundings and the exponential's; dX's sum
+    top, parts = logits.amax(1), -(-vocab // 128)
+    e = 4 * U * (top + 1) + (parts / 8 + 16) * 2.0 ** -20 + 4 * U * top + 4 * U * (2 * top + 1) + 2.0 ** -20
+    bound = B16 * 2 * left + e + (vocab + 32) * SUM * 2 * left
+    inside(dX[:, 0], torch.zeros_like(top), bound * (1 + B16), "the sum of dZ")
+
+
 def test_no_token_counts(z):
     c = Case(200, 600, 640, 136, 2)
     c.labels.fill_(-100)

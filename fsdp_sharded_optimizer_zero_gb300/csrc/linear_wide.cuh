@@ -64,7 +64,7 @@ struct LinearParams {
   uint8_t* zs;
   float scale;                    // dw
   const float* count;             // dw: nullable, what the scale is divided by (1 at least)
-  int chunks, chunk_blocks;       // dw, fp32: the contraction in chunks of chunk_blocks K blocks (1 chunk otherwise)
+  int chunks, chunk_blocks;       // fp32 dw, logits: the contraction in chunks of chunk_blocks K blocks (1 chunk otherwise)
 };
 
 // ------------------------------------------------------------------------------------

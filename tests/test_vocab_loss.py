@@ -19,7 +19,8 @@ SUM, U, B16 = 2.0 ** -23, 2.0 ** -24, 2.0 ** -8
 SHAPES = [(1, 1, 8, 8, 1), (1, 1000, 1000, 72, 1), (5, 129, 144, 64, 2), (130, 255, 256, 136, 1), (256, 256, 256, 256, 1),
           (300, 257, 264, 264, 1), (257, 513, 640, 520, 5), (1003, 1157, 1160, 520, 5), (64, 5000, 5120, 768, 8),
           (700, 2100, 2560, 328, 4), (31, 1400, 2048, 136, 8), (2049, 3000, 3008, 128, 2), (20, 4100, 4224, 1032, 3),
-          (520, 640, 640, 2056, 16), (4400, 2900, 2944, 192, 1), (600, 700, 704, 8200, 2), (300, 5000, 5120, 1096, 8)]
+          (520, 640, 640, 2056, 16), (4400, 2900, 2944, 192, 1), (600, 700, 704, 8200, 2), (300, 5000, 5120, 1096, 8),
+          (4400, 2900, 2944, 1096, 2)]
 
 
 @pytest.fixture(scope="module")

@@ -20,7 +20,8 @@ LIB = PKG / "libzero_gb300.so"
 SOURCES = ["capi.cu", "fused_step.cu", "step_kernels.cu", "fsdp_gemm.cu", "fsdp_unit.cu", "fsdp_zero3.cu",
            "fsdp_static_scratch.cu", "fsdp_linear.cu", "fsdp_checkpoint8.cu", "fsdp_norm.cu",
            "fsdp_embedding.cu", "fsdp_vocab_loss.cu"]
-HEADERS = ["internal.h", "device_common.cuh", "step_common.cuh", "tcgen05.cuh", "linear_math.cuh", "linear_wide.cuh"]
+HEADERS = ["internal.h", "device_common.cuh", "step_common.cuh", "tcgen05.cuh", "linear_math.cuh", "linear_wide.cuh",
+           "linear_narrow.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = [
     "-O3", "-std=c++17", "-lineinfo", *ARCH,

@@ -6,7 +6,8 @@
 //   backward  in pieces of the vocabulary: Z again from X and the piece of W, dZ = (exp(Z - lse) - onehot) w
 //             in bf16, then the piece's rows of dW = c dZ^T X, and dX += c dZ W
 //
-// The products run in linear_wide_kernel; what is here are its epilogues and the joining passes. Softmax
+// The products run in linear_wide_kernel, of few tokens in linear_narrow_kernel; what is here are their epilogues and the
+// joining passes. Softmax
 // statistics and all sums are fp32. dZ is rounded to bf16, as the gradient of a linear unit's output is
 // everywhere in the library: the tensor cores multiply bf16, and its gradients are bf16. The factor c that all tokens
 // share (the loss's scale, one over the count) is left for the fp32 sums: in dZ it would be rounded alike in every
@@ -16,8 +17,9 @@
 // Bound by tensor work: forward 8192 x 50257 from 768 346 us (1.83 PFLOP/s; tensor pipe 83 % active), of which joining
 // the parts takes about 10, from 4096 (vocabulary 32000) 1135 us (1.89); gradients 8192 x 32000 from 4096 3.55 ms
 // (1.82; at the power limit 3.97), 8192 x 50257 from 768 1.16-1.18 ms (1.61-1.64: dZ's product 386 us, held up by the
-// 824 MB that it writes, tensor pipe 74 %; dW's 360, dX's 344). Of few tokens: W's bytes, 1 of 50257 x 768 29 us.
-#include "linear_wide.cuh"
+// 824 MB that it writes, tensor pipe 74 %; dW's 360, dX's 344). Of few tokens: W's bytes, one of 32000 x 4096 45 us (5.8
+// TB/s), its gradients 157 (W read twice, dW written; 50257 x 768 21 and 69 us).
+#include "linear_narrow.cuh"
 
 namespace zgb {
 namespace {
@@ -297,6 +299,65 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
   if (lane == 0) bulk_wait_group_all();  // no store still reads shared memory
 }
 
+// ------------------------------------------------------------------------------------
+// few tokens: the narrow kernel's epilogue, a row's 128 columns in a warp, 4 a lane
+// ------------------------------------------------------------------------------------
+struct RowOfLoss {  // loaded while the main loop runs, all lanes the same
+  long long label;
+  float lse, dloss;
+  __device__ __forceinline__ void load(const VocabParams& p, int row, int) {
+    if (row >= p.m) return;
+    if (p.labels_wide) {
+      asm volatile("ld.global.nc.s64 %0, [%1];" : "=l"(label) : "l"(static_cast<const long long*>(p.labels) + row));
+    } else {
+      int l;
+      asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(l) : "l"(static_cast<const int*>(p.labels) + row));
+      label = l;
+    }
+    if (p.lse) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(lse) : "l"(p.lse + row));
+    if (p.dloss) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(dloss) : "l"(p.dloss + row));
+  }
+};
+template <> struct Side4<OP_LSE> : RowOfLoss {};
+template <> struct Side4<OP_DLOGITS> : RowOfLoss {};
+
+template <int OP, int ACT>
+__device__ __forceinline__ void epilogue4(const typename Wide<OP>::Params& p, int row, int col, uint2, const Side4<OP>& side,
+                                          f2 (&v)[2]) {
+  float z[4];
+  f2_split(v[0], z[0], z[1]);
+  f2_split(v[1], z[2], z[3]);
+  const bool counted = side.label >= 0 && side.label < p.vocab;
+  const int at = counted ? static_cast<int>(side.label) - p.w_row0 - col : -1;  // the label's, of this lane's columns
+  if constexpr (OP == OP_LSE) {
+    if (row == 0 && col == 0) *p.ticket = 0u;
+    if (at >= 0 && at < 4) p.z_label[row] = at == 0 ? z[0] : at == 1 ? z[1] : at == 2 ? z[2] : z[3];
+    float top = __int_as_float(0xff800000);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = col + j < p.n ? z[j] : __int_as_float(0xff800000), top = max_nan(top, z[j]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = __fmul_rn(top, kLog2e);
+    const float base = -finite_or_0(top);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum = __fadd_rn(sum, exp2_fast(__fmaf_rn(z[j], kLog2e, base)));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+    if ((threadIdx.x & 31) == 0) p.part[static_cast<size_t>(col >> 7) * p.m + row] = make_float2(top, sum);
+  } else {
+    const float lse2 = __fmul_rn(side.lse, kLog2e), weight = p.dloss ? side.dloss : 1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float e = __fmul_rn(exp2_fast(__fmaf_rn(z[j], kLog2e, -lse2)), weight);
+      z[j] = counted && col + j < p.n ? (at == j ? __fsub_rn(e, weight) : e) : 0.0f;
+    }
+    if (col < p.cols)
+      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(row) * p.ld + col) =
+          make_uint2(f2_to_bf16x2(f2_make(z[0], z[1])), f2_to_bf16x2(f2_make(z[2], z[3])));
+  }
+}
+
 // lse and loss from the parts of a row: a block takes 32 rows, its warps the parts in turn, kAtOnce of them in
 // flight; their largest maximum is found first. With total, a block also leaves its rows' sum of losses and count,
 // and the block that comes last (a ticket, left at 0 by the product before) adds them, in the order of the
@@ -431,9 +492,36 @@ int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t
   return one_copy ? launch_wide<OP, COPIES_ONE>(p, st, who) : launch_wide<OP, COPIES_EQUAL>(p, st, who);
 }
 
+template <int OP, int TN>
+int launch_few(const VocabParams& p, int splits, cudaStream_t st, const char* who) {
+  return p.w_levels > 1 ? launch_narrow<OP, TN, true>(p, splits, st, who) : launch_narrow<OP, TN, false>(p, splits, st, who);
+}
+
+// X's logits (p.a's map is set here too). The kernel follows from m, the whole vocabulary and k, so that the forward and
+// each of the backward's pieces sum alike. The narrow kernel (wide in brackets, us) for up to 32 tokens: one of 50257 x
+// 768 21 (28), of 32000 x 4096 45 (77), 16 of 131072 x 1024 55 (58); for up to 64 while its tiles are resident at once:
+// 64 of 32000 x 4096 48 (55), but of 50257 x 2048 48 (46); and where so few that the contraction is split: 100 of 2000 x
+// 4096 13 (27), 256 of 1157 x 520 12.1 (12.4), unsplit 1003 of 1157 x 520 14.8 (12.8), 128 of 32000 x 4096 62 (55).
 template <int OP, int OP_PARTS>
-int launch_logits(VocabParams& p, const Weights& w, cudaStream_t st, const char* who) {
-  return p.k > kPartBlocks * BK ? launch_product<OP_PARTS>(p, w, true, st, who) : launch_product<OP>(p, w, true, st, who);
+int launch_logits(VocabParams& p, const Weights& w, const zero_bf16* x, cudaStream_t st, const char* who) {
+  int rc;
+  const int blocks = (p.k + BK - 1) / BK;
+  Choice c = choose(OP_FWD, p.m, p.vocab, p.k, false);
+  const bool resident = (p.vocab + 127) / 128 <= 2 * num_sms();
+  c.wide = c.wide || (c.splits == 1 && p.m > (resident ? 64 : 32));
+  // its accumulators and splits have to make parts of kPartBlocks
+  while (!c.wide && (blocks + c.splits - 1) / c.splits > kPartBlocks * (kLogitCols / c.tn)) {
+    c.splits *= 2;
+    c.wide = c.splits > (c.tn == 128 ? 4 : 8);
+  }
+  if ((rc = encode(&p.a, x, p.m, p.k, p.k, BK, c.wide ? 128 : c.tn, false, who))) return rc;
+  if (c.wide) return blocks > kPartBlocks ? launch_product<OP_PARTS>(p, w, true, st, who) : launch_product<OP>(p, w, true, st, who);
+  bool one_copy = false;
+  p.shard_rows = w.shard_rows, p.chunk_blocks = kPartBlocks;
+  if ((rc = encode_w(p, w.n, w.w, p.vocab, true, kCutFrom, &one_copy, who))) return rc;
+  return c.tn == 32   ? launch_few<OP, 32>(p, c.splits, st, who)
+         : c.tn == 64 ? launch_few<OP, 64>(p, c.splits, st, who)
+                      : launch_few<OP, 128>(p, c.splits, st, who);
 }
 
 // The backward's pieces and its workspace: dZ of a piece [m, ld], and where dX is summed in parts, those.
@@ -570,8 +658,7 @@ extern "C" int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_sha
   p.part = static_cast<float2*>(workspace);
   p.z_label = reinterpret_cast<float*>(ws + sp.z_label);
   p.ticket = reinterpret_cast<unsigned int*>(ws + sp.ticket);
-  if ((rc = encode(&p.a, X, p.m, p.k, p.k, BK, 128, false, who))) return rc;
-  if ((rc = launch_logits<OP_LSE, OP_LSE_PARTS>(p, w, st, who))) return rc;
+  if ((rc = launch_logits<OP_LSE, OP_LSE_PARTS>(p, w, X, st, who))) return rc;
   const cudaError_t e =
       launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>((m_tokens + 31) / 32)), dim3(32 * kJoinWarps), 0, 1, st, p.part,
                         sp.parts, p.m, p.z_label, labels, p.labels_wide, p.vocab, loss, lse,
@@ -636,8 +723,7 @@ extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_sh
     p.cols = (cols + 7) / 8 * 8, p.ld = ld, p.y = dz;
     p.labels = labels, p.labels_wide = label_bytes == 8;
     p.lse = lse, p.dloss = dloss;
-    if ((rc = encode(&p.a, X, m, k, k, BK, 128, false, who))) return rc;
-    if ((rc = launch_logits<OP_DLOGITS, OP_DLOGITS_PARTS>(p, w, st, who))) return rc;
+    if ((rc = launch_logits<OP_DLOGITS, OP_DLOGITS_PARTS>(p, w, X, st, who))) return rc;
     if (dW && (rc = launch_linear_dw(dz, ld, X, m, cols, k, scale, count, dW + c0 * k_in, st, who))) return rc;
     if (!dX) continue;
     VocabParams d;

@@ -24,11 +24,13 @@ namespace {
 //   OP_LSE, OP_DLOGITS      the loss over the vocabulary: its forward's and backward's logits
 //   OP_LSE_PARTS, OP_DLOGITS_PARTS    the same, their contraction summed in parts
 //   OP_DX_SPLIT             an input gradient whose contraction is split over pairs
-enum { OP_FWD, OP_DX, OP_DW, OP_LSE, OP_LSE_PARTS, OP_DLOGITS, OP_DLOGITS_PARTS, OP_DX_SPLIT };
+//   OP_DW_SHORT             a bf16 weight gradient of few tokens, bound by its stores: eight epilogue warps, not four
+enum { OP_FWD, OP_DX, OP_DW, OP_DW_SHORT, OP_LSE, OP_LSE_PARTS, OP_DLOGITS, OP_DLOGITS_PARTS, OP_DX_SPLIT };
 __host__ __device__ constexpr bool is_lse(int op) { return op == OP_LSE || op == OP_LSE_PARTS; }
 __host__ __device__ constexpr bool is_dlogits(int op) { return op == OP_DLOGITS || op == OP_DLOGITS_PARTS; }
 __host__ __device__ constexpr bool is_logits(int op) { return is_lse(op) || is_dlogits(op); }
 __host__ __device__ constexpr bool loads_as_fwd(int op) { return op == OP_FWD || is_logits(op); }
+__host__ __device__ constexpr bool is_dw(int op) { return op == OP_DW || op == OP_DW_SHORT; }
 __host__ __device__ constexpr bool loads_as_dx(int op) { return op == OP_DX || op == OP_DX_SPLIT; }
 
 constexpr int BK = 64;                        // contraction elements of one stage (128 bytes of bf16)
@@ -318,7 +320,7 @@ __device__ __forceinline__ void stage_store_half(uint8_t* buf, const uint4 (&w)[
 // CTAs' shared memory. Persistent, two accumulators in tensor memory.
 //   warp 0       producer: lane i issues the i-th copy of a stage (TMA), both CTAs
 //   warp 1       MMA issuer (even CTA), tensor-memory allocation
-//   then 8 (dw: 4) epilogue warps, two (one) per tensor-memory lane quarter, sharing its columns
+//   then 8 (dw: 4, of few tokens 8) epilogue warps, two (one) per tensor-memory lane quarter, sharing its columns
 // What bounds it: at 8192 tokens, 14336 x 4096, tensor work at the power limit (forward with bias,
 // SiLU and 8-bit Z 512-656 us by the board's temperature, 1.47-1.88 PFLOP/s; alone and cool 505-516 us,
 // tensor pipe 86-88 % active; dx with the derivative from 8 bits 507; dW 490 us, 93-97 %, to fp32 515). The pair tile
@@ -460,7 +462,7 @@ template <int OP, int COPIES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<OP>::THREADS, 1)
     linear_wide_kernel(const __grid_constant__ typename Wide<OP>::Params p) {
   using C = Wide<OP>;
-  constexpr bool A_MN = OP == OP_DW, B_MN = !loads_as_fwd(OP);
+  constexpr bool A_MN = is_dw(OP), B_MN = !loads_as_fwd(OP);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[C::STAGES];
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];

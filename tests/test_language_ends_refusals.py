@@ -35,7 +35,7 @@ NAN, INF = float("nan"), float("inf")
 CSRC = Path(__file__).resolve().parents[1] / "fsdp_sharded_optimizer_zero_gb300" / "csrc"
 
 
-@pytest.mark.parametrize("name", ["linear_wide.cuh", "fsdp_vocab_loss.cu"])
+@pytest.mark.parametrize("name", ["linear_wide.cuh", "linear_narrow.cuh", "fsdp_vocab_loss.cu"])
 def test_warps_of_the_products_meet_only_where_they_agree_on_leaving(name):
     """As in the linear unit: a role's loops end when a bounded wait gives up, which its warps may see at different
     tiles, so no named barrier counts them. (That wait is not provoked on a GPU: the source has no such barrier.)"""

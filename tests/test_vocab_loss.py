@@ -20,7 +20,10 @@ SHAPES = [(1, 1, 8, 8, 1), (1, 1000, 1000, 72, 1), (5, 129, 144, 64, 2), (130, 2
           (300, 257, 264, 264, 1), (257, 513, 640, 520, 5), (1003, 1157, 1160, 520, 5), (64, 5000, 5120, 768, 8),
           (700, 2100, 2560, 328, 4), (31, 1400, 2048, 136, 8), (2049, 3000, 3008, 128, 2), (20, 4100, 4224, 1032, 3),
           (520, 640, 640, 2056, 16), (4400, 2900, 2944, 192, 1), (600, 700, 704, 8200, 2), (300, 5000, 5120, 1096, 8),
-          (4400, 2900, 2944, 1096, 2)]
+          (4400, 2900, 2944, 1096, 2),
+          # few tokens or few words, and rows long enough for several accumulators
+          (7, 3000, 3008, 2056, 1), (33, 2000, 2048, 8200, 2), (64, 5100, 5120, 4104, 8), (32, 1000, 1024, 16392, 1),
+          (500, 2000, 2048, 4104, 1), (300, 260, 320, 1288, 5)]
 
 
 @pytest.fixture(scope="module")
@@ -170,11 +173,11 @@ def test_flat_and_peaked_logits(z, std):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("k,piece", [(776, 0), (4104, 0), (8200, 256)])
-def test_what_is_left_of_sure_tokens_adds_up_to_nothing(z, k, piece):
+@pytest.mark.parametrize("m,k,piece", [(130, 776, 0), (130, 4104, 0), (130, 8200, 256), (20, 4104, 256), (1500, 4104, 512)])
+def test_what_is_left_of_sure_tokens_adds_up_to_nothing(z, m, k, piece):
     """The gradients of a token's logits add up to 0. Column 0 of X is 0 and of W 1, so dX's is their sum: small
     where the label's probability is near 1, however large the logits, if the backward's logits are the forward's."""
-    m, vocab = 130, 600
+    vocab = 600 if m < 1000 else 5000
     x = randn(m, k).abs().add(0.5).to(BF)
     w = (1.0 + 0.01 * randn(vocab, k, key=1)) * (26.0 / (1.3 * k))
     w[7] *= 40.0 / 26.0

@@ -384,7 +384,7 @@ int launch(LinearParams& p, const Operands& o, cudaStream_t st, const char* who)
       return rc;
   } else {
     if ((rc = encode(&p.a, o.a, p.m, p.k, o.lda, BK, c.wide ? 128 : c.tn, false, who))) return rc;
-    if ((rc = encode_w(p, o.n_shards, o.w, static_cast<int64_t>(o.n_shards) * p.shard_rows, OP == OP_FWD, kCutFrom, &fast,
+    if ((rc = encode_w(p, o.n_shards, o.w, static_cast<int64_t>(o.n_shards) * p.shard_rows, OP == OP_FWD, kCutFrom, false, &fast,
                        who)))
       return rc;
   }

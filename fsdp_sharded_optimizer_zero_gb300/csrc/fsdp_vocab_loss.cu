@@ -27,7 +27,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-struct VocabParams : LinearParams {
+struct VocabParams : ProductParams {
+  CUtensorMap w[2 * kGemmMaxPieces];  // as LinearParams', for two heights of any number of shards
   int w_row0;              // the row of W where this launch's columns (dx: contraction) begin
   int splits, slot_rows;   // dx: parts of the contraction, each its own [slot_rows, n] of y32
   bool add;                // dx: to what y32 holds
@@ -478,6 +479,12 @@ struct Weights {
   const uint16_t* w[kGemmMaxPieces];
 };
 
+// Shards for which there would be one height of copies only, that of 8 rows for a vocabulary of odd size, in 16 maps: the
+// lowest and the highest, in up to 32, where they are long enough to be cut at few of the tiles (16 shards, in one height:
+// 8192 of 50257 x 768 353 us (455-497), gradients 1.15-1.18 ms (1.57); 2000 of 4900 x 768, 312 rows a shard, 29 (33), of
+// 2700 x 768, 176 rows, 21.6 (19.7)). Up to 8 shards, 16 maps do as well.
+bool long_shards(const Weights& w) { return w.n > kGemmMaxPieces / 2 && w.shard_rows >= 256; }
+
 template <int OP>
 int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t st, const char* who) {
   p.shard_rows = w.shard_rows;
@@ -487,7 +494,7 @@ int launch_product(VocabParams& p, const Weights& w, bool one_copy, cudaStream_t
   int rc;
   // a vocabulary's shards are long: copies as high as they can be, cut at the few places where a shard ends
   const bool fwd = OP != OP_DX_SPLIT;
-  if ((rc = encode_w(p, w.n, w.w, p.vocab, fwd, fwd ? 128 : BK, &one_copy, who))) return rc;
+  if ((rc = encode_w(p, w.n, w.w, p.vocab, fwd, fwd ? 128 : BK, long_shards(w), &one_copy, who))) return rc;
   if (p.w_levels > 1) return launch_wide<OP, COPIES_CUT>(p, st, who);
   return one_copy ? launch_wide<OP, COPIES_ONE>(p, st, who) : launch_wide<OP, COPIES_EQUAL>(p, st, who);
 }
@@ -518,7 +525,7 @@ int launch_logits(VocabParams& p, const Weights& w, const zero_bf16* x, cudaStre
   if (c.wide) return blocks > kPartBlocks ? launch_product<OP_PARTS>(p, w, true, st, who) : launch_product<OP>(p, w, true, st, who);
   bool one_copy = false;
   p.shard_rows = w.shard_rows, p.chunk_blocks = kPartBlocks;
-  if ((rc = encode_w(p, w.n, w.w, p.vocab, true, kCutFrom, &one_copy, who))) return rc;
+  if ((rc = encode_w(p, w.n, w.w, p.vocab, true, kCutFrom, long_shards(w), &one_copy, who))) return rc;
   return c.tn == 32   ? launch_few<OP, 32>(p, c.splits, st, who)
          : c.tn == 64 ? launch_few<OP, 64>(p, c.splits, st, who)
                       : launch_few<OP, 128>(p, c.splits, st, who);

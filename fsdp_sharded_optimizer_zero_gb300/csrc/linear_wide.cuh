@@ -43,16 +43,13 @@ constexpr unsigned int kErrAccE = (5u << 8) | 3u;   // MMA waiting for a drained
 constexpr unsigned int kErrAccF = (5u << 8) | 4u;   // epilogue waiting for a finished accumulator
 constexpr unsigned int kErrDrain = (5u << 8) | 5u;  // waiting for copies or MMAs in flight
 
-struct LinearParams {
-  // fwd, dx: the row shards of W, boxes of 64 columns x w_box rows; where they are cut to fit (w_levels > 1),
-  // again with boxes of 4 w_box, 16 w_box rows
-  CUtensorMap w[kGemmMaxPieces];
+struct ProductParams {
   CUtensorMap a;                  // fwd: X, dx: dZ (K-major, box 64 x 128 or TN rows); dw: dZ (MN-major, box 64 x 64)
   CUtensorMap b;                  // dw: X (MN-major, box 64 x 64)
   CUtensorMap out;                // wide kernel, fp32 dW: the output, boxes of 32 columns x 32 rows
   int m, n, k;                    // the product: out [m, n], contraction over k
   int n_shards, shard_rows;       // fwd, dx
-  int w_levels;
+  int w_levels, w_shift;          // heights of W's copies: w_box, w_box << w_shift, ..
   int w_box, w_box_log;           // rows of W per copy: the largest power of two <= 128 (fwd) or 64 (dx) that divides shard_rows
   const uint16_t *bias, *res;     // fwd: bias; fwd, dx: residual
   int act;
@@ -67,6 +64,11 @@ struct LinearParams {
   float scale;                    // dw
   const float* count;             // dw: nullable, what the scale is divided by (1 at least)
   int chunks, chunk_blocks;       // fp32 dw, logits: the contraction in chunks of chunk_blocks K blocks (1 chunk otherwise)
+};
+// fwd, dx: the row shards of W, boxes of 64 columns x w_box rows; where they are cut to fit (w_levels > 1), again with
+// boxes of the other heights
+struct LinearParams : ProductParams {
+  CUtensorMap w[kGemmMaxPieces];
 };
 
 // ------------------------------------------------------------------------------------
@@ -137,12 +139,12 @@ struct Copy {
   uint32_t base;
 };
 // W cut to fit: copy number c.piece of ROWS rows from row c.row of shard c.shard, each as high as the
-// shard allows of w_box, 4 w_box, .., ROWS; false if there are fewer. Rows past the last one count to
+// shard allows of the heights up to ROWS; false if there are fewer. Rows past the last one count to
 // the last shard, past its end (they read zeros).
-template <int ROWS>
-__device__ __forceinline__ bool w_piece(const LinearParams& p, Copy& c) {
+template <int ROWS, class P>
+__device__ __forceinline__ bool w_piece(const P& p, Copy& c) {
   int shard = c.shard, y = c.row, at = 0, level = p.w_levels - 1;
-  const auto box = [&](int l) { return min(p.w_box << (2 * l), ROWS); };
+  const auto box = [&](int l) { return min(p.w_box << (p.w_shift * l), ROWS); };
   if (shard + 1 == p.n_shards || p.shard_rows - y >= ROWS) {
     at = c.piece * box(level), y += at;
   } else {
@@ -161,8 +163,8 @@ __device__ __forceinline__ bool w_piece(const LinearParams& p, Copy& c) {
   return true;
 }
 // to the next K block; false: this lane has nothing to copy for it (had: whether it had for this one)
-template <bool CUT>
-__device__ __forceinline__ bool copy_advance(const LinearParams& p, Copy& c, bool had) {
+template <bool CUT, class P>
+__device__ __forceinline__ bool copy_advance(const P& p, Copy& c, bool had) {
   if (c.k_major) {
     c.x += BK;
   } else if (CUT && c.w_rows) {
@@ -185,15 +187,16 @@ __device__ __forceinline__ bool copy_advance(const LinearParams& p, Copy& c, boo
 }
 // the shard that holds row `row` of W; rows past the last one stay in the last shard, past
 // its end (they read zeros)
-__device__ __forceinline__ void copy_seek(const LinearParams& p, Copy& c, int row) {
+template <class P>
+__device__ __forceinline__ void copy_seek(const P& p, Copy& c, int row) {
   c.shard = min(row / p.shard_rows, p.n_shards - 1);
   c.map = &p.w[c.shard];
   c.y = row - c.shard * p.shard_rows;
 }
 // copies of W (fwd): 128 output columns from n0, K-major, 128 / w_box copies of w_box rows, or (CUT) up to
 // as many lanes with `has` true
-template <bool CUT>
-__device__ __forceinline__ int w_copies_k_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c,
+template <bool CUT, class P>
+__device__ __forceinline__ int w_copies_k_major(const P& p, int i, int n0, int kb0, uint32_t dst, Copy& c,
                                                 bool& has) {
   const int count = 128 >> p.w_box_log;
   if (i >= 0 && i < count) {
@@ -213,8 +216,8 @@ __device__ __forceinline__ int w_copies_k_major(const LinearParams& p, int i, in
 }
 // copies of W (dx): 128 output columns from n0, MN-major: two chunks of 64 columns, the 64 rows
 // of a K block in 64 / w_box copies each, or (CUT) up to as many
-template <bool CUT>
-__device__ __forceinline__ int w_copies_mn_major(const LinearParams& p, int i, int n0, int kb0, uint32_t dst, Copy& c,
+template <bool CUT, class P>
+__device__ __forceinline__ int w_copies_mn_major(const P& p, int i, int n0, int kb0, uint32_t dst, Copy& c,
                                                  bool& has) {
   const int per = 64 >> p.w_box_log, count = 2 * per;
   if (i >= 0 && i < count) {
@@ -714,11 +717,13 @@ int set_smem(OncePerDevice& once, K kernel, uint32_t bytes, const char* who) {
 // The maps of W, given as n row shards of p.shard_rows rows, as a forward (K-major, rows of k elements) or dx
 // (MN-major, rows of n elements) loads it: p.w, p.n_shards, p.shard_rows, p.w_box and p.w_levels. Of its rows
 // those from `rows` on are not there (they read zeros): the last shard's end may be padding. cut_from: copies of
-// fewer rows than this are cut to fit. one_copy: whether an operand of a stage may be one copy; cleared where
-// W's shards do not allow it.
-int encode_w(LinearParams& p, int n, const uint16_t* const* w, int64_t rows, bool fwd, int cut_from, bool* one_copy,
+// fewer rows than this are cut to fit, as many heights as there are maps for: each four times the one before, or
+// (long_shards, whose rows are cut at few places) the lowest and the highest only. one_copy: whether an operand of a
+// stage may be one copy; cleared where W's shards do not allow it.
+template <class P>
+int encode_w(P& p, int n, const uint16_t* const* w, int64_t rows, bool fwd, int cut_from, bool long_shards, bool* one_copy,
              const char* who) {
-  const int most = fwd ? 128 : BK;
+  const int most = fwd ? 128 : BK, maps = long_shards ? static_cast<int>(sizeof(p.w) / sizeof(p.w[0])) : kGemmMaxPieces;
   const int64_t cols = fwd ? p.k : p.n;
   p.n_shards = n;
   // shards that lie back to back are one matrix: one map, and boxes of any height
@@ -729,13 +734,15 @@ int encode_w(LinearParams& p, int n, const uint16_t* const* w, int64_t rows, boo
   // one shard: rows past the last are zeros in any box, so it may be whole
   p.w_box = p.n_shards == 1 ? most : std::min(p.shard_rows & -p.shard_rows, most);
   for (p.w_box_log = 3; (1 << p.w_box_log) < p.w_box;) ++p.w_box_log;
-  // as many as fit in a copy of 4, 16 times the rows
-  p.w_levels = 1;
-  if (p.w_box < cut_from)
-    while ((p.w_levels + 1) * p.n_shards <= kGemmMaxPieces && (p.w_box << (2 * (p.w_levels - 1))) < most) ++p.w_levels;
+  p.w_levels = 1, p.w_shift = 2;
+  if (p.w_box < cut_from) {
+    if (long_shards)
+      for (; p.w_box << p.w_shift < most;) ++p.w_shift;
+    while ((p.w_levels + 1) * p.n_shards <= maps && (p.w_box << (p.w_shift * (p.w_levels - 1))) < most) ++p.w_levels;
+  }
   *one_copy = *one_copy && p.w_box == most && (fwd || p.n % 64 == 0);
   for (int i = 0; i < p.w_levels * p.n_shards; ++i) {
-    const int s = i % p.n_shards, box = std::min(p.w_box << (2 * (i / p.n_shards)), most);
+    const int s = i % p.n_shards, box = std::min(p.w_box << (p.w_shift * (i / p.n_shards)), most);
     const int64_t left = std::min<int64_t>(p.shard_rows, rows - static_cast<int64_t>(s) * p.shard_rows);
     const int rc = !fwd && *one_copy ? encode_mn(&p.w[i], w[s], left, cols, cols, who)
                                      : encode(&p.w[i], w[s], left, cols, cols, 64, box, false, who);

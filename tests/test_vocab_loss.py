@@ -23,7 +23,9 @@ SHAPES = [(1, 1, 8, 8, 1), (1, 1000, 1000, 72, 1), (5, 129, 144, 64, 2), (130, 2
           (4400, 2900, 2944, 1096, 2),
           # few tokens or few words, and rows long enough for several accumulators
           (7, 3000, 3008, 2056, 1), (33, 2000, 2048, 8200, 2), (64, 5100, 5120, 4104, 8), (32, 1000, 1024, 16392, 1),
-          (500, 2000, 2048, 4104, 1), (300, 260, 320, 1288, 5)]
+          (500, 2000, 2048, 4104, 1), (300, 260, 320, 1288, 5),
+          # many long shards cut at multiples of 8 rows
+          (300, 5001, 5248, 264, 16), (700, 4900, 4992, 1096, 16), (20, 4000, 4400, 520, 10)]
 
 
 @pytest.fixture(scope="module")

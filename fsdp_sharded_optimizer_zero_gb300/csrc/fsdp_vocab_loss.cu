@@ -3,16 +3,19 @@
 //
 //   forward   lse_i = log sum_v exp Z_iv, loss_i = lse_i - Z_i[label]: each 256 x 256 tile of Z leaves, per
 //             row and 128 columns, its maximum and the sum of exponentials below it (2 fp32), joined after
-//   backward  in pieces of the vocabulary: Z again from X and the piece of W, dZ = (exp(Z - lse) - onehot) w
-//             in bf16, then the piece's rows of dW = c dZ^T X, and dX += c dZ W
+//   backward  in pieces of the vocabulary: Z again from X and the piece of W, dZ = exp(Z - lse) - onehot in bf16,
+//             then the piece's rows of dW = dZ^T (c g X), and dX += c g dZ W; c what all tokens share (the loss's
+//             scale, one over the count), g a token's own factor
 //
 // The products run in linear_wide_kernel, of few tokens in linear_narrow_kernel; what is here are their epilogues and the
 // joining passes. Softmax
 // statistics and all sums are fp32. dZ is rounded to bf16, as the gradient of a linear unit's output is
-// everywhere in the library: the tensor cores multiply bf16, and its gradients are bf16. The factor c that all tokens
-// share (the loss's scale, one over the count) is left for the fp32 sums: in dZ it would be rounded alike in every
-// label's element, which is about -c, and so bias every gradient by up to 2^-9 (8192 x 32000 from 4096 with c in dZ:
-// 3.7e-3 of the gradients' norm off, now 1.7e-3, the outputs' own rounding).
+// everywhere in the library: the tensor cores multiply bf16, and its gradients are bf16. The factors are left out of it:
+// the label's element is about -1 and so hardly rounded, while with c it would be rounded alike for every token, which
+// biases every gradient by up to 2^-9 (8192 x 32000 from 4096: 3.7e-3 of the gradients' norm off, without 1.7e-3, the
+// outputs' own rounding). c and g multiply fp32 sums; only for dW, whose sums are over the tokens, g (and c with it) goes
+// into X, rounded to bf16 once more: a word that is the label of one token gets that product, which the output no longer
+// rounds (777 x 50257 from 768, with g in dZ: dW 2.4e-3 off).
 //
 // Bound by tensor work: forward 8192 x 50257 from 768 346 us (1.83 PFLOP/s; tensor pipe 83 % active), of which joining
 // the parts takes about 10, from 4096 (vocabulary 32000) 1135 us (1.89); gradients 8192 x 32000 from 4096 3.55 ms
@@ -39,7 +42,7 @@ struct VocabParams : ProductParams {
   float2* part;            // lse: [2 ceil(n / 256)][m]: base-2 maximum, sum of 2^(z log2 e - maximum)
   unsigned int* ticket;    // lse: set to 0 for the kernel that joins the parts
   float* z_label;          // lse: [m]
-  const float *lse, *dloss;
+  const float *lse, *dloss;  // dlogits; dx
 };
 
 template <> struct Wide<OP_LSE> {
@@ -114,15 +117,19 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
     // while the products run: the row's label, as a column of this launch
     int target = -1;
     bool counted = false;
-    float lse2 = 0.0f, weight = 0.0f;
+    float lse2 = 0.0f;
     if (OP != OP_DX_SPLIT && row < p.m) {
       const int label = label_at(p.labels, p.labels_wide, row, p.vocab);
       counted = label >= 0;
       target = counted ? label - p.w_row0 : -1;
       if (is_dlogits(OP) && counted) {
         lse2 = __fmul_rn(__ldg(p.lse + row), kLog2e);
-        weight = p.dloss ? __ldg(p.dloss + row) : 1.0f;
       }
+    }
+    float own = scale;  // dx: of this row
+    if (OP == OP_DX_SPLIT && p.dloss) {
+      own = 0.0f;
+      if (row < p.m && label_at(p.labels, p.labels_wide, row, p.vocab) >= 0) own = __fmul_rn(scale, __ldg(p.dloss + row));
     }
     // 32 logits of the row, of columns col0 ..: joined to s
     Softmax s{__int_as_float(0xff800000), 0.0f};
@@ -165,7 +172,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
       for (int j = 0; j < 32; j += 2) {
         float x, y;
         f2_split(f2_fma(f2_make(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_both(kLog2e), f2_both(-lse2)), x, y);
-        word[j >> 1] = f2_to_bf16x2(f2_mul(f2_make(exp2_fast(x), exp2_fast(y)), f2_both(weight)));
+        word[j >> 1] = f2_to_bf16x2(f2_make(exp2_fast(x), exp2_fast(y)));
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) word[j] = counted ? word[j] : 0u;  // whatever the logits are
@@ -181,7 +188,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
         float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) z = at == j ? __uint_as_float(r[j]) : z;
-        const float v = __fsub_rn(__fmul_rn(exp2_fast(__fmaf_rn(z, kLog2e, -lse2)), weight), weight);
+        const float v = __fsub_rn(exp2_fast(__fmaf_rn(z, kLog2e, -lse2)), 1.0f);
         *reinterpret_cast<uint16_t*>(buf + staged_at(lane, 4 * h + (at >> 3)) + 2 * (at & 7)) = f32_to_bf16_bits(v);
       }
       if (h == 1 || col0 + 32 >= p.cols) {
@@ -251,7 +258,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
     if constexpr (OP == OP_DX_SPLIT) {
       if (p.y32) {
-        if (r0 < p.m) store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, scale, p.add, stage, stores, lane);
+        if (r0 < p.m) store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, own, p.add, stage, stores, lane);
       } else {
 #pragma unroll 1
         for (int c = 0; c < C::EPI_COLS; c += 32) {
@@ -262,7 +269,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
           tmem_ld_32cols(taddr + c, r);
           if (col0 >= p.n) continue;
           const auto two = [&](int i) {
-            return f2_to_bf16x2(f2_mul(f2_make(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_both(scale)));
+            return f2_to_bf16x2(f2_mul(f2_make(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_both(own)));
           };
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -305,7 +312,7 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
 // ------------------------------------------------------------------------------------
 struct RowOfLoss {  // loaded while the main loop runs, all lanes the same
   long long label;
-  float lse, dloss;
+  float lse;
   __device__ __forceinline__ void load(const VocabParams& p, int row, int) {
     if (row >= p.m) return;
     if (p.labels_wide) {
@@ -316,7 +323,6 @@ struct RowOfLoss {  // loaded while the main loop runs, all lanes the same
       label = l;
     }
     if (p.lse) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(lse) : "l"(p.lse + row));
-    if (p.dloss) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(dloss) : "l"(p.dloss + row));
   }
 };
 template <> struct Side4<OP_LSE> : RowOfLoss {};
@@ -347,11 +353,11 @@ __device__ __forceinline__ void epilogue4(const typename Wide<OP>::Params& p, in
     for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
     if ((threadIdx.x & 31) == 0) p.part[static_cast<size_t>(col >> 7) * p.m + row] = make_float2(top, sum);
   } else {
-    const float lse2 = __fmul_rn(side.lse, kLog2e), weight = p.dloss ? side.dloss : 1.0f;
+    const float lse2 = __fmul_rn(side.lse, kLog2e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float e = __fmul_rn(exp2_fast(__fmaf_rn(z[j], kLog2e, -lse2)), weight);
-      z[j] = counted && col + j < p.n ? (at == j ? __fsub_rn(e, weight) : e) : 0.0f;
+      const float e = exp2_fast(__fmaf_rn(z[j], kLog2e, -lse2));
+      z[j] = counted && col + j < p.n ? (at == j ? __fsub_rn(e, 1.0f) : e) : 0.0f;
     }
     if (col < p.cols)
       *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(row) * p.ld + col) =
@@ -461,6 +467,31 @@ __global__ void __launch_bounds__(kThreads) sum_slots_kernel(const float* __rest
   }
 }
 
+// c g X in bf16, a warp a row; zeros where the token is not counted
+__global__ void __launch_bounds__(kThreads) weigh_rows_kernel(const uint16_t* __restrict__ x, int m, int pieces, const void* labels,
+                                                              int wide, int vocab, const float* __restrict__ dloss, float scale,
+                                                              const float* count, uint16_t* __restrict__ out) {
+  allow_next_grid();
+  wait_for_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const float c = dw_scale(scale, count);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); row < m;
+       row += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+    const bool counted = label_at(labels, wide, row, vocab) >= 0;
+    const f2 w = f2_both(__fmul_rn(c, __ldg(dloss + row)));
+    const uint4* from = reinterpret_cast<const uint4*>(x) + row * pieces;
+    uint4* to = reinterpret_cast<uint4*>(out) + row * pieces;
+#pragma unroll 4
+    for (int j = lane; j < pieces; j += 32) {
+      f2 v[4];
+      unpack8(__ldg(from + j), v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = counted ? f2_mul(v[i], w) : 0ull;
+      to[j] = make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------------
 // host side
 // ------------------------------------------------------------------------------------
@@ -531,7 +562,7 @@ int launch_logits(VocabParams& p, const Weights& w, const zero_bf16* x, cudaStre
                       : launch_few<OP, 128>(p, c.splits, st, who);
 }
 
-// The backward's pieces and its workspace: dZ of a piece [m, ld], and where dX is summed in parts, those.
+// The backward's pieces and its workspace: dZ of a piece [m, ld], c g X, and where dX is summed in parts, those.
 // The default piece is as much of the vocabulary as a dZ of kPieceBytes holds: each piece is three launches,
 // and more of them than one share dX through memory.
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
@@ -539,7 +570,7 @@ struct BackwardPlan {
   int64_t piece, pieces, ld, slot_rows;
   int splits;      // of dX's contraction over a piece
   bool slots;      // dX is summed in slots, else written by the product
-  uint64_t dz_bytes, bytes;
+  uint64_t x_at, slots_at, bytes;
   BackwardPlan(int64_t m, int64_t vocab, int64_t k, int64_t asked) {
     piece = asked;
     if (piece == 0) {
@@ -563,8 +594,9 @@ struct BackwardPlan {
       if (s == 1 || t < best) best = t, splits = s;
     }
     slots = splits > 1 || pieces > 1;
-    dz_bytes = up256(2 * static_cast<uint64_t>(m) * static_cast<uint64_t>(ld));
-    bytes = dz_bytes + (slots ? up256(4 * static_cast<uint64_t>(splits) * static_cast<uint64_t>(slot_rows) * static_cast<uint64_t>(k)) : 0);
+    x_at = up256(2 * static_cast<uint64_t>(m) * static_cast<uint64_t>(ld));
+    slots_at = x_at + up256(2 * static_cast<uint64_t>(m) * static_cast<uint64_t>(k));
+    bytes = slots_at + (slots ? up256(4 * static_cast<uint64_t>(splits) * static_cast<uint64_t>(slot_rows) * static_cast<uint64_t>(k)) : 0);
   }
 };
 
@@ -714,13 +746,20 @@ extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_sh
                      workspace ? (unsigned long long)workspace_bytes : 0ull, (unsigned long long)plan.bytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint16_t* dz = static_cast<uint16_t*>(workspace);
-  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.dz_bytes);
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.slots_at);
+  uint16_t* xw = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + plan.x_at);
   const int m = static_cast<int>(m_tokens), k = static_cast<int>(k_in), ld = static_cast<int>(plan.ld);
   const float* count = total ? total + 1 : nullptr;
   cudaError_t e = cudaSuccess;
   if (dW && rows_out > vocab)  // the padding's rows
     e = cudaMemsetAsync(dW + vocab * k_in, 0, static_cast<size_t>(rows_out - vocab) * static_cast<size_t>(k_in) * 2, st);
   if (e != cudaSuccess) return set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  if (dW && dloss) {
+    const int64_t blocks = std::min<int64_t>((m_tokens + kThreads / 32 - 1) / (kThreads / 32), static_cast<int64_t>(num_sms()) * 8);
+    e = launch_overlapped(weigh_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, 1, st, X, m, k / 8, labels,
+                          label_bytes == 8 ? 1 : 0, static_cast<int>(vocab), dloss, scale, count, xw);
+    if (e != cudaSuccess) return set_error(ZERO_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  }
   for (int64_t c0 = 0; c0 < vocab; c0 += plan.piece) {
     const int cols = static_cast<int>(std::min(plan.piece, vocab - c0));
     VocabParams p;
@@ -729,14 +768,17 @@ extern "C" int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_sh
     p.w_row0 = static_cast<int>(c0), p.vocab = static_cast<int>(vocab);
     p.cols = (cols + 7) / 8 * 8, p.ld = ld, p.y = dz;
     p.labels = labels, p.labels_wide = label_bytes == 8;
-    p.lse = lse, p.dloss = dloss;
+    p.lse = lse;
     if ((rc = launch_logits<OP_DLOGITS, OP_DLOGITS_PARTS>(p, w, X, st, who))) return rc;
-    if (dW && (rc = launch_linear_dw(dz, ld, X, m, cols, k, scale, count, dW + c0 * k_in, st, who))) return rc;
+    if (dW && (rc = dloss ? launch_linear_dw(dz, ld, xw, m, cols, k, 1.0f, nullptr, dW + c0 * k_in, st, who)
+                          : launch_linear_dw(dz, ld, X, m, cols, k, scale, count, dW + c0 * k_in, st, who)))
+      return rc;
     if (!dX) continue;
     VocabParams d;
     memset(static_cast<void*>(&d), 0, sizeof(d));
     d.m = m, d.n = k, d.k = cols;
     d.w_row0 = p.w_row0, d.vocab = p.vocab, d.scale = scale, d.count = count;
+    d.labels = labels, d.labels_wide = p.labels_wide, d.dloss = dloss;
     // a shorter last piece may have fewer K blocks than there are parts: a part has one at least
     d.splits = static_cast<int>(std::min<int64_t>(plan.splits, (cols + BK - 1) / BK));
     d.slot_rows = static_cast<int>(plan.slot_rows), d.add = c0 > 0;

@@ -662,19 +662,19 @@ ZERO_API int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_shard
                                      int label_bytes, float* loss, float* lse, float* total, void* workspace,
                                      uint64_t workspace_bytes, zero_stream_t stream);
 
-/* Bytes of device workspace fsdp_vocab_loss_backward needs: dZ of one piece, 2 * m_tokens * piece, and
- * fp32 sums of dX where they are made in parts. piece: columns of the vocabulary at a time, a multiple of
+/* Bytes of device workspace fsdp_vocab_loss_backward needs: dZ of one piece, 2 * m_tokens * piece, X times the tokens'
+ * factors, 2 * m_tokens * k_in, and fp32 sums of dX where they are made in parts. piece: columns of the vocabulary at a time, a multiple of
  * 256; 0: as many as a dZ of 2^30 bytes holds. */
 ZERO_API int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab, int64_t k_in, int64_t piece,
                                                 uint64_t* bytes);
 
-/* Gradients of c times the sum over the counted tokens of dloss[i] loss[i], c = scale / max(total[1], 1), with
- * dloss (fp32 [m_tokens]) and total (as the forward wrote it) nullable, then 1: dZ = (exp(Z - lse) -
- * onehot(label)) dloss, computed piece by piece from X and W again (the forward's Z, bit for bit) and rounded to bf16; dX = bf16(c dZ W)
- * [m_tokens, k_in] and dW = bf16(c dZ^T X) [rows_out, k_in], c applied to the fp32 sums, one of the two nullable. (A
- * factor that all tokens share belongs in scale: in dloss it is rounded alike with every label's element.) A token
- * that is not counted has zeros in dZ and dX whatever its logits, but its row of X enters dW's product, times zero:
- * it has to be finite. The result's bits depend on piece through the rounding of fp32 sums only. */
+/* Gradients of c times the sum over the counted tokens of g[i] loss[i], c = scale / max(total[1], 1), g = dloss
+ * (fp32 [m_tokens]); dloss and total (as the forward wrote it) are nullable, then 1: dZ = exp(Z - lse) - onehot(label),
+ * computed piece by piece from X and W again (the forward's Z, bit for bit) and rounded to bf16; dX = bf16(c g dZ W)
+ * [m_tokens, k_in], c g applied to the fp32 sums, and dW = bf16(c dZ^T X) [rows_out, k_in], with dloss bf16(dZ^T
+ * bf16(c g X)), one of the two nullable. A token that is not counted has zeros in dZ and dX whatever its logits and its
+ * dloss; without dloss its row of X enters dW's product, times zero: it has to be finite. The result's bits depend on
+ * piece through the rounding of fp32 sums only. */
 ZERO_API int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
                                       int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
                                       int label_bytes, const float* lse, const float* dloss, const float* total,

@@ -122,23 +122,26 @@ class Case:
         return dX[:-64].view(self.m, self.k) if dx else None, dW[:-64].view(self.rows, self.k) if dw else None
 
     def check_backward(self, z, lse, dX, dW, scale, dloss, total, pieces):
-        w = self.weights(dloss)[:, None]
-        c = float(scale) / (1.0 if total is None else max(1.0, float(total[1])))  # on the sums: 2 roundings
+        c = torch.tensor(scale, device=DEV) / (1.0 if total is None else total[1].clamp(min=1.0))
+        cg = (c * self.weights(dloss).float()).double()[:, None]  # rounded twice, as it is there, and where it multiplies
         p = torch.exp(self.z - lse.double()[:, None])
         hot = torch.zeros_like(p).scatter_(1, self.at[:, None], 1.0) * self.real[:, None]
-        dz = (p - hot) * w
-        # z, the argument's roundings (of z, lse and their difference), the exponential, the weight's product
+        dz = (p - hot) * self.real[:, None]
+        # z, the argument's roundings (of z, lse and their difference), the exponential
         size = self.z.abs() + lse.double().abs()[:, None] + 1
-        e = w.abs() * (p * (self.ez + 4 * U * size + 2.0 ** -20) * 1.1 + 4 * U * hot) + 4 * U * dz.abs()
+        e = (p * (self.ez + 4 * U * size + 2.0 ** -20) * 1.1 + 4 * U * hot) * self.real[:, None] + 4 * U * dz.abs()
         lo, hi = ((dz + s * e).float().to(BF).double() for s in (-1.0, 1.0))
         mid, rad = (lo + hi) / 2, (hi - lo) / 2
-        want = c * (mid @ self.w64)
-        bound = abs(c) * (rad @ self.w64.abs() + (self.vocab + 32 + pieces) * SUM * (mid.abs() @ self.w64.abs())) + 3 * U * want.abs()
+        want = cg * (mid @ self.w64)
+        bound = cg.abs() * (rad @ self.w64.abs() + (self.vocab + 32 + pieces) * SUM * (mid.abs() @ self.w64.abs())) + 3 * U * want.abs()
         if dX is not None:
             inside(dX, want, bound + B16 * (want.abs() + bound), "dX")
             assert not bool(dX[~self.real].any())
-        want = c * (mid.t() @ self.x64)
-        bound = abs(c) * (rad.t() @ self.x64.abs() + (self.m + 1) * SUM * (mid.abs().t() @ self.x64.abs())) + 3 * U * want.abs()
+        # with factors of the tokens, X times them is rounded to bf16; else c multiplies the sums
+        x = self.x64 if dloss is None else (cg.float() * self.x.float()).to(BF).double()
+        c = c.double() if dloss is None else torch.ones((), dtype=torch.float64, device=DEV)
+        want = c * (mid.t() @ x)
+        bound = c.abs() * (rad.t() @ x.abs() + (self.m + 1) * SUM * (mid.abs().t() @ x.abs())) + 3 * U * want.abs()
         if dW is not None:
             inside(dW[:self.vocab], want, bound + B16 * (want.abs() + bound), "dW")
             assert not bool(dW[self.vocab:].any())
@@ -172,6 +175,20 @@ def test_flat_and_peaked_logits(z, std):
     _, lse, total = c.check_forward(z)
     dX, dW = c.backward(z, lse, total=total)
     c.check_backward(z, lse, dX, dW, 1.0, None, total, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,vocab", [(20, 300), (300, 5000)])
+def test_padded_tokens_may_hold_anything_with_factors(z, m, vocab):
+    c = Case(m, vocab, (vocab + 7) // 8 * 8, 264, 1)
+    _, lse, total = c.forward(z)
+    g = torch.rand(m, generator=gen_of(m, 9), device=DEV)
+    dX, dW = c.backward(z, lse, 2.0, g, total)
+    c.x[~c.real], g[~c.real] = float("nan"), float("inf")
+    loss, lse1, total1 = c.forward(z)
+    assert torch.equal(total1, total) and torch.equal(lse1[c.real], lse[c.real]) and not bool(loss[~c.real].any())
+    dX1, dW1 = c.backward(z, lse1, 2.0, g, total)
+    assert torch.equal(dX1, dX) and torch.equal(dW1, dW) and not bool(dX1[~c.real].any())
 
 
 @pytest.mark.gpu

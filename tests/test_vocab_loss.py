@@ -220,6 +220,7 @@ def test_what_is_left_of_sure_tokens_adds_up_to_nothing(z, m, k, piece):
     inside(dX[:, 0], torch.zeros_like(top), bound * (1 + B16), "the sum of dZ")
 
 
+@pytest.mark.gpu
 def test_no_token_counts(z):
     c = Case(200, 600, 640, 136, 2)
     c.labels.fill_(-100)

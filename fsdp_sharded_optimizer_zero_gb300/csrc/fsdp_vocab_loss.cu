@@ -427,12 +427,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const float
   __syncthreads();
   if (!last) return;
   __threadfence();
-  float sum = 0.0f, lost = 0.0f;  // a thread keeps what its additions round off
+  float sum = 0.0f, lost = 0.0f;  // a thread keeps what its additions round off, as long as the sum is finite
   int count = 0;
   for (int64_t i = threadIdx.x; i < gridDim.x; i += 32 * kJoinWarps) {
     const float2 v = __ldcg(block_total + i);
     const float x = __fsub_rn(v.x, lost), t = __fadd_rn(sum, x);
-    lost = __fsub_rn(__fsub_rn(t, sum), x);
+    lost = finite_or_0(__fsub_rn(__fsub_rn(t, sum), x));
     sum = t;
     count += __float_as_int(v.y);
   }

@@ -656,7 +656,9 @@ ZERO_API int fsdp_vocab_loss_forward_workspace(int64_t m_tokens, int64_t vocab, 
  * [m_tokens]. total (nullable, 2 fp32): the sum of the losses and the number of counted tokens; their
  * quotient is the mean loss. X [m_tokens, k_in], W [rows_out, k_in] bf16 as row shards of a multiple of 8
  * rows. Z is an fp32 sum of exact bf16 products, in parts of 1024 (bound as fsdp_unit_forward) that are added with
- * rounding to nearest; exponentials are fp32 within 2^-21 of themselves. */
+ * rounding to nearest. The softmax is taken below the row's maximum: exponentials are fp32, within 2^-22 (1 + |Z -
+ * max|) of themselves, and loss[i] is (max - Z[label]) + log(sum), not made from the rounded lse[i]: a finite one is never
+ * below 0. */
 ZERO_API int fsdp_vocab_loss_forward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
                                      int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,
                                      int label_bytes, float* loss, float* lse, float* total, void* workspace,

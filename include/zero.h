@@ -672,7 +672,8 @@ ZERO_API int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab,
 
 /* Gradients of c times the sum over the counted tokens of g[i] loss[i], c = scale / max(total[1], 1), g = dloss
  * (fp32 [m_tokens]); dloss and total (as the forward wrote it) are nullable, then 1: dZ = exp(Z - lse) - onehot(label),
- * computed piece by piece from X and W again (the forward's Z, bit for bit) and rounded to bf16; dX = bf16(c g dZ W)
+ * computed piece by piece from X and W again (the forward's Z, bit for bit; exponentials of the rounded lse within 2^-22 (1 +
+ * |Z - lse|) of themselves) and rounded to bf16; dX = bf16(c g dZ W)
  * [m_tokens, k_in], c g applied to the fp32 sums, and dW = bf16(c dZ^T X) [rows_out, k_in], with dloss bf16(dZ^T
  * bf16(c g X)), one of the two nullable. A token that is not counted has zeros in dZ and dX whatever its logits and its
  * dloss; without dloss its row of X enters dW's product, times zero: it has to be finite. The result's bits depend on

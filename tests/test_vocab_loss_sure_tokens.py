@@ -74,3 +74,25 @@ def test_losses(z, shape):
     assert bool(sure[0]) and not bool(c.loss[sure].any())
     lse = top + log
     assert bool(((c.lse.double() - lse).abs() <= off + U * lse.abs() + 2.0 ** -30).all())
+
+
+@pytest.mark.parametrize("piece", [0, 256])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_gradients(z, shape, piece):
+    """dX's first column, the sum of dZ times W's first."""
+    c = Sure(z, *shape)
+    dX = torch.empty_like(c.x)
+    z.fsdp_vocab_loss_backward([c.shard], c.x, c.labels, c.lse, dX, None, vocab=c.vocab, piece=piece)
+    z.zero_device_status()
+    d = c.z - c.lse.double()[:, None]
+    p = torch.exp(d)
+    hot = torch.zeros_like(p).scatter_(1, c.labels[:, None], 1.0)
+    dz, w = p - hot, c.w[:, 0].double()
+    # the argument's difference, product and rounded log2 e, the exponential, the label's subtraction, then bf16; fp32 sums
+    e = p * (4 * U * d.abs() + EX) + U * dz.abs() * hot
+    e = e + B16 * (dz.abs() + e)
+    want = dz @ w
+    bound = e @ w.abs() + (c.vocab + 32) * SUM * (dz.abs() @ w.abs())
+    off = (dX[:, 0].double() - want).abs()
+    bad = off - bound - B16 * (want.abs() + bound)
+    assert bool((bad <= 0).all()), (float(bad.max()), int((bad > 0).sum()))

@@ -122,18 +122,14 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
     const int c0 = nb * 256 + part * C::EPI_COLS;
     // while the products run: the row's label, as a column of this launch
     int target = -1;
-    bool counted = false;
-    float lse = 0.0f;
-    if (OP != OP_DX_SPLIT && row < p.m) {
+    bool counted = false;  // not: dZ and dX are 0, selected and not multiplied, whatever X and W hold
+    float lse = 0.0f, own = scale;  // own: dx, of this row
+    if (row < p.m) {
       const int label = label_at(p.labels, p.labels_wide, row, p.vocab);
       counted = label >= 0;
       target = counted ? label - p.w_row0 : -1;
       if (is_dlogits(OP) && counted) lse = __ldg(p.lse + row);
-    }
-    float own = scale;  // dx: of this row
-    if (OP == OP_DX_SPLIT && p.dloss) {
-      own = 0.0f;
-      if (row < p.m && label_at(p.labels, p.labels_wide, row, p.vocab) >= 0) own = __fmul_rn(scale, __ldg(p.dloss + row));
+      if (OP == OP_DX_SPLIT && counted && p.dloss) own = __fmul_rn(scale, __ldg(p.dloss + row));
     }
     // 32 logits of the row, of columns col0 ..: joined to s
     Softmax s{__int_as_float(0xff800000), 0.0f};
@@ -261,7 +257,8 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * 256 + part * C::EPI_COLS;
     if constexpr (OP == OP_DX_SPLIT) {
       if (p.y32) {
-        if (r0 < p.m) store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, own, p.add, stage, stores, lane);
+        if (r0 < p.m)
+          store_sums<C::EPI_COLS>(&p.out, taddr, part_k * p.slot_rows + r0, c0, p.n, own, p.add, stage, stores, lane, counted);
       } else {
 #pragma unroll 1
         for (int c = 0; c < C::EPI_COLS; c += 32) {
@@ -271,6 +268,8 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
           uint32_t r[32];
           tmem_ld_32cols(taddr + c, r);
           if (col0 >= p.n) continue;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = counted ? r[j] : 0u;
           const auto two = [&](int i) {
             return f2_to_bf16x2(f2_mul(f2_make(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_both(own)));
           };

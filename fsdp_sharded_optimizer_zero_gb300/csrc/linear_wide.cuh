@@ -400,15 +400,17 @@ __device__ __forceinline__ float dw_scale(float scale, const float* count) {
 // made: the two buffers alternate over all of them, across tiles, and a buffer is written again once all
 // stores but the newest, which reads the other one, have read theirs. Counted by a tile's own columns, two
 // stores in a row would leave from buffer 0 where a tile at the right edge has an odd number of 32-column
-// blocks. add: to what is there.
+// blocks. add: to what is there. live: whether this thread's row is anything but zeros.
 template <int COLS>
 __device__ __forceinline__ void store_sums(const CUtensorMap* out, uint32_t taddr, int row, int c0, int n, float scale,
-                                           bool add, uint8_t* stage, uint32_t& stores, int lane) {
+                                           bool add, uint8_t* stage, uint32_t& stores, int lane, bool live = true) {
 #pragma unroll 1
   for (int c = 0; c < COLS; c += 32) {
     uint32_t r[32];
     tmem_ld_32cols(taddr + c, r);
     if (c0 + c >= n) continue;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = live ? r[j] : 0u;
     const f2 s = f2_both(scale);
     uint8_t* buf = stage + (stores++ & 1u) * 4096u;
     if (lane == 0) bulk_wait_group_read<1>();

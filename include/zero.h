@@ -675,8 +675,8 @@ ZERO_API int fsdp_vocab_loss_backward_workspace(int64_t m_tokens, int64_t vocab,
  * computed piece by piece from X and W again (the forward's Z, bit for bit; exponentials of the rounded lse within 2^-22 (1 +
  * |Z - lse|) of themselves) and rounded to bf16; dX = bf16(c g dZ W)
  * [m_tokens, k_in], c g applied to the fp32 sums, and dW = bf16(c dZ^T X) [rows_out, k_in], with dloss bf16(dZ^T
- * bf16(c g X)), one of the two nullable. A token that is not counted has zeros in dZ and dX whatever its logits and its
- * dloss; without dloss its row of X enters dW's product, times zero: it has to be finite. The result's bits depend on
+ * bf16(c g X)), one of the two nullable. A token that is not counted has zeros in dZ and dX whatever its logits, its dloss
+ * and W are; without dloss its row of X enters dW's product, times zero: it has to be finite. The result's bits depend on
  * piece through the rounding of fp32 sums only. */
 ZERO_API int fsdp_vocab_loss_backward(int n_ranks, const zero_bf16* const w_shards[], int64_t rows_out, int64_t vocab,
                                       int64_t k_in, const zero_bf16* X, int64_t m_tokens, const void* labels,

@@ -49,3 +49,23 @@ def test_total_of_many_tokens(z, m):
     d = loss.double()
     assert abs(float(total[0]) - float(d.sum())) <= 28 * U * float(d.abs().sum())
     assert float(total[1]) == float(c.real.sum())
+
+
+@pytest.mark.parametrize("factors", [False, True])
+@pytest.mark.parametrize("m,vocab,k,piece", [(200, 60, 72, 0), (20, 60, 72, 0), (200, 5000, 264, 0), (200, 5000, 264, 1024), (20, 5000, 1096, 0)])
+def test_padded_tokens_have_no_gradient_beside_words_that_are_not_finite(z, m, vocab, k, piece, factors):
+    """dX of a token that is not counted is 0, whatever W holds: in one part and in several, in one piece and in more."""
+    rows = (vocab + 7) // 8 * 8
+    c = Case(m, vocab, rows, k, 1)
+    g = torch.rand(m, generator=gen_of(m, 9), device=DEV) if factors else None
+    _, lse, total = c.forward(z)
+    want, _ = c.backward(z, lse, 2.0, g, total, piece, dw=False)
+    w = c.shards[0]
+    w[11, 3], w[vocab // 2, 5], w[vocab - 1, 7] = math.nan, math.inf, -math.inf
+    _, lse1, total1 = c.forward(z)
+    assert bool((~c.real).any()) and bool(lse1[c.real].isnan().all()) and float(total1[1]) == float(total[1])
+    dX, _ = c.backward(z, lse1, 2.0, g, total1, piece, dw=False)
+    assert not bool(dX[~c.real].any()) and bool(dX[c.real].isnan().any(1).all())
+    # with the finite words' lse the rows of counted tokens are not finite where W is not, and the others' are 0 still
+    dX, _ = c.backward(z, lse, 2.0, g, total, piece, dw=False)
+    assert not bool(dX[~c.real].any())

@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPass
 }
 
 // exclusive sums over all of count, in place, by one block: where there are so many blocks that each of them cannot
-// add up the others' counts itself
+// add up the others' counts itself. One block is slow at that, 4096 counts a round: 262144 tokens into 50257 x 768 fp32 take
+// 199 us (floor 82), 1048576 641 (261); without it 131072 take 98 (53).
 constexpr int kOwnScan = 64;
 __global__ void __launch_bounds__(1024) sort_scan_kernel(int* count, int64_t n) {
   __shared__ int warp_sum[32];

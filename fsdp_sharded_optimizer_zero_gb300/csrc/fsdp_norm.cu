@@ -494,8 +494,9 @@ __global__ void __launch_bounds__(512) norm_params_kernel(const float* __restric
 }
 
 // ------------------------------------------------------------------------------------
-// rows wider than a block holds: a block a row, read again from L2 for each pass (2000 x 40000: 75 us, 4.3 TB/s;
-// backward with residual 199 us)
+// rows wider than a block holds: a block a row, read again from L2 for each pass. 2000 x 40000: 75 us, 4.3 TB/s (floor 47):
+// three passes over a row, with two sums over the block between them that nothing hides; backward with residual 199 us
+// (94): the column sums are a launch that reads X and dY once more from memory, 47 us of it
 // ------------------------------------------------------------------------------------
 // N values summed over the block, given to all threads
 template <int N>
@@ -687,8 +688,9 @@ auto with_backward_shape(int64_t cols, F&& f) {
 }
 
 // dgamma and dbeta in the launch that computes dX: up to 1024 rows. With residual, in one launch and in two: 1 x 4096
-// 2.2 and 4.7 us, 777 x 2304 8.3 and 9.6, 777 x 14336 22 and 31, 1024 x 4096 12.2 and 13.4, 1024 x 2304 12.3 and 10.8,
-// 2048 x 4096 22.4 and 18.0.
+// 2.2 and 4.7 us, 777 x 2304 8.3 and 9.6, 777 x 14336 22 and 31, 1024 x 4096 12.2 and 13.4, 2048 x 4096 22.4 and 18.0.
+// Rows alone do not quite decide: 1024 x 2304 takes 12.3 in one launch and would take 10.8 in two, since its rows no
+// longer fit beside the columns' blocks in one round.
 constexpr int64_t kFewRows = 1024;
 bool few_rows_backward(int64_t rows, int64_t cols) { return rows <= kFewRows && cols <= kWidest; }
 // blocks of the backward kernel, and so partial sums a column

@@ -15,13 +15,18 @@
 // biases every gradient by up to 2^-9 (8192 x 32000 from 4096: 3.7e-3 of the gradients' norm off, without 1.7e-3, the
 // outputs' own rounding). c and g multiply fp32 sums; only for dW, whose sums are over the tokens, g (and c with it) goes
 // into X, rounded to bf16 once more: a word that is the label of one token gets that product, which the output no longer
-// rounds (777 x 50257 from 768, with g in dZ: dW 2.4e-3 off).
+// rounds (777 x 50257 from 768: dW 2.2e-3 off, with g in dZ 2.4e-3; where words are many tokens' labels up to 2.6e-3; the
+// output's rounding alone 1.7e-3). What that rounds off, as a second part of X, would take dW's product once more, a third
+// of the call.
 //
-// Bound by tensor work: forward 8192 x 50257 from 768 346 us (1.83 PFLOP/s; tensor pipe 83 % active), of which joining
-// the parts takes about 10, from 4096 (vocabulary 32000) 1135 us (1.89); gradients 8192 x 32000 from 4096 3.55 ms
-// (1.82; at the power limit 3.97), 8192 x 50257 from 768 1.16-1.18 ms (1.61-1.64: dZ's product 386 us, held up by the
-// 824 MB that it writes, tensor pipe 74 %; dW's 360, dX's 344). Of few tokens: W's bytes, one of 32000 x 4096 45 us (5.8
-// TB/s), its gradients 157 (W read twice, dW written; 50257 x 768 21 and 69 us).
+// Bound by tensor work. On the device, in a graph of a few ms, W as 8 shards back to back: forward 8192 x 50257 from 768
+// 347-357 us (1.78-1.82 PFLOP/s; tensor pipe 82 % active), of which joining the parts takes about 10, from 4096 (vocabulary
+// 32000) 1128 us (1.90); gradients 8192 x 32000 from 4096 3.52-3.62 ms (1.78-1.83), 8192 x 50257 from 768 1.13-1.19 ms
+// (1.59-1.69: dZ's product 394 us, held up by the 824 MB that it writes, tensor pipe 73 %; dW's 361, dX's 340). Called
+// again and again the board is at its power limit: the first 385-402 us, the third 3.9-4.1 ms. Shards that lie apart and end
+// inside tiles cost copies: 50257 x 768 361 us and 1.25 ms. Of few tokens: W's bytes, one of 32000 x 4096 45 us (5.8 TB/s;
+// shards apart 51), its gradients 157 (W read twice, dW written). One of 50257 x 768 23 and 69 us: 393 tiles of 128 words
+// are more than the 304 CTAs that are resident, so a second round has 89, and one lane of the joining pass has all 393 parts.
 #include "linear_narrow.cuh"
 
 namespace zgb {
@@ -207,7 +212,9 @@ __device__ __forceinline__ void wide_epilogue(const typename Wide<OP>::Params& p
                      : "memory");
     };
     if constexpr (OP == OP_LSE_PARTS || OP == OP_DLOGITS_PARTS) {
-      // the row's 128 logits, added up part by part with rounding to nearest
+      // the row's 128 logits, added up part by part with rounding to nearest: 128 of the 168 registers that ten warps leave a
+      // thread, so some spill (bytes stored and loaded a thread: dZ 532 and 564, the loss 40 and 72), once a tile. Half the
+      // columns a warp needs sixteen epilogue warps, 112 registers
       f2 z[C::EPI_COLS / 2];
 #pragma unroll
       for (int j = 0; j < C::EPI_COLS / 2; ++j) z[j] = 0ull;
